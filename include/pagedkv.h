@@ -79,6 +79,8 @@ typedef enum pkv_dtype { PKV_F16 = 0, PKV_BF16 = 1, PKV_INT8 = 2 } pkv_dtype;
                                         > max_blocks_per_seq*block_size (clamped)      */
 #define PKV_DEVERR_COPY_PAIR   0x8u  /* copy pair entry outside [0, num_blocks)       */
 #define PKV_DEVERR_TIMEOUT     0x10u /* a bounded wait on an async copy gave up       */
+#define PKV_DEVERR_ROPE_AXIS   0x20u /* axis_of_pair entry outside [0, num_axes)      */
+#define PKV_DEVERR_KEPT        0x40u /* kept position outside the context, or (in place) below its rank */
 
 /*
  * pkv_reshape_and_cache -- write each new token's K and V rows into its slot.
@@ -291,6 +293,119 @@ PKV_API pkv_status pkv_paged_attention_decode_shared_prefix(
     int block_size, float scale, void *out, void *workspace, size_t workspace_bytes,
     int partition_size, pkv_dtype dtype, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Operators that a model's layers run around plain attention.  The pages have
+ * no counterpart for them: rotary positions, score forms and masks belong to
+ * the model, and eviction bounds a context that the pages let grow.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * pkv_rope_reshape_and_cache -- rotary positions with one to four axes on the
+ * queries and the new keys, and the cache write: q_out gets the rotated
+ * queries, the slot of each token its rotated K row and its V row.  For token
+ * n, pair i = 0 .. rotary_dim/2 - 1 of a head's channels turns by
+ *     angle = positions[axis_of_pair[i]][n] * inv_freq[i]:
+ *     (a, b) -> (a cos - b sin, b cos + a sin)
+ * where pair i is channels (i, i + rotary_dim/2), or (2i, 2i + 1) with
+ * interleaved != 0; the channels from rotary_dim on are copied.  Several axes
+ * serve tokens with several positions (time, height and width of a video's
+ * patches); axis_of_pair may assign them in sections or in turn.
+ *
+ *   q, k_new, v_new   rows of [num_tokens] tokens, [heads][head_dim] dense
+ *                  within a token and q_stride / k_stride / v_stride elements
+ *                  from token to token (multiples of 8, at least a row): the
+ *                  parts of a fused projection's output are taken in place.
+ *   positions      [num_axes][num_tokens] int64, device; any value (negative
+ *                  ones turn backwards).
+ *   axis_of_pair   [rotary_dim/2] int32, device; NULL: axis 0 for every pair.
+ *                  An entry outside [0, num_axes) raises PKV_DEVERR_ROPE_AXIS
+ *                  and leaves its pair unrotated.
+ *   inv_freq       [rotary_dim/2] double, device: radians per position.
+ *   rotary_dim     a multiple of 16 up to head_dim (else PKV_ERR_UNSUPPORTED
+ *                  / PKV_ERR_INVALID_ARG).
+ *   slot_mapping   as pkv_reshape_and_cache; a token whose slot is negative or
+ *                  out of range writes no cache row, its q_out row is written.
+ *   q_out          q_out_stride elements from token to token; may be q itself
+ *                  (same pointer and stride), else must not overlap the inputs.
+ * The angle is reduced modulo one turn in 64-bit integers, so positions in
+ * the millions keep their angles (error |position| * 2^-53 turns); sine,
+ * cosine and the rotation are fp32, rounded once to the stored type.
+ */
+PKV_API pkv_status pkv_rope_reshape_and_cache(
+    const void *q, int64_t q_stride, const void *k_new, int64_t k_stride, const void *v_new,
+    int64_t v_stride, const int64_t *positions, int num_axes, const int32_t *axis_of_pair,
+    const double *inv_freq, int rotary_dim, int interleaved, const int64_t *slot_mapping,
+    int64_t num_tokens, void *q_out, int64_t q_out_stride, void *k_cache, void *v_cache,
+    int64_t num_blocks, int64_t block_stride_elems, int num_q_heads, int num_kv_heads,
+    int head_dim, int block_size, pkv_dtype dtype, void *stream);
+
+/* pkv_rope_reshape_and_cache into an INT8 cache: the rotated K row (fp32) and
+ * the V row are quantised as by pkv_reshape_and_cache_int8. */
+PKV_API pkv_status pkv_rope_reshape_and_cache_int8(
+    const void *q, int64_t q_stride, const void *k_new, int64_t k_stride, const void *v_new,
+    int64_t v_stride, const int64_t *positions, int num_axes, const int32_t *axis_of_pair,
+    const double *inv_freq, int rotary_dim, int interleaved, const int64_t *slot_mapping,
+    int64_t num_tokens, void *q_out, int64_t q_out_stride, int8_t *k_cache, int8_t *v_cache,
+    int64_t num_blocks, int64_t block_stride_elems, int num_q_heads, int num_kv_heads,
+    int head_dim, int block_size, const float *k_scale, const float *v_scale, pkv_dtype dtype,
+    void *stream);
+
+/*
+ * pkv_evict_select -- which tokens of each (sequence, KV head) stay in the
+ * cache.  A context of L = context_lens[i] tokens keeps n = min(L, budget):
+ * all of them when L <= budget, else the first `sinks`, the last `recent` and
+ * the budget - sinks - recent heaviest of those between (equal weights: the
+ * lower position; a NaN weight ranks below every number).
+ *
+ *   weights        [num_seqs][num_kv_heads][weights_stride] fp32, device: the
+ *                  weight of each cached token, as
+ *                  pkv_paged_attention_decode_scored accumulates it.
+ *   context_lens   [num_seqs] int32, device; max_context_len bounds them on
+ *                  the host (a value outside raises PKV_DEVERR_CONTEXT_LEN and
+ *                  is clamped) and must not exceed weights_stride.
+ *   sinks + recent <= budget, budget > 0.
+ *   weights_out    NULL, or a buffer of the same shape that gets the kept
+ *                  tokens' weights in their new places [0, n) and zeros in
+ *                  [n, L); the rest of a row is left as it is.  May be
+ *                  `weights` itself, else must not overlap it.
+ *   kept           [num_seqs][num_kv_heads][budget] int32: the kept positions,
+ *                  ascending, then -1.
+ *   kept_lens      [num_seqs] int32: n, the context lengths after eviction.
+ */
+PKV_API pkv_status pkv_evict_select(const float *weights, int64_t weights_stride,
+                                    const int32_t *context_lens, int max_context_len,
+                                    int num_seqs, int num_kv_heads, int budget, int sinks,
+                                    int recent, float *weights_out, int32_t *kept,
+                                    int32_t *kept_lens, void *stream);
+
+/*
+ * pkv_evict_compact -- move the K and V rows of the kept tokens to the front of
+ * each sequence's context (bit-exact): row kept[i][h][j] of head h becomes row
+ * j, for j < kept_lens[i].  dtype is the cache's: PKV_F16, PKV_BF16 or PKV_INT8.
+ *
+ *   block_tables, context_lens   the contexts before eviction.
+ *   kept, kept_lens, budget      as pkv_evict_select writes them.
+ *   dst_block_tables  [num_seqs][dst_max_blocks_per_seq] int32, device: fresh
+ *                  blocks for the compacted contexts, none of which belongs to
+ *                  any of the source contexts; the sources are left as they
+ *                  are.  NULL (or block_tables itself) compacts in place: then
+ *                  kept must ascend, and every block that gets rows must belong
+ *                  to its sequence alone (pkv_bm_make_private).
+ * Rows of the destination past kept_lens[i] are left as they are.  A kept
+ * position outside its context (or, in place, below its rank) raises
+ * PKV_DEVERR_KEPT, a bad table entry PKV_DEVERR_BLOCK_TABLE, and that row is
+ * skipped; lengths that do not fit raise PKV_DEVERR_CONTEXT_LEN and skip the
+ * sequence.  Afterwards the context lengths are kept_lens, and the blocks past
+ * them can be freed (pkv_bm_truncate).
+ */
+PKV_API pkv_status pkv_evict_compact(void *k_cache, void *v_cache, int64_t num_blocks,
+                                     int64_t block_stride_elems, int num_kv_heads, int head_dim,
+                                     int block_size, const int32_t *block_tables,
+                                     int max_blocks_per_seq, const int32_t *context_lens,
+                                     int num_seqs, const int32_t *kept, const int32_t *kept_lens,
+                                     int budget, const int32_t *dst_block_tables,
+                                     int dst_max_blocks_per_seq, pkv_dtype dtype, void *stream);
+
 /*
  * pkv_prefill_workspace_bytes -- workspace of pkv_paged_attention_prefill for
  * these arguments on the current device: 0 when the KV range is not split,
@@ -471,6 +586,18 @@ PKV_API pkv_status pkv_bm_share_prefix(pkv_block_manager *bm, int64_t src_id, in
  * changes); PKV_ERR_INVALID_ARG for an unknown id or a full table. */
 PKV_API pkv_status pkv_bm_append_token(pkv_block_manager *bm, int64_t seq_id, int64_t *slot,
                                        int64_t *cow_src, int64_t *cow_dst);
+/* Make the blocks that hold a sequence's first num_tokens tokens its own, so that
+ * they can be rewritten in place: each one that another sequence references is
+ * replaced by a fresh block, and cow_pairs[*num_cow_pairs][2] (host) names the
+ * copies to perform (pkv_copy_blocks) before the write.  cow_pairs has room for
+ * ceil(num_tokens / block_size) pairs (may be NULL when that is 0).  num_tokens
+ * in [0, length]; PKV_ERR_OUT_OF_BLOCKS when the pool cannot cover the copies
+ * (nothing changes). */
+PKV_API pkv_status pkv_bm_make_private(pkv_block_manager *bm, int64_t seq_id, int64_t num_tokens,
+                                       int64_t *cow_pairs, int64_t *num_cow_pairs);
+/* Cut a sequence to its first num_tokens tokens (in [0, length]): the blocks past
+ * them lose this sequence's reference, and return to the pool at zero. */
+PKV_API pkv_status pkv_bm_truncate(pkv_block_manager *bm, int64_t seq_id, int64_t num_tokens);
 /* Drop a sequence; its blocks' reference counts fall and blocks at zero return
  * to the pool. */
 PKV_API pkv_status pkv_bm_free_sequence(pkv_block_manager *bm, int64_t seq_id);

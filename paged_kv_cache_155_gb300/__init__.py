@@ -9,6 +9,9 @@ thin PyTorch binding.
                           cache with per-channel scales
   paged_attention_prefill chunked prefill: each sequence's new tokens attend causally
                           over its paged cache
+  rope_reshape_and_cache  rotary positions (one to four axes) on q and K, with the
+                          cache write; _int8 for an INT8 cache
+  evict_select / evict_compact   keep the heaviest tokens of each KV head's context
 
 Each call has a ``prepare_*`` twin that checks and marshals its arguments once
 and returns a callable (``PreparedCall``) for loops that reuse their buffers.
@@ -25,7 +28,10 @@ from .ops import (F16, BF16, INT8, copy_blocks, debug_wait_timeout,  # noqa: F40
                   split_pool, PreparedCall, prepare_paged_attention_decode,
                   prepare_paged_attention_decode_int8,
                   prepare_paged_attention_decode_shared_prefix, prepare_reshape_and_cache,
-                  prepare_reshape_and_cache_int8)
+                  prepare_reshape_and_cache_int8, rope_reshape_and_cache,
+                  prepare_rope_reshape_and_cache, rope_reshape_and_cache_int8,
+                  prepare_rope_reshape_and_cache_int8, evict_select, prepare_evict_select,
+                  evict_compact, prepare_evict_compact)
 from .block_table import slot_mapping  # noqa: F401
 from ._lib import PagedKVError  # noqa: F401
 
@@ -36,4 +42,7 @@ __all__ = ["reshape_and_cache", "paged_attention_decode", "paged_attention_decod
            "debug_wait_timeout", "slot_mapping", "PagedKVError", "PreparedCall",
            "prepare_paged_attention_decode", "prepare_paged_attention_decode_int8",
            "prepare_paged_attention_decode_shared_prefix", "prepare_reshape_and_cache",
-           "prepare_reshape_and_cache_int8"]
+           "prepare_reshape_and_cache_int8", "rope_reshape_and_cache",
+           "prepare_rope_reshape_and_cache", "rope_reshape_and_cache_int8",
+           "prepare_rope_reshape_and_cache_int8", "evict_select", "prepare_evict_select",
+           "evict_compact", "prepare_evict_compact"]

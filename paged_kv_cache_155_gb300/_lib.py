@@ -56,6 +56,14 @@ SIGNATURES = {
     "pkv_paged_attention_prefill": (I32, [P, P, P, I64, I64, P, I32, P, P, I32, I32, I32, I32,
                                           I32, I32, I32, I32, ctypes.c_float, P, P, SZ, I32, I32,
                                           P]),
+    "pkv_rope_reshape_and_cache": (I32, [P, I64, P, I64, P, I64, P, I32, P, P, I32, I32, P, I64, P,
+                                         I64, P, P, I64, I64, I32, I32, I32, I32, I32, P]),
+    "pkv_rope_reshape_and_cache_int8": (I32, [P, I64, P, I64, P, I64, P, I32, P, P, I32, I32, P, I64,
+                                              P, I64, P, P, I64, I64, I32, I32, I32, I32, P, P, I32,
+                                              P]),
+    "pkv_evict_select": (I32, [P, I64, P, I32, I32, I32, I32, I32, I32, P, P, P, P]),
+    "pkv_evict_compact": (I32, [P, P, I64, I64, I32, I32, I32, P, I32, P, I32, P, P, I32, P, I32,
+                                I32, P]),
     "pkv_bm_create": (P, [I64, I32, I32]),
     "pkv_bm_destroy": (None, [P]),
     "pkv_bm_num_free": (I64, [P]),
@@ -64,6 +72,8 @@ SIGNATURES = {
     "pkv_bm_fork": (I32, [P, I64, I64]),
     "pkv_bm_share_prefix": (I32, [P, I64, I64, I64]),
     "pkv_bm_append_token": (I32, [P, I64, P, P, P]),
+    "pkv_bm_make_private": (I32, [P, I64, I64, P, ctypes.POINTER(I64)]),
+    "pkv_bm_truncate": (I32, [P, I64, I64]),
     "pkv_bm_free_sequence": (I32, [P, I64]),
     "pkv_bm_seq_len": (I64, [P, I64]),
     "pkv_bm_block_table": (I32, [P, I64, P, I32, ctypes.POINTER(I32)]),
@@ -72,7 +82,8 @@ SIGNATURES = {
 
 STATUS = {0: "PKV_OK", 1: "PKV_ERR_INVALID_ARG", 2: "PKV_ERR_UNSUPPORTED", 3: "PKV_ERR_CUDA",
           4: "PKV_ERR_DEVICE", 5: "PKV_ERR_SCRATCH_LIMIT", 6: "PKV_ERR_OUT_OF_BLOCKS"}
-DEVERR = {0x1: "slot", 0x2: "block_table", 0x4: "context_len", 0x8: "copy_pair", 0x10: "timeout"}
+DEVERR = {0x1: "slot", 0x2: "block_table", 0x4: "context_len", 0x8: "copy_pair", 0x10: "timeout",
+          0x20: "rope_axis", 0x40: "kept"}
 
 
 class PagedKVError(RuntimeError):

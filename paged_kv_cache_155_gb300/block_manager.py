@@ -68,6 +68,20 @@ class BlockManager:
                "pkv_bm_append_token")
         return slot.value, (src.value, dst.value)
 
+    def make_private(self, seq_id: int, num_tokens: int) -> np.ndarray:
+        """Make the blocks of the sequence's first num_tokens tokens its own; returns the
+        copies to perform first (int64 [n, 2], the input of copy_blocks)."""
+        pairs = np.zeros((max(1, -(-int(num_tokens) // self.block_size)), 2), dtype=np.int64)
+        n = ctypes.c_int64()
+        _check(self._lib.pkv_bm_make_private(self._h, int(seq_id), int(num_tokens),
+                                             pairs.ctypes.data_as(ctypes.c_void_p), ctypes.byref(n)),
+               "pkv_bm_make_private")
+        return pairs[:n.value].copy()
+
+    def truncate(self, seq_id: int, num_tokens: int) -> None:
+        """Cut the sequence to its first num_tokens tokens, freeing the blocks past them."""
+        _check(self._lib.pkv_bm_truncate(self._h, int(seq_id), int(num_tokens)), "pkv_bm_truncate")
+
     def free_sequence(self, seq_id: int) -> None:
         _check(self._lib.pkv_bm_free_sequence(self._h, int(seq_id)), "pkv_bm_free_sequence")
 

@@ -140,6 +140,44 @@ PKV_API pkv_status pkv_bm_append_token(pkv_block_manager *bm, int64_t seq_id, in
     return PKV_OK;
 }
 
+PKV_API pkv_status pkv_bm_make_private(pkv_block_manager *bm, int64_t seq_id, int64_t num_tokens,
+                                       int64_t *cow_pairs, int64_t *num_cow_pairs) {
+    if (!bm || !num_cow_pairs) return PKV_ERR_INVALID_ARG;
+    pkv_block_manager::Seq *s = find(bm, seq_id);
+    if (!s || num_tokens < 0 || num_tokens > s->len || (num_tokens > 0 && !cow_pairs))
+        return PKV_ERR_INVALID_ARG;
+    const int64_t nblk = (num_tokens + bm->block_size - 1) / bm->block_size;
+    int64_t shared = 0;
+    for (int64_t i = 0; i < nblk; ++i) shared += bm->refcount[s->table[static_cast<size_t>(i)]] > 1;
+    if (shared > static_cast<int64_t>(bm->free_stack.size())) return PKV_ERR_OUT_OF_BLOCKS;
+    int64_t n = 0;
+    for (int64_t i = 0; i < nblk; ++i) {
+        int32_t &entry = s->table[static_cast<size_t>(i)];
+        if (bm->refcount[entry] <= 1) continue;
+        const int32_t fresh = bm->take_block();
+        cow_pairs[2 * n] = entry;
+        cow_pairs[2 * n + 1] = fresh;
+        ++n;
+        bm->release_block(entry);  // others still hold it
+        entry = fresh;
+    }
+    *num_cow_pairs = n;
+    return PKV_OK;
+}
+
+PKV_API pkv_status pkv_bm_truncate(pkv_block_manager *bm, int64_t seq_id, int64_t num_tokens) {
+    if (!bm) return PKV_ERR_INVALID_ARG;
+    pkv_block_manager::Seq *s = find(bm, seq_id);
+    if (!s || num_tokens < 0 || num_tokens > s->len) return PKV_ERR_INVALID_ARG;
+    const size_t nblk = static_cast<size_t>((num_tokens + bm->block_size - 1) / bm->block_size);
+    while (s->table.size() > nblk) {
+        bm->release_block(s->table.back());
+        s->table.pop_back();
+    }
+    s->len = num_tokens;
+    return PKV_OK;
+}
+
 PKV_API pkv_status pkv_bm_free_sequence(pkv_block_manager *bm, int64_t seq_id) {
     if (!bm) return PKV_ERR_INVALID_ARG;
     auto it = bm->seqs.find(seq_id);

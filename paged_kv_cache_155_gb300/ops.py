@@ -61,6 +61,11 @@ class PreparedCall:
     given at preparation)."""
     __slots__ = ("_fn", "_args", "_dev", "_what", "_tensors", "_result")
 
+    @property
+    def result(self):
+        """What the call returns (its output tensors, written by each call)."""
+        return self._result
+
     def __init__(self, what: str, args: tuple, device: torch.device, tensors: tuple, result=None):
         self._fn = getattr(lib(), what)
         self._args = args
@@ -70,7 +75,11 @@ class PreparedCall:
         self._result = result
 
     def __call__(self):
-        st = self._fn(*self._args, _raw_stream(self._dev))
+        if torch.cuda.current_device() != self._dev:  # the library launches on the current device
+            with torch.cuda.device(self._dev):
+                st = self._fn(*self._args, _raw_stream(self._dev))
+        else:
+            st = self._fn(*self._args, _raw_stream(self._dev))
         if st != 0:
             raise PagedKVError(self._what, st)
         return self._result
@@ -437,6 +446,223 @@ def prepare_paged_attention_decode_int8(q: torch.Tensor, k_cache: torch.Tensor,
     return PreparedCall("pkv_paged_attention_decode_int8", args, q.device,
                         (q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out,
                          workspace), out)
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions with the cache write
+# ---------------------------------------------------------------------------
+
+def _one_device(anchor: torch.Tensor, **tensors) -> None:
+    """Every given tensor is on the anchor's device, a CUDA device."""
+    for name, t in tensors.items():
+        if t is not None and t.device != anchor.device:
+            raise ValueError(f"{name} must be on {anchor.device}, not {t.device}")
+    if anchor.device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+
+
+def _token_rows(t: torch.Tensor, name: str, tokens: int, heads: Optional[int], d: int) -> Tuple[int, int]:
+    """(heads, elements between tokens) of a [tokens, heads, d] tensor dense within a token."""
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [{tokens}, {'num_q_heads' if heads is None else heads}, {d}]")
+    h = int(t.shape[1])
+    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name} must be dense within a token")
+    stride = int(t.stride(0)) if tokens > 1 else h * d
+    if stride < h * d or stride % 8:
+        raise ValueError(f"{name}'s tokens must be a multiple of 8 elements apart and not overlap")
+    return h, stride
+
+
+def _rope_args(q, k_new, v_new, positions, inv_freq, slot_mapping, k_cache, v_cache, q_out, axis_of_pair,
+               interleaved, geometry):
+    nb, hkv, bs, d, stride = geometry
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, num_q_heads, {d}]")
+    t = int(q.shape[0])
+    hq, q_stride = _token_rows(q, "q", t, None, d)
+    _, k_stride = _token_rows(k_new, "k_new", t, hkv, d)
+    _, v_stride = _token_rows(v_new, "v_new", t, hkv, d)
+    if k_new.dtype != q.dtype or v_new.dtype != q.dtype:
+        raise ValueError("q, k_new and v_new must have one dtype")
+    if q_out is None:
+        q_out = torch.empty((t, hq, d), dtype=q.dtype, device=q.device)
+    if q_out.dtype != q.dtype:
+        raise ValueError("q_out must have q's dtype")
+    _, q_out_stride = _token_rows(q_out, "q_out", t, hq, d)
+    if positions.dtype != torch.int64 or positions.dim() not in (1, 2) or positions.shape[-1] != t \
+            or not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous int64 [T] or [num_axes, T]")
+    axes = int(positions.shape[0]) if positions.dim() == 2 else 1
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 [rotary_dim / 2]")
+    if axis_of_pair is not None and (axis_of_pair.dtype != torch.int32 or axis_of_pair.shape != inv_freq.shape
+                                     or not axis_of_pair.is_contiguous()):
+        raise ValueError("axis_of_pair must be a contiguous int32 [rotary_dim / 2]")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != t or not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be a contiguous int64 [T]")
+    _one_device(k_cache, q=q, k_new=k_new, v_new=v_new, positions=positions, inv_freq=inv_freq,
+                slot_mapping=slot_mapping, v_cache=v_cache, q_out=q_out, axis_of_pair=axis_of_pair)
+    args = (q.data_ptr(), q_stride, k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride, positions.data_ptr(),
+            axes, None if axis_of_pair is None else axis_of_pair.data_ptr(), inv_freq.data_ptr(),
+            2 * int(inv_freq.numel()), int(bool(interleaved)), slot_mapping.data_ptr(), t, q_out.data_ptr(),
+            q_out_stride, k_cache.data_ptr(), v_cache.data_ptr(), nb, stride, hq, hkv, d, bs)
+    return args, (q, k_new, v_new, positions, inv_freq, slot_mapping, k_cache, v_cache, q_out, axis_of_pair), q_out
+
+
+def rope_reshape_and_cache(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, positions: torch.Tensor,
+                           inv_freq: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                           v_cache: torch.Tensor, q_out: Optional[torch.Tensor] = None, *,
+                           axis_of_pair: Optional[torch.Tensor] = None, interleaved: bool = False) -> torch.Tensor:
+    """Rotate q [T, Hq, d] and k_new [T, Hkv, d] by their positions and write the rotated
+    K rows and the V rows into their slots; returns the rotated q (``q_out``).
+
+    positions: int64 [T], or [num_axes, T] (up to four) with axis_of_pair int32
+    [rotary_dim/2] naming the axis that each pair of channels follows; inv_freq:
+    float64 [rotary_dim/2], radians per position.  Pairs are channels (i, i +
+    rotary_dim/2), or (2i, 2i + 1) when ``interleaved``; channels from rotary_dim on
+    are copied.  q, k_new and v_new may be views of one projection's rows (dense
+    within a token).  slot < 0 writes no cache row.  q_out may be q."""
+    return prepare_rope_reshape_and_cache(q, k_new, v_new, positions, inv_freq, slot_mapping, k_cache, v_cache, q_out,
+                                          axis_of_pair=axis_of_pair, interleaved=interleaved)()
+
+
+def prepare_rope_reshape_and_cache(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                                   positions: torch.Tensor, inv_freq: torch.Tensor, slot_mapping: torch.Tensor,
+                                   k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                   q_out: Optional[torch.Tensor] = None, *,
+                                   axis_of_pair: Optional[torch.Tensor] = None,
+                                   interleaved: bool = False) -> PreparedCall:
+    """rope_reshape_and_cache, checked and marshalled once (see PreparedCall)."""
+    geometry = _cache_geometry(k_cache, v_cache)
+    if q.dtype != k_cache.dtype:
+        raise ValueError("q, k_new and v_new must have the cache's dtype")
+    args, held, q_out = _rope_args(q, k_new, v_new, positions, inv_freq, slot_mapping, k_cache, v_cache, q_out,
+                                   axis_of_pair, interleaved, geometry)
+    return PreparedCall("pkv_rope_reshape_and_cache", args + (_dtype_code(q),), k_cache.device, held, q_out)
+
+
+def rope_reshape_and_cache_int8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, positions: torch.Tensor,
+                                inv_freq: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                                v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                                q_out: Optional[torch.Tensor] = None, *,
+                                axis_of_pair: Optional[torch.Tensor] = None,
+                                interleaved: bool = False) -> torch.Tensor:
+    """rope_reshape_and_cache into an INT8 cache: the rotated K rows and the V rows are
+    quantised with the per-channel scales [Hkv, d]."""
+    return prepare_rope_reshape_and_cache_int8(q, k_new, v_new, positions, inv_freq, slot_mapping, k_cache, v_cache,
+                                               k_scale, v_scale, q_out, axis_of_pair=axis_of_pair,
+                                               interleaved=interleaved)()
+
+
+def prepare_rope_reshape_and_cache_int8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                                        positions: torch.Tensor, inv_freq: torch.Tensor, slot_mapping: torch.Tensor,
+                                        k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                                        v_scale: torch.Tensor, q_out: Optional[torch.Tensor] = None, *,
+                                        axis_of_pair: Optional[torch.Tensor] = None,
+                                        interleaved: bool = False) -> PreparedCall:
+    """rope_reshape_and_cache_int8, checked and marshalled once (see PreparedCall)."""
+    geometry = _check_int8_cache(k_cache, v_cache, k_scale, v_scale)
+    args, held, q_out = _rope_args(q, k_new, v_new, positions, inv_freq, slot_mapping, k_cache, v_cache, q_out,
+                                   axis_of_pair, interleaved, geometry)
+    return PreparedCall("pkv_rope_reshape_and_cache_int8",
+                        args + (k_scale.data_ptr(), v_scale.data_ptr(), _dtype_code(q)), k_cache.device,
+                        held + (k_scale, v_scale), q_out)
+
+
+# ---------------------------------------------------------------------------
+# Eviction by accumulated attention weight
+# ---------------------------------------------------------------------------
+
+def evict_select(weights: torch.Tensor, context_lens: torch.Tensor, budget: int, *, sinks: int = 0, recent: int = 0,
+                 max_context_len: Optional[int] = None, weights_out: Optional[torch.Tensor] = None,
+                 kept: Optional[torch.Tensor] = None,
+                 kept_lens: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Which tokens of each (sequence, KV head) stay: (kept int32 [B, Hkv, budget] ascending
+    positions then -1, kept_lens int32 [B] = min(length, budget)).
+
+    A longer context keeps its first ``sinks``, its last ``recent`` and the heaviest of
+    the tokens between (equal weights: the lower position).  weights: fp32 [B, Hkv, W],
+    W >= max_context_len, as paged_attention_decode_scored accumulates them;
+    ``weights_out`` (may be ``weights``) gets the kept weights in their new places and
+    zeros up to the old length."""
+    return prepare_evict_select(weights, context_lens, budget, sinks=sinks, recent=recent,
+                                max_context_len=max_context_len, weights_out=weights_out, kept=kept,
+                                kept_lens=kept_lens)()
+
+
+def prepare_evict_select(weights: torch.Tensor, context_lens: torch.Tensor, budget: int, *, sinks: int = 0,
+                         recent: int = 0, max_context_len: Optional[int] = None,
+                         weights_out: Optional[torch.Tensor] = None, kept: Optional[torch.Tensor] = None,
+                         kept_lens: Optional[torch.Tensor] = None) -> PreparedCall:
+    """evict_select, checked and marshalled once (see PreparedCall); the call returns
+    (kept, kept_lens)."""
+    if weights.dtype != torch.float32 or weights.dim() != 3 or not weights.is_contiguous():
+        raise ValueError("weights must be a contiguous float32 [num_seqs, num_kv_heads, max_tokens]")
+    b, hkv, width = (int(x) for x in weights.shape)
+    if context_lens.dtype != torch.int32 or context_lens.numel() != b or not context_lens.is_contiguous():
+        raise ValueError("context_lens must be a contiguous int32 [num_seqs]")
+    if weights_out is not None and (weights_out.dtype != torch.float32 or weights_out.shape != weights.shape
+                                    or not weights_out.is_contiguous()):
+        raise ValueError("weights_out must match weights")
+    if budget <= 0 or sinks < 0 or recent < 0 or sinks + recent > budget:
+        raise ValueError("budget must be positive and cover sinks + recent")
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item()) if b else 0
+    if max_context_len > width:
+        raise ValueError("weights must have a column for every context token")
+    if kept is None:
+        kept = torch.empty((b, hkv, budget), dtype=torch.int32, device=weights.device)
+    elif kept.dtype != torch.int32 or kept.shape != (b, hkv, budget) or not kept.is_contiguous():
+        raise ValueError("kept must be a contiguous int32 [num_seqs, num_kv_heads, budget]")
+    if kept_lens is None:
+        kept_lens = torch.empty(b, dtype=torch.int32, device=weights.device)
+    elif kept_lens.dtype != torch.int32 or kept_lens.numel() != b or not kept_lens.is_contiguous():
+        raise ValueError("kept_lens must be a contiguous int32 [num_seqs]")
+    _one_device(weights, context_lens=context_lens, weights_out=weights_out, kept=kept, kept_lens=kept_lens)
+    args = (weights.data_ptr(), width, context_lens.data_ptr(), int(max_context_len), b, hkv, int(budget), int(sinks),
+            int(recent), None if weights_out is None else weights_out.data_ptr(), kept.data_ptr(),
+            kept_lens.data_ptr())
+    return PreparedCall("pkv_evict_select", args, weights.device, (weights, context_lens, weights_out, kept, kept_lens),
+                        (kept, kept_lens))
+
+
+def evict_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                  context_lens: torch.Tensor, kept: torch.Tensor, kept_lens: torch.Tensor, *,
+                  dst_block_tables: Optional[torch.Tensor] = None) -> None:
+    """Move the K and V rows of the kept tokens (evict_select) to the front of each
+    sequence's context: into the fresh blocks of ``dst_block_tables``, or in place (the
+    blocks that get rows must belong to their sequence alone: BlockManager.make_private).
+    Afterwards kept_lens are the context lengths."""
+    prepare_evict_compact(k_cache, v_cache, block_tables, context_lens, kept, kept_lens,
+                          dst_block_tables=dst_block_tables)()
+
+
+def prepare_evict_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                          context_lens: torch.Tensor, kept: torch.Tensor, kept_lens: torch.Tensor, *,
+                          dst_block_tables: Optional[torch.Tensor] = None) -> PreparedCall:
+    """evict_compact, checked and marshalled once (see PreparedCall)."""
+    nb, hkv, bs, d, stride = _cache_geometry(k_cache, v_cache)
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or not block_tables.is_contiguous():
+        raise ValueError("block_tables must be a contiguous int32 [num_seqs, max_blocks_per_seq]")
+    b = int(block_tables.shape[0])
+    for name, t in (("context_lens", context_lens), ("kept_lens", kept_lens)):
+        if t.dtype != torch.int32 or t.numel() != b or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 [num_seqs]")
+    if kept.dtype != torch.int32 or kept.dim() != 3 or tuple(kept.shape[:2]) != (b, hkv) or not kept.is_contiguous():
+        raise ValueError("kept must be a contiguous int32 [num_seqs, num_kv_heads, budget]")
+    if dst_block_tables is not None and (dst_block_tables.dtype != torch.int32 or dst_block_tables.dim() != 2
+                                         or dst_block_tables.shape[0] != b or not dst_block_tables.is_contiguous()):
+        raise ValueError("dst_block_tables must be a contiguous int32 [num_seqs, blocks]")
+    _one_device(k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens, kept=kept,
+                kept_lens=kept_lens, dst_block_tables=dst_block_tables)
+    dst = dst_block_tables
+    args = (k_cache.data_ptr(), v_cache.data_ptr(), nb, stride, hkv, d, bs, block_tables.data_ptr(),
+            int(block_tables.shape[1]), context_lens.data_ptr(), b, kept.data_ptr(), kept_lens.data_ptr(),
+            int(kept.shape[2]), None if dst is None else dst.data_ptr(), 0 if dst is None else int(dst.shape[1]),
+            _cache_dtype_code(k_cache))
+    return PreparedCall("pkv_evict_compact", args, k_cache.device,
+                        (k_cache, v_cache, block_tables, context_lens, kept, kept_lens, dst))
 
 
 def get_device_error(device: Optional[torch.device] = None) -> Tuple[int, list]:

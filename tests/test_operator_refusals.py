@@ -1,0 +1,162 @@
+"""The operators around plain attention refuse what their contracts exclude, on the host: the C ABI before any CUDA
+call, the binding before the library."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_155_gb300 as pkv
+from paged_kv_cache_155_gb300 import _build
+from paged_kv_cache_155_gb300.block_manager import BlockManager, OutOfBlocks
+
+INVALID, UNSUPPORTED = 1, 2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    from paged_kv_cache_155_gb300._lib import lib as load
+    return load()
+
+
+def _rope(lib, int8=False, **kw):
+    a = dict(q=16, qs=512, k=16, ks=128, v=16, vs=128, pos=16, axes=1, axis=None, inv=16, rot=64, inter=0, slots=16, t=4,
+             out=16, outs=512, kc=16, vc=16, nb=8, stride=2 * 2 * 16 * 64, hq=8, hkv=2, d=64, bs=16, sk=16, sv=16, dt=0)
+    a.update(kw)
+    head = [a[n] for n in ("q", "qs", "k", "ks", "v", "vs", "pos", "axes", "axis", "inv", "rot", "inter", "slots", "t", "out",
+                           "outs", "kc", "vc", "nb", "stride", "hq", "hkv", "d", "bs")]
+    if int8:
+        return lib.pkv_rope_reshape_and_cache_int8(*head, a["sk"], a["sv"], a["dt"], None)
+    return lib.pkv_rope_reshape_and_cache(*head, a["dt"], None)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_rope_refusals(lib, int8):
+    call = lambda **kw: _rope(lib, int8, **kw)
+    assert call(t=0) == 0
+    for kw in (dict(d=96), dict(bs=4), dict(dt=2), dict(rot=24), dict(rot=8)):
+        assert call(**kw) == UNSUPPORTED, kw
+    for kw in (dict(rot=0), dict(rot=128), dict(axes=0), dict(axes=5), dict(t=-1), dict(hq=0), dict(hkv=0), dict(nb=0),
+               dict(qs=504), dict(qs=516), dict(ks=120), dict(vs=132), dict(outs=0), dict(q=8), dict(out=24), dict(k=None),
+               dict(pos=12), dict(inv=None), dict(slots=4), dict(axis=2), dict(kc=None), dict(vc=8), dict(stride=100),
+               dict(stride=2 * 2 * 16 * 64 + 4)):
+        assert call(**kw) == INVALID, kw
+    if int8:
+        assert call(sk=None) == INVALID and call(sv=8) == INVALID and call(stride=2 * 2 * 16 * 64 + 8) == INVALID
+
+
+def test_evict_refusals(lib):
+    def select(**kw):
+        a = dict(w=16, ws=64, cl=16, maxl=64, b=2, hkv=2, budget=8, sinks=1, recent=2, wo=None, kept=16, kl=16)
+        a.update(kw)
+        return lib.pkv_evict_select(a["w"], a["ws"], a["cl"], a["maxl"], a["b"], a["hkv"], a["budget"], a["sinks"],
+                                    a["recent"], a["wo"], a["kept"], a["kl"], None)
+
+    assert select(b=0) == 0
+    for kw in (dict(budget=0), dict(sinks=7), dict(sinks=-1), dict(recent=-1), dict(recent=2 ** 31 - 1, budget=2 ** 31 - 1),
+               dict(ws=63), dict(b=-1), dict(b=70000), dict(hkv=0), dict(maxl=-1), dict(w=None), dict(kept=2), dict(kl=None),
+               dict(wo=2)):
+        assert select(**kw) == INVALID, kw
+
+    def compact(**kw):
+        a = dict(kc=16, vc=16, nb=8, stride=2 * 2 * 16 * 64, hkv=2, d=64, bs=16, bt=16, mb=4, cl=16, b=2, kept=16, kl=16,
+                 budget=8, dst=32, dmb=2, dt=0)
+        a.update(kw)
+        return lib.pkv_evict_compact(a["kc"], a["vc"], a["nb"], a["stride"], a["hkv"], a["d"], a["bs"], a["bt"], a["mb"],
+                                     a["cl"], a["b"], a["kept"], a["kl"], a["budget"], a["dst"], a["dmb"], a["dt"], None)
+
+    assert compact(b=0) == 0
+    for kw in (dict(d=80), dict(bs=12), dict(dt=3)):
+        assert compact(**kw) == UNSUPPORTED, kw
+    for kw in (dict(nb=0), dict(mb=0), dict(budget=0), dict(dmb=0), dict(bt=None), dict(cl=2), dict(kept=None), dict(kl=1),
+               dict(dst=18), dict(kc=8), dict(vc=None), dict(stride=64), dict(hkv=0), dict(b=-1), dict(b=70000),
+               dict(dst=16, dmb=3)):
+        assert compact(**kw) == INVALID, kw
+
+
+def test_binding_refuses_before_the_library():
+    kv = torch.zeros((4, 2, 2, 16, 64), dtype=torch.float16)
+    k, v = pkv.split_pool(kv)
+    q, kn = torch.zeros((3, 4, 64), dtype=torch.float16), torch.zeros((3, 2, 64), dtype=torch.float16)
+    good = dict(positions=torch.zeros(3, dtype=torch.int64), inv_freq=torch.ones(32, dtype=torch.float64),
+                slot_mapping=torch.zeros(3, dtype=torch.int64))
+
+    def rope(q=q, kn=kn, vn=kn, **kw):
+        a = dict(good)
+        extra = {n: kw.pop(n) for n in list(kw) if n not in a}
+        a.update(kw)
+        return pkv.rope_reshape_and_cache(q, kn, vn, a["positions"], a["inv_freq"], a["slot_mapping"], k, v, **extra)
+
+    with pytest.raises(ValueError, match="CUDA"):
+        rope()                                              # host tensors
+    for kw in (dict(q=q.float()), dict(q=q[:2]), dict(q=q.transpose(1, 2)), dict(kn=kn[:, :1]), dict(vn=kn.bfloat16()),
+               dict(positions=torch.zeros(3)), dict(positions=torch.zeros((2, 4), dtype=torch.int64)),
+               dict(inv_freq=torch.ones(32)), dict(slot_mapping=torch.zeros(2, dtype=torch.int64)),
+               dict(axis_of_pair=torch.zeros(32)), dict(axis_of_pair=torch.zeros(31, dtype=torch.int32)),
+               dict(q_out=torch.zeros((3, 4, 64)))):
+        with pytest.raises(ValueError):
+            rope(**kw)
+    w, n = torch.zeros((2, 2, 64)), torch.tensor([5, 64], dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkv.evict_select(w, n, 8)
+    for kw in (dict(budget=0), dict(budget=4, sinks=3, recent=2), dict(budget=8, max_context_len=65),
+               dict(budget=8, weights_out=torch.zeros((2, 2, 63))), dict(budget=8, kept=torch.zeros((2, 2, 7)))):
+        with pytest.raises(ValueError):
+            pkv.evict_select(w, n, **kw)
+    with pytest.raises(ValueError):
+        pkv.evict_select(w.double(), n, 8)
+    kept = torch.zeros((2, 2, 8), dtype=torch.int32)
+    bt = torch.zeros((2, 4), dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkv.evict_compact(k, v, bt, n, kept, n)
+    for args in ((bt.long(), n, kept, n), (bt, n[:1], kept, n), (bt, n, kept[:, :1], n), (bt, n, kept, n.long())):
+        with pytest.raises(ValueError):
+            pkv.evict_compact(k, v, *args)
+    with pytest.raises(ValueError):
+        pkv.evict_compact(k, v, bt, n, kept, n, dst_block_tables=bt[:1])
+
+
+def test_block_manager_make_private_and_truncate():
+    bm = BlockManager(10, 4, 8)
+    bm.add_sequence(1)
+    for _ in range(18):
+        bm.append_token(1)
+    old = bm.block_table(1)
+    assert len(bm.make_private(1, 18)) == 0                 # nothing shared
+    bm.fork(1, 2)
+    with pytest.raises(ValueError):
+        BlockManager(0, 4, 8)
+    pairs = bm.make_private(1, 9)                           # three of the five shared blocks
+    assert pairs[:, 0].tolist() == old[:3]
+    assert bm.block_table(1) == pairs[:, 1].tolist() + old[3:]
+    assert [bm.refcount(b) for b in old] == [1, 1, 1, 2, 2] and bm.num_free == 2
+    assert len(bm.make_private(1, 9)) == 0
+    bm.fork(2, 3)
+    with pytest.raises(OutOfBlocks):
+        bm.make_private(2, 18)                              # five copies, two blocks free
+    assert bm.block_table(2) == old and bm.num_free == 2    # nothing changed
+    bm.truncate(1, 9)
+    assert bm.seq_len(1) == 9 and len(bm.block_table(1)) == 3 and bm.refcount(old[4]) == 2
+    bm.truncate(1, 9)
+    bm.truncate(1, 8)
+    assert len(bm.block_table(1)) == 2 and bm.num_free == 3
+    slot, pair = bm.append_token(1)                         # grows again from the cut
+    assert pair == (-1, -1) and slot % 4 == 0 and bm.seq_len(1) == 9
+    bm.truncate(1, 0)
+    assert bm.block_table(1) == [] and bm.num_free == 5
+    for bad in (-1, 1):
+        with pytest.raises(Exception):
+            bm.truncate(1, bad)
+        with pytest.raises(Exception):
+            bm.make_private(1, bad)
+    with pytest.raises(Exception):
+        bm.truncate(99, 0)
+    n = ctypes.c_int64()
+    assert bm._lib.pkv_bm_make_private(bm._h, 2, 4, None, ctypes.byref(n)) == INVALID
+    assert bm._lib.pkv_bm_make_private(bm._h, 2, 0, None, ctypes.byref(n)) == 0 and n.value == 0
+    bm.free_sequence(2)
+    bm.free_sequence(3)
+    bm.free_sequence(1)
+    assert bm.num_free == 10
+    assert isinstance(pairs, np.ndarray)
