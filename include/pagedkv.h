@@ -351,6 +351,67 @@ PKV_API pkv_status pkv_rope_reshape_and_cache_int8(
     void *stream);
 
 /*
+ * pkv_decode_scored_workspace_bytes -- workspace of
+ * pkv_paged_attention_decode_scored (int8_cache 0) or its INT8-cache form for
+ * these arguments on the current device; want_weights != 0 when weights_out is
+ * given.  0 when none is needed, (size_t)-1 for arguments out of contract.
+ */
+PKV_API size_t pkv_decode_scored_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
+                                                 int head_dim, int block_size, int max_context_len,
+                                                 int window, int want_weights, int int8_cache,
+                                                 int partition_size);
+
+/*
+ * pkv_paged_attention_decode_scored -- pkv_paged_attention_decode with the
+ * score forms and masks of a model's layers, and the attention weights for
+ * eviction.  The query of sequence i sits at position p = context_lens[i] - 1;
+ * head hq's score of token t is
+ *     x = scale * q . k_t;   x = softcap * tanh(x / softcap)   (softcap > 0);
+ *     x = x + slopes[hq] * (t - p)                             (slopes given)
+ * and the softmax runs over the tokens lo <= t <= p with
+ *     lo = max(0, p + 1 - window  (window > 0),  starts[i]  (starts given)).
+ *
+ *   softcap        0 (none) or in [1e-3, 1e6].
+ *   slopes         [num_q_heads] fp32, device, or NULL.
+ *   window         0: the whole context.
+ *   starts         [num_seqs] int32, device, or NULL: the first visible token,
+ *                  e.g. of the sequence's last document.  A sequence that sees
+ *                  nothing (starts[i] >= context_lens[i]) gets a zero row.
+ *   weights, weights_out   fp32 [num_seqs][num_kv_heads][weights_stride],
+ *                  device: for every token t of the context
+ *                      weights_out[i][h][t] = weights[i][h][t] + sum over KV
+ *                      head h's query heads of their softmax weight of t
+ *                  (weights NULL: plus nothing); columns past the context are
+ *                  left as they are.  The same array may be both; else they
+ *                  must not overlap.  weights_stride >= max_context_len.
+ *                  weights_out NULL: not wanted.
+ *   workspace      >= pkv_decode_scored_workspace_bytes(...).
+ * Tokens before lo are not read: table entries of blocks that lie before lo
+ * are never dereferenced (a window's past blocks may be freed), and what lo's
+ * block holds before it does not matter, NaN or infinities included.  Other
+ * arguments and errors as pkv_paged_attention_decode.
+ */
+PKV_API pkv_status pkv_paged_attention_decode_scored(
+    const void *q, const void *k_cache, const void *v_cache, int64_t num_blocks,
+    int64_t block_stride_elems, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *context_lens, int max_context_len, int num_seqs, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, float scale, float softcap,
+    const float *slopes, int window, const int32_t *starts, const float *weights,
+    float *weights_out, int64_t weights_stride, void *out, void *workspace,
+    size_t workspace_bytes, int partition_size, pkv_dtype dtype, void *stream);
+
+/* pkv_paged_attention_decode_scored over an INT8 cache (the score forms and
+ * masks; no weights: its scores carry the fp16 rounding of the folded query). */
+PKV_API pkv_status pkv_paged_attention_decode_scored_int8(
+    const void *q, const int8_t *k_cache, const int8_t *v_cache, const float *k_scale,
+    const float *v_scale, int64_t num_blocks, int64_t block_stride_elems,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+    int max_context_len, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, float scale, float softcap, const float *slopes, int window,
+    const int32_t *starts, void *out, void *workspace, size_t workspace_bytes,
+    int partition_size, pkv_dtype dtype, void *stream);
+
+/*
  * pkv_evict_select -- which tokens of each (sequence, KV head) stay in the
  * cache.  A context of L = context_lens[i] tokens keeps n = min(L, budget):
  * all of them when L <= budget, else the first `sinks`, the last `recent` and

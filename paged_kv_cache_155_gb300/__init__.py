@@ -11,6 +11,8 @@ thin PyTorch binding.
                           over its paged cache
   rope_reshape_and_cache  rotary positions (one to four axes) on q and K, with the
                           cache write; _int8 for an INT8 cache
+  paged_attention_decode_scored   the decode with capped or distance-biased scores, a
+                          window, and the accumulated attention weights; _int8
   evict_select / evict_compact   keep the heaviest tokens of each KV head's context
 
 Each call has a ``prepare_*`` twin that checks and marshals its arguments once
@@ -31,7 +33,10 @@ from .ops import (F16, BF16, INT8, copy_blocks, debug_wait_timeout,  # noqa: F40
                   prepare_reshape_and_cache_int8, rope_reshape_and_cache,
                   prepare_rope_reshape_and_cache, rope_reshape_and_cache_int8,
                   prepare_rope_reshape_and_cache_int8, evict_select, prepare_evict_select,
-                  evict_compact, prepare_evict_compact)
+                  evict_compact, prepare_evict_compact, decode_scored_workspace_bytes,
+                  paged_attention_decode_scored, prepare_paged_attention_decode_scored,
+                  paged_attention_decode_scored_int8,
+                  prepare_paged_attention_decode_scored_int8)
 from .block_table import slot_mapping  # noqa: F401
 from ._lib import PagedKVError  # noqa: F401
 
@@ -45,4 +50,7 @@ __all__ = ["reshape_and_cache", "paged_attention_decode", "paged_attention_decod
            "prepare_reshape_and_cache_int8", "rope_reshape_and_cache",
            "prepare_rope_reshape_and_cache", "rope_reshape_and_cache_int8",
            "prepare_rope_reshape_and_cache_int8", "evict_select", "prepare_evict_select",
-           "evict_compact", "prepare_evict_compact"]
+           "evict_compact", "prepare_evict_compact",
+           "decode_scored_workspace_bytes", "paged_attention_decode_scored",
+           "prepare_paged_attention_decode_scored", "paged_attention_decode_scored_int8",
+           "prepare_paged_attention_decode_scored_int8"]

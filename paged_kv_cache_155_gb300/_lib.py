@@ -61,6 +61,13 @@ SIGNATURES = {
     "pkv_rope_reshape_and_cache_int8": (I32, [P, I64, P, I64, P, I64, P, I32, P, P, I32, I32, P, I64,
                                               P, I64, P, P, I64, I64, I32, I32, I32, I32, P, P, I32,
                                               P]),
+    "pkv_decode_scored_workspace_bytes": (SZ, [I32] * 10),
+    "pkv_paged_attention_decode_scored": (I32, [P, P, P, I64, I64, P, I32, P, I32, I32, I32, I32, I32,
+                                                I32, ctypes.c_float, ctypes.c_float, P, I32, P, P, P,
+                                                I64, P, P, SZ, I32, I32, P]),
+    "pkv_paged_attention_decode_scored_int8": (I32, [P, P, P, P, P, I64, I64, P, I32, P, I32, I32, I32,
+                                                     I32, I32, I32, ctypes.c_float, ctypes.c_float, P,
+                                                     I32, P, P, P, SZ, I32, I32, P]),
     "pkv_evict_select": (I32, [P, I64, P, I32, I32, I32, I32, I32, I32, P, P, P, P]),
     "pkv_evict_compact": (I32, [P, P, I64, I64, I32, I32, I32, P, I32, P, I32, P, P, I32, P, I32,
                                 I32, P]),

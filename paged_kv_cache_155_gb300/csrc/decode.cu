@@ -4,6 +4,7 @@
 #include <cmath>
 
 #include "decode_launch.cuh"
+#include "decode_weights.cuh"
 
 namespace pkv {
 
@@ -217,8 +218,37 @@ bool encode_decode_maps(pkv::DecodeMaps *maps, const void *k_cache, const void *
                                 block_size, dtype, rows);
 }
 
+// What the scored decode adds to a call.
+struct ScoredArgs {
+    float softcap;
+    const float *slopes;
+    int window;
+    const int32_t *starts;
+    const float *weights;
+    float *weights_out;
+    int64_t weights_stride;
+};
+
+// The longest token range a scored sequence attends over, from the block of its
+// first visible token on.
+int scored_span(int max_context_len, int window, int block_size) {
+    if (window <= 0) return max_context_len;
+    return static_cast<int>(std::min<int64_t>(max_context_len, static_cast<int64_t>(window) + block_size - 1));
+}
+int64_t score_stride_of(int span) { return (static_cast<int64_t>(span) + 31) / 32 * 32; }
+
+// Scored workspace: the partials (also of a single partition when the weights are
+// wanted: their kernel reads m and l), then the scores.
+size_t scored_workspace(int num_seqs, int num_q_heads, int head_dim, int nparts, int span, bool weights) {
+    if (!weights) return workspace_for(num_seqs, num_q_heads, head_dim, nparts);
+    const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads;
+    const size_t partials = rows * nparts * (static_cast<size_t>(head_dim) + 2);
+    return ((partials + 3) / 4 * 4 + rows * static_cast<size_t>(score_stride_of(span))) * sizeof(float);
+}
+
 // Decode over a 16-bit cache (k_scale == v_scale == nullptr) or an INT8 cache
-// with per-channel scales.  Element strides and offsets count cache elements.
+// with per-channel scales; `scored`, if given, selects the scored form.  Element
+// strides and offsets count cache elements.
 pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache,
                        const float *k_scale, const float *v_scale, bool int8_kv,
                        int64_t num_blocks, int64_t block_stride_elems,
@@ -226,7 +256,8 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache,
                        const int32_t *context_lens, int max_context_len, int num_seqs,
                        int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                        float scale, void *out, void *workspace, size_t workspace_bytes,
-                       int partition_size, pkv_dtype dtype, void *stream) {
+                       int partition_size, pkv_dtype dtype, void *stream,
+                       const ScoredArgs *scored = nullptr) {
     if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
     if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
     if (block_size != 8 && block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
@@ -243,24 +274,38 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache,
         return PKV_ERR_INVALID_ARG;
     if (int8_kv && (!k_scale || !v_scale || !pkv::aligned16(k_scale) || !pkv::aligned16(v_scale)))
         return PKV_ERR_INVALID_ARG;
+    if (scored) {
+        const ScoredArgs &a = *scored;
+        // a cap far outside the scores' range would overflow score / softcap
+        if (a.softcap != 0.f && !(a.softcap >= 1e-3f && a.softcap <= 1e6f)) return PKV_ERR_INVALID_ARG;
+        if (a.window < 0 || (a.weights && !a.weights_out) ||
+            (a.weights_out && a.weights_stride < max_context_len) ||
+            ((reinterpret_cast<uintptr_t>(a.slopes) | reinterpret_cast<uintptr_t>(a.starts) |
+              reinterpret_cast<uintptr_t>(a.weights) | reinterpret_cast<uintptr_t>(a.weights_out)) & 3u))
+            return PKV_ERR_INVALID_ARG;
+        if (a.weights_out && (int8_kv || num_q_heads / num_kv_heads > pkv::kMaxWeightHeads))
+            return PKV_ERR_UNSUPPORTED;
+    }
     if (num_seqs == 0) return PKV_OK;
     if (!q || !out || !block_tables || !context_lens || !pkv::aligned16(q) || !pkv::aligned16(out))
         return PKV_ERR_INVALID_ARG;
 
     int part = 0, nparts = 0, gh = 0, merge = 0;
+    const bool want_weights = scored && scored->weights_out;
+    const int span = scored ? scored_span(max_context_len, scored->window, block_size) : max_context_len;
     // Validate the shape first (no CUDA call), then plan for the real SM count.
     pkv_status plan = plan_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
-                                  max_context_len, partition_size, 1, int8_kv, &part, &nparts, &gh,
+                                  span, partition_size, 1, int8_kv, &part, &nparts, &gh,
                                   &merge);
     if (plan != PKV_OK) return plan;
     if (partition_size == 0) {
         const int sm = pkv::current_sm_count();
         if (sm <= 0) return PKV_ERR_CUDA;
         plan = plan_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
-                           max_context_len, 0, sm, int8_kv, &part, &nparts, &gh, &merge);
+                           span, 0, sm, int8_kv, &part, &nparts, &gh, &merge);
         if (plan != PKV_OK) return plan;
     }
-    const size_t need = workspace_for(num_seqs, num_q_heads, head_dim, nparts);
+    const size_t need = scored_workspace(num_seqs, num_q_heads, head_dim, nparts, span, want_weights);
     if (need > 0 && (!workspace || workspace_bytes < need || !pkv::aligned16(workspace)))
         return PKV_ERR_INVALID_ARG;
     unsigned int *status = pkv::status_word_ptr();
@@ -294,6 +339,23 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache,
     p.num_partitions = nparts;
     p.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
 
+    if (scored) {
+        p.slopes = scored->slopes;
+        p.starts = scored->starts;
+        p.window = scored->window;
+        p.block_size = block_size;
+        if (scored->softcap > 0.f) {
+            p.cap_in = static_cast<float>(0.6931471805599453 / scored->softcap);
+            p.cap_out = static_cast<float>(scored->softcap * 1.4426950408889634);
+        }
+        if (want_weights) {
+            p.always_partial = 1;
+            merge = 1;
+            const size_t partials = rows * (static_cast<size_t>(head_dim) + 2);
+            p.ws_s = p.ws_o + (partials + 3) / 4 * 4;
+            p.score_stride = score_stride_of(span);
+        }
+    }
     const int merge_rows = merge ? num_seqs * num_q_heads : 0;
     p.trigger_dependents = merge_rows > 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -306,6 +368,18 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache,
         !encode_decode_maps(&maps, k_cache, v_cache, int8_kv, num_blocks, block_stride_elems,
                             num_kv_heads, block_size, dtype))
         return PKV_ERR_CUDA;
+    if (scored) {
+        auto launch = int8_kv ? (dtype == PKV_F16 ? pkv::launch_scored_i8_f16 : pkv::launch_scored_i8_bf16)
+                              : (dtype == PKV_F16 ? pkv::launch_scored_f16 : pkv::launch_scored_bf16);
+        const pkv_status st = launch(p, maps, head_dim, block_size, gh, grid, merge_rows, s);
+        if (st != PKV_OK || !want_weights || max_context_len == 0) return st;
+        const pkv::WeightParams w{scored->weights, scored->weights_out, scored->weights_stride};
+        const dim3 wgrid(static_cast<unsigned>((max_context_len + pkv::kWeightTokens - 1) / pkv::kWeightTokens),
+                         static_cast<unsigned>(num_kv_heads), static_cast<unsigned>(num_seqs));
+        pkv::decode_weights_kernel<<<wgrid, pkv::kWeightThreads, 0, s>>>(p, w);
+        pkv::count_launch();
+        return pkv::launch_status();
+    }
     if (int8_kv)
         return dtype == PKV_F16
                    ? pkv::launch_decode_i8_f16(p, maps, head_dim, block_size, gh, grid, merge_rows, s)
@@ -376,6 +450,51 @@ PKV_API pkv_status pkv_paged_attention_decode_int8(
                        block_stride_elems, block_tables, max_blocks_per_seq, context_lens,
                        max_context_len, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                        scale, out, workspace, workspace_bytes, partition_size, dtype, stream);
+}
+
+PKV_API size_t pkv_decode_scored_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
+                                                 int head_dim, int block_size, int max_context_len,
+                                                 int window, int want_weights, int int8_cache,
+                                                 int partition_size) {
+    if (window < 0) return static_cast<size_t>(-1);
+    const int sm = partition_size > 0 ? 1 : pkv::current_sm_count();
+    if (sm <= 0) return static_cast<size_t>(-1);
+    const int span = scored_span(max_context_len, window, block_size);
+    int part = 0, nparts = 0;
+    if (plan_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, span, partition_size, sm,
+                    int8_cache != 0, &part, &nparts, nullptr, nullptr) != PKV_OK)
+        return static_cast<size_t>(-1);
+    return scored_workspace(num_seqs, num_q_heads, head_dim, nparts, span, want_weights != 0);
+}
+
+PKV_API pkv_status pkv_paged_attention_decode_scored(
+    const void *q, const void *k_cache, const void *v_cache, int64_t num_blocks,
+    int64_t block_stride_elems, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *context_lens, int max_context_len, int num_seqs, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, float scale, float softcap, const float *slopes,
+    int window, const int32_t *starts, const float *weights, float *weights_out,
+    int64_t weights_stride, void *out, void *workspace, size_t workspace_bytes, int partition_size,
+    pkv_dtype dtype, void *stream) {
+    const ScoredArgs a{softcap, slopes, window, starts, weights, weights_out, weights_stride};
+    return decode_impl(q, k_cache, v_cache, nullptr, nullptr, false, num_blocks, block_stride_elems,
+                       block_tables, max_blocks_per_seq, context_lens, max_context_len, num_seqs,
+                       num_q_heads, num_kv_heads, head_dim, block_size, scale, out, workspace,
+                       workspace_bytes, partition_size, dtype, stream, &a);
+}
+
+PKV_API pkv_status pkv_paged_attention_decode_scored_int8(
+    const void *q, const int8_t *k_cache, const int8_t *v_cache, const float *k_scale,
+    const float *v_scale, int64_t num_blocks, int64_t block_stride_elems,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+    int max_context_len, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, float scale, float softcap, const float *slopes, int window,
+    const int32_t *starts, void *out, void *workspace, size_t workspace_bytes, int partition_size,
+    pkv_dtype dtype, void *stream) {
+    const ScoredArgs a{softcap, slopes, window, starts, nullptr, nullptr, 0};
+    return decode_impl(q, k_cache, v_cache, k_scale, v_scale, true, num_blocks, block_stride_elems,
+                       block_tables, max_blocks_per_seq, context_lens, max_context_len, num_seqs,
+                       num_q_heads, num_kv_heads, head_dim, block_size, scale, out, workspace,
+                       workspace_bytes, partition_size, dtype, stream, &a);
 }
 
 }  // extern "C"

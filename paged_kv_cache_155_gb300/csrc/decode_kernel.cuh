@@ -111,6 +111,16 @@ struct DecodeParams {
     // CTAs signal at their start that it may be placed.  Without it the next kernel
     // of the stream starts only when this grid has completed.
     int trigger_dependents;
+    // Scored form only (score_modified and span_of): what a score and its mask are.
+    const float *slopes;    // [num_q_heads] or null: bias slope * (t - query position)
+    const int32_t *starts;  // [num_seqs] or null: first visible token
+    float *ws_s;            // or null: every score (log2 units, masked ones -inf), row
+                            // (sequence, query head) at row * score_stride + t - span begin
+    int64_t score_stride;   // a multiple of 32
+    int window;             // visible tokens of a sequence, its last ones; 0: all
+    int block_size;
+    float cap_in;           // ln 2 / softcap: a score in log2 units -> score / softcap
+    float cap_out;          // softcap * log2(e); 0: scores are not capped
 };
 
 // Tensor maps of the two pool halves for the forms that stage by tiled TMA
@@ -124,6 +134,53 @@ struct DecodeMaps {
 __device__ __forceinline__ int partitions_of(const DecodeParams &p, int len) {
     const int span = len - p.tok_begin;
     return span > 0 ? (span + p.partition_size - 1) / p.partition_size : 1;
+}
+
+// Scored form: the visible tokens [lo, len) of a sequence, and where its partitions
+// begin -- at the block that holds lo, so that no table entry before it is read (a
+// window's past blocks may be free already).  An empty range begins at len.
+struct DecodeSpan {
+    int lo, begin;
+};
+__device__ __forceinline__ DecodeSpan span_of(const DecodeParams &p, int seq, int len) {
+    int lo = p.window > 0 ? len - p.window : 0;
+    if (p.starts) lo = max(lo, p.starts[seq]);
+    lo = max(lo, 0);
+    if (lo >= len) return DecodeSpan{len, len};
+    return DecodeSpan{lo, lo & ~(p.block_size - 1)};
+}
+__device__ __forceinline__ int partitions_of_span(const DecodeParams &p, const DecodeSpan &s, int len) {
+    return s.begin < len ? (len - s.begin + p.partition_size - 1) / p.partition_size : 1;
+}
+
+// cap * tanh(score / cap) of a score y in log2 units (y log2(e)-scaled, and so is the
+// result): x = y cap_in, result cap_out tanh(x).  For |x| <= 3/4 as y (1 + u Q(u)),
+// u = x^2, with Q a degree-5 Chebyshev fit of (tanh(x)/x - 1)/u (relative error
+// 2^-26): no exponential, and no cancellation near 0, so a capped score is as exact
+// as an uncapped one.  Beyond, cap_out (1 - 2 / (1 + e^(2|x|))) with y's sign, whose
+// absolute error of 2^-22 cap_out is as small relative to a score of that size.
+__device__ __forceinline__ float soft_cap(float y, float cap_in, float cap_out) {
+    const float x = y * cap_in;
+    const float u = x * x;
+    float q = fmaf(u, 0.0019145392579957843f, -0.00794092658907175f);
+    q = fmaf(u, q, 0.02161884680390358f);
+    q = fmaf(u, q, -0.05393656715750694f);
+    q = fmaf(u, q, 0.13333185017108917f);
+    q = fmaf(u, q, -0.3333333134651184f);
+    float r = fmaf(y, u * q, y);
+    if (!(u <= 0.5625f)) {  // NaN too
+        const float e = fast_exp2(fabsf(x) * 2.885390081777927f);  // e^(2|x|)
+        r = copysignf(cap_out * (1.f - 2.f * fast_rcp(1.f + e)), x);
+        if (x != x) r = x;
+    }
+    return r;
+}
+
+// A score y = scale * log2(e) * (q . k) of the token at distance dist = t - query
+// position (<= 0), capped, then biased (slope2 = slope * log2(e)).
+__device__ __forceinline__ float score_modified(const DecodeParams &p, float y, float slope2, int dist) {
+    if (p.cap_out > 0.f) y = soft_cap(y, p.cap_in, p.cap_out);
+    return fmaf(slope2, static_cast<float>(dist), y);
 }
 
 // Values per lane vector of the CUDA-core kernel (see DecodeGeom).
@@ -205,8 +262,11 @@ struct DecodeGeom {
 // one head, 128 bytes each -- all 128 INT8 codes, or 64 16-bit values -- with a
 // 128-byte swizzle), used by the warp-MMA forms at head_dim 128; the other forms
 // ignore them.
-template <typename T, typename KT, int D, int BS, int GH>
-__global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 ? 2 : 3) : 1)
+// kScored: scores capped, biased and masked from below (DecodeParams::slopes ..
+// cap_out), and kept for the weights when ws_s is given; a form of its own, so that
+// the plain one carries none of it.
+template <typename T, typename KT, int D, int BS, int GH, bool kScored = false>
+__global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 ? 2 : 3) : (GH >= 4 && kScored) ? 4 : 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                                               const __grid_constant__ CUtensorMap tmap_v,
                                                               const DecodeParams p) {
@@ -251,12 +311,15 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
     // ---- the partition's first table entries are fetched together with the context
     //      length (where the partition starts does not depend on it), so the first
     //      tile copies wait for one global-memory round trip, not two
-    const int tok0 = p.tok_begin + part * p.partition_size;
-    const int blk0 = tok0 / BS;
+    //      (in the scored form the start does depend on it)
+    int tok0 = p.tok_begin + part * p.partition_size;
+    int blk0 = tok0 / BS;
     const int32_t *trow = p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq + blk0;
     int first_entry = 0;  // entry threadIdx.x of the slice, if the table has it
-    if (static_cast<int>(threadIdx.x) < min(p.max_blocks_per_seq - blk0, p.partition_size / BS))
-        first_entry = trow[threadIdx.x];
+    if constexpr (!kScored) {
+        if (static_cast<int>(threadIdx.x) < min(p.max_blocks_per_seq - blk0, p.partition_size / BS))
+            first_entry = trow[threadIdx.x];
+    }
 
     // ---- context length (device value, range-checked) and partition bounds
     int len = p.context_lens[seq];
@@ -265,8 +328,22 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
             raise_flag(p.status, PKV_DEVERR_CONTEXT_LEN);
         len = len < 0 ? 0 : p.len_cap;
     }
-    const int nparts = partitions_of(p, len);
+    DecodeSpan span{0, 0};
+    int nparts;
+    if constexpr (kScored) {
+        span = span_of(p, seq, len);
+        nparts = partitions_of_span(p, span, len);
+    } else {
+        nparts = partitions_of(p, len);
+    }
     if (part >= nparts) return;  // uniform over the CTA
+    if constexpr (kScored) {
+        tok0 = span.begin + part * p.partition_size;
+        blk0 = tok0 / BS;
+        trow = p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq + blk0;
+        if (static_cast<int>(threadIdx.x) < min(p.max_blocks_per_seq - blk0, p.partition_size / BS))
+            first_entry = trow[threadIdx.x];
+    }
     const int tok1 = min(len, tok0 + p.partition_size);
     const int ntok = max(0, tok1 - tok0);
     const int nchunks = (ntok + TILE - 1) / TILE;
@@ -509,6 +586,22 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
             hqb[e] = __shfl_sync(0xffffffffu, mqb, 4 * (2 * mt + e));
         }
     }
+    // scored form: the slopes (log2 units) of the heads whose scores this lane holds, and
+    // the row of scores that it writes
+    constexpr int kSlopes = kMma ? 2 : GH;
+    float slope2[kScored ? kSlopes : 1];
+    if constexpr (kScored) {
+#pragma unroll
+        for (int e = 0; e < kSlopes; ++e) {
+            // INT8 MMA: heads 2 mt, 2 mt + 1; 16-bit MMA: mg, mg + 8; lanes: head e
+            const int h = kMma ? (kQuant ? 2 * mt + e : mg + 8 * e) : e;
+            slope2[e] = p.slopes && h < GH ? p.slopes[hq0 + h] * 1.4426950408889634f : 0.f;
+        }
+    }
+    const int qpos = len - 1;  // the query's position
+    auto score_row = [&](int h) {  // scores of head hq0 + h from the partition's first token on
+        return p.ws_s + (static_cast<int64_t>(seq) * p.num_q_heads + hq0 + h) * p.score_stride + (tok0 - span.begin);
+    };
     float acc[GH][VL];
     float m[GH], l[GH];
 #pragma unroll
@@ -582,6 +675,14 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         sc[e] = tb + mg + 8 * (e >> 1) < valid ? fmaf(sacc[e], hqs[e & 1], -hqb[e & 1]) : -INFINITY;
+                    if constexpr (kScored) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int t = tb + mg + 8 * (e >> 1), tpos = tok0 + c * TILE + t;
+                            sc[e] = t < valid && tpos >= span.lo ? score_modified(p, sc[e], slope2[e & 1], tpos - qpos)
+                                                                 : -INFINITY;
+                        }
+                    }
                     // per head, the maximum over the step's tokens (the eight lanes with this
                     // mt hold them): finite, as token tb is in the context
                     float mx[2];
@@ -612,8 +713,11 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                     // into the B layout of O^T += V^T P^T (k = tokens, columns = heads) by 8 x 8
                     // transposes
                     float r[4];
-                    const uint32_t p0 = pack_mma2<false>(fast_exp2(sc[0] - mh[0]), fast_exp2(sc[1] - mh[1]), r[0], r[1]);
-                    const uint32_t p1 = pack_mma2<false>(fast_exp2(sc[2] - mh[0]), fast_exp2(sc[3] - mh[1]), r[2], r[3]);
+                    // (scored: a step may hold no visible token, and then -inf - -inf is kept away)
+                    const float m0 = kScored && mh[0] == -INFINITY ? 0.f : mh[0];
+                    const float m1 = kScored && mh[1] == -INFINITY ? 0.f : mh[1];
+                    const uint32_t p0 = pack_mma2<false>(fast_exp2(sc[0] - m0), fast_exp2(sc[1] - m1), r[0], r[1]);
+                    const uint32_t p1 = pack_mma2<false>(fast_exp2(sc[2] - m0), fast_exp2(sc[3] - m1), r[2], r[3]);
                     lh[0] += r[0] + r[2];
                     lh[1] += r[1] + r[3];
                     const uint32_t pb0 = movmatrix_trans(p0);
@@ -719,6 +823,27 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                             for (int e = 0; e < 2; ++e)
                                 sc2[2 * h + e] = tb + 8 * h + 2 * mt + e < valid ? sacc[h][2 + e] * mqs : -INFINITY;
                     }
+                    if constexpr (kScored) {
+#pragma unroll
+                        for (int e = 0; e < STEP / 4; ++e) {
+                            const int t = tb + 8 * (e >> 1) + 2 * mt + (e & 1), tpos = tok0 + c * TILE + t;
+                            const bool seen = t < valid && tpos >= span.lo;
+                            sc[e] = seen ? score_modified(p, sc[e], slope2[0], tpos - qpos) : -INFINITY;
+                            if constexpr (kRows16)
+                                sc2[e] = seen ? score_modified(p, sc2[e], slope2[1], tpos - qpos) : -INFINITY;
+                        }
+                        if (p.ws_s) {
+#pragma unroll
+                            for (int h = 0; h < STEP / 8; ++h) {
+                                const int at = c * TILE + tb + 8 * h + 2 * mt;
+                                if (mg < GH)
+                                    *reinterpret_cast<float2 *>(score_row(mg) + at) = make_float2(sc[2 * h], sc[2 * h + 1]);
+                                if constexpr (kRows16)
+                                    *reinterpret_cast<float2 *>(score_row(mg + 8) + at) =
+                                        make_float2(sc2[2 * h], sc2[2 * h + 1]);
+                            }
+                        }
+                    }
                     float mx = sc[0], mx2 = kRows16 ? sc2[0] : -INFINITY;
 #pragma unroll
                     for (int e = 1; e < STEP / 4; ++e) {
@@ -755,18 +880,23 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                     }
                     // the weights meet V rounded to the cache type (as the A fragment of P V,
                     // rows and k indices those of S); the row sum adds the rounded values
+                    // (scored: a step may hold no visible token, and then -inf - -inf is kept away;
+                    // with the weights wanted the sum adds the unrounded ones, whose quotients
+                    // they are)
+                    const float mb = kScored && mrow == -INFINITY ? 0.f : mrow;
+                    const float mb2 = kScored && mrow2 == -INFINITY ? 0.f : mrow2;
                     uint32_t pa[STEP / 8], pb[STEP / 8];
 #pragma unroll
                     for (int h = 0; h < STEP / 8; ++h) {
                         float r0, r1;
-                        pa[h] = pack_mma2<kMmaBF16>(fast_exp2(sc[2 * h] - mrow), fast_exp2(sc[2 * h + 1] - mrow),
-                                                    r0, r1);
-                        lrow += r0 + r1;
+                        const float e0 = fast_exp2(sc[2 * h] - mb), e1 = fast_exp2(sc[2 * h + 1] - mb);
+                        pa[h] = pack_mma2<kMmaBF16>(e0, e1, r0, r1);
+                        lrow += kScored && p.ws_s ? e0 + e1 : r0 + r1;
                         pb[h] = 0u;
                         if constexpr (kRows16) {
-                            pb[h] = pack_mma2<kMmaBF16>(fast_exp2(sc2[2 * h] - mrow2),
-                                                        fast_exp2(sc2[2 * h + 1] - mrow2), r0, r1);
-                            lrow2 += r0 + r1;
+                            const float f0 = fast_exp2(sc2[2 * h] - mb2), f1 = fast_exp2(sc2[2 * h + 1] - mb2);
+                            pb[h] = pack_mma2<kMmaBF16>(f0, f1, r0, r1);
+                            lrow2 += kScored && p.ws_s ? f0 + f1 : r0 + r1;
                         }
                     }
                     // O += P V: B column mg of n-tile nt is channel (D / 8) mg + nt; lane
@@ -808,13 +938,16 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                             }
                         }
                     }
-                    if (tb + STEP > valid) {  // warp-uniform: a step that ends past the context
+                    // (scored: the same for rows before the first visible token)
+                    const int vlo = kScored ? span.lo - (tok0 + c * TILE) : 0;  // visible rows of the tile: [vlo, valid)
+                    if (tb + STEP > valid || (kScored && tb < vlo)) {  // warp-uniform: a step that ends past the context
                         // rows past the context are unwritten slots of the last block; their
                         // weight is 0, but 0 * NaN or 0 * Inf would still poison O, so the
                         // rows themselves are zeroed before they reach the MMA
 #pragma unroll
                         for (int r = 0; r < STEP / 4; ++r) {
-                            if (tb + (r >> 1) * 8 + 2 * mt + (r & 1) >= valid) {
+                            const int vt_row = tb + (r >> 1) * 8 + 2 * mt + (r & 1);
+                            if (vt_row >= valid || (kScored && vt_row < vlo)) {
 #pragma unroll
                                 for (int w = 0; w < VW; ++w) x[r][w] = 0u;
                             }
@@ -882,6 +1015,27 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                             for (int g = 0; g < GH; ++g) sc[it][g] = -INFINITY;
                         }
                     }
+                    if constexpr (kScored) {
+#pragma unroll
+                        for (int it = 0; it < IT_STEP; ++it) {
+                            const int t = (it0 + it) * TPG + grp, tpos = tok0 + c * TILE + t;
+                            const bool seen = t < valid && tpos >= span.lo;
+#pragma unroll
+                            for (int g = 0; g < GH; ++g)
+                                sc[it][g] = seen ? score_modified(p, sc[it][g], slope2[g], tpos - qpos) : -INFINITY;
+                        }
+                        if (!kQuant && p.ws_s) {
+                            // every lane of a token row holds its score: lane `sub` writes the row of
+                            // step it0 + sub, so a store covers IT_STEP * TPG tokens
+#pragma unroll
+                            for (int g = 0; g < GH; ++g) {
+                                float mine = sc[0][g];
+#pragma unroll
+                                for (int it = 1; it < IT_STEP; ++it) mine = sub == it ? sc[it][g] : mine;
+                                if (sub < IT_STEP) score_row(g)[c * TILE + (it0 + sub) * TPG + grp] = mine;
+                            }
+                        }
+                    }
                     // online softmax update (P1 §7.2), m warp-uniform
 #pragma unroll
                     for (int g = 0; g < GH; ++g) {
@@ -898,9 +1052,11 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                             for (int e = 0; e < VL; ++e) acc[g][e] *= alpha;
                             m[g] = mx;
                         }
+                        // (scored: a step may hold no visible token, and then -inf - -inf is kept away)
+                        const float mg_ref = kScored && m[g] == -INFINITY ? 0.f : m[g];
 #pragma unroll
                         for (int it = 0; it < IT_STEP; ++it) {
-                            sc[it][g] = fast_exp2(sc[it][g] - m[g]);  // masked rows -> 0
+                            sc[it][g] = fast_exp2(sc[it][g] - mg_ref);  // masked rows -> 0
                             // INT8: the weight meets V in fp16; the sum adds the rounded value
                             if constexpr (kQuant) sc[it][g] = __half2float(__float2half_rn(sc[it][g]));
                             l[g] += sc[it][g];
@@ -910,7 +1066,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
 #pragma unroll
                     for (int it = 0; it < IT_STEP; ++it) {
                         const int t = (it0 + it) * TPG + grp;
-                        if (t < valid) {
+                        if (t < valid && (!kScored || tok0 + c * TILE + t >= span.lo)) {
                             if constexpr (kQuant) {
                                 uint32_t vh[VL / 2];
                                 load_codes_f16<VL>(vs + t * D + sub * VL, vh);
@@ -1103,7 +1259,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
 constexpr int kMergeUnroll = 8;
 constexpr int kMergeWideFrom = 32;  // partitions per row from which four warps share a row
 
-template <typename T, int D, int WPR>
+template <typename T, int D, int WPR, bool kScored = false>
 __global__ void __launch_bounds__(128) paged_decode_merge_kernel(const DecodeParams p,
                                                                  int num_rows) {
     static_assert(WPR == 1 || WPR == 4, "one or four warps per row");
@@ -1122,7 +1278,9 @@ __global__ void __launch_bounds__(128) paged_decode_merge_kernel(const DecodePar
         raise_flag(p.status, PKV_DEVERR_CONTEXT_LEN);  // shorter than the shared prefix
     if (len < 0) len = 0;
     if (len > p.len_cap) len = p.len_cap;
-    const int nparts = p.slot_base + partitions_of(p, len);  // slots holding partials
+    int nparts;  // slots holding partials
+    if constexpr (kScored) nparts = partitions_of_span(p, span_of(p, seq, len), len);
+    else nparts = p.slot_base + partitions_of(p, len);
     if (nparts <= 1 && !p.always_partial) return;           // written by the decode kernel
     const int mine = nparts > share ? (nparts - share + WPR - 1) / WPR : 0;  // this warp's partitions
     const int64_t base = static_cast<int64_t>(row) * p.num_partitions;

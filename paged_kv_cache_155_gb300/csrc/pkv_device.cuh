@@ -134,6 +134,12 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // max(a, b, c) / min(a, b, c) in one instruction (sm_100 and later).
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float d;

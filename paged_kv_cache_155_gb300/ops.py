@@ -571,6 +571,155 @@ def prepare_rope_reshape_and_cache_int8(q: torch.Tensor, k_new: torch.Tensor, v_
 
 
 # ---------------------------------------------------------------------------
+# Scored attention: capped and biased scores, windows and starts, weights
+# ---------------------------------------------------------------------------
+
+def decode_scored_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                                  window=0, want_weights=False, int8=False, partition_size=0) -> int:
+    n = lib().pkv_decode_scored_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                                max_context_len, window, int(want_weights), int(int8),
+                                                partition_size)
+    if n == ctypes.c_size_t(-1).value:
+        raise PagedKVError("pkv_decode_scored_workspace_bytes", 1)
+    return int(n)
+
+
+def _own_workspace(device: torch.device, nbytes: int, given: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """The caller's workspace, or one of this call's own: two prepared calls, or two
+    captured graphs, never meet in it."""
+    if given is not None:
+        if given.device != device or not given.is_contiguous():
+            raise ValueError("workspace must be contiguous and on the tensors' device")
+        return given
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _check_scores(softcap, slopes, window, hq):
+    if softcap != 0.0 and not 1e-3 <= softcap <= 1e6:
+        raise ValueError("softcap must be 0 or in [1e-3, 1e6]")
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.numel() != hq or not slopes.is_contiguous()):
+        raise ValueError("slopes must be a contiguous float32 [num_q_heads]")
+    if window < 0:
+        raise ValueError("window must not be negative")
+
+
+def _prepare_decode_scored(what, q, k_cache, v_cache, scales, block_tables, context_lens, scale, out, softcap, slopes,
+                           window, starts, weights, weights_out, max_context_len, partition_size, workspace):
+    nb, hkv, bs, d, stride = _check_int8_cache(k_cache, v_cache, *scales) if scales else _cache_geometry(k_cache, v_cache)
+    if q.dim() != 3 or q.shape[2] != d or not q.is_contiguous():
+        raise ValueError(f"q must be a contiguous [num_seqs, num_q_heads, {d}]")
+    b, hq = int(q.shape[0]), int(q.shape[1])
+    if not scales and q.dtype != k_cache.dtype:
+        raise ValueError("q dtype must match the cache")
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != b \
+            or not block_tables.is_contiguous():
+        raise ValueError("block_tables must be a contiguous int32 [num_seqs, max_blocks_per_seq]")
+    if context_lens.dtype != torch.int32 or context_lens.numel() != b or not context_lens.is_contiguous():
+        raise ValueError("context_lens must be a contiguous int32 [num_seqs]")
+    _check_scores(softcap, slopes, window, hq)
+    if starts is not None and (starts.dtype != torch.int32 or starts.numel() != b or not starts.is_contiguous()):
+        raise ValueError("starts must be a contiguous int32 [num_seqs]")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item()) if b else 0
+    if weights is not None and weights_out is None:
+        raise ValueError("weights need weights_out (which may be the same tensor)")
+    for name, t in (("weights", weights), ("weights_out", weights_out)):
+        if t is not None and (t.dtype != torch.float32 or t.dim() != 3 or tuple(t.shape[:2]) != (b, hkv)
+                              or t.shape[2] < max_context_len or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous float32 [num_seqs, num_kv_heads, >= max_context_len]")
+    if weights is not None and weights.shape != weights_out.shape:
+        raise ValueError("weights and weights_out must have one shape")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out must match q")
+    _one_device(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens, out=out,
+                slopes=slopes, starts=starts, weights=weights, weights_out=weights_out)
+    with torch.cuda.device(q.device):
+        need = decode_scored_workspace_bytes(b, hq, hkv, d, bs, max_context_len, window, weights_out is not None,
+                                             bool(scales), partition_size)
+    workspace = _own_workspace(q.device, need, workspace)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    args = [q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()]
+    args += [t.data_ptr() for t in scales]
+    args += [nb, stride, block_tables.data_ptr(), int(block_tables.shape[1]), context_lens.data_ptr(),
+             int(max_context_len), b, hq, hkv, d, bs, float(scale), float(softcap), ptr(slopes), int(window), ptr(starts)]
+    if not scales:
+        args += [ptr(weights), ptr(weights_out), 0 if weights_out is None else int(weights_out.shape[2])]
+    args += [out.data_ptr(), ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+             int(partition_size), _dtype_code(q)]
+    return PreparedCall(what, tuple(args), q.device,
+                        (q, k_cache, v_cache, scales, block_tables, context_lens, out, slopes, starts, weights,
+                         weights_out, workspace), out)
+
+
+def paged_attention_decode_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                  block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                  scale: Optional[float] = None, out: Optional[torch.Tensor] = None, *,
+                                  softcap: float = 0.0, slopes: Optional[torch.Tensor] = None, window: int = 0,
+                                  starts: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None,
+                                  weights_out: Optional[torch.Tensor] = None, max_context_len: Optional[int] = None,
+                                  partition_size: int = 0, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_attention_decode with capped scores (softcap * tanh(x / softcap)), a distance
+    bias (slopes fp32 [Hq] times t - position), the last ``window`` tokens only, and a
+    first visible token per sequence (starts int32 [B]); a sequence that sees nothing
+    gets zeros.  ``weights_out`` fp32 [B, Hkv, W] receives ``weights`` (None: zeros) plus
+    each context token's softmax weight summed over its KV head's query heads; it may be
+    ``weights`` itself."""
+    return prepare_paged_attention_decode_scored(
+        q, k_cache, v_cache, block_tables, context_lens, scale, out, softcap=softcap, slopes=slopes, window=window,
+        starts=starts, weights=weights, weights_out=weights_out, max_context_len=max_context_len,
+        partition_size=partition_size, workspace=workspace)()
+
+
+def prepare_paged_attention_decode_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                          block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                          scale: Optional[float] = None, out: Optional[torch.Tensor] = None, *,
+                                          softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+                                          window: int = 0, starts: Optional[torch.Tensor] = None,
+                                          weights: Optional[torch.Tensor] = None,
+                                          weights_out: Optional[torch.Tensor] = None,
+                                          max_context_len: Optional[int] = None, partition_size: int = 0,
+                                          workspace: Optional[torch.Tensor] = None) -> PreparedCall:
+    """paged_attention_decode_scored, checked and marshalled once (see PreparedCall); the
+    call returns ``out``.  Without ``workspace`` it holds one of its own."""
+    return _prepare_decode_scored("pkv_paged_attention_decode_scored", q, k_cache, v_cache, (), block_tables,
+                                  context_lens, scale, out, softcap, slopes, window, starts, weights, weights_out,
+                                  max_context_len, partition_size, workspace)
+
+
+def paged_attention_decode_scored_int8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                       k_scale: torch.Tensor, v_scale: torch.Tensor, block_tables: torch.Tensor,
+                                       context_lens: torch.Tensor, scale: Optional[float] = None,
+                                       out: Optional[torch.Tensor] = None, *, softcap: float = 0.0,
+                                       slopes: Optional[torch.Tensor] = None, window: int = 0,
+                                       starts: Optional[torch.Tensor] = None, max_context_len: Optional[int] = None,
+                                       partition_size: int = 0,
+                                       workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_attention_decode_scored over an INT8 cache (score forms and masks, no weights)."""
+    return prepare_paged_attention_decode_scored_int8(
+        q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, out, softcap=softcap, slopes=slopes,
+        window=window, starts=starts, max_context_len=max_context_len, partition_size=partition_size,
+        workspace=workspace)()
+
+
+def prepare_paged_attention_decode_scored_int8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                               k_scale: torch.Tensor, v_scale: torch.Tensor,
+                                               block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                               scale: Optional[float] = None, out: Optional[torch.Tensor] = None, *,
+                                               softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+                                               window: int = 0, starts: Optional[torch.Tensor] = None,
+                                               max_context_len: Optional[int] = None, partition_size: int = 0,
+                                               workspace: Optional[torch.Tensor] = None) -> PreparedCall:
+    """paged_attention_decode_scored_int8, checked and marshalled once (see PreparedCall)."""
+    return _prepare_decode_scored("pkv_paged_attention_decode_scored_int8", q, k_cache, v_cache, (k_scale, v_scale),
+                                  block_tables, context_lens, scale, out, softcap, slopes, window, starts, None, None,
+                                  max_context_len, partition_size, workspace)
+
+
+# ---------------------------------------------------------------------------
 # Eviction by accumulated attention weight
 # ---------------------------------------------------------------------------
 

@@ -84,3 +84,22 @@ def attend_row(q, k, v, scale, softcap, slope, pos, lo, hi):
         w[seen] = torch.softmax(x[seen], 0)
     vs = v[seen].double()
     return w[seen] @ vs, w, w[seen] @ vs.abs()
+
+
+def score_slack(q, k, scale, softcap, slope, span, int8=False):
+    """How far a kernel's fp32 score of q [d] against rows k [n, d] may be from exact: every product of the dot product and
+    every partial sum rounds once at 2^-23 (tensor cores truncate) of the summed magnitudes; an INT8 cache's query is first
+    rounded to fp16 after scaling by a power of two (2^-11 of each product, or 2^-24 of the largest query channel);
+    capping and the bias add a few roundings of the score's and the bias's size."""
+    mag = (k.double().abs() @ q.double().abs()).max().item() * abs(scale) if k.shape[0] else 0.0
+    d = q.shape[0]
+    slack = mag * (d + 8) * 2.0 ** -23
+    if int8 and k.shape[0]:
+        slack += mag * 2.0 ** -11 + abs(scale) * d * 2.0 ** -24 * q.abs().max().item() * k.abs().max().item()
+    return slack + (mag + min(softcap, mag) + abs(slope) * span) * 2.0 ** -21
+
+
+def check_attention(got, ref, absref, slack, p_half, what):
+    """An attention output row [d] against exact `ref`: each weight is off by the score slack on both sides of the quotient
+    (factor 2) and by one rounding of the weights to the MMA's type, which the row sum shares (factor 2)."""
+    rounded_close(got, ref, absref * (2 * slack + 2 * p_half + 2.0 ** -18), what)

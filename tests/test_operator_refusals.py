@@ -46,6 +46,58 @@ def test_rope_refusals(lib, int8):
         assert call(sk=None) == INVALID and call(sv=8) == INVALID and call(stride=2 * 2 * 16 * 64 + 8) == INVALID
 
 
+def _scored(lib, int8=False, **kw):
+    a = dict(q=16, k=16, v=16, ks=16, vs=16, nb=64, stride=2 * 4 * 16 * 64, bt=16, mb=8, cl=16, maxl=100, b=4, hq=4, hkv=4, d=64,
+             bs=16, scale=0.125, cap=0.0, slopes=None, window=0, starts=None, w=None, wo=None, ws=0, out=16, wk=None, wkb=0,
+             part=128, dt=0)
+    a.update(kw)
+    head = [a[n] for n in ("nb", "stride", "bt", "mb", "cl", "maxl", "b", "hq", "hkv", "d", "bs", "scale", "cap", "slopes",
+                           "window", "starts")]
+    tail = [a[n] for n in ("out", "wk", "wkb", "part", "dt")] + [None]
+    if int8:
+        return lib.pkv_paged_attention_decode_scored_int8(a["q"], a["k"], a["v"], a["ks"], a["vs"], *head, *tail)
+    return lib.pkv_paged_attention_decode_scored(a["q"], a["k"], a["v"], *head, a["w"], a["wo"], a["ws"], *tail)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_scored_decode_refusals(lib, int8):
+    call = lambda **kw: _scored(lib, int8, **kw)
+    assert call(b=0) == 0
+    for kw in (dict(d=96), dict(bs=64), dict(dt=7)):
+        assert call(**kw) == UNSUPPORTED, kw
+    for kw in (dict(cap=-1.0), dict(cap=1e-9), dict(cap=1e9), dict(cap=float("nan")), dict(cap=float("inf")), dict(window=-1),
+               dict(slopes=2), dict(starts=1), dict(hq=6), dict(maxl=129), dict(q=None), dict(out=8), dict(cl=None),
+               dict(scale=float("inf")), dict(part=24), dict(part=64)):     # 64: two partitions and no workspace
+        assert call(**kw) == INVALID, kw
+    if not int8:
+        for kw in (dict(w=16), dict(wo=16, ws=99), dict(wo=2, ws=100), dict(w=2, wo=16, ws=100), dict(wo=16, ws=100)):
+            assert call(**kw) == INVALID, kw                                # the last: the weights need a workspace
+        assert call(wo=16, ws=100, hq=4 * 129) == UNSUPPORTED
+    size = lib.pkv_decode_scored_workspace_bytes
+    assert size(4, 4, 4, 64, 16, 100, 0, 0, 0, 128) == 0
+    assert size(4, 4, 4, 64, 16, 100, 40, 0, 0, 64) == 0                    # the window's 55 tokens fit one partition
+    assert size(4, 4, 4, 64, 16, 100, 0, 1, 0, 128) == 4 * (4 * 4 * 66 + 4 * 4 * 128)
+    assert size(4, 4, 4, 64, 16, 100, -1, 0, 0, 128) == 2 ** 64 - 1
+
+
+def test_scored_decode_binding_refusals():
+    kv = torch.zeros((8, 2, 2, 16, 64), dtype=torch.float16)
+    k, v = pkv.split_pool(kv)
+    q, bt, n = torch.zeros((2, 4, 64), dtype=torch.float16), torch.zeros((2, 4), dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    call = lambda *a, **kw: pkv.paged_attention_decode_scored(*a, max_context_len=64, **kw)
+    with pytest.raises(ValueError, match="CUDA"):
+        call(q, k, v, bt, n)
+    w = torch.zeros((2, 2, 64))
+    for kw in (dict(softcap=-2.0), dict(window=-1), dict(slopes=torch.zeros(3)), dict(slopes=torch.zeros(4).double()),
+               dict(starts=n[:1]), dict(starts=n.long()), dict(weights=w), dict(weights_out=w[:, :, :63]),
+               dict(weights_out=w.double()), dict(weights=w, weights_out=torch.zeros((2, 2, 65))), dict(out=q.float())):
+        with pytest.raises(ValueError):
+            call(q, k, v, bt, n, **kw)
+    for a in ((q.bfloat16(), k, v, bt, n), (q, k, v, bt.long(), n), (q, k, v, bt[:1], n), (q, k, v, bt, n.long())):
+        with pytest.raises(ValueError):
+            call(*a)
+
+
 def test_evict_refusals(lib):
     def select(**kw):
         a = dict(w=16, ws=64, cl=16, maxl=64, b=2, hkv=2, budget=8, sinks=1, recent=2, wo=None, kept=16, kl=16)
