@@ -514,6 +514,44 @@ PKV_API pkv_status pkv_paged_attention_prefill(
     int block_size, float scale, void *out, void *workspace, size_t workspace_bytes,
     int kv_splits, pkv_dtype dtype, void *stream);
 
+/*
+ * pkv_prefill_scored_workspace_bytes -- workspace of
+ * pkv_paged_attention_prefill_scored, as pkv_prefill_workspace_bytes;
+ * has_prefix != 0 when prefix_lens is given.
+ */
+PKV_API size_t pkv_prefill_scored_workspace_bytes(int num_rows, int num_seqs, int num_q_heads,
+                                                  int num_kv_heads, int head_dim, int block_size,
+                                                  int max_query_len, int max_context_len, int window,
+                                                  int has_prefix, int kv_splits);
+
+/*
+ * pkv_paged_attention_prefill_scored -- pkv_paged_attention_prefill with the
+ * score forms of pkv_paged_attention_decode_scored (softcap, slopes) and an
+ * interval of visible tokens per row: the chunk row at position p of sequence i
+ * attends to the tokens lo <= t < hi with
+ *     lo = max(0, p + 1 - window  (window > 0),  starts[row]  (starts given))
+ *     hi = max(p + 1, min(context_lens[i], prefix_lens[i])  (prefix_lens given))
+ *   starts         [num_rows] int32, device, or NULL: each query row's first
+ *                  visible token (the start of its document in a packed
+ *                  sequence).  A row with lo >= hi gets zeros.
+ *   prefix_lens    [num_seqs] int32, device, or NULL: the first tokens of each
+ *                  sequence that every one of its rows sees, also before its
+ *                  own position (a prefix mask, e.g. over an image).
+ *   workspace      >= pkv_prefill_scored_workspace_bytes(...) when that is > 0.
+ * The key range of 128 query rows runs from the smallest lo among them to the
+ * largest hi; blocks outside it are not read, so a window's past blocks may be
+ * freed.  Inside it, the V rows that some of the 128 rows do not see must be
+ * finite.  Other arguments and errors as pkv_paged_attention_prefill.
+ */
+PKV_API pkv_status pkv_paged_attention_prefill_scored(
+    const void *q, const void *k_cache, const void *v_cache, int64_t num_blocks,
+    int64_t block_stride_elems, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *query_start, const int32_t *context_lens, int num_rows, int max_query_len,
+    int max_context_len, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, float scale, float softcap, const float *slopes, int window,
+    const int32_t *starts, const int32_t *prefix_lens, void *out, void *workspace,
+    size_t workspace_bytes, int kv_splits, pkv_dtype dtype, void *stream);
+
 /* Size of the library's built-in decode scratch array (per device). */
 #define PKV_STATIC_SCRATCH_BYTES (32u << 20) /* 32 MiB */
 

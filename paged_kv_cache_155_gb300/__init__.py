@@ -13,6 +13,8 @@ thin PyTorch binding.
                           cache write; _int8 for an INT8 cache
   paged_attention_decode_scored   the decode with capped or distance-biased scores, a
                           window, and the accumulated attention weights; _int8
+  paged_attention_prefill_scored  the chunked prefill with the same score forms,
+                          document starts and a prefix that every row sees
   evict_select / evict_compact   keep the heaviest tokens of each KV head's context
 
 Each call has a ``prepare_*`` twin that checks and marshals its arguments once
@@ -36,7 +38,9 @@ from .ops import (F16, BF16, INT8, copy_blocks, debug_wait_timeout,  # noqa: F40
                   evict_compact, prepare_evict_compact, decode_scored_workspace_bytes,
                   paged_attention_decode_scored, prepare_paged_attention_decode_scored,
                   paged_attention_decode_scored_int8,
-                  prepare_paged_attention_decode_scored_int8)
+                  prepare_paged_attention_decode_scored_int8,
+                  prefill_scored_workspace_bytes, paged_attention_prefill_scored,
+                  prepare_paged_attention_prefill_scored)
 from .block_table import slot_mapping  # noqa: F401
 from ._lib import PagedKVError  # noqa: F401
 
@@ -53,4 +57,5 @@ __all__ = ["reshape_and_cache", "paged_attention_decode", "paged_attention_decod
            "evict_compact", "prepare_evict_compact",
            "decode_scored_workspace_bytes", "paged_attention_decode_scored",
            "prepare_paged_attention_decode_scored", "paged_attention_decode_scored_int8",
-           "prepare_paged_attention_decode_scored_int8"]
+           "prepare_paged_attention_decode_scored_int8", "prefill_scored_workspace_bytes",
+           "paged_attention_prefill_scored", "prepare_paged_attention_prefill_scored"]

@@ -68,6 +68,10 @@ SIGNATURES = {
     "pkv_paged_attention_decode_scored_int8": (I32, [P, P, P, P, P, I64, I64, P, I32, P, I32, I32, I32,
                                                      I32, I32, I32, ctypes.c_float, ctypes.c_float, P,
                                                      I32, P, P, P, SZ, I32, I32, P]),
+    "pkv_prefill_scored_workspace_bytes": (SZ, [I32] * 11),
+    "pkv_paged_attention_prefill_scored": (I32, [P, P, P, I64, I64, P, I32, P, P, I32, I32, I32, I32,
+                                                 I32, I32, I32, I32, ctypes.c_float, ctypes.c_float, P,
+                                                 I32, P, P, P, P, SZ, I32, I32, P]),
     "pkv_evict_select": (I32, [P, I64, P, I32, I32, I32, I32, I32, I32, P, P, P, P]),
     "pkv_evict_compact": (I32, [P, P, I64, I64, I32, I32, I32, P, I32, P, I32, P, P, I32, P, I32,
                                 I32, P]),

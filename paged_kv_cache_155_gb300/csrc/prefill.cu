@@ -3,11 +3,9 @@
 // plan, and the launches of the persistent paged_prefill_tc_kernel and its
 // merge.
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 
-#include "prefill_tc_kernel.cuh"
-#include "pkv_host.h"
+#include "prefill_launch.cuh"
 
 namespace {
 
@@ -23,7 +21,7 @@ struct PrefillPlan {
 
 pkv_status plan_prefill(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                         int block_size, int max_query_len, int max_context_len, int kv_splits,
-                        int sm_count, PrefillPlan *pp) {
+                        int sm_count, PrefillPlan *pp, int window = 0, bool has_prefix = false) {
     if (head_dim != 128) return PKV_ERR_UNSUPPORTED;
     if (block_size != 8 && block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads ||
@@ -35,6 +33,11 @@ pkv_status plan_prefill(int num_seqs, int num_q_heads, int num_kv_heads, int hea
     pp->tile_tokens = 128 / group;
     const int64_t row_tiles = (static_cast<int64_t>(max_query_len) + pp->tile_tokens - 1) / pp->tile_tokens;
     pp->row_tiles = static_cast<int>(row_tiles);
+    // the longest token range of a row tile: with a window (and no prefix behind it) its
+    // rows' windows, from the block that holds the first
+    if (window > 0 && !has_prefix)
+        max_context_len = static_cast<int>(std::min<int64_t>(
+            max_context_len, static_cast<int64_t>(window) + pp->tile_tokens - 1 + block_size - 1));
     const int64_t ctx_tiles = std::max<int64_t>(1, (max_context_len + 127) / 128);
     int64_t want = kv_splits;
     if (want == 0) {
@@ -59,74 +62,22 @@ size_t prefill_workspace(int num_rows, int num_q_heads, int splits) {
     return static_cast<size_t>(num_rows) * num_q_heads * splits * (128 + 2) * sizeof(float);
 }
 
-template <typename T, int BS, int ORDER>
-pkv_status launch_prefill_one(const pkv::PrefillParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
-                              const CUtensorMap &tv, const CUtensorMap &to, int grid, cudaStream_t stream) {
-    static std::atomic<uint64_t> configured_devices{0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
-    const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
-    if (!bit || !(configured_devices.load(std::memory_order_acquire) & bit)) {
-        if (cudaFuncSetAttribute(pkv::paged_prefill_tc_kernel<T, BS, ORDER>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 pkv::PrefillLayout::kSmemBytes) != cudaSuccess)
-            return PKV_ERR_CUDA;
-        configured_devices.fetch_or(bit, std::memory_order_acq_rel);
-    }
-    pkv::paged_prefill_tc_kernel<T, BS, ORDER>
-        <<<grid, pkv::PrefillLayout::kThreads, pkv::PrefillLayout::kSmemBytes, stream>>>(tq, tk, tv, to, p);
-    pkv::count_launch();
-    return pkv::launch_status();
-}
+// What the scored prefill adds to a call.
+struct ScoredPrefillArgs {
+    float softcap;
+    const float *slopes;
+    int window;
+    const int32_t *starts;
+    const int32_t *prefix_lens;
+};
 
-template <typename T, int BS>
-pkv_status launch_prefill_bs(const pkv::PrefillParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
-                             const CUtensorMap &tv, const CUtensorMap &to, int grid, cudaStream_t s) {
-    if (p.order == pkv::kOrderSortedGroups)
-        return launch_prefill_one<T, BS, pkv::kOrderSortedGroups>(p, tq, tk, tv, to, grid, s);
-    if (p.order == pkv::kOrderPairs) return launch_prefill_one<T, BS, pkv::kOrderPairs>(p, tq, tk, tv, to, grid, s);
-    return launch_prefill_one<T, BS, pkv::kOrderRowTiles>(p, tq, tk, tv, to, grid, s);
-}
-
-template <typename T>
-pkv_status launch_prefill(const pkv::PrefillParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
-                          const CUtensorMap &tv, const CUtensorMap &to, int block_size, int grid,
-                          int max_query_len, cudaStream_t s) {
-    pkv_status st = PKV_ERR_UNSUPPORTED;
-    if (block_size == 8) st = launch_prefill_bs<T, 8>(p, tq, tk, tv, to, grid, s);
-    else if (block_size == 16) st = launch_prefill_bs<T, 16>(p, tq, tk, tv, to, grid, s);
-    else if (block_size == 32) st = launch_prefill_bs<T, 32>(p, tq, tk, tv, to, grid, s);
-    if (st != PKV_OK || p.splits == 1) return st;
-    const int64_t rows = static_cast<int64_t>(max_query_len) * p.num_q_heads;
-    const dim3 mgrid(static_cast<unsigned>((rows + 3) / 4), static_cast<unsigned>(p.num_seqs));
-    pkv::paged_prefill_merge_kernel<T><<<mgrid, 128, 0, s>>>(p);
-    pkv::count_launch();
-    return pkv::launch_status();
-}
-
-}  // namespace
-
-extern "C" {
-
-PKV_API size_t pkv_prefill_workspace_bytes(int num_rows, int num_seqs, int num_q_heads,
-                                           int num_kv_heads, int head_dim, int block_size,
-                                           int max_query_len, int max_context_len, int kv_splits) {
-    const int sm = kv_splits > 0 ? 1 : pkv::current_sm_count();
-    if (sm <= 0 || num_rows < 0) return static_cast<size_t>(-1);
-    PrefillPlan pp;
-    if (plan_prefill(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_query_len,
-                     max_context_len, kv_splits, sm, &pp) != PKV_OK)
-        return static_cast<size_t>(-1);
-    return prefill_workspace(num_rows, num_q_heads, pp.splits);
-}
-
-PKV_API pkv_status pkv_paged_attention_prefill(
+pkv_status prefill_impl(
     const void *q, const void *k_cache, const void *v_cache, int64_t num_blocks,
     int64_t block_stride_elems, const int32_t *block_tables, int max_blocks_per_seq,
     const int32_t *query_start, const int32_t *context_lens, int num_rows, int max_query_len,
     int max_context_len, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
     int block_size, float scale, void *out, void *workspace, size_t workspace_bytes,
-    int kv_splits, pkv_dtype dtype, void *stream) {
+    int kv_splits, pkv_dtype dtype, void *stream, const ScoredPrefillArgs *scored) {
     if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
     if (head_dim != 128) return PKV_ERR_UNSUPPORTED;
     if (block_size != 8 && block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
@@ -140,6 +91,16 @@ PKV_API pkv_status pkv_paged_attention_prefill(
     if (block_stride_elems < half_elems || block_stride_elems % 8) return PKV_ERR_INVALID_ARG;
     if (!k_cache || !v_cache || !pkv::aligned16(k_cache) || !pkv::aligned16(v_cache))
         return PKV_ERR_INVALID_ARG;
+    const int window = scored ? scored->window : 0;
+    const bool has_prefix = scored && scored->prefix_lens;
+    if (scored) {
+        // a cap far outside the scores' range would overflow score / softcap
+        if (scored->softcap != 0.f && !(scored->softcap >= 1e-3f && scored->softcap <= 1e6f))
+            return PKV_ERR_INVALID_ARG;
+        if (window < 0 || ((reinterpret_cast<uintptr_t>(scored->slopes) | reinterpret_cast<uintptr_t>(scored->starts) |
+                            reinterpret_cast<uintptr_t>(scored->prefix_lens)) & 3u))
+            return PKV_ERR_INVALID_ARG;
+    }
     if (num_seqs == 0 || num_rows == 0 || max_query_len == 0) return PKV_OK;
     if (!q || !out || !block_tables || !query_start || !context_lens || !pkv::aligned16(q) ||
         !pkv::aligned16(out))
@@ -147,14 +108,14 @@ PKV_API pkv_status pkv_paged_attention_prefill(
     PrefillPlan pp;
     // shape first (no CUDA call), then the plan for the real SM count
     pkv_status st = plan_prefill(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
-                                 max_query_len, max_context_len, kv_splits, 1, &pp);
+                                 max_query_len, max_context_len, kv_splits, 1, &pp, window, has_prefix);
     if (st != PKV_OK) return st;
     int sm = 0;
     if (kv_splits == 0) {
         sm = pkv::current_sm_count();
         if (sm <= 0) return PKV_ERR_CUDA;
         st = plan_prefill(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_query_len,
-                          max_context_len, 0, sm, &pp);
+                          max_context_len, 0, sm, &pp, window, has_prefix);
         if (st != PKV_OK) return st;
     }
     const size_t need = prefill_workspace(num_rows, num_q_heads, pp.splits);
@@ -217,12 +178,84 @@ PKV_API pkv_status pkv_paged_attention_prefill(
               : num_seqs <= pkv::kSortedGroupsMaxSeqs ? pkv::kOrderSortedGroups
                                                       : pkv::kOrderRowTiles;
     p.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
+    if (scored) {
+        p.slopes = scored->slopes;
+        p.starts = scored->starts;
+        p.prefix_lens = scored->prefix_lens;
+        p.window = window;
+        p.block_size = block_size;
+        if (scored->softcap > 0.f) {
+            p.cap_in = scale / scored->softcap;
+            p.cap_out = static_cast<float>(scored->softcap * 1.4426950408889634);
+        }
+    }
     // persistent: one CTA per SM (or per item when there are fewer)
     const int grid = std::min(pp.items, sm);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (scored)
+        return dtype == PKV_F16
+                   ? pkv::launch_prefill_scored_f16(p, tq, tk, tv, to, block_size, grid, max_query_len, s)
+                   : pkv::launch_prefill_scored_bf16(p, tq, tk, tv, to, block_size, grid, max_query_len, s);
     return dtype == PKV_F16
-               ? launch_prefill<__half>(p, tq, tk, tv, to, block_size, grid, max_query_len, s)
-               : launch_prefill<__nv_bfloat16>(p, tq, tk, tv, to, block_size, grid, max_query_len, s);
+               ? pkv::launch_prefill<__half>(p, tq, tk, tv, to, block_size, grid, max_query_len, s)
+               : pkv::launch_prefill<__nv_bfloat16>(p, tq, tk, tv, to, block_size, grid, max_query_len, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+PKV_API size_t pkv_prefill_workspace_bytes(int num_rows, int num_seqs, int num_q_heads,
+                                           int num_kv_heads, int head_dim, int block_size,
+                                           int max_query_len, int max_context_len, int kv_splits) {
+    const int sm = kv_splits > 0 ? 1 : pkv::current_sm_count();
+    if (sm <= 0 || num_rows < 0) return static_cast<size_t>(-1);
+    PrefillPlan pp;
+    if (plan_prefill(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_query_len,
+                     max_context_len, kv_splits, sm, &pp) != PKV_OK)
+        return static_cast<size_t>(-1);
+    return prefill_workspace(num_rows, num_q_heads, pp.splits);
+}
+
+PKV_API pkv_status pkv_paged_attention_prefill(
+    const void *q, const void *k_cache, const void *v_cache, int64_t num_blocks,
+    int64_t block_stride_elems, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *query_start, const int32_t *context_lens, int num_rows, int max_query_len,
+    int max_context_len, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, float scale, void *out, void *workspace, size_t workspace_bytes,
+    int kv_splits, pkv_dtype dtype, void *stream) {
+    return prefill_impl(q, k_cache, v_cache, num_blocks, block_stride_elems, block_tables, max_blocks_per_seq,
+                        query_start, context_lens, num_rows, max_query_len, max_context_len, num_seqs,
+                        num_q_heads, num_kv_heads, head_dim, block_size, scale, out, workspace,
+                        workspace_bytes, kv_splits, dtype, stream, nullptr);
+}
+
+PKV_API size_t pkv_prefill_scored_workspace_bytes(int num_rows, int num_seqs, int num_q_heads,
+                                                  int num_kv_heads, int head_dim, int block_size,
+                                                  int max_query_len, int max_context_len, int window,
+                                                  int has_prefix, int kv_splits) {
+    const int sm = kv_splits > 0 ? 1 : pkv::current_sm_count();
+    if (sm <= 0 || num_rows < 0 || window < 0) return static_cast<size_t>(-1);
+    PrefillPlan pp;
+    if (plan_prefill(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_query_len,
+                     max_context_len, kv_splits, sm, &pp, window, has_prefix != 0) != PKV_OK)
+        return static_cast<size_t>(-1);
+    return prefill_workspace(num_rows, num_q_heads, pp.splits);
+}
+
+PKV_API pkv_status pkv_paged_attention_prefill_scored(
+    const void *q, const void *k_cache, const void *v_cache, int64_t num_blocks,
+    int64_t block_stride_elems, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *query_start, const int32_t *context_lens, int num_rows, int max_query_len,
+    int max_context_len, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, float scale, float softcap, const float *slopes, int window, const int32_t *starts,
+    const int32_t *prefix_lens, void *out, void *workspace, size_t workspace_bytes, int kv_splits,
+    pkv_dtype dtype, void *stream) {
+    const ScoredPrefillArgs a{softcap, slopes, window, starts, prefix_lens};
+    return prefill_impl(q, k_cache, v_cache, num_blocks, block_stride_elems, block_tables, max_blocks_per_seq,
+                        query_start, context_lens, num_rows, max_query_len, max_context_len, num_seqs,
+                        num_q_heads, num_kv_heads, head_dim, block_size, scale, out, workspace,
+                        workspace_bytes, kv_splits, dtype, stream, &a);
 }
 
 }  // extern "C"

@@ -102,6 +102,14 @@ struct PrefillParams {
     FastDiv div_row_tiles, div_kv_heads, div_group, div_splits, div_per_tile;  // make_fast_div of
                        // row_tiles, num_kv_heads, group, splits, num_kv_heads * num_seqs * splits
     float scale_log2;
+    // Scored form only (kScored): what a score and its mask are (prefill_range, soft_cap).
+    const float *slopes;         // [num_q_heads] or null: bias slope * (t - query position)
+    const int32_t *starts;       // [num_rows] or null: a row's first visible token
+    const int32_t *prefix_lens;  // [num_seqs] or null: tokens that every row sees
+    int window;                  // visible tokens up to the row's own, 0: all
+    int block_size;
+    float cap_in;                // scale / softcap: a raw score -> score / softcap
+    float cap_out;               // softcap * log2(e), 0: scores are not capped
 };
 
 // Item orders (PrefillParams::order), see prefill_item.
@@ -153,6 +161,29 @@ __device__ __forceinline__ bool prefill_seq(const PrefillParams &p, const Prefil
            len <= p.len_cap;
 }
 
+// Scored form: the tokens that chunk tokens j0 .. j1 of a sequence see between them,
+// as one range [lo, hi), and where their tiles begin -- at the block that holds lo, so
+// that no table entry before it is read.  Row j sees
+//     max(0, pos + 1 - window, starts[row]) <= t < max(pos + 1, min(len, prefix)).
+// Rows that see nothing between them give the empty range at hi.  Called by whole
+// warps (the minimum of the starts is a warp reduction).
+struct PrefillRange {
+    int lo, hi, begin;
+};
+__device__ __forceinline__ PrefillRange prefill_range(const PrefillParams &p, int seq, int q0, int len, int base_pos,
+                                                      int j0, int j1) {
+    int lo = p.window > 0 ? max(0, base_pos + j0 + 1 - p.window) : 0;
+    if (p.starts) {
+        int first = 0x7fffffff;
+        for (int j = j0 + static_cast<int>(threadIdx.x & 31); j <= j1; j += 32) first = min(first, p.starts[q0 + j]);
+        lo = max(lo, __reduce_min_sync(0xffffffffu, first));
+    }
+    int hi = base_pos + j1 + 1;
+    if (p.prefix_lens) hi = max(hi, min(len, p.prefix_lens[seq]));
+    if (lo >= hi) return PrefillRange{hi, hi, hi};
+    return PrefillRange{lo, hi, lo & ~(p.block_size - 1)};
+}
+
 struct PrefillItem {
     int q0, chunk, len;  // the sequence's chunk start row, chunk length, context length
     int kvh, split, row_tile;
@@ -162,6 +193,7 @@ struct PrefillItem {
     int tok_lo, tok_hi;  // the item's KV tokens
     int ntiles;          // 128-token KV tiles
     int seq;
+    int lo;              // scored form: the row tile's first visible token (tokens before it are masked)
 };
 
 // Item i of the static order.
@@ -181,7 +213,7 @@ struct PrefillItem {
 // (sequence, KV head) pairs in L2.  False when the item holds no work: a row tile
 // past the chunk, a split past the tile's causal limit, or a sequence out of
 // contract (flagged once when `flag`).
-template <int ORDER>
+template <int ORDER, bool kScored = false>
 __device__ __forceinline__ bool prefill_item(const PrefillParams &p, int i, const PrefillSeqVals &sv,
                                              bool flag, PrefillItem &it, const unsigned char *by_len) {
     if constexpr (ORDER == kOrderSortedGroups) {
@@ -219,6 +251,19 @@ __device__ __forceinline__ bool prefill_item(const PrefillParams &p, int i, cons
     if (it.row0 >= it.rows) return false;
     const int last_row = min(it.rows, it.row0 + p.tile_rows) - 1;
     it.base_pos = it.len - it.chunk;
+    if constexpr (kScored) {
+        const PrefillRange r = prefill_range(p, it.seq, it.q0, it.len, it.base_pos, fast_div(it.row0, p.div_group),
+                                             fast_div(last_row, p.div_group));
+        it.lo = r.lo;
+        it.tok_lo = r.begin + it.split * p.split_tokens;
+        it.tok_hi = min(r.hi, it.tok_lo + p.split_tokens);
+        it.ntiles = (it.tok_hi - it.tok_lo + 127) / 128;
+        if (r.begin == r.hi && it.split == 0) {
+            it.ntiles = 1;  // rows that see nothing: a tile without tokens, so that their zeros are written
+            return true;
+        }
+        return it.tok_hi > it.tok_lo;
+    }
     const int pos_max = it.base_pos + fast_div(last_row, p.div_group);
     it.tok_lo = it.split * p.split_tokens;
     it.tok_hi = min(min(it.len, pos_max + 1), it.tok_lo + p.split_tokens);
@@ -273,7 +318,72 @@ struct PrefillLayout {
     static_assert(kSmemBytes <= 232448, "dynamic shared memory per block");
 };
 
-template <typename T, int BS, int ORDER>
+// tanh(z) / z in powers of z^2, |z| <= 3/4.
+__device__ constexpr float kTanh[6] = {1.0f, -0.3333296775817871f, 0.13325515389442444f, -0.053349819034338f, 0.01959378644824028f, -0.004723952151834965f};
+
+// Scored form: 64 raw scores of a row (columns dist0, dist0 + 1, ... from the query's
+// position) -> scores in log2 units, capped and biased.
+// Cap: cap * tanh(s / cap) with s = scale * x is x R(x^2) while |s / cap| <= 3/4, R the
+// degree-5 Chebyshev fit of tanh(z)/z in z^2 (relative error 2^-24) whose coefficients
+// are scaled to take x itself: three packed FMAs a score and no exponential, where the
+// softmax already spends one.  A warp with a larger score takes the closed form
+// cap (1 - 2 / (1 + e^(2 z))), an exponential and a reciprocal more.
+__device__ __forceinline__ void score_row(const PrefillParams &p, float (&x)[64], float slope2, int dist0) {
+    if (p.cap_out > 0.f) {
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) big = fmax3(big, fabsf(x[i]), fabsf(x[i + 1]));
+        const float k2 = p.cap_in * p.cap_in;
+        if (__any_sync(0xffffffffu, !(big * fabsf(p.cap_in) <= 0.75f))) {
+            const float k = p.cap_in * 2.885390081777927f;  // 2 log2(e) / cap
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+                x[i] = p.cap_out - 2.f * p.cap_out * fast_rcp(1.f + fast_exp2(x[i] * k));
+        } else {
+            const float c0 = p.scale_log2 * kTanh[0], c1 = p.scale_log2 * kTanh[1] * k2;
+            const float c2 = p.scale_log2 * kTanh[2] * k2 * k2, c3 = p.scale_log2 * kTanh[3] * k2 * k2 * k2;
+            const float c4 = p.scale_log2 * kTanh[4] * k2 * k2 * k2 * k2;
+            const float c5 = p.scale_log2 * kTanh[5] * k2 * k2 * k2 * k2 * k2;
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+                float u0 = 0.f, u1 = 0.f, r0 = c4, r1 = c4, s0 = c3, s1 = c3;
+                fma_f32x2(u0, u1, x[i], x[i + 1], x[i], x[i + 1]);
+                fma_f32x2(r0, r1, u0, u1, c5, c5);
+                fma_f32x2(s0, s1, u0, u1, r0, r1);
+                r0 = r1 = c2;
+                fma_f32x2(r0, r1, u0, u1, s0, s1);
+                s0 = s1 = c1;
+                fma_f32x2(s0, s1, u0, u1, r0, r1);
+                r0 = r1 = c0;
+                fma_f32x2(r0, r1, u0, u1, s0, s1);
+                x[i] *= r0;
+                x[i + 1] *= r1;
+            }
+        }
+        if (!p.slopes) return;
+        const float base = slope2 * static_cast<float>(dist0);
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+            float b0 = base, b1 = base;
+            fma_f32x2(b0, b1, slope2, slope2, static_cast<float>(i), static_cast<float>(i + 1));
+            add_f32x2(x[i], x[i + 1], b0, b1);
+        }
+        return;
+    }
+    const float base = slope2 * static_cast<float>(dist0);
+#pragma unroll
+    for (int i = 0; i < 64; i += 2) {
+        float b0 = base, b1 = base;
+        fma_f32x2(b0, b1, slope2, slope2, static_cast<float>(i), static_cast<float>(i + 1));
+        fma_f32x2(b0, b1, x[i], x[i + 1], p.scale_log2, p.scale_log2);
+        x[i] = b0;
+        x[i + 1] = b1;
+    }
+}
+
+// kScored: scores capped, biased and masked to an interval of tokens per row; a form of
+// its own, so that the plain one carries none of it.
+template <typename T, int BS, int ORDER, bool kScored = false>
 __global__ void __launch_bounds__(384, 1)
     paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                             const __grid_constant__ CUtensorMap tmap_k,
@@ -387,7 +497,7 @@ __global__ void __launch_bounds__(384, 1)
         int jt = 0, n = 0;  // tiles and items so far
         for (int ki = 0, item = prefill_slot_item<ORDER>(p, 0); item < p.num_items && ok; item = prefill_slot_item<ORDER>(p, ++ki)) {
             PrefillItem it;
-            if (!prefill_item<ORDER>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), kv == 0, it, by_len)) continue;
+            if (!prefill_item<ORDER, kScored>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), kv == 0, it, by_len)) continue;
             const int32_t *trow = p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks_per_seq;
             auto entry = [&](int j) -> int {  // this lane's block of tile j (-1: none or bad)
                 const int t0 = it.tok_lo + j * TILE;
@@ -420,7 +530,8 @@ __global__ void __launch_bounds__(384, 1)
                                     it.kvh * p.group, it.q0 + it.row_tile * p.tile_tokens, &q_full[qb], q_policy);
                 q_issue[qb] = n;
                 q_pending = false;
-                // the next item's Q box into L2 now, so its load does not wait for HBM
+                // the next item's Q box into L2 now, so its load does not wait for HBM (lane 0
+                // alone: the scored form's token range, a warp's work, is not needed for it)
                 PrefillItem nx;
                 for (int k2 = ki + 1, i2 = prefill_slot_item<ORDER>(p, k2); i2 < p.num_items; i2 = prefill_slot_item<ORDER>(p, ++k2)) {
                     if (!prefill_item<ORDER>(p, i2, prefill_seq_vals<ORDER>(p, i2, by_len), false, nx, by_len)) continue;
@@ -502,7 +613,7 @@ __global__ void __launch_bounds__(384, 1)
         int jt = 0, n = 0;
         for (int ki = 0, item = prefill_slot_item<ORDER>(p, 0); item < p.num_items && ok; item = prefill_slot_item<ORDER>(p, ++ki)) {
             PrefillItem it;
-            if (!prefill_item<ORDER>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) continue;
+            if (!prefill_item<ORDER, kScored>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) continue;
             const int qb = n % QB;
             int go = 1;
             if (lane == 0) go = tc_wait(&q_full[qb], (n / QB) & 1, abort_flag, p.status);
@@ -547,7 +658,7 @@ __global__ void __launch_bounds__(384, 1)
         int jt = 0, n_staged = 0;
         for (int ki = 0, item = prefill_slot_item<ORDER>(p, 0); item < p.num_items && ok; item = prefill_slot_item<ORDER>(p, ++ki)) {
             PrefillItem it;
-            if (!prefill_item<ORDER>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) continue;
+            if (!prefill_item<ORDER, kScored>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) continue;
             const bool staged = prefill_staged(p, it);
             for (int j = 0; j < it.ntiles; ++j, ++jt) {
                 int go = 1;
@@ -650,11 +761,22 @@ __global__ void __launch_bounds__(384, 1)
         };
         for (int ki = 0, item = prefill_slot_item<ORDER>(p, 0); item < p.num_items && ok; item = prefill_slot_item<ORDER>(p, ++ki)) {
             PrefillItem it;
-            if (!prefill_item<ORDER>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) continue;
+            if (!prefill_item<ORDER, kScored>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) continue;
             const int row = it.row0 + r;
             const bool live = r < R && row < it.rows;
             const int jtok = live ? fast_div(row, p.div_group) : 0;
             const int pos = it.base_pos + jtok;  // this row sees tokens 0 .. pos
+            int row_lo = 0, row_hi = 0;          // ... in the scored form [row_lo, row_hi)
+            float slope2 = 0.f;                  // and its bias per token, in log2 units
+            if constexpr (kScored) {
+                if (live) {
+                    row_lo = p.window > 0 ? max(0, pos + 1 - p.window) : 0;
+                    if (p.starts) row_lo = max(row_lo, p.starts[it.q0 + jtok]);
+                    row_hi = pos + 1;
+                    if (p.prefix_lens) row_hi = max(row_hi, min(it.len, p.prefix_lens[it.seq]));
+                    if (p.slopes) slope2 = p.slopes[it.kvh * p.group + row - jtok * p.group] * 1.4426950408889634f;
+                }
+            }
             float m_ref = -INFINITY, l = 0.f;
             for (int j = 0; j < it.ntiles && ok; ++j, ++jt) {
                 const int b = jt % SB;
@@ -673,11 +795,24 @@ __global__ void __launch_bounds__(384, 1)
                 for (int c = 0; c < 64; c += 16) tc::tmem_ld_x16(lane_base + 128 * b + c0 + c, x + c);
                 tc::tmem_ld_wait();
                 // tiles every row of the warp sees completely skip the per-column masks
-                const bool full = __all_sync(0xffffffffu, vr == TILE);
+                // (scored: columns [clo, chi) of this half)
+                const int clo = kScored ? min(64, max(0, row_lo - t0 - c0)) : 0;
+                const int chi = kScored ? min(64, max(0, min(valid, row_hi - t0) - c0)) : 0;
+                const bool full = __all_sync(0xffffffffu, kScored ? clo == 0 && chi == 64 : vr == TILE);
                 // partial maximum of the visible scaled scores: the extreme raw score times
                 // the scale (the maximum for a positive scale, the minimum otherwise)
                 float pmax = -INFINITY;
-                if (vh > 0) {
+                if constexpr (kScored) {
+                    // the scores themselves replace the raw ones: capped, biased, masked to -inf
+                    score_row(p, x, slope2, t0 + c0 - pos);
+                    if (!full) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) x[i] = i >= clo && i < chi ? x[i] : -INFINITY;
+                    }
+                    pmax = fmaxf(x[0], x[63]);
+#pragma unroll
+                    for (int i = 1; i + 1 < 63; i += 2) pmax = fmax3(pmax, x[i], x[i + 1]);
+                } else if (vh > 0) {
                     const bool pos_scale = p.scale_log2 > 0.f;
                     float ext = x[0];
                     if (full) {
@@ -740,6 +875,8 @@ __global__ void __launch_bounds__(384, 1)
                 // sum l adds the fp32 values
                 const uint32_t pcol = lane_base + 128 * b + 32 * half;
                 float l0 = 0.f, l1 = 0.f;
+                // scored: -inf - m is 0 weight, and a row that has seen nothing yet subtracts 0
+                const float m_sub = kScored && m_ref == -INFINITY ? 0.f : m_ref;
                 // two copies of the loop, so fully visible tiles carry no per-column mask
                 auto weights = [&](auto masked) {
 #pragma unroll
@@ -749,8 +886,9 @@ __global__ void __launch_bounds__(384, 1)
                         for (int i = 0; i < 16; ++i) {
                             const int t = c16 * 32 + 2 * i;
                             // s * scale - m for two columns in one packed FMA
-                            float e0 = -m_ref, e1 = -m_ref;
-                            fma_f32x2(e0, e1, x[t], x[t + 1], p.scale_log2, p.scale_log2);
+                            float e0 = -m_sub, e1 = -m_sub;
+                            if constexpr (kScored) add_f32x2(e0, e1, x[t], x[t + 1]);
+                            else fma_f32x2(e0, e1, x[t], x[t + 1], p.scale_log2, p.scale_log2);
                             float p0 = fast_exp2(e0);
                             float p1 = fast_exp2(e1);
                             if constexpr (decltype(masked)::value) {
@@ -763,10 +901,11 @@ __global__ void __launch_bounds__(384, 1)
                         tc::tmem_st_x16(pcol + 16 * c16, packed);
                     }
                 };
-                if (full) weights(std::false_type{});
+                if (kScored || full) weights(std::false_type{});
                 else weights(std::true_type{});
                 l += l0 + l1;
-                if (valid < TILE) {
+                const int skip = kScored ? it.lo - t0 : 0;  // rows before the row tile's first visible token
+                if (valid < TILE || (kScored && skip > 0)) {
                     // V rows past the loaded range: zero this half so 0 * stale never reaches
                     // the MMA.  The parity wait cannot alias an older phase of the slot: S(jt)
                     // exists only once PV(jt - kSB) has completed, so V(jt - kVS), the slot's
@@ -778,7 +917,7 @@ __global__ void __launch_bounds__(384, 1)
                         ok = false;
                         break;
                     }
-                    if (r >= valid) {
+                    if (r >= valid || (kScored && r < skip)) {
                         uint4 *vrow = reinterpret_cast<uint4 *>(sm + L::kOffV + (jt % VS) * L::kPanel + half * L::kHalf +
                                                                 r * 128);
 #pragma unroll
@@ -866,7 +1005,8 @@ __global__ void __launch_bounds__(384, 1)
 
 // Log-sum-exp merge of a prefill's KV splits: one warp per (chunk row, query
 // head); the row at position pos has partials in splits 0 .. pos / split_tokens.
-template <typename T>
+// (scored form: the splits that the row's tile spans).
+template <typename T, bool kScored = false>
 __global__ void __launch_bounds__(128) paged_prefill_merge_kernel(const PrefillParams p) {
     constexpr int D = 128, PER_LANE = D / 32;
     const int seq = blockIdx.y;
@@ -878,7 +1018,12 @@ __global__ void __launch_bounds__(128) paged_prefill_merge_kernel(const PrefillP
     const int jtok = idx / p.num_q_heads, hq = idx - jtok * p.num_q_heads;
     if (jtok >= chunk) return;
     const int pos = len - chunk + jtok;
-    const int nsp = min(p.splits, pos / p.split_tokens + 1);
+    int nsp = min(p.splits, pos / p.split_tokens + 1);
+    if constexpr (kScored) {
+        const int j0 = jtok / p.tile_tokens * p.tile_tokens, j1 = min(chunk, j0 + p.tile_tokens) - 1;
+        const PrefillRange r = prefill_range(p, seq, q0, len, len - chunk, j0, j1);
+        nsp = (r.hi - r.begin + p.split_tokens - 1) / p.split_tokens;
+    }
     const int64_t orow = (static_cast<int64_t>(q0) + jtok) * p.num_q_heads + hq;
     const int64_t base = orow * p.splits;
     float mmax = -INFINITY;

@@ -719,6 +719,83 @@ def prepare_paged_attention_decode_scored_int8(q: torch.Tensor, k_cache: torch.T
                                   max_context_len, partition_size, workspace)
 
 
+def prefill_scored_workspace_bytes(num_rows, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                   max_query_len, max_context_len, window=0, has_prefix=False, kv_splits=0) -> int:
+    n = lib().pkv_prefill_scored_workspace_bytes(num_rows, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                                 max_query_len, max_context_len, window, int(has_prefix), kv_splits)
+    if n == ctypes.c_size_t(-1).value:
+        raise PagedKVError("pkv_prefill_scored_workspace_bytes", 1)
+    return int(n)
+
+
+def paged_attention_prefill_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                   block_tables: torch.Tensor, query_start: torch.Tensor, context_lens: torch.Tensor,
+                                   scale: Optional[float] = None, out: Optional[torch.Tensor] = None, *,
+                                   max_query_len: int, max_context_len: int, softcap: float = 0.0,
+                                   slopes: Optional[torch.Tensor] = None, window: int = 0,
+                                   starts: Optional[torch.Tensor] = None, prefix_lens: Optional[torch.Tensor] = None,
+                                   kv_splits: int = 0, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_attention_prefill with capped scores, a distance bias (slopes fp32 [Hq]), and an
+    interval of visible tokens per row: the last ``window`` up to the row's position, from
+    ``starts`` (int32 [num_rows], the row's document) on, and always the sequence's first
+    ``prefix_lens`` (int32 [B]) tokens that the interval reaches; a row that sees nothing
+    gets zeros."""
+    return prepare_paged_attention_prefill_scored(
+        q, k_cache, v_cache, block_tables, query_start, context_lens, scale, out, max_query_len=max_query_len,
+        max_context_len=max_context_len, softcap=softcap, slopes=slopes, window=window, starts=starts,
+        prefix_lens=prefix_lens, kv_splits=kv_splits, workspace=workspace)()
+
+
+def prepare_paged_attention_prefill_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                           block_tables: torch.Tensor, query_start: torch.Tensor,
+                                           context_lens: torch.Tensor, scale: Optional[float] = None,
+                                           out: Optional[torch.Tensor] = None, *, max_query_len: int,
+                                           max_context_len: int, softcap: float = 0.0,
+                                           slopes: Optional[torch.Tensor] = None, window: int = 0,
+                                           starts: Optional[torch.Tensor] = None,
+                                           prefix_lens: Optional[torch.Tensor] = None, kv_splits: int = 0,
+                                           workspace: Optional[torch.Tensor] = None) -> PreparedCall:
+    """paged_attention_prefill_scored, checked and marshalled once (see PreparedCall); the
+    call returns ``out``.  Without ``workspace`` it holds one of its own."""
+    nb, hkv, bs, d, stride = _cache_geometry(k_cache, v_cache)
+    if q.dim() != 3 or q.shape[2] != d or not q.is_contiguous() or q.dtype != k_cache.dtype:
+        raise ValueError(f"q must be a contiguous [num_rows, num_q_heads, {d}] of the cache dtype")
+    rows, hq = int(q.shape[0]), int(q.shape[1])
+    b = int(context_lens.numel())
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != b \
+            or not block_tables.is_contiguous():
+        raise ValueError("block_tables must be a contiguous int32 [num_seqs, max_blocks_per_seq]")
+    if query_start.dtype != torch.int32 or query_start.numel() != b + 1 or not query_start.is_contiguous():
+        raise ValueError("query_start must be a contiguous int32 [num_seqs + 1]")
+    if context_lens.dtype != torch.int32 or not context_lens.is_contiguous():
+        raise ValueError("context_lens must be a contiguous int32 [num_seqs]")
+    _check_scores(softcap, slopes, window, hq)
+    for name, t, n in (("starts", starts, rows), ("prefix_lens", prefix_lens, b)):
+        if t is not None and (t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 [{n}]")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out must match q")
+    _one_device(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, query_start=query_start,
+                context_lens=context_lens, out=out, slopes=slopes, starts=starts, prefix_lens=prefix_lens)
+    with torch.cuda.device(q.device):
+        need = prefill_scored_workspace_bytes(rows, b, hq, hkv, d, bs, max_query_len, max_context_len, window,
+                                              prefix_lens is not None, kv_splits)
+    workspace = _own_workspace(q.device, need, workspace)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, stride, block_tables.data_ptr(),
+            int(block_tables.shape[1]), query_start.data_ptr(), context_lens.data_ptr(), rows, int(max_query_len),
+            int(max_context_len), b, hq, hkv, d, bs, float(scale), float(softcap), ptr(slopes), int(window),
+            ptr(starts), ptr(prefix_lens), out.data_ptr(), ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), int(kv_splits), _dtype_code(q))
+    return PreparedCall("pkv_paged_attention_prefill_scored", args, q.device,
+                        (q, k_cache, v_cache, block_tables, query_start, context_lens, out, slopes, starts,
+                         prefix_lens, workspace), out)
+
+
 # ---------------------------------------------------------------------------
 # Eviction by accumulated attention weight
 # ---------------------------------------------------------------------------

@@ -98,6 +98,48 @@ def test_scored_decode_binding_refusals():
             call(*a)
 
 
+def test_scored_prefill_refusals(lib):
+    def call(**kw):
+        a = dict(q=16, k=16, v=16, nb=64, stride=2 * 4 * 16 * 128, bt=16, mb=8, qs=16, cl=16, rows=10, maxq=10, maxl=100, b=2,
+                 hq=4, hkv=4, d=128, bs=16, scale=0.1, cap=0.0, slopes=None, window=0, starts=None, prefix=None, out=16, wk=None,
+                 wkb=0, splits=1, dt=0)
+        a.update(kw)
+        names = ("q", "k", "v", "nb", "stride", "bt", "mb", "qs", "cl", "rows", "maxq", "maxl", "b", "hq", "hkv", "d", "bs",
+                 "scale", "cap", "slopes", "window", "starts", "prefix", "out", "wk", "wkb", "splits", "dt")
+        return lib.pkv_paged_attention_prefill_scored(*[a[n] for n in names], None)
+
+    assert call(b=0) == 0 and call(rows=0) == 0
+    for kw in (dict(d=64), dict(bs=64), dict(dt=2)):
+        assert call(**kw) == UNSUPPORTED, kw
+    for kw in (dict(cap=-1.0), dict(cap=1e-9), dict(cap=float("nan")), dict(window=-1), dict(slopes=2), dict(starts=1),
+               dict(prefix=3), dict(hq=6), dict(maxl=129), dict(maxq=101), dict(q=None), dict(out=8), dict(qs=None),
+               dict(scale=float("nan")), dict(splits=-1), dict(mb=64, maxl=1000, splits=2)):  # the last: no workspace
+        assert call(**kw) == INVALID, kw
+    size = lib.pkv_prefill_scored_workspace_bytes
+    assert size(10, 2, 4, 4, 128, 16, 10, 1000, 0, 0, 2) == 10 * 4 * 2 * 130 * 4
+    assert size(10, 2, 4, 4, 128, 16, 10, 1000, 0, 0, 1) == 0
+    assert size(10, 2, 4, 4, 128, 16, 10, 1000, 100, 0, 8) == 10 * 4 * 2 * 130 * 4   # 100 + 127 + 15 tokens: two tiles
+    assert size(10, 2, 4, 4, 128, 16, 10, 1000, 100, 1, 8) == 10 * 4 * 8 * 130 * 4
+    assert size(10, 2, 4, 4, 128, 16, 10, 1000, -1, 0, 1) == 2 ** 64 - 1
+
+
+def test_scored_prefill_binding_refusals():
+    kv = torch.zeros((8, 2, 2, 16, 128), dtype=torch.float16)
+    k, v = pkv.split_pool(kv)
+    q, bt = torch.zeros((6, 4, 128), dtype=torch.float16), torch.zeros((2, 4), dtype=torch.int32)
+    qs, n = torch.tensor([0, 3, 6], dtype=torch.int32), torch.tensor([3, 3], dtype=torch.int32)
+    call = lambda *a, **kw: pkv.paged_attention_prefill_scored(*a, max_query_len=3, max_context_len=64, **kw)
+    with pytest.raises(ValueError, match="CUDA"):
+        call(q, k, v, bt, qs, n)
+    for kw in (dict(softcap=-2.0), dict(window=-1), dict(slopes=torch.zeros(3)), dict(starts=n), dict(prefix_lens=qs),
+               dict(starts=torch.zeros(6)), dict(out=q.float())):
+        with pytest.raises(ValueError):
+            call(q, k, v, bt, qs, n, **kw)
+    for a in ((q.bfloat16(), k, v, bt, qs, n), (q, k, v, bt, n, n), (q, k, v, bt[:1], qs, n), (q, k, v, bt, qs, n.long())):
+        with pytest.raises(ValueError):
+            call(*a)
+
+
 def test_evict_refusals(lib):
     def select(**kw):
         a = dict(w=16, ws=64, cl=16, maxl=64, b=2, hkv=2, budget=8, sinks=1, recent=2, wo=None, kept=16, kl=16)
