@@ -244,16 +244,17 @@ def _handle(s, make):
 
 def _own_rope(s):
     import paged_kv_cache_155_gb300 as pkv
-    k_cache, v_cache = s["kv"][:, 0], s["kv"][:, 1]
-    kw = dict(axis_of_pair=s["axis"], interleaved=s["case"]["interleaved"])
-    if s["case"]["int8"]:
-        call = _handle(s, lambda: pkv.prepare_rope_reshape_and_cache_int8(
-            s["q"], s["k"], s["v"], s["positions"], s["inv_freq"], s["slots"], k_cache, v_cache, s["k_scale"],
-            s["v_scale"], s["q_out"], **kw))
-        return dict(q=call(), kv=_dequantised(s))
-    call = _handle(s, lambda: pkv.prepare_rope_reshape_and_cache(
-        s["q"], s["k"], s["v"], s["positions"], s["inv_freq"], s["slots"], k_cache, v_cache, s["q_out"], **kw))
-    return dict(q=call(), kv=s["kv"])
+    c = s["case"]
+
+    def make():
+        args = (s["q"], s["k"], s["v"], s["positions"], s["inv_freq"], s["slots"], s["kv"][:, 0], s["kv"][:, 1])
+        kw = dict(axis_of_pair=s["axis"], interleaved=c["interleaved"])
+        if c["int8"]:
+            return pkv.prepare_rope_reshape_and_cache_int8(*args, s["k_scale"], s["v_scale"], s["q_out"], **kw)
+        return pkv.prepare_rope_reshape_and_cache(*args, s["q_out"], **kw)
+
+    q = _handle(s, make)()
+    return dict(q=q, kv=_dequantised(s) if c["int8"] else s["kv"])
 
 
 def _own_decode(s):
