@@ -22,8 +22,28 @@
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;      // rows of a thread whose loads are in flight together
-constexpr int kMaxPairs = 64;   // head_dim / 2
+// Steps of a thread whose loads are in flight together, and CTAs per SM (48 registers,
+// 64 with the quantiser): the bytes in flight.  Measured on 8192 tokens of 64 + 2 x 8
+// heads: 59 us; four steps and three CTAs 68, one step and six CTAs 70.
+constexpr int kDepth = 2;
+constexpr int kBlocks16 = 5, kBlocksInt8 = 4;
+// Tokens per CTA from kManyTokens tokens on: two share the angles' latency (59.0 us
+// against 59.8 with one, 61.9 with four); below, one, so that the SMs share the work.
+constexpr int kTok = 2, kManyTokens = 2048;
+
+// quantize_int8 (pkv_device.cuh) without a division in most cases: the quotient by an
+// approximate reciprocal is off by less than 2^-20 of itself, so its rounding to an
+// integer is quantize_int8's unless it lies within 1e-3 of a tie (|quotient| <= 127:
+// an error below 1.3e-4); those, and scales whose reciprocal could overflow or
+// vanish, take the division.  Adding 1.5 * 2^23 rounds to nearest even and leaves the
+// code in the low byte.
+__device__ __forceinline__ uint32_t quantize_int8_byte(float x, float s) {
+    const float q = fminf(fmaxf(x * pkv::fast_rcp(s), -127.f), 127.f);
+    const float t = q + 12582912.f;
+    const bool in_range = __float_as_uint(s) - 0x0d800000u < 0x64000000u;  // 2^-100 <= s < 2^100
+    if (in_range && fabsf(q - (t - 12582912.f)) < 0.499f) return __float_as_uint(t) & 0xffu;
+    return static_cast<uint32_t>(pkv::quantize_int8(x, s)) & 0xffu;
+}
 
 struct RopeParams {
     const char *q, *k_new, *v_new;  // rows of [heads][head_dim]
@@ -49,27 +69,24 @@ __device__ __forceinline__ int turn_fraction(double inv_freq, int64_t position) 
     return static_cast<int>(static_cast<uint32_t>((static_cast<uint64_t>(position) * f) >> 32));
 }
 
-// One CTA per token.  LANES = D / 16 threads share a row of one head, each taking
-// two 16-byte vectors: pairs 8 c .. 8 c + 7 of the rotation (the vectors at channels
-// 8 c and pairs + 8 c for split halves, 16 c and 16 c + 8 for adjacent channels) or
-// two vectors behind the rotated channels, so that a thread's angles are the same
-// in every row and a rotation never crosses threads.  The rows are the q heads,
-// then K, then V; the loads of a thread's first rows are issued before the angles
-// are computed.
-template <typename T, bool QUANT, int D, bool ADJACENT>
-__global__ void __launch_bounds__(kThreads) rope_reshape_and_cache_kernel(const RopeParams p) {
+// One CTA per TOK consecutive tokens.  LANES = D / 16 threads share a row of one
+// head, each taking two 16-byte vectors: pairs 8 c .. 8 c + 7 of the rotation (the
+// vectors at channels 8 c and pairs + 8 c for split halves, 16 c and 16 c + 8 for
+// adjacent channels) or two vectors behind the rotated channels, so that a thread's
+// angles are the same in every row of a token and a rotation never crosses threads.
+// The rows are the q heads, then K, then V; a thread's first rows are loaded before
+// the angles are computed, one pair of one token per thread.
+template <typename T, bool QUANT, int D, bool ADJACENT, int TOK>
+__global__ void __launch_bounds__(kThreads, QUANT ? kBlocksInt8 : kBlocks16) rope_reshape_and_cache_kernel(const RopeParams p) {
     constexpr int LANES = D / 16;
     constexpr int ROWS = kThreads / LANES;  // rows in flight per step
-    __shared__ float2 turn[kMaxPairs];      // (cos, sin)
-    const int64_t n = blockIdx.x;
+    static_assert(TOK * (D / 2) <= kThreads, "one thread per angle");
+    __shared__ float2 turn[TOK][D / 2];     // (cos, sin)
+    __shared__ int64_t slots[TOK];          // -1: skip
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * TOK;
     const int c = threadIdx.x % LANES;
     const int row0 = threadIdx.x / LANES;
     const int rows_q = p.num_q_heads, rows_k = rows_q + p.num_kv_heads, rows = rows_k + p.num_kv_heads;
-
-    const int64_t slot = p.slot_mapping[n];
-    const bool store_kv = slot >= 0 && slot < p.num_slots;
-    if (slot >= p.num_slots && threadIdx.x == 0) pkv::raise_flag(p.status, PKV_DEVERR_SLOT);
-    const int last = store_kv ? rows : rows_q;  // a skipped token still gets its rotated q
 
     // this thread's two vectors of a row, in 16-byte units
     const int groups = p.pairs / 8;  // rotation groups of 8 pairs
@@ -83,119 +100,148 @@ __global__ void __launch_bounds__(kThreads) rope_reshape_and_cache_kernel(const 
         v1 = rotates ? c + groups : 2 * c + 1;
     }
 
-    auto source = [&](int r) -> const uint4 * {
-        if (r < rows_q) return reinterpret_cast<const uint4 *>(p.q + n * p.q_stride) + r * (D / 8);
-        if (r < rows_k) return reinterpret_cast<const uint4 *>(p.k_new + n * p.k_stride) + (r - rows_q) * (D / 8);
-        return reinterpret_cast<const uint4 *>(p.v_new + n * p.v_stride) + (r - rows_k) * (D / 8);
+    // The CTA's steps: step j is rows (j % steps) ROWS + row0 of token n0 + j / steps.
+    // A thread keeps kDepth steps' loads in flight: those of step j + kDepth are issued
+    // as step j's vectors have been used.
+    const int steps = (rows + ROWS - 1) / ROWS;
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(TOK), p.num_tokens - n0));
+    const char *q_row = p.q + n0 * p.q_stride, *k_row = p.k_new + n0 * p.k_stride, *v_row = p.v_new + n0 * p.v_stride;
+    uint4 x0[kDepth], x1[kDepth];
+    int lk = 0, lr = row0;  // token and row of the next load
+    auto load = [&](int u) {
+        if (lk < tokens && lr < rows) {  // (a skipped token's K and V rows are read for nothing)
+            const char *src = lr < rows_q   ? q_row + lk * p.q_stride + lr * (2 * D)
+                              : lr < rows_k ? k_row + lk * p.k_stride + (lr - rows_q) * (2 * D)
+                                            : v_row + lk * p.v_stride + (lr - rows_k) * (2 * D);
+            x0[u] = reinterpret_cast<const uint4 *>(src)[v0];
+            x1[u] = reinterpret_cast<const uint4 *>(src)[v1];
+        }
+        lr += ROWS;
+        if (lr >= steps * ROWS) {
+            lr = row0;
+            ++lk;
+        }
     };
-    uint4 x0[kUnroll], x1[kUnroll];
-    auto load = [&](int base) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int r = base + u * ROWS;
-            if (r < last) {
-                const uint4 *src = source(r);
-                x0[u] = src[v0];
-                x1[u] = src[v1];
-            }
-        }
-    };
-    load(row0);
+    for (int u = 0; u < kDepth; ++u) load(u);
 
-    if (static_cast<int>(threadIdx.x) < p.pairs) {
-        int axis = p.axis_of_pair ? p.axis_of_pair[threadIdx.x] : 0;
-        float2 cs = make_float2(1.f, 0.f);
-        if (axis < 0 || axis >= p.num_axes) {
-            if (n == 0) pkv::raise_flag(p.status, PKV_DEVERR_ROPE_AXIS);  // left unrotated
-        } else {
-            const int fr = turn_fraction(p.inv_freq[threadIdx.x], p.positions[axis * p.num_tokens + n]);
-            sincospif(static_cast<float>(fr) * 4.656612873077393e-10f, &cs.y, &cs.x);  // 2 fr / 2^32
+    if (static_cast<int>(threadIdx.x) < tokens) {
+        int64_t slot = p.slot_mapping[n0 + threadIdx.x];
+        if (slot >= p.num_slots) {
+            pkv::raise_flag(p.status, PKV_DEVERR_SLOT);
+            slot = -1;
         }
-        turn[threadIdx.x] = cs;
+        slots[threadIdx.x] = slot;
+    }
+    if (static_cast<int>(threadIdx.x) < TOK * (D / 2)) {
+        const int i = threadIdx.x % (D / 2), k = threadIdx.x / (D / 2);
+        if (i < p.pairs && k < tokens) {
+            const int axis = p.axis_of_pair ? p.axis_of_pair[i] : 0;
+            float2 cs = make_float2(1.f, 0.f);
+            if (axis < 0 || axis >= p.num_axes) {
+                if (n0 + k == 0) pkv::raise_flag(p.status, PKV_DEVERR_ROPE_AXIS);  // left unrotated
+            } else {
+                const int fr = turn_fraction(p.inv_freq[i], p.positions[axis * p.num_tokens + n0 + k]);
+                sincospif(static_cast<float>(fr) * 4.656612873077393e-10f, &cs.y, &cs.x);  // 2 fr / 2^32
+            }
+            turn[k][(i % 8) * LANES + i / 8] = cs;  // a row's lanes read consecutive words
+        }
     }
     __syncthreads();
-    float cosv[8], sinv[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float2 cs = rotates ? turn[8 * c + e] : make_float2(1.f, 0.f);
-        cosv[e] = cs.x;
-        sinv[e] = cs.y;
-    }
 
-    const int64_t blk = store_kv ? slot / p.block_size : 0;
-    const int off = store_kv ? static_cast<int>(slot - blk * p.block_size) : 0;
-    for (int base = row0; base < last; base += kUnroll * ROWS) {
-        if (base != row0) load(base);
+    auto process = [&](uint4 y0, uint4 y1, int k, int r) {
+        const int64_t slot = slots[k];
+        if (r >= rows || (slot < 0 && r >= rows_q)) return;  // a skipped token still gets its rotated q
+        float f0[8], f1[8];
+        const bool turned = rotates && r < rows_k;
+        if (turned || (QUANT && r >= rows_q)) {
+            pkv::Elem<T>::to_f32x8(y0, f0);
+            pkv::Elem<T>::to_f32x8(y1, f1);
+        }
+        if (turned) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int r = base + u * ROWS;
-            if (r >= last) break;
-            uint4 y0 = x0[u], y1 = x1[u];
-            float f0[8], f1[8];
-            const bool turned = rotates && r < rows_k;
-            if (turned || (QUANT && r >= rows_q)) {
-                pkv::Elem<T>::to_f32x8(y0, f0);
-                pkv::Elem<T>::to_f32x8(y1, f1);
+            for (int e = 0; e < 8; ++e) {
+                const float2 cs = turn[k][e * LANES + c];
+                // split halves: pair e is (f0[e], f1[e]); adjacent: channels 2 e, 2 e + 1 of the 16
+                float &a = ADJACENT ? (e < 4 ? f0[(2 * e) & 7] : f1[(2 * e) & 7]) : f0[e];
+                float &b = ADJACENT ? (e < 4 ? f0[(2 * e + 1) & 7] : f1[(2 * e + 1) & 7]) : f1[e];
+                const float a0 = a, b0 = b;
+                a = a0 * cs.x - b0 * cs.y;
+                b = b0 * cs.x + a0 * cs.y;
             }
-            if (turned) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    // split halves: pair e is (f0[e], f1[e]); adjacent: channels 2 e, 2 e + 1 of the 16
-                    float &a = ADJACENT ? (e < 4 ? f0[(2 * e) & 7] : f1[(2 * e) & 7]) : f0[e];
-                    float &b = ADJACENT ? (e < 4 ? f0[(2 * e + 1) & 7] : f1[(2 * e + 1) & 7]) : f1[e];
-                    const float a0 = a, b0 = b;
-                    a = a0 * cosv[e] - b0 * sinv[e];
-                    b = b0 * cosv[e] + a0 * sinv[e];
-                }
-                if (!QUANT || r < rows_q) {
-                    y0 = make_uint4(pkv::Elem<T>::pack2(f0[0], f0[1]), pkv::Elem<T>::pack2(f0[2], f0[3]),
-                                    pkv::Elem<T>::pack2(f0[4], f0[5]), pkv::Elem<T>::pack2(f0[6], f0[7]));
-                    y1 = make_uint4(pkv::Elem<T>::pack2(f1[0], f1[1]), pkv::Elem<T>::pack2(f1[2], f1[3]),
-                                    pkv::Elem<T>::pack2(f1[4], f1[5]), pkv::Elem<T>::pack2(f1[6], f1[7]));
-                }
+            if (!QUANT || r < rows_q) {
+                y0 = make_uint4(pkv::Elem<T>::pack2(f0[0], f0[1]), pkv::Elem<T>::pack2(f0[2], f0[3]),
+                                pkv::Elem<T>::pack2(f0[4], f0[5]), pkv::Elem<T>::pack2(f0[6], f0[7]));
+                y1 = make_uint4(pkv::Elem<T>::pack2(f1[0], f1[1]), pkv::Elem<T>::pack2(f1[2], f1[3]),
+                                pkv::Elem<T>::pack2(f1[4], f1[5]), pkv::Elem<T>::pack2(f1[6], f1[7]));
             }
-            if (r < rows_q) {
-                uint4 *dst = reinterpret_cast<uint4 *>(p.q_out + n * p.q_out_stride) + r * (D / 8);
-                dst[v0] = y0;
-                dst[v1] = y1;
-                continue;
+        }
+        if (r < rows_q) {
+            uint4 *dst = reinterpret_cast<uint4 *>(p.q_out + (n0 + k) * p.q_out_stride + r * (2 * D));
+            dst[v0] = y0;
+            dst[v1] = y1;
+            return;
+        }
+        const bool is_v = r >= rows_k;
+        const int h = is_v ? r - rows_k : r - rows_q;
+        const int64_t blk = slot / p.block_size;
+        const int off = static_cast<int>(slot - blk * p.block_size);
+        char *row = (is_v ? p.v_cache : p.k_cache) + blk * p.block_stride +
+                    (static_cast<int64_t>(h) * p.block_size + off) * (D * (QUANT ? 1 : 2));
+        if constexpr (QUANT) {
+            const float *scale = (is_v ? p.v_scale : p.k_scale) + h * D;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int v = half ? v1 : v0;
+                const float *f = half ? f1 : f0;
+                const float4 sa = reinterpret_cast<const float4 *>(scale)[2 * v];
+                const float4 sb = reinterpret_cast<const float4 *>(scale)[2 * v + 1];
+                const float s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+                uint32_t w[2] = {0u, 0u};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    w[e / 4] |= quantize_int8_byte(f[e], s[e]) << (8 * (e % 4));
+                reinterpret_cast<uint2 *>(row)[v] = make_uint2(w[0], w[1]);
             }
-            const bool is_v = r >= rows_k;
-            const int h = is_v ? r - rows_k : r - rows_q;
-            char *row = (is_v ? p.v_cache : p.k_cache) + blk * p.block_stride +
-                        (static_cast<int64_t>(h) * p.block_size + off) * (D * (QUANT ? 1 : 2));
-            if constexpr (QUANT) {
-                const float *scale = (is_v ? p.v_scale : p.k_scale) + h * D;
+        } else {
+            reinterpret_cast<uint4 *>(row)[v0] = y0;
+            reinterpret_cast<uint4 *>(row)[v1] = y1;
+        }
+    };
+    int k = 0, r = row0;
+    while (k < tokens) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int v = half ? v1 : v0;
-                    const float *f = half ? f1 : f0;
-                    const float4 sa = reinterpret_cast<const float4 *>(scale)[2 * v];
-                    const float4 sb = reinterpret_cast<const float4 *>(scale)[2 * v + 1];
-                    const float s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
-                    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        w[e / 4] |= (static_cast<uint32_t>(pkv::quantize_int8(f[e], s[e])) & 0xffu) << (8 * (e % 4));
-                    reinterpret_cast<uint2 *>(row)[v] = make_uint2(w[0], w[1]);
-                }
-            } else {
-                reinterpret_cast<uint4 *>(row)[v0] = y0;
-                reinterpret_cast<uint4 *>(row)[v1] = y1;
+        for (int u = 0; u < kDepth; ++u) {
+            if (k < tokens) process(x0[u], x1[u], k, r);
+            load(u);
+            r += ROWS;
+            if (r >= steps * ROWS) {
+                r = row0;
+                ++k;
             }
         }
     }
 }
 
+template <typename T, bool QUANT, int D, bool ADJACENT>
+void launch_rope_form(const RopeParams &p, cudaStream_t s) {
+    if (p.num_tokens >= kManyTokens) {
+        const unsigned grid = static_cast<unsigned>((p.num_tokens + kTok - 1) / kTok);
+        rope_reshape_and_cache_kernel<T, QUANT, D, ADJACENT, kTok><<<grid, kThreads, 0, s>>>(p);
+    } else {
+        rope_reshape_and_cache_kernel<T, QUANT, D, ADJACENT, 1>
+            <<<static_cast<unsigned>(p.num_tokens), kThreads, 0, s>>>(p);
+    }
+}
+
 template <typename T, bool QUANT>
 void launch_rope(const RopeParams &p, int head_dim, bool adjacent, cudaStream_t s) {
-    const unsigned grid = static_cast<unsigned>(p.num_tokens);
     if (head_dim == 128) {
-        if (adjacent) rope_reshape_and_cache_kernel<T, QUANT, 128, true><<<grid, kThreads, 0, s>>>(p);
-        else rope_reshape_and_cache_kernel<T, QUANT, 128, false><<<grid, kThreads, 0, s>>>(p);
+        if (adjacent) launch_rope_form<T, QUANT, 128, true>(p, s);
+        else launch_rope_form<T, QUANT, 128, false>(p, s);
     } else {
-        if (adjacent) rope_reshape_and_cache_kernel<T, QUANT, 64, true><<<grid, kThreads, 0, s>>>(p);
-        else rope_reshape_and_cache_kernel<T, QUANT, 64, false><<<grid, kThreads, 0, s>>>(p);
+        if (adjacent) launch_rope_form<T, QUANT, 64, true>(p, s);
+        else launch_rope_form<T, QUANT, 64, false>(p, s);
     }
 }
 

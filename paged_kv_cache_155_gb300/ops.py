@@ -39,6 +39,11 @@ def _dtype_code(t: torch.Tensor) -> int:
 _raw_stream_getter = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+# the current device's index (without torch's initialisation check: a prepared call's
+# tensors are on a device already)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _raw_stream(device_index: int) -> int:
     """cudaStream_t of the device's current stream, as an integer."""
     if _raw_stream_getter is not None:
@@ -75,7 +80,7 @@ class PreparedCall:
         self._result = result
 
     def __call__(self):
-        if torch.cuda.current_device() != self._dev:  # the library launches on the current device
+        if _current_device() != self._dev:  # the library launches on the current device
             with torch.cuda.device(self._dev):
                 st = self._fn(*self._args, _raw_stream(self._dev))
         else:

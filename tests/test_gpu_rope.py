@@ -142,6 +142,41 @@ def test_rope_int8_codes(tokens, hq, hkv, d, bs, rot, dtype, interleaved):
     assert torch.equal(got.permute(0, 3, 1, 2, 4)[mask], before.permute(0, 3, 1, 2, 4)[mask])
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["f16", "bf16"])
+def test_int8_v_codes_are_the_plain_writes(dtype):
+    """The V rows, and K rows at position 0, get reshape_and_cache_int8's codes exactly: ties, clamped values, infinities, NaN
+    and extreme scales among them."""
+    dev = device()
+    t, hkv, d, bs = 64, 4, 64, 16
+    g = torch.Generator().manual_seed(2)
+    scale = (torch.rand((hkv, d), generator=g) + 0.5) / 20
+    scale[0] = 0.125                                                 # exact quotients: every multiple of 1/16 a tie
+    scale[1, ::3], scale[1, 1::3] = 1e-38, 3e38
+    x = torch.randn((t, hkv, d), generator=g)
+    x[:, 0] = torch.randint(-300, 300, (t, d), generator=g) / 16
+    x[::5, 2], x[1::5, 2], x[2::7, 3] = float("inf"), -float("inf"), float("nan")
+    x[3::7, 1] = 0.0
+    if dtype == torch.bfloat16:
+        x[4::7, 1] = 3e38
+    x = x.to(dtype).to(dev)
+    slots = torch.randperm(5 * bs, generator=g)[:t].to(dev)
+    pools = [torch.zeros((5, 2, hkv, bs, d), dtype=torch.int8, device=dev) for _ in range(2)]
+    sc = scale.to(dev)
+    pkv.reshape_and_cache_int8(x, x, slots, *pkv.split_pool(pools[0]), sc, sc)
+    fin = torch.nan_to_num(x.float(), nan=0.0, posinf=1.0, neginf=-1.0).to(dtype)      # a rotation mixes infinities into NaN
+    pkv.rope_reshape_and_cache_int8(x[:, :1].contiguous(), x, x, torch.zeros(t, dtype=torch.int64, device=dev),
+                                    torch.ones(16, dtype=torch.float64, device=dev), slots, *pkv.split_pool(pools[1]), sc, sc)
+    torch.cuda.synchronize()
+    check_no_device_flags(dev)
+    assert torch.equal(pools[0][:, 1], pools[1][:, 1])
+    kpools = [torch.zeros((5, 2, hkv, bs, d), dtype=torch.int8, device=dev) for _ in range(2)]
+    pkv.reshape_and_cache_int8(fin, fin, slots, *pkv.split_pool(kpools[0]), sc, sc)
+    pkv.rope_reshape_and_cache_int8(fin[:, :1].contiguous(), fin, fin, torch.zeros(t, dtype=torch.int64, device=dev),
+                                    torch.ones(16, dtype=torch.float64, device=dev), slots, *pkv.split_pool(kpools[1]), sc, sc)
+    torch.cuda.synchronize()
+    assert torch.equal(kpools[0], kpools[1])
+
+
 def test_bad_slots_and_axes_are_flagged_and_skipped():
     dev = device()
     c = _case(dev, 4, 4, 2, 64, 16, torch.float16, 2, 64, seed=8, packed=False)
