@@ -4,7 +4,6 @@
 #include <cmath>
 
 #include "decode_launch.cuh"
-#include "decode_weights.cuh"
 
 namespace pkv {
 
@@ -87,6 +86,7 @@ namespace {
 constexpr int kTargetWaves = 8;        // CTA waves the automatic split aims for
 constexpr int kMinAutoPartition = 256; // tokens: below this the per-CTA set-up dominates
 constexpr int kMergeShare = 32;        // a partition's K/V bytes >= this x its partial bytes
+constexpr double kScoredFillSlack = 0.03;
 constexpr double kFillSlack = 0.15;    // wave fill given up for fewer, longer partitions (two-per-SM forms)
 
 // Decode CTAs resident per SM for each kernel form (their stage budgets and
@@ -120,7 +120,8 @@ size_t workspace_for(int num_seqs, int num_q_heads, int head_dim, int num_partit
 pkv_status plan_decode(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                        int block_size, int max_context_len, int partition_size, int sm_count,
                        bool int8_kv, int *out_partition_size, int *out_num_partitions,
-                       int *out_heads_per_block, int *out_needs_merge, int resident = 0) {
+                       int *out_heads_per_block, int *out_needs_merge, int resident = 0,
+                       bool scored = false) {
     if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
     if (block_size != 8 && block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_context_len < 0 ||
@@ -160,7 +161,13 @@ pkv_status plan_decode(int num_seqs, int num_q_heads, int num_kv_heads, int head
         // start-up costs its SM half its streams.  Take the fewest partitions in
         // [n / 2, n] whose CTAs fill whole waves within kFillSlack of the best count.
         const int64_t n = len > 0 ? (len + p - 1) / p : 1;
-        if (n > 1 && units * n < target && slots <= 2LL * sm_count) {
+        // The scored form's CTAs start later (a span depends on the length, the table on
+        // the span), so partial waves cost it more: every form of it takes the fewest
+        // partitions within kScoredFillSlack of the best.  Measured: 32 x 4096 tokens of 32
+        // heads in 2 instead of 3 partitions 317 us against 328; 2 x 32768 tokens of 64 / 8
+        // heads in 57 instead of 61 (exactly two waves) 55.6 against 62.0.
+        const double slack = scored ? kScoredFillSlack : kFillSlack;
+        if (n > 1 && (scored || (units * n < target && slots <= 2LL * sm_count))) {
             auto fill = [&](int64_t parts) {  // CTAs / (rounds x slots)
                 const int64_t ctas = units * parts;
                 return static_cast<double>(ctas) / static_cast<double>((ctas + slots - 1) / slots * slots);
@@ -173,7 +180,7 @@ pkv_status plan_decode(int num_seqs, int num_q_heads, int num_kv_heads, int head
                 if (part_for(k) <= max_partition) best = std::max(best, fill((len + part_for(k) - 1) / part_for(k)));
             for (int64_t k = (n + 1) / 2; k < n; ++k) {
                 const int64_t pk = part_for(k);
-                if (pk <= max_partition && fill((len + pk - 1) / pk) >= best - kFillSlack) {
+                if (pk <= max_partition && fill((len + pk - 1) / pk) >= best - slack) {
                     p = pk;
                     break;
                 }
@@ -296,13 +303,13 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache,
     // Validate the shape first (no CUDA call), then plan for the real SM count.
     pkv_status plan = plan_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                                   span, partition_size, 1, int8_kv, &part, &nparts, &gh,
-                                  &merge);
+                                  &merge, 0, scored != nullptr);
     if (plan != PKV_OK) return plan;
     if (partition_size == 0) {
         const int sm = pkv::current_sm_count();
         if (sm <= 0) return PKV_ERR_CUDA;
         plan = plan_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
-                           span, 0, sm, int8_kv, &part, &nparts, &gh, &merge);
+                           span, 0, sm, int8_kv, &part, &nparts, &gh, &merge, 0, scored != nullptr);
         if (plan != PKV_OK) return plan;
     }
     const size_t need = scored_workspace(num_seqs, num_q_heads, head_dim, nparts, span, want_weights);
@@ -356,6 +363,18 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache,
             p.score_stride = score_stride_of(span);
         }
     }
+    pkv::WeightParams w{};
+    if (want_weights) {
+        w.weights = scored->weights;
+        w.weights_out = scored->weights_out;
+        w.weights_stride = scored->weights_stride;
+        w.chunks = (max_context_len + pkv::kWeightTokens - 1) / pkv::kWeightTokens;
+        w.vectors = w.weights_stride % 4 == 0 && pkv::aligned16(w.weights) && pkv::aligned16(w.weights_out);
+        // one block per merge row at most, and per chunk of weights
+        if (static_cast<int64_t>(num_seqs) * num_q_heads +
+                static_cast<int64_t>(w.chunks) * num_kv_heads * num_seqs > 0x7fffffff)
+            return PKV_ERR_INVALID_ARG;
+    }
     const int merge_rows = merge ? num_seqs * num_q_heads : 0;
     p.trigger_dependents = merge_rows > 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -371,14 +390,7 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache,
     if (scored) {
         auto launch = int8_kv ? (dtype == PKV_F16 ? pkv::launch_scored_i8_f16 : pkv::launch_scored_i8_bf16)
                               : (dtype == PKV_F16 ? pkv::launch_scored_f16 : pkv::launch_scored_bf16);
-        const pkv_status st = launch(p, maps, head_dim, block_size, gh, grid, merge_rows, s);
-        if (st != PKV_OK || !want_weights || max_context_len == 0) return st;
-        const pkv::WeightParams w{scored->weights, scored->weights_out, scored->weights_stride};
-        const dim3 wgrid(static_cast<unsigned>((max_context_len + pkv::kWeightTokens - 1) / pkv::kWeightTokens),
-                         static_cast<unsigned>(num_kv_heads), static_cast<unsigned>(num_seqs));
-        pkv::decode_weights_kernel<<<wgrid, pkv::kWeightThreads, 0, s>>>(p, w);
-        pkv::count_launch();
-        return pkv::launch_status();
+        return launch(p, maps, head_dim, block_size, gh, grid, merge_rows, s, w);
     }
     if (int8_kv)
         return dtype == PKV_F16
@@ -462,7 +474,7 @@ PKV_API size_t pkv_decode_scored_workspace_bytes(int num_seqs, int num_q_heads, 
     const int span = scored_span(max_context_len, window, block_size);
     int part = 0, nparts = 0;
     if (plan_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, span, partition_size, sm,
-                    int8_cache != 0, &part, &nparts, nullptr, nullptr) != PKV_OK)
+                    int8_cache != 0, &part, &nparts, nullptr, nullptr, 0, true) != PKV_OK)
         return static_cast<size_t>(-1);
     return scored_workspace(num_seqs, num_q_heads, head_dim, nparts, span, want_weights != 0);
 }

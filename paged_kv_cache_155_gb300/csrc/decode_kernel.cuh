@@ -177,10 +177,10 @@ __device__ __forceinline__ float soft_cap(float y, float cap_in, float cap_out) 
 }
 
 // A score y = scale * log2(e) * (q . k) of the token at distance dist = t - query
-// position (<= 0), capped, then biased (slope2 = slope * log2(e)).
-__device__ __forceinline__ float score_modified(const DecodeParams &p, float y, float slope2, int dist) {
+// position (<= 0, exact in fp32), capped, then biased (slope2 = slope * log2(e)).
+__device__ __forceinline__ float score_modified(const DecodeParams &p, float y, float slope2, float dist) {
     if (p.cap_out > 0.f) y = soft_cap(y, p.cap_in, p.cap_out);
-    return fmaf(slope2, static_cast<float>(dist), y);
+    return fmaf(slope2, dist, y);
 }
 
 // Values per lane vector of the CUDA-core kernel (see DecodeGeom).
@@ -599,6 +599,8 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
         }
     }
     const int qpos = len - 1;  // the query's position
+    // a lane's rows follow its chunk's by this much (plus constants)
+    const float lane_dist = static_cast<float>(kMma ? (kQuant ? mg : 2 * mt) : grp);
     auto score_row = [&](int h) {  // scores of head hq0 + h from the partition's first token on
         return p.ws_s + (static_cast<int64_t>(seq) * p.num_q_heads + hq0 + h) * p.score_stride + (tok0 - span.begin);
     };
@@ -630,6 +632,10 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
         }
         const int c = warp + i * NW;
         const int valid = min(TILE, ntok - c * TILE);  // >= 1
+        // scored form: the chunk's distance from the query (converted once; the lanes add
+        // small constants), and whether any of its rows is masked
+        const float dist0 = kScored ? static_cast<float>(tok0 + c * TILE - qpos) : 0.f;
+        const bool masked = kScored && (valid < TILE || tok0 + c * TILE < span.lo);
         if (tbl[(c * TILE) / BS] >= 0) {
             const KT *ks = reinterpret_cast<const KT *>(my_stages + s * G::kStageBytes);
             const KT *vs = ks + TILE * D;
@@ -678,9 +684,11 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                     if constexpr (kScored) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int t = tb + mg + 8 * (e >> 1), tpos = tok0 + c * TILE + t;
-                            sc[e] = t < valid && tpos >= span.lo ? score_modified(p, sc[e], slope2[e & 1], tpos - qpos)
-                                                                 : -INFINITY;
+                            const int t = tb + mg + 8 * (e >> 1);
+                            sc[e] = score_modified(p, sc[e], slope2[e & 1],
+                                                   (dist0 + static_cast<float>(tb + 8 * (e >> 1))) + lane_dist);
+                            if (STEP == 8 && e >= 2) sc[e] = -INFINITY;  // a step of 8 tokens has no rows mg + 8
+                            else if (masked && (t >= valid || tok0 + c * TILE + t < span.lo)) sc[e] = -INFINITY;
                         }
                     }
                     // per head, the maximum over the step's tokens (the eight lanes with this
@@ -826,11 +834,15 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                     if constexpr (kScored) {
 #pragma unroll
                         for (int e = 0; e < STEP / 4; ++e) {
-                            const int t = tb + 8 * (e >> 1) + 2 * mt + (e & 1), tpos = tok0 + c * TILE + t;
-                            const bool seen = t < valid && tpos >= span.lo;
-                            sc[e] = seen ? score_modified(p, sc[e], slope2[0], tpos - qpos) : -INFINITY;
-                            if constexpr (kRows16)
-                                sc2[e] = seen ? score_modified(p, sc2[e], slope2[1], tpos - qpos) : -INFINITY;
+                            const int t = tb + 8 * (e >> 1) + 2 * mt + (e & 1);
+                            const float dist = (dist0 + static_cast<float>(tb + 8 * (e >> 1) + (e & 1))) + lane_dist;
+                            const bool hidden = masked && (t >= valid || tok0 + c * TILE + t < span.lo);
+                            sc[e] = score_modified(p, sc[e], slope2[0], dist);
+                            if (hidden) sc[e] = -INFINITY;
+                            if constexpr (kRows16) {
+                                sc2[e] = score_modified(p, sc2[e], slope2[1], dist);
+                                if (hidden) sc2[e] = -INFINITY;
+                            }
                         }
                         if (p.ws_s) {
 #pragma unroll
@@ -1018,11 +1030,14 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                     if constexpr (kScored) {
 #pragma unroll
                         for (int it = 0; it < IT_STEP; ++it) {
-                            const int t = (it0 + it) * TPG + grp, tpos = tok0 + c * TILE + t;
-                            const bool seen = t < valid && tpos >= span.lo;
+                            const int t = (it0 + it) * TPG + grp;
+                            const float dist = (dist0 + static_cast<float>((it0 + it) * TPG)) + lane_dist;
+                            const bool hidden = masked && (t >= valid || tok0 + c * TILE + t < span.lo);
 #pragma unroll
-                            for (int g = 0; g < GH; ++g)
-                                sc[it][g] = seen ? score_modified(p, sc[it][g], slope2[g], tpos - qpos) : -INFINITY;
+                            for (int g = 0; g < GH; ++g) {
+                                sc[it][g] = score_modified(p, sc[it][g], slope2[g], dist);
+                                if (hidden) sc[it][g] = -INFINITY;
+                            }
                         }
                         if (!kQuant && p.ws_s) {
                             // every lane of a token row holds its score: lane `sub` writes the row of
@@ -1066,7 +1081,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
 #pragma unroll
                     for (int it = 0; it < IT_STEP; ++it) {
                         const int t = (it0 + it) * TPG + grp;
-                        if (t < valid && (!kScored || tok0 + c * TILE + t >= span.lo)) {
+                        if (t < valid && (!masked || tok0 + c * TILE + t >= span.lo)) {
                             if constexpr (kQuant) {
                                 uint32_t vh[VL / 2];
                                 load_codes_f16<VL>(vs + t * D + sub * VL, vh);
@@ -1090,6 +1105,12 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                         }
                     }
                 }
+            }
+        }
+        if constexpr (kScored && !kQuant) {
+            // a flagged table entry's tokens get no weight
+            if (p.ws_s && tbl[(c * TILE) / BS] < 0) {
+                for (int k = lane; k < GH * TILE; k += 32) score_row(k / TILE)[c * TILE + k % TILE] = -INFINITY;
             }
         }
         __syncwarp();
@@ -1259,17 +1280,15 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
 constexpr int kMergeUnroll = 8;
 constexpr int kMergeWideFrom = 32;  // partitions per row from which four warps share a row
 
-template <typename T, int D, int WPR, bool kScored = false>
-__global__ void __launch_bounds__(128) paged_decode_merge_kernel(const DecodeParams p,
-                                                                 int num_rows) {
+template <typename T, int D, int WPR, bool kScored>
+__device__ __forceinline__ void merge_rows(const DecodeParams &p, int num_rows, int block) {
     static_assert(WPR == 1 || WPR == 4, "one or four warps per row");
-    pdl_wait();
     constexpr int PER_LANE = D / 32;
     using Part = typename std::conditional<PER_LANE == 4, float4, float2>::type;
     static_assert(PER_LANE == 4 || PER_LANE == 2, "head_dim 128 or 64");
     __shared__ float comb[WPR == 4 ? 4 : 1][D + 2];  // four warps' (o, m, l) of one row
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = blockIdx.x * (4 / WPR) + warp / WPR;  // uniform over a block when WPR == 4
+    const int row = block * (4 / WPR) + warp / WPR;  // uniform over a block when WPR == 4
     const int share = warp % WPR;                          // this warp takes partitions share + WPR i
     if (row >= num_rows) return;
     const int seq = row / p.num_q_heads;
@@ -1350,6 +1369,12 @@ __global__ void __launch_bounds__(128) paged_decode_merge_kernel(const DecodePar
     T *dst = static_cast<T *>(p.out) + static_cast<int64_t>(row) * D + lane * PER_LANE;
 #pragma unroll
     for (int e = 0; e < PER_LANE; ++e) dst[e] = Elem<T>::from_f32(lsum > 0.f ? o[e] / lsum : 0.f);
+}
+
+template <typename T, int D, int WPR>
+__global__ void __launch_bounds__(128) paged_decode_merge_kernel(const DecodeParams p, int num_rows) {
+    pdl_wait();
+    merge_rows<T, D, WPR, false>(p, num_rows, blockIdx.x);
 }
 
 }  // namespace pkv

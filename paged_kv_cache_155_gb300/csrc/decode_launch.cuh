@@ -8,6 +8,7 @@
 #include <utility>
 
 #include "decode_kernel.cuh"
+#include "decode_weights.cuh"
 #include "prefix_tc_kernel.cuh"
 #include "pkv_host.h"
 
@@ -79,7 +80,8 @@ pkv_status launch_decode_gh(const DecodeParams &p, const DecodeMaps &m, int gh, 
 // programmatic dependent and waits for its partials.
 template <typename T, typename KT = T, bool kScored = false>
 pkv_status launch_decode_typed(const DecodeParams &p, const DecodeMaps &m, int head_dim,
-                               int block_size, int gh, dim3 grid, int merge_rows, cudaStream_t s) {
+                               int block_size, int gh, dim3 grid, int merge_rows, cudaStream_t s,
+                               const WeightParams &w = WeightParams{}) {
     pkv_status st = PKV_ERR_UNSUPPORTED;
     const bool overlap = p.wait_prior_grid != 0;
     if (head_dim == 128) {
@@ -97,12 +99,19 @@ pkv_status launch_decode_typed(const DecodeParams &p, const DecodeMaps &m, int h
     const bool wide = p.num_partitions >= kMergeWideFrom;
     const unsigned blocks = static_cast<unsigned>(wide ? merge_rows : (merge_rows + 3) / 4);
     cudaError_t err;
-    if (head_dim == 128)
-        err = wide ? launch_kernel(paged_decode_merge_kernel<T, 128, 4, kScored>, dim3(blocks), dim3(128), 0, s, true, p, merge_rows)
-                   : launch_kernel(paged_decode_merge_kernel<T, 128, 1, kScored>, dim3(blocks), dim3(128), 0, s, true, p, merge_rows);
+    if constexpr (kScored) {
+        const int64_t chunks = static_cast<int64_t>(w.chunks) * (p.num_q_heads / p.group) * p.num_seqs;
+        if (blocks + chunks > 0x7fffffff) return PKV_ERR_INVALID_ARG;  // (the caller checked before the first launch)
+        auto tail = head_dim == 128 ? (wide ? paged_decode_scored_tail_kernel<T, 128, 4> : paged_decode_scored_tail_kernel<T, 128, 1>)
+                                    : (wide ? paged_decode_scored_tail_kernel<T, 64, 4> : paged_decode_scored_tail_kernel<T, 64, 1>);
+        err = launch_kernel(tail, dim3(static_cast<unsigned>(blocks + chunks)), dim3(kWeightThreads), 0, s, true, p, merge_rows,
+                            static_cast<int>(blocks), w);
+    } else if (head_dim == 128)
+        err = wide ? launch_kernel(paged_decode_merge_kernel<T, 128, 4>, dim3(blocks), dim3(128), 0, s, true, p, merge_rows)
+                   : launch_kernel(paged_decode_merge_kernel<T, 128, 1>, dim3(blocks), dim3(128), 0, s, true, p, merge_rows);
     else
-        err = wide ? launch_kernel(paged_decode_merge_kernel<T, 64, 4, kScored>, dim3(blocks), dim3(128), 0, s, true, p, merge_rows)
-                   : launch_kernel(paged_decode_merge_kernel<T, 64, 1, kScored>, dim3(blocks), dim3(128), 0, s, true, p, merge_rows);
+        err = wide ? launch_kernel(paged_decode_merge_kernel<T, 64, 4>, dim3(blocks), dim3(128), 0, s, true, p, merge_rows)
+                   : launch_kernel(paged_decode_merge_kernel<T, 64, 1>, dim3(blocks), dim3(128), 0, s, true, p, merge_rows);
     if (err != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
@@ -151,13 +160,13 @@ pkv_status launch_decode_bf16(const DecodeParams &p, const DecodeMaps &m, int he
                               int block_size, int gh, dim3 grid, int merge_rows, cudaStream_t s);
 // The scored form of the same four (decode_scored_f16.cu / _bf16.cu / _i8.cu).
 pkv_status launch_scored_f16(const DecodeParams &p, const DecodeMaps &m, int head_dim,
-                             int block_size, int gh, dim3 grid, int merge_rows, cudaStream_t s);
+                             int block_size, int gh, dim3 grid, int merge_rows, cudaStream_t s, const WeightParams &w);
 pkv_status launch_scored_bf16(const DecodeParams &p, const DecodeMaps &m, int head_dim,
-                              int block_size, int gh, dim3 grid, int merge_rows, cudaStream_t s);
+                              int block_size, int gh, dim3 grid, int merge_rows, cudaStream_t s, const WeightParams &w);
 pkv_status launch_scored_i8_f16(const DecodeParams &p, const DecodeMaps &m, int head_dim,
-                                int block_size, int gh, dim3 grid, int merge_rows, cudaStream_t s);
+                                int block_size, int gh, dim3 grid, int merge_rows, cudaStream_t s, const WeightParams &w);
 pkv_status launch_scored_i8_bf16(const DecodeParams &p, const DecodeMaps &m, int head_dim,
-                                 int block_size, int gh, dim3 grid, int merge_rows, cudaStream_t s);
+                                 int block_size, int gh, dim3 grid, int merge_rows, cudaStream_t s, const WeightParams &w);
 pkv_status launch_prefix_tc_f16(const PrefixParams &p, const CUtensorMap &tk, const CUtensorMap &tv,
                                 int block_size, dim3 grid, cudaStream_t s);
 pkv_status launch_prefix_tc_bf16(const PrefixParams &p, const CUtensorMap &tk, const CUtensorMap &tv,

@@ -1,30 +1,54 @@
-// decode_weights.cuh -- the accumulated attention weights of the scored decode.
+// decode_weights.cuh -- what follows the scored decode: the merge of its partitions and
+// the accumulated attention weights, in one launch.
 #pragma once
 
 #include "decode_kernel.cuh"
 
 namespace pkv {
 
-// The scored decode's accumulated weights: weights_out[b][h][t] = weights[b][h][t] +
-// the sum over KV head h's query heads of their softmax weights 2^(s - M) / L at token
-// t, for every t of the context (masked tokens keep their weight).  The decode kernel
-// left the scores s and each partition's (m, l); a block first joins the partitions of
-// its heads to M and 1 / L, as the merge does, then takes kWeightTokens tokens.
-// Bound by the scores' bytes (4 per query head and token, mostly still in L2) and the
-// two fp32 arrays.  Launched behind the decode as its programmatic dependent.
+// weights_out[b][h][t] = weights[b][h][t] + the sum over KV head h's query heads of their
+// softmax weights 2^(s - M) / L at token t, for every t of the context (masked tokens
+// keep their weight).  The decode kernel left the scores s and each partition's (m, l).
 struct WeightParams {
     const float *weights;  // or null: zeros
-    float *weights_out;
+    float *weights_out;    // null: the merge alone
     int64_t weights_stride;
+    int chunks;            // blocks per (sequence, KV head): of kWeightTokens tokens each
+    int vectors;           // rows of weights start 16-byte aligned
 };
 constexpr int kWeightThreads = 128;
-constexpr int kWeightTokens = 4 * kWeightThreads;
+constexpr int kWeightStep = 4 * kWeightThreads;   // four tokens per thread
+constexpr int kWeightTokens = 4 * kWeightStep;    // a block's chunk: four steps share the joining
 constexpr int kMaxWeightHeads = 128;  // query heads per KV head
 
-__global__ void __launch_bounds__(kWeightThreads) decode_weights_kernel(const DecodeParams p, const WeightParams w) {
+// Maximum and sum of one row over its partitions, by a warp: every lane gets M and L.
+__device__ __forceinline__ void join_row(const DecodeParams &p, int64_t base, int nparts, float &m, float &l) {
+    const int lane = threadIdx.x & 31;
+    float mq = -INFINITY, lq = 0.f;
+    if (lane < nparts) {
+        mq = p.ws_m[base + lane];
+        lq = p.ws_l[base + lane];
+    }
+    m = mq;
+    for (int q = lane + 32; q < nparts; q += 32) m = fmaxf(m, p.ws_m[base + q]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    l = mq == -INFINITY ? 0.f : fast_exp2(mq - m) * lq;
+    for (int q = lane + 32; q < nparts; q += 32) {
+        const float mo = p.ws_m[base + q];
+        if (mo != -INFINITY) l += fast_exp2(mo - m) * p.ws_l[base + q];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+}
+
+// The weights of one chunk: four consecutive tokens per thread, the scores of four heads
+// in flight; the first four are on their way while the block joins its heads' partitions.
+__device__ __forceinline__ void weights_chunk(const DecodeParams &p, const WeightParams &w, int idx) {
     __shared__ float head_max[kMaxWeightHeads], head_inv[kMaxWeightHeads];
-    const int seq = blockIdx.z, kvh = blockIdx.y, t0 = blockIdx.x * kWeightTokens;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int num_kv_heads = p.num_q_heads / p.group;
+    const int t0 = idx % w.chunks * kWeightTokens, kvh = idx / w.chunks % num_kv_heads, seq = idx / w.chunks / num_kv_heads;
+    const int warp = threadIdx.x >> 5;
     int len = p.context_lens[seq];
     if (len < 0) len = 0;
     if (len > p.len_cap) len = p.len_cap;
@@ -32,36 +56,71 @@ __global__ void __launch_bounds__(kWeightThreads) decode_weights_kernel(const De
     const DecodeSpan span = span_of(p, seq, len);
     const int nparts = partitions_of_span(p, span, len);
     const int64_t row0 = static_cast<int64_t>(seq) * p.num_q_heads + kvh * p.group;
+    const int64_t out_row = (static_cast<int64_t>(seq) * num_kv_heads + kvh) * w.weights_stride;
+    const int t1 = min(len, t0 + kWeightTokens);
+    int t = t0 + 4 * static_cast<int>(threadIdx.x);
+    // a span that is not empty begins at a multiple of 8 and the rows of scores at multiples
+    // of 32, so four tokens are one aligned vector; it may start before the first visible
+    // token (-inf) or reach past the context
+    const auto inside = [&] { return t < t1 && t + 4 > span.lo && span.begin < len; };
+    const float *scores = p.ws_s + row0 * p.score_stride - span.begin;
+    float4 s[4];
+    const auto load = [&](int g0) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            if (inside() && g0 + g < p.group) s[g] = *reinterpret_cast<const float4 *>(scores + (g0 + g) * p.score_stride + t);
+    };
+    load(0);
     for (int g = warp; g < p.group; g += kWeightThreads / 32) {
-        const int64_t base = (row0 + g) * p.num_partitions;
-        float m = -INFINITY, l = 0.f;
-        for (int q = lane; q < nparts; q += 32) m = fmaxf(m, p.ws_m[base + q]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        for (int q = lane; q < nparts; q += 32) {
-            const float mq = p.ws_m[base + q];
-            if (mq != -INFINITY) l += fast_exp2(mq - m) * p.ws_l[base + q];
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (lane == 0) {
+        float m, l;
+        join_row(p, (row0 + g) * p.num_partitions, nparts, m, l);
+        if ((threadIdx.x & 31) == 0) {
             head_max[g] = m == -INFINITY ? 0.f : m;  // an empty row: every score is -inf, every weight 0
             head_inv[g] = l > 0.f ? 1.f / l : 0.f;
         }
     }
     __syncthreads();
-    const int64_t wrow = (static_cast<int64_t>(seq) * (p.num_q_heads / p.group) + kvh) * w.weights_stride;
+    for (; t < t1; t += kWeightStep, load(0)) {
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (inside()) {
+            for (int g0 = 0; g0 < p.group; g0 += 4) {
+                if (g0 > 0) load(g0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = t0 + i * kWeightThreads + threadIdx.x;
-        if (t >= len) break;
-        float sum = 0.f;
-        if (t >= span.lo) {
-            const float *s = p.ws_s + row0 * p.score_stride + (t - span.begin);
-            for (int g = 0; g < p.group; ++g) sum = fmaf(fast_exp2(s[g * p.score_stride] - head_max[g]), head_inv[g], sum);
+                for (int g = 0; g < 4; ++g) {
+                    if (g0 + g >= p.group) break;
+                    const float m = head_max[g0 + g], inv = head_inv[g0 + g];
+                    sum.x = fmaf(fast_exp2(s[g].x - m), inv, sum.x);
+                    sum.y = fmaf(fast_exp2(s[g].y - m), inv, sum.y);
+                    sum.z = fmaf(fast_exp2(s[g].z - m), inv, sum.z);
+                    sum.w = fmaf(fast_exp2(s[g].w - m), inv, sum.w);
+                }
+            }
         }
-        w.weights_out[wrow + t] = w.weights ? w.weights[wrow + t] + sum : sum;
+        const int64_t at = out_row + t;
+        if (w.vectors && t + 4 <= len) {
+            if (w.weights) {
+                const float4 old = *reinterpret_cast<const float4 *>(w.weights + at);
+                sum = make_float4(old.x + sum.x, old.y + sum.y, old.z + sum.z, old.w + sum.w);
+            }
+            *reinterpret_cast<float4 *>(w.weights_out + at) = sum;
+        } else {
+            const float add[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (t + i < len) w.weights_out[at + i] = w.weights ? w.weights[at + i] + add[i] : add[i];
+        }
     }
+}
+
+// The first merge_blocks blocks merge the partitions (paged_decode_merge_kernel's work),
+// the others take a chunk of weights each.  Launched behind the decode kernel as its
+// programmatic dependent.
+template <typename T, int D, int WPR>
+__global__ void __launch_bounds__(kWeightThreads) paged_decode_scored_tail_kernel(const DecodeParams p, int num_rows,
+                                                                                  int merge_blocks, const WeightParams w) {
+    pdl_wait();
+    if (static_cast<int>(blockIdx.x) < merge_blocks) merge_rows<T, D, WPR, true>(p, num_rows, blockIdx.x);
+    else weights_chunk(p, w, static_cast<int>(blockIdx.x) - merge_blocks);
 }
 
 }  // namespace pkv

@@ -238,6 +238,13 @@ def test_bad_lengths_and_entries_are_flagged():
     ref, _, absref = refs.attend_row(c["q"][1, 0], rows_of(c, 1, 0, 0), rows_of(c, 1, 1, 0), c["scale"], 3.0, 0, 39, 0, 40)
     refs.check_attention(out.cpu()[1, 0], ref, absref, refs.score_slack(c["q"][1, 0], rows_of(c, 1, 0, 0), c["scale"], 3.0, 0, 0),
                          2.0 ** -11, "clamped to the bound")
+    w = torch.full((2, 2, 40), 7.0, device=dev)
+    for hq in (4, 2):                                        # the MMA and the lane form
+        pkv.paged_attention_decode_scored(c["q"][:, :hq].contiguous().to(dev), *pkv.split_pool(kv), c["tables"].to(dev),
+                                          torch.tensor([40, 40], dtype=torch.int32, device=dev), weights_out=w,
+                                          max_context_len=40)
+        assert pkv.get_device_error(dev)[1] == ["block_table"]
+        assert (w[0, :, 16:32] == 0).all() and ((w[0].sum(1) - hq / 2).abs() < 1e-3).all()   # the bad block's tokens weigh nothing
 
 
 def test_two_graphs_and_two_streams_do_not_share_a_workspace():
