@@ -368,7 +368,13 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache,
         w.weights = scored->weights;
         w.weights_out = scored->weights_out;
         w.weights_stride = scored->weights_stride;
-        w.chunks = (max_context_len + pkv::kWeightTokens - 1) / pkv::kWeightTokens;
+        const int64_t row_steps = (static_cast<int64_t>(max_context_len) + pkv::kWeightStep - 1) / pkv::kWeightStep;
+        const int sms = pkv::current_sm_count();
+        if (sms <= 0) return PKV_ERR_CUDA;
+        w.steps = static_cast<int>(std::min<int64_t>(
+            pkv::kMaxWeightSteps,
+            std::max<int64_t>(1, row_steps * num_kv_heads * num_seqs / (pkv::kWeightBlocksPerSm * sms))));
+        w.chunks = static_cast<int>((row_steps + w.steps - 1) / w.steps);
         w.vectors = w.weights_stride % 4 == 0 && pkv::aligned16(w.weights) && pkv::aligned16(w.weights_out);
         // one block per merge row at most, and per chunk of weights
         if (static_cast<int64_t>(num_seqs) * num_q_heads +
