@@ -187,6 +187,8 @@ pkv_status prefill_impl(
         if (scored->softcap > 0.f) {
             p.cap_in = scale / scored->softcap;
             p.cap_out = static_cast<float>(scored->softcap * 1.4426950408889634);
+            p.cap_near = p.cap_out <= 200.f ? 0.25f : 0.f;
+            p.fixed_ref = p.cap_out <= pkv::kFixedRefMax && !p.slopes;
         }
     }
     // persistent: one CTA per SM (or per item when there are fewer)

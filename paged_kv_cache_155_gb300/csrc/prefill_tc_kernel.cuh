@@ -110,7 +110,10 @@ struct PrefillParams {
     int block_size;
     float cap_in;                // scale / softcap: a raw score -> score / softcap
     float cap_out;               // softcap * log2(e), 0: scores are not capped
+    float cap_near;              // |score / softcap| up to which the short polynomial serves
+    int fixed_ref;               // |score| <= cap_out <= kFixedRefMax and no bias: see the softmax warps
 };
+constexpr float kFixedRefMax = 80.f;
 
 // Item orders (PrefillParams::order), see prefill_item.
 constexpr int kOrderRowTiles = 0, kOrderPairs = 1, kOrderSortedGroups = 2;
@@ -318,66 +321,101 @@ struct PrefillLayout {
     static_assert(kSmemBytes <= 232448, "dynamic shared memory per block");
 };
 
-// tanh(z) / z in powers of z^2, |z| <= 3/4.
-__device__ constexpr float kTanh[6] = {1.0f, -0.3333296775817871f, 0.13325515389442444f, -0.053349819034338f, 0.01959378644824028f, -0.004723952151834965f};
+// Two fp32 values in one 64-bit register and the packed arithmetic on them (sm_100 and
+// later); unlike fma_f32x2 the result is a register of its own, so a constant addend
+// needs no copy.
+using F32x2 = unsigned long long;
+__device__ __forceinline__ F32x2 pack_f32(float lo, float hi) {
+    F32x2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void unpack_f32(F32x2 v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ F32x2 fma2(F32x2 a, F32x2 b, F32x2 c) {
+    F32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ F32x2 mul2(F32x2 a, F32x2 b) {
+    F32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ F32x2 add2(F32x2 a, F32x2 b) {
+    F32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// tanh(z) / z in powers of z^2: Chebyshev fits, relative error below 2^-24 for |z| <= 3/4
+// (six terms) and 2^-21 for |z| <= 1/4 (three).
+__device__ constexpr float kTanh6[6] = {1.f, -0.3333296775817871f, 0.13325515389442444f, -0.053349819034338f, 0.01959378644824028f, -0.004723952151834965f};
+__device__ constexpr float kTanh3[3] = {0.9999995827674866f, -0.3332192897796631f, 0.12841935455799103f};
 
 // Scored form: 64 raw scores of a row (columns dist0, dist0 + 1, ... from the query's
 // position) -> scores in log2 units, capped and biased.
-// Cap: cap * tanh(s / cap) with s = scale * x is x R(x^2) while |s / cap| <= 3/4, R the
-// degree-5 Chebyshev fit of tanh(z)/z in z^2 (relative error 2^-24) whose coefficients
-// are scaled to take x itself: three packed FMAs a score and no exponential, where the
-// softmax already spends one.  A warp with a larger score takes the closed form
-// cap (1 - 2 / (1 + e^(2 z))), an exponential and a reciprocal more.
+// Cap: cap * tanh(s / cap) with s = scale * x is x R(x^2), R a polynomial of tanh(z)/z
+// whose coefficients are scaled to take x itself: no exponential, where the softmax
+// already spends one.  A warp takes the three-term R when its scores stay within a
+// quarter of the cap (and the cap is small enough for that fit's error to stay below
+// 2e-5 of a score), the six-term one within three quarters, and beyond that the closed
+// form cap (1 - 2 / (1 + e^(2 z))), an exponential and a reciprocal more.
 __device__ __forceinline__ void score_row(const PrefillParams &p, float (&x)[64], float slope2, int dist0) {
     if (p.cap_out > 0.f) {
-        float big = 0.f;
+        float big = fmaxf(fabsf(x[0]), fabsf(x[1]));
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) big = fmax3(big, fabsf(x[i]), fabsf(x[i + 1]));
+        for (int i = 2; i < 64; i += 2) big = fmax3(big, fabsf(x[i]), fabsf(x[i + 1]));
+        big *= fabsf(p.cap_in);
         const float k2 = p.cap_in * p.cap_in;
-        if (__any_sync(0xffffffffu, !(big * fabsf(p.cap_in) <= 0.75f))) {
-            const float k = p.cap_in * 2.885390081777927f;  // 2 log2(e) / cap
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-                x[i] = p.cap_out - 2.f * p.cap_out * fast_rcp(1.f + fast_exp2(x[i] * k));
-        } else {
-            const float c0 = p.scale_log2 * kTanh[0], c1 = p.scale_log2 * kTanh[1] * k2;
-            const float c2 = p.scale_log2 * kTanh[2] * k2 * k2, c3 = p.scale_log2 * kTanh[3] * k2 * k2 * k2;
-            const float c4 = p.scale_log2 * kTanh[4] * k2 * k2 * k2 * k2;
-            const float c5 = p.scale_log2 * kTanh[5] * k2 * k2 * k2 * k2 * k2;
+        if (__all_sync(0xffffffffu, big <= p.cap_near)) {
+            const float r0 = p.scale_log2 * kTanh3[0], r1 = p.scale_log2 * kTanh3[1] * k2;
+            const float r2 = p.scale_log2 * kTanh3[2] * k2 * k2;
+            const F32x2 c0 = pack_f32(r0, r0), c1 = pack_f32(r1, r1), c2 = pack_f32(r2, r2);
 #pragma unroll
             for (int i = 0; i < 64; i += 2) {
-                float u0 = 0.f, u1 = 0.f, r0 = c4, r1 = c4, s0 = c3, s1 = c3;
-                fma_f32x2(u0, u1, x[i], x[i + 1], x[i], x[i + 1]);
-                fma_f32x2(r0, r1, u0, u1, c5, c5);
-                fma_f32x2(s0, s1, u0, u1, r0, r1);
-                r0 = r1 = c2;
-                fma_f32x2(r0, r1, u0, u1, s0, s1);
-                s0 = s1 = c1;
-                fma_f32x2(s0, s1, u0, u1, r0, r1);
-                r0 = r1 = c0;
-                fma_f32x2(r0, r1, u0, u1, s0, s1);
-                x[i] *= r0;
-                x[i + 1] *= r1;
+                const F32x2 v = pack_f32(x[i], x[i + 1]);
+                const F32x2 u = mul2(v, v);
+                unpack_f32(mul2(v, fma2(u, fma2(u, c2, c1), c0)), x[i], x[i + 1]);
             }
+        } else if (__all_sync(0xffffffffu, big <= 0.75f)) {
+            float r[6], k = p.scale_log2;
+            F32x2 c[6];
+#pragma unroll
+            for (int j = 0; j < 6; ++j, k *= k2) {
+                r[j] = k * kTanh6[j];
+                c[j] = pack_f32(r[j], r[j]);
+            }
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+                const F32x2 v = pack_f32(x[i], x[i + 1]);
+                const F32x2 u = mul2(v, v);
+                F32x2 q = fma2(u, c[5], c[4]);
+#pragma unroll
+                for (int j = 3; j >= 0; --j) q = fma2(u, q, c[j]);
+                unpack_f32(mul2(v, q), x[i], x[i + 1]);
+            }
+        } else {
+            const float k = p.cap_in * 2.885390081777927f;  // 2 log2(e) / cap
+#pragma unroll
+            for (int i = 0; i < 64; ++i) x[i] = p.cap_out - 2.f * p.cap_out * fast_rcp(1.f + fast_exp2(x[i] * k));
         }
         if (!p.slopes) return;
-        const float base = slope2 * static_cast<float>(dist0);
-#pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-            float b0 = base, b1 = base;
-            fma_f32x2(b0, b1, slope2, slope2, static_cast<float>(i), static_cast<float>(i + 1));
-            add_f32x2(x[i], x[i + 1], b0, b1);
-        }
-        return;
     }
-    const float base = slope2 * static_cast<float>(dist0);
+    // bias: a pair of columns after the other adds two slopes; started afresh every 16
+    // columns, so that the sum's rounding stays within a few steps
+    const F32x2 one = pack_f32(1.f, 1.f), scale = pack_f32(p.scale_log2, p.scale_log2);
+    const F32x2 f = p.cap_out > 0.f ? one : scale, step = pack_f32(2.f * slope2, 2.f * slope2);
+    F32x2 bias = 0ull;
 #pragma unroll
     for (int i = 0; i < 64; i += 2) {
-        float b0 = base, b1 = base;
-        fma_f32x2(b0, b1, slope2, slope2, static_cast<float>(i), static_cast<float>(i + 1));
-        fma_f32x2(b0, b1, x[i], x[i + 1], p.scale_log2, p.scale_log2);
-        x[i] = b0;
-        x[i + 1] = b1;
+        if (i % 16 == 0) {
+            const float b = slope2 * static_cast<float>(dist0 + i);
+            bias = pack_f32(b, b + slope2);
+        }
+        unpack_f32(fma2(pack_f32(x[i], x[i + 1]), f, bias), x[i], x[i + 1]);
+        bias = add2(bias, step);
     }
 }
 
@@ -678,7 +716,8 @@ __global__ void __launch_bounds__(384, 1)
                         const uint64_t bd = tc::smem_desc_sw128(va + k * 2048, L::kHalf, 1024);
                         // P from TMEM (16 tokens = 8 columns per step); the item's first
                         // tile starts O afresh
-                        tc::mma_f16_ts(tmem + L::kOCol, tmem + 128 * b + 8 * k, bd, idesc_pv, j > 0 || k > 0);
+                        const int pc = kScored && k >= TILE / 32 ? 64 + 8 * (k - TILE / 32) : 8 * k;
+                        tc::mma_f16_ts(tmem + L::kOCol, tmem + 128 * b + pc, bd, idesc_pv, j > 0 || k > 0);
                     }
                     tc::mma_commit(&o_done[b]);
                     tc::mma_commit(&s_empty[b]);  // S[b] / P[b] free for QK^T(jt + SB)
@@ -736,6 +775,10 @@ __global__ void __launch_bounds__(384, 1)
         // S[b] only after PV(jt), which waits for both warps).  An item's row sums go
         // through shared memory; a slot is rewritten only after the next tile's
         // exchange, which the partner reaches after reading it.
+        // Scored form: half 1 keeps its P in its own columns, 64 .. 95, and exchanges through
+        // column 96, so that a tile without an exchange (fixed_ref below) needs no order
+        // between the two warps.
+        constexpr int kX1 = kScored ? 96 : 64;  // half 1's exchange column
         auto pair_sync = [&](int step) -> bool {
             __syncwarp();
             uint64_t *pb = &pair_bar[quarter * 2 + (step & 1)];
@@ -744,12 +787,12 @@ __global__ void __launch_bounds__(384, 1)
         };
         auto exchange_max = [&](int step, int b, float mine, float &other) -> bool {
             const uint32_t sb = lane_base + 128 * b;
-            tc::tmem_st_x1(sb + (half ? 64 : 32), mine);
+            tc::tmem_st_x1(sb + (half ? kX1 : 32), mine);
             tc::tmem_st_wait();
             tc::fence_before_sync();
             if (!pair_sync(step)) return false;
             tc::fence_after_sync();
-            other = tc::tmem_ld_x1(sb + (half ? 32 : 64));
+            other = tc::tmem_ld_x1(sb + (half ? 32 : kX1));
             tc::tmem_ld_wait();
             return true;
         };
@@ -777,7 +820,11 @@ __global__ void __launch_bounds__(384, 1)
                     if (p.slopes) slope2 = p.slopes[it.kvh * p.group + row - jtok * p.group] * 1.4426950408889634f;
                 }
             }
-            float m_ref = -INFINITY, l = 0.f;
+            // Scored form, bf16, capped and not biased: |score| <= cap_out, so 0 serves as every
+            // row's reference: bf16 and fp32 hold 2^-80 .. 2^80 as exactly as 1 (fp16 does not),
+            // and the maximum, its exchange between the two warps and the rescaling fall away
+            const bool fixed_ref = kScored && kBF16 && p.fixed_ref;
+            float m_ref = fixed_ref ? 0.f : -INFINITY, l = 0.f;
             for (int j = 0; j < it.ntiles && ok; ++j, ++jt) {
                 const int b = jt % SB;
                 const int t0 = it.tok_lo + j * TILE;
@@ -809,9 +856,11 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                         for (int i = 0; i < 64; ++i) x[i] = i >= clo && i < chi ? x[i] : -INFINITY;
                     }
-                    pmax = fmaxf(x[0], x[63]);
+                    if (!fixed_ref) {
+                        pmax = fmaxf(x[0], x[63]);
 #pragma unroll
-                    for (int i = 1; i + 1 < 63; i += 2) pmax = fmax3(pmax, x[i], x[i + 1]);
+                        for (int i = 1; i + 1 < 63; i += 2) pmax = fmax3(pmax, x[i], x[i + 1]);
+                    }
                 } else if (vh > 0) {
                     const bool pos_scale = p.scale_log2 > 0.f;
                     float ext = x[0];
@@ -827,58 +876,61 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     pmax = ext * p.scale_log2;
                 }
-                float pmax_other;
-                if (!exchange_max(xs++, b, pmax, pmax_other)) {
-                    ok = false;
-                    break;
-                }
-                const float tmax = fmaxf(pmax, pmax_other);
-                // the reference maximum moves only by more than kRescaleLog2 (a row that sees
-                // nothing keeps -inf and alpha 1); both warps of the pair take the same
-                // decision for a row; TMEM loads and stores are warp-wide, so the warp
-                // rescales its half of O if any of its rows must
-                const float new_ref = tmax > m_ref + L::kRescaleLog2 ? tmax : m_ref;
-                const float alpha = new_ref == m_ref ? 1.f : fast_exp2(m_ref - new_ref);
-                if (__any_sync(0xffffffffu, new_ref != m_ref)) {
-                    if (j > 0) {
-                        // O holds tiles < j: wait for PV(j-1), rescale this half of O in TMEM
-                        if (!tc_wait_warp(&o_done[(jt - 1) % SB], ((jt - 1) / SB) & 1, abort_flag, p.status)) {
-                            ok = false;
-                            break;
-                        }
-                        tc::fence_after_sync();
-#pragma unroll
-                        for (int c = 0; c < 64; c += 16) {
-                            float o[16];
-                            tc::tmem_ld_x16(lane_base + L::kOCol + c0 + c, o);
-                            tc::tmem_ld_wait();
-                            uint32_t w[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * alpha);
-                            asm volatile(
-                                "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, "
-                                "%8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(lane_base + L::kOCol + c0 + c),
-                                "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
-                                "r"(w[7]), "r"(w[8]), "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]),
-                                "r"(w[13]), "r"(w[14]), "r"(w[15])
-                                : "memory");
-                        }
-                        tc::tmem_st_wait();
+                if (!fixed_ref) {
+                    float pmax_other;
+                    if (!exchange_max(xs++, b, pmax, pmax_other)) {
+                        ok = false;
+                        break;
                     }
-                    l *= alpha;
-                    m_ref = new_ref;
+                    const float tmax = fmaxf(pmax, pmax_other);
+                    // the reference maximum moves only by more than kRescaleLog2 (a row that sees
+                    // nothing keeps -inf and alpha 1); both warps of the pair take the same
+                    // decision for a row; TMEM loads and stores are warp-wide, so the warp
+                    // rescales its half of O if any of its rows must
+                    const float new_ref = tmax > m_ref + L::kRescaleLog2 ? tmax : m_ref;
+                    const float alpha = new_ref == m_ref ? 1.f : fast_exp2(m_ref - new_ref);
+                    if (__any_sync(0xffffffffu, new_ref != m_ref)) {
+                        if (j > 0) {
+                            // O holds tiles < j: wait for PV(j-1), rescale this half of O in TMEM
+                            if (!tc_wait_warp(&o_done[(jt - 1) % SB], ((jt - 1) / SB) & 1, abort_flag, p.status)) {
+                                ok = false;
+                                break;
+                            }
+                            tc::fence_after_sync();
+    #pragma unroll
+                            for (int c = 0; c < 64; c += 16) {
+                                float o[16];
+                                tc::tmem_ld_x16(lane_base + L::kOCol + c0 + c, o);
+                                tc::tmem_ld_wait();
+                                uint32_t w[16];
+    #pragma unroll
+                                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * alpha);
+                                asm volatile(
+                                    "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, "
+                                    "%8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(lane_base + L::kOCol + c0 + c),
+                                    "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
+                                    "r"(w[7]), "r"(w[8]), "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]),
+                                    "r"(w[13]), "r"(w[14]), "r"(w[15])
+                                    : "memory");
+                            }
+                            tc::tmem_st_wait();
+                        }
+                        l *= alpha;
+                        m_ref = new_ref;
+                    }
                 }
                 // P = 2^(s - m_ref) on visible columns (0 elsewhere), rounded to T and packed
                 // two per 32-bit column over the first 64 columns of S[b] (tokens 64 half ..
                 // +63 -> columns 32 half .. +31; both warps of the pair have read their
                 // scores, the exchange above orders it), where the PV MMA reads it; the row
                 // sum l adds the fp32 values
-                const uint32_t pcol = lane_base + 128 * b + 32 * half;
+                const uint32_t pcol = lane_base + 128 * b + (kScored ? 64 : 32) * half;
                 float l0 = 0.f, l1 = 0.f;
-                // scored: -inf - m is 0 weight, and a row that has seen nothing yet subtracts 0
+                // scored: a masked -inf gets weight 0, and a row that has seen nothing yet subtracts 0
                 const float m_sub = kScored && m_ref == -INFINITY ? 0.f : m_ref;
+                const F32x2 minus_m = pack_f32(-m_sub, -m_sub);
                 // two copies of the loop, so fully visible tiles carry no per-column mask
-                auto weights = [&](auto masked) {
+                auto weights = [&](auto masked, auto shifted) {
 #pragma unroll
                     for (int c16 = 0; c16 < 2; ++c16) {
                         uint32_t packed[16];
@@ -887,7 +939,8 @@ __global__ void __launch_bounds__(384, 1)
                             const int t = c16 * 32 + 2 * i;
                             // s * scale - m for two columns in one packed FMA
                             float e0 = -m_sub, e1 = -m_sub;
-                            if constexpr (kScored) add_f32x2(e0, e1, x[t], x[t + 1]);
+                            if constexpr (!decltype(shifted)::value) e0 = x[t], e1 = x[t + 1];
+                            else if constexpr (kScored) unpack_f32(add2(pack_f32(x[t], x[t + 1]), minus_m), e0, e1);
                             else fma_f32x2(e0, e1, x[t], x[t + 1], p.scale_log2, p.scale_log2);
                             float p0 = fast_exp2(e0);
                             float p1 = fast_exp2(e1);
@@ -901,8 +954,9 @@ __global__ void __launch_bounds__(384, 1)
                         tc::tmem_st_x16(pcol + 16 * c16, packed);
                     }
                 };
-                if (kScored || full) weights(std::false_type{});
-                else weights(std::true_type{});
+                if (kScored && fixed_ref) weights(std::false_type{}, std::false_type{});
+                else if (kScored || full) weights(std::false_type{}, std::true_type{});
+                else weights(std::true_type{}, std::true_type{});
                 l += l0 + l1;
                 const int skip = kScored ? it.lo - t0 : 0;  // rows before the row tile's first visible token
                 if (valid < TILE || (kScored && skip > 0)) {
@@ -934,6 +988,9 @@ __global__ void __launch_bounds__(384, 1)
             // partial slot.  TMEM loads are warp-wide: every lane loads, only live rows store.
             float l_other = 0.f;
             if (ok) ok = exchange_sum(xs++, l, l_other);
+            // without the tiles' exchanges the partner may still be reading when this warp
+            // writes the next item's sum
+            if (ok && fixed_ref) ok = pair_sync(xs++);
             const float lt = l + l_other;
             if (ok) ok = tc_wait_warp(&o_done[(jt - 1) % SB], ((jt - 1) / SB) & 1, abort_flag, p.status);
             if (ok && prefill_staged(p, it)) {
