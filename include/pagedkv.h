@@ -516,7 +516,8 @@ PKV_API pkv_status pkv_paged_attention_prefill(
 
 /*
  * pkv_prefill_scored_workspace_bytes -- workspace of
- * pkv_paged_attention_prefill_scored, as pkv_prefill_workspace_bytes;
+ * pkv_paged_attention_prefill_scored, as pkv_prefill_workspace_bytes (an item
+ * table of 32 bytes per row tile when the KV range is not split);
  * has_prefix != 0 when prefix_lens is given.
  */
 PKV_API size_t pkv_prefill_scored_workspace_bytes(int num_rows, int num_seqs, int num_q_heads,

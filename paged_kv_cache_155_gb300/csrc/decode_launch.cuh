@@ -14,26 +14,6 @@
 
 namespace pkv {
 
-// Launch `kernel` on `stream`; with `overlap`, as a programmatic dependent launch:
-// it may start while the kernel before it in the stream still runs, once every
-// CTA of that kernel has executed pdl_trigger (and must order itself after that
-// kernel with pdl_wait where it needs to).
-template <typename... Params, typename... Args>
-cudaError_t launch_kernel(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
-                          cudaStream_t stream, bool overlap, Args &&...args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = overlap ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-
 template <typename T, typename KT, int D, int BS, int GH, bool kScored>
 pkv_status launch_decode_one(const DecodeParams &p, const DecodeMaps &maps, dim3 grid, cudaStream_t stream,
                              bool overlap) {

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "../../include/pagedkv.h"
 
 namespace pkv {
@@ -40,6 +42,26 @@ bool encode_query_map(CUtensorMap *map, const void *q, int num_rows, int num_q_h
                       int tokens, pkv_dtype dt);
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Launch `kernel` on `stream`; with `overlap`, as a programmatic dependent launch:
+// it may start while the kernel before it in the stream still runs, once every
+// CTA of that kernel has executed pdl_trigger (and must order itself after that
+// kernel with pdl_wait where it needs to).
+template <typename... Params, typename... Args>
+cudaError_t launch_kernel(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                          cudaStream_t stream, bool overlap, Args &&...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
 
 inline pkv_status launch_status() {
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;

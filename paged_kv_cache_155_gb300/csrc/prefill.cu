@@ -4,6 +4,7 @@
 // merge.
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 
 #include "prefill_launch.cuh"
 
@@ -11,7 +12,7 @@ namespace {
 
 constexpr int kMinSplitTokens = 512;  // a KV split covers at least 4 tiles
 
-struct PrefillPlan {
+struct PrefillShape {
     int tile_tokens = 0;   // chunk tokens per row tile: 128 / group
     int row_tiles = 0;     // row tiles of the longest chunk
     int splits = 0;
@@ -21,7 +22,7 @@ struct PrefillPlan {
 
 pkv_status plan_prefill(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                         int block_size, int max_query_len, int max_context_len, int kv_splits,
-                        int sm_count, PrefillPlan *pp, int window = 0, bool has_prefix = false) {
+                        int sm_count, PrefillShape *pp, int window = 0, bool has_prefix = false) {
     if (head_dim != 128) return PKV_ERR_UNSUPPORTED;
     if (block_size != 8 && block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads ||
@@ -57,9 +58,19 @@ pkv_status plan_prefill(int num_seqs, int num_q_heads, int num_kv_heads, int hea
     return PKV_OK;
 }
 
+// The scored prefill plans its items on the device (paged_prefill_plan_kernel) when the
+// KV ranges are not split and the row tiles fit the plan's one block.
+bool planned(const PrefillShape &pp, int num_seqs) {
+    return pp.splits == 1 && static_cast<int64_t>(pp.row_tiles) * num_seqs <= pkv::kMaxPlanEntries;
+}
+
 size_t prefill_workspace(int num_rows, int num_q_heads, int splits) {
     if (splits <= 1) return 0;
     return static_cast<size_t>(num_rows) * num_q_heads * splits * (128 + 2) * sizeof(float);
+}
+
+size_t plan_bytes(const PrefillShape &pp, int num_seqs) {
+    return offsetof(pkv::PrefillPlan, entry) + sizeof(pkv::PrefillEntry) * static_cast<size_t>(pp.row_tiles) * num_seqs;
 }
 
 // What the scored prefill adds to a call.
@@ -105,7 +116,7 @@ pkv_status prefill_impl(
     if (!q || !out || !block_tables || !query_start || !context_lens || !pkv::aligned16(q) ||
         !pkv::aligned16(out))
         return PKV_ERR_INVALID_ARG;
-    PrefillPlan pp;
+    PrefillShape pp;
     // shape first (no CUDA call), then the plan for the real SM count
     pkv_status st = plan_prefill(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                                  max_query_len, max_context_len, kv_splits, 1, &pp, window, has_prefix);
@@ -118,7 +129,9 @@ pkv_status prefill_impl(
                           max_context_len, 0, sm, &pp, window, has_prefix);
         if (st != PKV_OK) return st;
     }
-    const size_t need = prefill_workspace(num_rows, num_q_heads, pp.splits);
+    const bool plan_items = scored && planned(pp, num_seqs);
+    const size_t partials = prefill_workspace(num_rows, num_q_heads, pp.splits);
+    const size_t need = plan_items ? plan_bytes(pp, num_seqs) : partials;
     if (need > 0 && (!workspace || workspace_bytes < need || !pkv::aligned16(workspace)))
         return PKV_ERR_INVALID_ARG;
     unsigned int *status = pkv::status_word_ptr();
@@ -140,9 +153,9 @@ pkv_status prefill_impl(
     p.q = q;
     p.out = out;
     const size_t slots = static_cast<size_t>(num_rows) * num_q_heads * pp.splits;
-    p.ws_o = need ? static_cast<float *>(workspace) : nullptr;
-    p.ws_m = need ? p.ws_o + slots * head_dim : nullptr;
-    p.ws_l = need ? p.ws_m + slots : nullptr;
+    p.ws_o = partials ? static_cast<float *>(workspace) : nullptr;
+    p.ws_m = partials ? p.ws_o + slots * head_dim : nullptr;
+    p.ws_l = partials ? p.ws_m + slots : nullptr;
     p.block_tables = block_tables;
     p.query_start = query_start;
     p.context_lens = context_lens;
@@ -187,13 +200,21 @@ pkv_status prefill_impl(
         if (scored->softcap > 0.f) {
             p.cap_in = scale / scored->softcap;
             p.cap_out = static_cast<float>(scored->softcap * 1.4426950408889634);
-            p.cap_near = p.cap_out <= 200.f ? 0.25f : 0.f;
+            p.cap_short = p.cap_out <= 200.f;
             p.fixed_ref = p.cap_out <= pkv::kFixedRefMax && !p.slopes;
         }
     }
     // persistent: one CTA per SM (or per item when there are fewer)
     const int grid = std::min(pp.items, sm);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (plan_items) {
+        auto *plan = static_cast<pkv::PrefillPlan *>(workspace);
+        p.plan = plan;
+        p.order = pkv::kOrderPlanned;
+        pkv::paged_prefill_plan_kernel<<<1, pkv::kPlanThreads, 0, s>>>(p, plan);
+        pkv::count_launch();
+        if (st = pkv::launch_status(); st != PKV_OK) return st;
+    }
     if (scored)
         return dtype == PKV_F16
                    ? pkv::launch_prefill_scored_f16(p, tq, tk, tv, to, block_size, grid, max_query_len, s)
@@ -212,7 +233,7 @@ PKV_API size_t pkv_prefill_workspace_bytes(int num_rows, int num_seqs, int num_q
                                            int max_query_len, int max_context_len, int kv_splits) {
     const int sm = kv_splits > 0 ? 1 : pkv::current_sm_count();
     if (sm <= 0 || num_rows < 0) return static_cast<size_t>(-1);
-    PrefillPlan pp;
+    PrefillShape pp;
     if (plan_prefill(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_query_len,
                      max_context_len, kv_splits, sm, &pp) != PKV_OK)
         return static_cast<size_t>(-1);
@@ -238,10 +259,11 @@ PKV_API size_t pkv_prefill_scored_workspace_bytes(int num_rows, int num_seqs, in
                                                   int has_prefix, int kv_splits) {
     const int sm = kv_splits > 0 ? 1 : pkv::current_sm_count();
     if (sm <= 0 || num_rows < 0 || window < 0) return static_cast<size_t>(-1);
-    PrefillPlan pp;
+    PrefillShape pp;
     if (plan_prefill(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_query_len,
                      max_context_len, kv_splits, sm, &pp, window, has_prefix != 0) != PKV_OK)
         return static_cast<size_t>(-1);
+    if (planned(pp, num_seqs)) return plan_bytes(pp, num_seqs);
     return prefill_workspace(num_rows, num_q_heads, pp.splits);
 }
 

@@ -23,8 +23,12 @@ pkv_status launch_prefill_one(const PrefillParams &p, const CUtensorMap &tq, con
             return PKV_ERR_CUDA;
         configured_devices.fetch_or(bit, std::memory_order_acq_rel);
     }
-    paged_prefill_tc_kernel<T, BS, ORDER, kScored>
-        <<<grid, PrefillLayout::kThreads, PrefillLayout::kSmemBytes, stream>>>(tq, tk, tv, to, p);
+    // planned order: placed while the plan kernel before it still runs
+    if (launch_kernel(paged_prefill_tc_kernel<T, BS, ORDER, kScored>, dim3(grid), dim3(PrefillLayout::kThreads),
+                      PrefillLayout::kSmemBytes, stream, ORDER == kOrderPlanned, tq, tk, tv, to, p) != cudaSuccess) {
+        cudaGetLastError();
+        return PKV_ERR_CUDA;
+    }
     count_launch();
     return launch_status();
 }
@@ -32,10 +36,14 @@ pkv_status launch_prefill_one(const PrefillParams &p, const CUtensorMap &tq, con
 template <typename T, int BS, bool kScored>
 pkv_status launch_prefill_bs(const PrefillParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
                              const CUtensorMap &tv, const CUtensorMap &to, int grid, cudaStream_t s) {
-    if (p.order == kOrderSortedGroups)
-        return launch_prefill_one<T, BS, kOrderSortedGroups, kScored>(p, tq, tk, tv, to, grid, s);
-    if (p.order == kOrderPairs) return launch_prefill_one<T, BS, kOrderPairs, kScored>(p, tq, tk, tv, to, grid, s);
-    return launch_prefill_one<T, BS, kOrderRowTiles, kScored>(p, tq, tk, tv, to, grid, s);
+    if constexpr (kScored) {
+        if (p.order == kOrderPlanned) return launch_prefill_one<T, BS, kOrderPlanned, true>(p, tq, tk, tv, to, grid, s);
+        return launch_prefill_one<T, BS, kOrderRowTiles, true>(p, tq, tk, tv, to, grid, s);
+    }
+    else if (p.order == kOrderSortedGroups)
+        return launch_prefill_one<T, BS, kOrderSortedGroups, false>(p, tq, tk, tv, to, grid, s);
+    else if (p.order == kOrderPairs) return launch_prefill_one<T, BS, kOrderPairs, false>(p, tq, tk, tv, to, grid, s);
+    else return launch_prefill_one<T, BS, kOrderRowTiles, false>(p, tq, tk, tv, to, grid, s);
 }
 
 template <typename T, bool kScored = false>

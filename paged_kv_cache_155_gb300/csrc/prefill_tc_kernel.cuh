@@ -110,13 +110,14 @@ struct PrefillParams {
     int block_size;
     float cap_in;                // scale / softcap: a raw score -> score / softcap
     float cap_out;               // softcap * log2(e), 0: scores are not capped
-    float cap_near;              // |score / softcap| up to which the short polynomial serves
+    int cap_short;               // the cap is small enough for the short polynomials
+    const struct PrefillPlan *plan;  // the item table (planned order)
     int fixed_ref;               // |score| <= cap_out <= kFixedRefMax and no bias: see the softmax warps
 };
 constexpr float kFixedRefMax = 80.f;
 
 // Item orders (PrefillParams::order), see prefill_item.
-constexpr int kOrderRowTiles = 0, kOrderPairs = 1, kOrderSortedGroups = 2;
+constexpr int kOrderRowTiles = 0, kOrderPairs = 1, kOrderSortedGroups = 2, kOrderPlanned = 3;
 constexpr int kSortedGroupsMaxSeqs = 32;  // sequences a block ranks by length itself
 
 // One sequence's chunk start, chunk end and context length, as read from the
@@ -185,6 +186,30 @@ __device__ __forceinline__ PrefillRange prefill_range(const PrefillParams &p, in
     if (p.prefix_lens) hi = max(hi, min(len, p.prefix_lens[seq]));
     if (lo >= hi) return PrefillRange{hi, hi, hi};
     return PrefillRange{lo, hi, lo & ~(p.block_size - 1)};
+}
+
+// Planned order (scored form, one split): the row tiles of all sequences that hold work,
+// most KV tiles first, as paged_prefill_plan_kernel writes them; item i is entry
+// i / num_kv_heads, KV head i % num_kv_heads.  The rounds go forth and back
+// (prefill_slot_item), which evens out the CTAs' shares for any mix of lengths, windows
+// and documents, and an item costs its role one prefetched load.
+struct PrefillEntry {
+    int q0, chunk, len, seq;
+    int row_tile, lo, tok_lo, tok_hi;
+};
+struct PrefillPlan {
+    int entries, pad[3];
+    PrefillEntry entry[1];
+};
+constexpr int kMaxPlanEntries = 4096;
+__device__ __forceinline__ PrefillEntry load_entry(const PrefillParams &p, int item, int num_items) {
+    PrefillEntry e{};
+    if (item < num_items) {
+        const int4 *src = reinterpret_cast<const int4 *>(p.plan->entry + fast_div(item, p.div_kv_heads));
+        const int4 a = src[0], b = src[1];
+        e = PrefillEntry{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    }
+    return e;
 }
 
 struct PrefillItem {
@@ -274,13 +299,50 @@ __device__ __forceinline__ bool prefill_item(const PrefillParams &p, int i, cons
     return it.tok_hi > it.tok_lo;
 }
 
+__device__ __forceinline__ void planned_item(const PrefillParams &p, int i, const PrefillEntry &e, PrefillItem &it) {
+    it.q0 = e.q0;
+    it.chunk = e.chunk;
+    it.len = e.len;
+    it.seq = e.seq;
+    it.kvh = i - fast_div(i, p.div_kv_heads) * p.num_kv_heads;
+    it.split = 0;
+    it.row_tile = e.row_tile;
+    it.rows = e.chunk * p.group;
+    it.row0 = e.row_tile * p.tile_rows;
+    it.base_pos = e.len - e.chunk;
+    it.lo = e.lo;
+    it.tok_lo = e.tok_lo;
+    it.tok_hi = e.tok_hi;
+    it.ntiles = max(1, (e.tok_hi - e.tok_lo + 127) / 128);  // rows that see nothing: a tile without tokens
+}
+
+// Scored form: what thread r's row of an item sees, [lo, hi), and its bias per token in
+// log2 units; a row past the item's rows sees nothing.
+struct PrefillRow {
+    int lo, hi;
+    float slope2;
+};
+__device__ __forceinline__ PrefillRow prefill_row(const PrefillParams &p, const PrefillItem &it, int r) {
+    PrefillRow v{0, 0, 0.f};
+    const int row = it.row0 + r;
+    if (r < p.tile_rows && row < it.rows) {
+        const int jtok = fast_div(row, p.div_group), pos = it.base_pos + jtok;
+        v.lo = p.window > 0 ? max(0, pos + 1 - p.window) : 0;
+        if (p.starts) v.lo = max(v.lo, p.starts[it.q0 + jtok]);
+        v.hi = pos + 1;
+        if (p.prefix_lens) v.hi = max(v.hi, min(it.len, p.prefix_lens[it.seq]));
+        if (p.slopes) v.slope2 = p.slopes[it.kvh * p.group + row - jtok * p.group] * 1.4426950408889634f;
+    }
+    return v;
+}
+
 // The k-th item of this CTA: items blockIdx.x + k * grid in the row-tile order,
 // the pairs (2 q, 2 q + 1) for q = blockIdx.x + (k / 2) * grid in pair order, and
-// item blockIdx.x of round k (counted from the end in odd rounds) in sorted-groups
-// order.
+// item blockIdx.x of round k (counted from the end in odd rounds) in sorted-groups and
+// planned order.
 template <int ORDER>
 __device__ __forceinline__ int prefill_slot_item(const PrefillParams &p, int k) {
-    if constexpr (ORDER == kOrderSortedGroups)
+    if constexpr (ORDER == kOrderSortedGroups || ORDER == kOrderPlanned)
         return k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     if constexpr (ORDER == kOrderPairs) return 2 * (blockIdx.x + (k >> 1) * gridDim.x) + (k & 1);
     return blockIdx.x + k * gridDim.x;
@@ -350,58 +412,60 @@ __device__ __forceinline__ F32x2 add2(F32x2 a, F32x2 b) {
 }
 
 // tanh(z) / z in powers of z^2: Chebyshev fits, relative error below 2^-24 for |z| <= 3/4
-// (six terms) and 2^-21 for |z| <= 1/4 (three).
+// (six terms), 2^-21.9 for |z| <= 0.45 (four) and 2^-21 for |z| <= 1/4 (three).
 __device__ constexpr float kTanh6[6] = {1.f, -0.3333296775817871f, 0.13325515389442444f, -0.053349819034338f, 0.01959378644824028f, -0.004723952151834965f};
+__device__ constexpr float kTanh4[4] = {0.9999997615814209f, -0.33329492807388306f, 0.13236714899539948f,
+                                        -0.046039558947086334f};
 __device__ constexpr float kTanh3[3] = {0.9999995827674866f, -0.3332192897796631f, 0.12841935455799103f};
 
+// x <- x R(x^2), R of N terms whose coefficients are scaled to give scale_log2 x at small x.
+template <int N>
+__device__ __forceinline__ void cap_poly(const PrefillParams &p, const float (&terms)[N], float (&x)[64]) {
+    const float k2 = p.cap_in * p.cap_in;
+    float k = p.scale_log2;
+    F32x2 c[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j, k *= k2) c[j] = pack_f32(k * terms[j], k * terms[j]);
+#pragma unroll
+    for (int i = 0; i < 64; i += 2) {
+        const F32x2 v = pack_f32(x[i], x[i + 1]);
+        const F32x2 u = mul2(v, v);
+        F32x2 q = fma2(u, c[N - 1], c[N - 2]);
+#pragma unroll
+        for (int j = N - 3; j >= 0; --j) q = fma2(u, q, c[j]);
+        unpack_f32(mul2(v, q), x[i], x[i + 1]);
+    }
+}
+
 // Scored form: 64 raw scores of a row (columns dist0, dist0 + 1, ... from the query's
-// position) -> scores in log2 units, capped and biased.
+// position) -> scores in log2 units, capped and biased; returns the factor that is left
+// to apply (scale_log2, when neither is asked for; else 1).
 // Cap: cap * tanh(s / cap) with s = scale * x is x R(x^2), R a polynomial of tanh(z)/z
 // whose coefficients are scaled to take x itself: no exponential, where the softmax
-// already spends one.  A warp takes the three-term R when its scores stay within a
-// quarter of the cap (and the cap is small enough for that fit's error to stay below
-// 2e-5 of a score), the six-term one within three quarters, and beyond that the closed
-// form cap (1 - 2 / (1 + e^(2 z))), an exponential and a reciprocal more.
-__device__ __forceinline__ void score_row(const PrefillParams &p, float (&x)[64], float slope2, int dist0) {
+// already spends one.  A warp takes a short R when its scores stay far below the cap (and
+// the cap is small enough for that fit's error to stay below 2.5e-5 of a score), the
+// six-term one within three quarters, and beyond that the closed form
+// cap (1 - 2 / (1 + e^(2 z))), an exponential and a reciprocal more.
+__device__ __forceinline__ float score_row(const PrefillParams &p, float (&x)[64], float slope2, int dist0) {
     if (p.cap_out > 0.f) {
         float big = fmaxf(fabsf(x[0]), fabsf(x[1]));
 #pragma unroll
         for (int i = 2; i < 64; i += 2) big = fmax3(big, fabsf(x[i]), fabsf(x[i + 1]));
         big *= fabsf(p.cap_in);
-        const float k2 = p.cap_in * p.cap_in;
-        if (__all_sync(0xffffffffu, big <= p.cap_near)) {
-            const float r0 = p.scale_log2 * kTanh3[0], r1 = p.scale_log2 * kTanh3[1] * k2;
-            const float r2 = p.scale_log2 * kTanh3[2] * k2 * k2;
-            const F32x2 c0 = pack_f32(r0, r0), c1 = pack_f32(r1, r1), c2 = pack_f32(r2, r2);
-#pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-                const F32x2 v = pack_f32(x[i], x[i + 1]);
-                const F32x2 u = mul2(v, v);
-                unpack_f32(mul2(v, fma2(u, fma2(u, c2, c1), c0)), x[i], x[i + 1]);
-            }
+        if (__all_sync(0xffffffffu, big <= 0.25f && p.cap_short)) {
+            cap_poly<3>(p, kTanh3, x);
+        } else if (__all_sync(0xffffffffu, big <= 0.45f && p.cap_short)) {
+            cap_poly<4>(p, kTanh4, x);
         } else if (__all_sync(0xffffffffu, big <= 0.75f)) {
-            float r[6], k = p.scale_log2;
-            F32x2 c[6];
-#pragma unroll
-            for (int j = 0; j < 6; ++j, k *= k2) {
-                r[j] = k * kTanh6[j];
-                c[j] = pack_f32(r[j], r[j]);
-            }
-#pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-                const F32x2 v = pack_f32(x[i], x[i + 1]);
-                const F32x2 u = mul2(v, v);
-                F32x2 q = fma2(u, c[5], c[4]);
-#pragma unroll
-                for (int j = 3; j >= 0; --j) q = fma2(u, q, c[j]);
-                unpack_f32(mul2(v, q), x[i], x[i + 1]);
-            }
+            cap_poly<6>(p, kTanh6, x);
         } else {
             const float k = p.cap_in * 2.885390081777927f;  // 2 log2(e) / cap
 #pragma unroll
             for (int i = 0; i < 64; ++i) x[i] = p.cap_out - 2.f * p.cap_out * fast_rcp(1.f + fast_exp2(x[i] * k));
         }
-        if (!p.slopes) return;
+        if (!p.slopes) return 1.f;
+    } else if (!p.slopes && p.scale_log2 > 0.f) {
+        return p.scale_log2;  // (a negative scale would turn maxima into minima: applied below)
     }
     // bias: a pair of columns after the other adds two slopes; started afresh every 16
     // columns, so that the sum's rounding stays within a few steps
@@ -417,6 +481,7 @@ __device__ __forceinline__ void score_row(const PrefillParams &p, float (&x)[64]
         unpack_f32(fma2(pack_f32(x[i], x[i + 1]), f, bias), x[i], x[i + 1]);
         bias = add2(bias, step);
     }
+    return 1.f;
 }
 
 // kScored: scores capped, biased and masked to an interval of tokens per row; a form of
@@ -513,6 +578,12 @@ __global__ void __launch_bounds__(384, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    constexpr bool kPlanned = ORDER == kOrderPlanned;
+    int num_items = p.num_items;
+    if constexpr (kPlanned) {
+        pdl_wait();  // for the item table, written by the kernel before this one
+        num_items = p.plan->entries * p.num_kv_heads;
+    }
 
     if (warp == 0 || warp == 10) {
         // ===================== TMA producers: K (warp 0), V (warp 10) =====================
@@ -533,9 +604,16 @@ __global__ void __launch_bounds__(384, 1)
         int q_issue[2] = {-1, -1};
         bool ok = true;
         int jt = 0, n = 0;  // tiles and items so far
-        for (int ki = 0, item = prefill_slot_item<ORDER>(p, 0); item < p.num_items && ok; item = prefill_slot_item<ORDER>(p, ++ki)) {
+        PrefillEntry ahead{};  // planned order: the next item's entry
+        if constexpr (kPlanned) ahead = load_entry(p, prefill_slot_item<ORDER>(p, 0), num_items);
+        for (int ki = 0, item = prefill_slot_item<ORDER>(p, 0); item < num_items && ok; item = prefill_slot_item<ORDER>(p, ++ki)) {
             PrefillItem it;
-            if (!prefill_item<ORDER, kScored>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), kv == 0, it, by_len)) continue;
+            if constexpr (kPlanned) {
+                planned_item(p, item, ahead, it);
+                ahead = load_entry(p, prefill_slot_item<ORDER>(p, ki + 1), num_items);
+            } else if (!prefill_item<ORDER, kScored>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), kv == 0, it, by_len)) {
+                continue;
+            }
             const int32_t *trow = p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks_per_seq;
             auto entry = [&](int j) -> int {  // this lane's block of tile j (-1: none or bad)
                 const int t0 = it.tok_lo + j * TILE;
@@ -571,6 +649,16 @@ __global__ void __launch_bounds__(384, 1)
                 // the next item's Q box into L2 now, so its load does not wait for HBM (lane 0
                 // alone: the scored form's token range, a warp's work, is not needed for it)
                 PrefillItem nx;
+                if constexpr (kPlanned) {
+                    const int i2 = prefill_slot_item<ORDER>(p, ki + 1);
+                    if (i2 < num_items) {
+                        planned_item(p, i2, ahead, nx);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            tc::tma_prefetch_3d(&tmap_q, c * 64, nx.kvh * p.group, nx.q0 + nx.row_tile * p.tile_tokens);
+                    }
+                    return;
+                }
                 for (int k2 = ki + 1, i2 = prefill_slot_item<ORDER>(p, k2); i2 < p.num_items; i2 = prefill_slot_item<ORDER>(p, ++k2)) {
                     if (!prefill_item<ORDER>(p, i2, prefill_seq_vals<ORDER>(p, i2, by_len), false, nx, by_len)) continue;
 #pragma unroll
@@ -649,9 +737,16 @@ __global__ void __launch_bounds__(384, 1)
         constexpr uint32_t idesc_qk = tc::idesc_f16_f32acc(kBF16, 128, 128, false, false);
         bool ok = true;
         int jt = 0, n = 0;
-        for (int ki = 0, item = prefill_slot_item<ORDER>(p, 0); item < p.num_items && ok; item = prefill_slot_item<ORDER>(p, ++ki)) {
+        PrefillEntry ahead{};  // planned order: the next item's entry
+        if constexpr (kPlanned) ahead = load_entry(p, prefill_slot_item<ORDER>(p, 0), num_items);
+        for (int ki = 0, item = prefill_slot_item<ORDER>(p, 0); item < num_items && ok; item = prefill_slot_item<ORDER>(p, ++ki)) {
             PrefillItem it;
-            if (!prefill_item<ORDER, kScored>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) continue;
+            if constexpr (kPlanned) {
+                planned_item(p, item, ahead, it);
+                ahead = load_entry(p, prefill_slot_item<ORDER>(p, ki + 1), num_items);
+            } else if (!prefill_item<ORDER, kScored>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) {
+                continue;
+            }
             const int qb = n % QB;
             int go = 1;
             if (lane == 0) go = tc_wait(&q_full[qb], (n / QB) & 1, abort_flag, p.status);
@@ -694,9 +789,16 @@ __global__ void __launch_bounds__(384, 1)
         constexpr uint32_t idesc_pv = tc::idesc_f16_f32acc(kBF16, 128, 128, false, true);
         bool ok = true;
         int jt = 0, n_staged = 0;
-        for (int ki = 0, item = prefill_slot_item<ORDER>(p, 0); item < p.num_items && ok; item = prefill_slot_item<ORDER>(p, ++ki)) {
+        PrefillEntry ahead{};  // planned order: the next item's entry
+        if constexpr (kPlanned) ahead = load_entry(p, prefill_slot_item<ORDER>(p, 0), num_items);
+        for (int ki = 0, item = prefill_slot_item<ORDER>(p, 0); item < num_items && ok; item = prefill_slot_item<ORDER>(p, ++ki)) {
             PrefillItem it;
-            if (!prefill_item<ORDER, kScored>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) continue;
+            if constexpr (kPlanned) {
+                planned_item(p, item, ahead, it);
+                ahead = load_entry(p, prefill_slot_item<ORDER>(p, ki + 1), num_items);
+            } else if (!prefill_item<ORDER, kScored>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) {
+                continue;
+            }
             const bool staged = prefill_staged(p, it);
             for (int j = 0; j < it.ntiles; ++j, ++jt) {
                 int go = 1;
@@ -802,24 +904,31 @@ __global__ void __launch_bounds__(384, 1)
             other = sum_x[(1 - half) * 128 + r];
             return true;
         };
-        for (int ki = 0, item = prefill_slot_item<ORDER>(p, 0); item < p.num_items && ok; item = prefill_slot_item<ORDER>(p, ++ki)) {
+        PrefillRow view{0, 0, 0.f};
+        PrefillEntry ahead{};  // planned order: the next item's entry
+        if constexpr (kPlanned) ahead = load_entry(p, prefill_slot_item<ORDER>(p, 0), num_items);
+        if constexpr (kPlanned) {
+            if (prefill_slot_item<ORDER>(p, 0) < num_items) {
+                PrefillItem first;
+                planned_item(p, prefill_slot_item<ORDER>(p, 0), ahead, first);
+                view = prefill_row(p, first, r);
+            }
+        }
+        for (int ki = 0, item = prefill_slot_item<ORDER>(p, 0); item < num_items && ok; item = prefill_slot_item<ORDER>(p, ++ki)) {
             PrefillItem it;
-            if (!prefill_item<ORDER, kScored>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) continue;
+            if constexpr (kPlanned) {
+                planned_item(p, item, ahead, it);
+                ahead = load_entry(p, prefill_slot_item<ORDER>(p, ki + 1), num_items);
+            } else if (!prefill_item<ORDER, kScored>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) {
+                continue;
+            }
             const int row = it.row0 + r;
             const bool live = r < R && row < it.rows;
             const int jtok = live ? fast_div(row, p.div_group) : 0;
             const int pos = it.base_pos + jtok;  // this row sees tokens 0 .. pos
-            int row_lo = 0, row_hi = 0;          // ... in the scored form [row_lo, row_hi)
-            float slope2 = 0.f;                  // and its bias per token, in log2 units
-            if constexpr (kScored) {
-                if (live) {
-                    row_lo = p.window > 0 ? max(0, pos + 1 - p.window) : 0;
-                    if (p.starts) row_lo = max(row_lo, p.starts[it.q0 + jtok]);
-                    row_hi = pos + 1;
-                    if (p.prefix_lens) row_hi = max(row_hi, min(it.len, p.prefix_lens[it.seq]));
-                    if (p.slopes) slope2 = p.slopes[it.kvh * p.group + row - jtok * p.group] * 1.4426950408889634f;
-                }
-            }
+            if constexpr (kScored && !kPlanned) view = prefill_row(p, it, r);
+            const int row_lo = view.lo, row_hi = view.hi;  // ... in the scored form [row_lo, row_hi)
+            const float slope2 = view.slope2;
             // Scored form, bf16, capped and not biased: |score| <= cap_out, so 0 serves as every
             // row's reference: bf16 and fp32 hold 2^-80 .. 2^80 as exactly as 1 (fp16 does not),
             // and the maximum, its exchange between the two warps and the rescaling fall away
@@ -848,10 +957,10 @@ __global__ void __launch_bounds__(384, 1)
                 const bool full = __all_sync(0xffffffffu, kScored ? clo == 0 && chi == 64 : vr == TILE);
                 // partial maximum of the visible scaled scores: the extreme raw score times
                 // the scale (the maximum for a positive scale, the minimum otherwise)
-                float pmax = -INFINITY;
+                float pmax = -INFINITY, factor = 1.f;
                 if constexpr (kScored) {
                     // the scores themselves replace the raw ones: capped, biased, masked to -inf
-                    score_row(p, x, slope2, t0 + c0 - pos);
+                    factor = score_row(p, x, slope2, t0 + c0 - pos);
                     if (!full) {
 #pragma unroll
                         for (int i = 0; i < 64; ++i) x[i] = i >= clo && i < chi ? x[i] : -INFINITY;
@@ -860,6 +969,7 @@ __global__ void __launch_bounds__(384, 1)
                         pmax = fmaxf(x[0], x[63]);
 #pragma unroll
                         for (int i = 1; i + 1 < 63; i += 2) pmax = fmax3(pmax, x[i], x[i + 1]);
+                        pmax *= factor;
                     }
                 } else if (vh > 0) {
                     const bool pos_scale = p.scale_log2 > 0.f;
@@ -928,7 +1038,7 @@ __global__ void __launch_bounds__(384, 1)
                 float l0 = 0.f, l1 = 0.f;
                 // scored: a masked -inf gets weight 0, and a row that has seen nothing yet subtracts 0
                 const float m_sub = kScored && m_ref == -INFINITY ? 0.f : m_ref;
-                const F32x2 minus_m = pack_f32(-m_sub, -m_sub);
+                const F32x2 minus_m = pack_f32(-m_sub, -m_sub), factor2 = pack_f32(factor, factor);
                 // two copies of the loop, so fully visible tiles carry no per-column mask
                 auto weights = [&](auto masked, auto shifted) {
 #pragma unroll
@@ -940,7 +1050,7 @@ __global__ void __launch_bounds__(384, 1)
                             // s * scale - m for two columns in one packed FMA
                             float e0 = -m_sub, e1 = -m_sub;
                             if constexpr (!decltype(shifted)::value) e0 = x[t], e1 = x[t + 1];
-                            else if constexpr (kScored) unpack_f32(add2(pack_f32(x[t], x[t + 1]), minus_m), e0, e1);
+                            else if constexpr (kScored) unpack_f32(fma2(pack_f32(x[t], x[t + 1]), factor2, minus_m), e0, e1);
                             else fma_f32x2(e0, e1, x[t], x[t + 1], p.scale_log2, p.scale_log2);
                             float p0 = fast_exp2(e0);
                             float p1 = fast_exp2(e1);
@@ -983,6 +1093,15 @@ __global__ void __launch_bounds__(384, 1)
                 fence_proxy_async_smem();  // zeroed V rows visible to the MMA
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[b]);
+            }
+            if constexpr (kPlanned) {
+                // the next item's row, on its way while this one is written out
+                const int i2 = prefill_slot_item<ORDER>(p, ki + 1);
+                if (i2 < num_items) {
+                    PrefillItem nx;
+                    planned_item(p, i2, ahead, nx);
+                    view = prefill_row(p, nx, r);
+                }
             }
             // the pair's row sum, then this half of the O row -> out (one split) or its
             // partial slot.  TMEM loads are warp-wide: every lane loads, only live rows store.
@@ -1058,6 +1177,92 @@ __global__ void __launch_bounds__(384, 1)
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, L::kTmemCols);
     }
+}
+
+// The item table of the planned order: one entry per row tile that holds work, sorted by
+// KV tiles, most first (a counting sort; the order among equals is free).  One block: a
+// row tile's first visible token is the minimum over its rows' starts, gathered row by
+// row in shared memory.  A sequence out of contract is flagged and gets no entry.
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanBuckets = 1024;
+inline __global__ void __launch_bounds__(kPlanThreads) paged_prefill_plan_kernel(const PrefillParams p, PrefillPlan *plan) {
+    __shared__ int first[kMaxPlanEntries];
+    __shared__ int bucket[kPlanBuckets];
+    __shared__ int warp_sum[kPlanThreads / 32];
+    __shared__ int total;
+    pdl_trigger();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int count = p.num_seqs * p.row_tiles;  // <= kMaxPlanEntries
+    for (int e = tid; e < count; e += kPlanThreads) first[e] = p.starts ? 0x7fffffff : 0;
+    bucket[tid] = 0;
+    __syncthreads();
+    if (p.starts) {
+        for (int row = tid; row < p.num_rows; row += kPlanThreads) {
+            int a = 0, b = p.num_seqs - 1;  // the last sequence whose chunk starts at or before the row
+            while (a < b) {
+                const int m = (a + b + 1) / 2;
+                if (p.query_start[m] <= row) a = m;
+                else b = m - 1;
+            }
+            const int j = row - p.query_start[a];
+            if (j >= 0 && row < p.query_start[a + 1] && j < p.qlen_cap)
+                atomicMin(&first[a * p.row_tiles + j / p.tile_tokens], p.starts[row]);
+        }
+        __syncthreads();
+    }
+    // entry e of this thread: its range, and its bucket by KV tiles
+    const auto make = [&](int e, PrefillEntry &v) -> int {  // KV tiles, or -1: no entry
+        const int seq = e / p.row_tiles, rt = e - seq * p.row_tiles;
+        const PrefillSeqVals sv{p.query_start[seq], p.query_start[seq + 1], p.context_lens[seq]};
+        int q0, chunk, len;
+        if (!prefill_seq(p, sv, q0, chunk, len)) return -1;
+        const int j0 = rt * p.tile_tokens, j1 = min(chunk, j0 + p.tile_tokens) - 1;
+        if (j0 >= chunk) return -1;
+        const int base_pos = len - chunk;
+        int lo = max(p.window > 0 ? max(0, base_pos + j0 + 1 - p.window) : 0, first[e]);
+        int hi = base_pos + j1 + 1;
+        if (p.prefix_lens) hi = max(hi, min(len, p.prefix_lens[seq]));
+        if (lo >= hi) lo = hi;
+        const int begin = lo == hi ? hi : lo & ~(p.block_size - 1);
+        v = PrefillEntry{q0, chunk, len, seq, rt, lo, begin, hi};
+        return max(1, (hi - begin + 127) / 128);
+    };
+    PrefillEntry v{};
+    for (int e = tid; e < count; e += kPlanThreads) {
+        const int seq = e / p.row_tiles;
+        const int n = make(e, v);
+        if (n > 0) {
+            atomicAdd(&bucket[max(0, kPlanBuckets - n)], 1);  // bucket 0: the most tiles
+        } else if (e == seq * p.row_tiles) {
+            const PrefillSeqVals sv{p.query_start[seq], p.query_start[seq + 1], p.context_lens[seq]};
+            int q0, chunk, len;
+            if (!prefill_seq(p, sv, q0, chunk, len)) raise_flag(p.status, PKV_DEVERR_CONTEXT_LEN);
+        }
+    }
+    __syncthreads();
+    // exclusive prefix over the buckets, one per thread
+    const int mine = bucket[tid];
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int before = incl - mine;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    bucket[tid] = before;
+    if (tid == kPlanThreads - 1) total = before + mine;
+    __syncthreads();
+    for (int e = tid; e < count; e += kPlanThreads) {
+        const int n = make(e, v);
+        if (n <= 0) continue;
+        int4 *dst = reinterpret_cast<int4 *>(plan->entry + atomicAdd(&bucket[max(0, kPlanBuckets - n)], 1));
+        dst[0] = make_int4(v.q0, v.chunk, v.len, v.seq);
+        dst[1] = make_int4(v.row_tile, v.lo, v.tok_lo, v.tok_hi);
+    }
+    if (tid == 0) plan->entries = total;
 }
 
 // Log-sum-exp merge of a prefill's KV splits: one warp per (chunk row, query

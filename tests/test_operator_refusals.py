@@ -117,7 +117,8 @@ def test_scored_prefill_refusals(lib):
         assert call(**kw) == INVALID, kw
     size = lib.pkv_prefill_scored_workspace_bytes
     assert size(10, 2, 4, 4, 128, 16, 10, 1000, 0, 0, 2) == 10 * 4 * 2 * 130 * 4
-    assert size(10, 2, 4, 4, 128, 16, 10, 1000, 0, 0, 1) == 0
+    assert size(10, 2, 4, 4, 128, 16, 10, 1000, 0, 0, 1) == 16 + 2 * 32          # an item table of one row tile a sequence
+    assert size(10 ** 6, 100, 4, 4, 128, 16, 10000, 10000, 0, 0, 1) == 0         # too many row tiles for a table
     assert size(10, 2, 4, 4, 128, 16, 10, 1000, 100, 0, 8) == 10 * 4 * 2 * 130 * 4   # 100 + 127 + 15 tokens: two tiles
     assert size(10, 2, 4, 4, 128, 16, 10, 1000, 100, 1, 8) == 10 * 4 * 8 * 130 * 4
     assert size(10, 2, 4, 4, 128, 16, 10, 1000, -1, 0, 1) == 2 ** 64 - 1
