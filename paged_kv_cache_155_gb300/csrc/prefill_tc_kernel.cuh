@@ -418,6 +418,9 @@ __device__ constexpr float kTanh4[4] = {0.9999997615814209f, -0.3332949280738830
                                         -0.046039558947086334f};
 __device__ constexpr float kTanh3[3] = {0.9999995827674866f, -0.3332192897796631f, 0.12841935455799103f};
 
+// The lowest n bits of a word (n <= 0: none, n >= 32: all).
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
 // x <- x R(x^2), R of N terms whose coefficients are scaled to give scale_log2 x at small x.
 template <int N>
 __device__ __forceinline__ void cap_poly(const PrefillParams &p, const float (&terms)[N], float (&x)[64]) {
@@ -962,8 +965,10 @@ __global__ void __launch_bounds__(384, 1)
                     // the scores themselves replace the raw ones: capped, biased, masked to -inf
                     factor = score_row(p, x, slope2, t0 + c0 - pos);
                     if (!full) {
+                        // one bit per column: a select and a bit test each
+                        const uint32_t seen[2] = {below(chi) & ~below(clo), below(chi - 32) & ~below(clo - 32)};
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) x[i] = i >= clo && i < chi ? x[i] : -INFINITY;
+                        for (int i = 0; i < 64; ++i) x[i] = (seen[i / 32] >> (i % 32)) & 1u ? x[i] : -INFINITY;
                     }
                     if (!fixed_ref) {
                         pmax = fmaxf(x[0], x[63]);
