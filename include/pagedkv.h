@@ -424,7 +424,7 @@ PKV_API pkv_status pkv_paged_attention_decode_scored_int8(
  *   context_lens   [num_seqs] int32, device; max_context_len bounds them on
  *                  the host (a value outside raises PKV_DEVERR_CONTEXT_LEN and
  *                  is clamped) and must not exceed weights_stride.
- *   sinks + recent <= budget, budget > 0.
+ *   sinks + recent <= budget, 0 < budget <= 2^30, max_context_len <= 2^30.
  *   weights_out    NULL, or a buffer of the same shape that gets the kept
  *                  tokens' weights in their new places [0, n) and zeros in
  *                  [n, L); the rest of a row is left as it is.  May be

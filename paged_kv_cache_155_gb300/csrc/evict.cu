@@ -33,6 +33,8 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+constexpr int kMaxTokens = 1 << 30;  // of a context or a budget: indices a step past it still fit 32 bits
+
 // ------------------------------------------------------------------ select
 // Order-preserving map of a weight to an unsigned key: larger weight, larger key;
 // -0 equals +0; NaN sorts lowest.  Key 0 is NaN's alone.
@@ -357,7 +359,8 @@ PKV_API pkv_status pkv_evict_select(const float *weights, int64_t weights_stride
                                     int recent, float *weights_out, int32_t *kept, int32_t *kept_lens,
                                     void *stream) {
     if (num_seqs < 0 || num_seqs > 65535 || num_kv_heads <= 0 || num_kv_heads > 65535 || max_context_len < 0 || budget <= 0 || sinks < 0 ||
-        recent < 0 || static_cast<int64_t>(sinks) + recent > budget || weights_stride < max_context_len)
+        recent < 0 || static_cast<int64_t>(sinks) + recent > budget || weights_stride < max_context_len ||
+        max_context_len > kMaxTokens || budget > kMaxTokens)
         return PKV_ERR_INVALID_ARG;
     if (num_seqs == 0) return PKV_OK;
     const auto bad = [](const void *q) { return !q || (reinterpret_cast<uintptr_t>(q) & 3u); };
@@ -399,7 +402,7 @@ PKV_API pkv_status pkv_evict_compact(void *k_cache, void *v_cache, int64_t num_b
     if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
     if (block_size != 8 && block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
     if (num_seqs < 0 || num_seqs > 65535 || num_kv_heads <= 0 || num_kv_heads > 65535 || num_blocks <= 0 ||
-        max_blocks_per_seq <= 0 || budget <= 0 || (dst_block_tables && dst_max_blocks_per_seq <= 0))
+        max_blocks_per_seq <= 0 || budget <= 0 || budget > kMaxTokens || (dst_block_tables && dst_max_blocks_per_seq <= 0))
         return PKV_ERR_INVALID_ARG;
     const int elem_bytes = dtype == PKV_INT8 ? 1 : 2;
     const int64_t half_elems = static_cast<int64_t>(num_kv_heads) * block_size * head_dim;

@@ -9,7 +9,7 @@
 
 namespace pkv {
 
-template <typename T, int BS, int ORDER, bool kScored>
+template <typename T, int BS, int ORDER, int kForm>
 pkv_status launch_prefill_one(const PrefillParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
                               const CUtensorMap &tv, const CUtensorMap &to, int grid, cudaStream_t stream) {
     static std::atomic<uint64_t> configured_devices{0};
@@ -17,14 +17,14 @@ pkv_status launch_prefill_one(const PrefillParams &p, const CUtensorMap &tq, con
     if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
     if (!bit || !(configured_devices.load(std::memory_order_acquire) & bit)) {
-        if (cudaFuncSetAttribute(paged_prefill_tc_kernel<T, BS, ORDER, kScored>,
+        if (cudaFuncSetAttribute(paged_prefill_tc_kernel<T, BS, ORDER, kForm>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  PrefillLayout::kSmemBytes) != cudaSuccess)
             return PKV_ERR_CUDA;
         configured_devices.fetch_or(bit, std::memory_order_acq_rel);
     }
     // planned order: placed while the plan kernel before it still runs
-    if (launch_kernel(paged_prefill_tc_kernel<T, BS, ORDER, kScored>, dim3(grid), dim3(PrefillLayout::kThreads),
+    if (launch_kernel(paged_prefill_tc_kernel<T, BS, ORDER, kForm>, dim3(grid), dim3(PrefillLayout::kThreads),
                       PrefillLayout::kSmemBytes, stream, ORDER == kOrderPlanned, tq, tk, tv, to, p) != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
@@ -37,13 +37,21 @@ template <typename T, int BS, bool kScored>
 pkv_status launch_prefill_bs(const PrefillParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
                              const CUtensorMap &tv, const CUtensorMap &to, int grid, cudaStream_t s) {
     if constexpr (kScored) {
-        if (p.order == kOrderPlanned) return launch_prefill_one<T, BS, kOrderPlanned, true>(p, tq, tk, tv, to, grid, s);
-        return launch_prefill_one<T, BS, kOrderRowTiles, true>(p, tq, tk, tv, to, grid, s);
+        if constexpr (!std::is_same<T, __half>::value) {
+            if (p.shift > 0.f)
+                return p.order == kOrderPlanned ? launch_prefill_one<T, BS, kOrderPlanned, kFixedForm>(p, tq, tk, tv, to, grid, s)
+                                                : launch_prefill_one<T, BS, kOrderRowTiles, kFixedForm>(p, tq, tk, tv, to, grid, s);
+        }
+        if (p.cap_out == 0.f)
+            return p.order == kOrderPlanned ? launch_prefill_one<T, BS, kOrderPlanned, kUncappedForm>(p, tq, tk, tv, to, grid, s)
+                                            : launch_prefill_one<T, BS, kOrderRowTiles, kUncappedForm>(p, tq, tk, tv, to, grid, s);
+        return p.order == kOrderPlanned ? launch_prefill_one<T, BS, kOrderPlanned, kScoredForm>(p, tq, tk, tv, to, grid, s)
+                                        : launch_prefill_one<T, BS, kOrderRowTiles, kScoredForm>(p, tq, tk, tv, to, grid, s);
     }
     else if (p.order == kOrderSortedGroups)
-        return launch_prefill_one<T, BS, kOrderSortedGroups, false>(p, tq, tk, tv, to, grid, s);
-    else if (p.order == kOrderPairs) return launch_prefill_one<T, BS, kOrderPairs, false>(p, tq, tk, tv, to, grid, s);
-    else return launch_prefill_one<T, BS, kOrderRowTiles, false>(p, tq, tk, tv, to, grid, s);
+        return launch_prefill_one<T, BS, kOrderSortedGroups, kPlainForm>(p, tq, tk, tv, to, grid, s);
+    else if (p.order == kOrderPairs) return launch_prefill_one<T, BS, kOrderPairs, kPlainForm>(p, tq, tk, tv, to, grid, s);
+    else return launch_prefill_one<T, BS, kOrderRowTiles, kPlainForm>(p, tq, tk, tv, to, grid, s);
 }
 
 template <typename T, bool kScored = false>

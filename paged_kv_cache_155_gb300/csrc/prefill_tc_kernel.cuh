@@ -112,9 +112,11 @@ struct PrefillParams {
     float cap_out;               // softcap * log2(e), 0: scores are not capped
     int cap_short;               // the cap is small enough for the short polynomials
     const struct PrefillPlan *plan;  // the item table (planned order)
-    int fixed_ref;               // |score| <= cap_out <= kFixedRefMax and no bias: see the softmax warps
+    float shift;                 // fixed form: every row's reference, cap_out / 2; else 0
 };
 constexpr float kFixedRefMax = 80.f;
+// see paged_prefill_tc_kernel
+constexpr int kPlainForm = 0, kScoredForm = 1, kFixedForm = 2, kUncappedForm = 3;
 
 // Item orders (PrefillParams::order), see prefill_item.
 constexpr int kOrderRowTiles = 0, kOrderPairs = 1, kOrderSortedGroups = 2, kOrderPlanned = 3;
@@ -421,11 +423,13 @@ __device__ constexpr float kTanh3[3] = {0.9999995827674866f, -0.3332192897796631
 // The lowest n bits of a word (n <= 0: none, n >= 32: all).
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
-// x <- x R(x^2), R of N terms whose coefficients are scaled to give scale_log2 x at small x.
+// x <- x R(x^2) - shift, R of N terms whose coefficients are scaled to give scale_log2 x at
+// small x.
 template <int N>
 __device__ __forceinline__ void cap_poly(const PrefillParams &p, const float (&terms)[N], float (&x)[64]) {
     const float k2 = p.cap_in * p.cap_in;
     float k = p.scale_log2;
+    const F32x2 shift = pack_f32(-p.shift, -p.shift);
     F32x2 c[N];
 #pragma unroll
     for (int j = 0; j < N; ++j, k *= k2) c[j] = pack_f32(k * terms[j], k * terms[j]);
@@ -436,44 +440,60 @@ __device__ __forceinline__ void cap_poly(const PrefillParams &p, const float (&t
         F32x2 q = fma2(u, c[N - 1], c[N - 2]);
 #pragma unroll
         for (int j = N - 3; j >= 0; --j) q = fma2(u, q, c[j]);
-        unpack_f32(mul2(v, q), x[i], x[i + 1]);
+        unpack_f32(fma2(v, q, shift), x[i], x[i + 1]);
     }
+}
+
+// Raw scores of a row -> capped scores in log2 units, less the fixed reference (p.shift,
+// else 0): cap * tanh(s / cap) with s = scale * x is x R(x^2), R a polynomial of tanh(z)/z
+// whose coefficients are scaled to take x itself: no exponential, where the softmax
+// already spends one.  A warp takes a short R when its scores stay far below the cap (and
+// the cap is small enough for that fit's error to stay below 2.5e-5 of a score), the
+// six-term one within three quarters, and beyond that the closed form
+// cap (1 - 2 / (1 + e^(2 z))), an exponential and a reciprocal more.  The choice looks at
+// every column: those without a token hold 0 (the QK^T issuer zeroes their K rows), not
+// what an earlier tile left there, or the last bits of a result would depend on it.
+__device__ __forceinline__ void cap_scores(const PrefillParams &p, float (&x)[64]) {
+    float big = fmaxf(fabsf(x[0]), fabsf(x[1]));
+#pragma unroll
+    for (int i = 2; i < 64; i += 2) big = fmax3(big, fabsf(x[i]), fabsf(x[i + 1]));
+    big *= fabsf(p.cap_in);
+    if (__all_sync(0xffffffffu, big <= 0.25f && p.cap_short)) {
+        cap_poly<3>(p, kTanh3, x);
+    } else if (__all_sync(0xffffffffu, big <= 0.45f && p.cap_short)) {
+        cap_poly<4>(p, kTanh4, x);
+    } else if (__all_sync(0xffffffffu, big <= 0.75f)) {
+        cap_poly<6>(p, kTanh6, x);
+    } else {
+        const float k = p.cap_in * 2.885390081777927f;  // 2 log2(e) / cap
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+            x[i] = (p.cap_out - p.shift) - 2.f * p.cap_out * fast_rcp(1.f + fast_exp2(x[i] * k));
+    }
+}
+
+// Columns of a row that it does not see (no bit in seen0 / seen1) -> -inf: a select and a bit
+// test each.
+__device__ __forceinline__ void hide(float (&x)[64], uint32_t seen0, uint32_t seen1) {
+#pragma unroll
+    for (int i = 0; i < 64; ++i) x[i] = ((i < 32 ? seen0 : seen1) >> (i % 32)) & 1u ? x[i] : -INFINITY;
 }
 
 // Scored form: 64 raw scores of a row (columns dist0, dist0 + 1, ... from the query's
 // position) -> scores in log2 units, capped and biased; returns the factor that is left
 // to apply (scale_log2, when neither is asked for; else 1).
-// Cap: cap * tanh(s / cap) with s = scale * x is x R(x^2), R a polynomial of tanh(z)/z
-// whose coefficients are scaled to take x itself: no exponential, where the softmax
-// already spends one.  A warp takes a short R when its scores stay far below the cap (and
-// the cap is small enough for that fit's error to stay below 2.5e-5 of a score), the
-// six-term one within three quarters, and beyond that the closed form
-// cap (1 - 2 / (1 + e^(2 z))), an exponential and a reciprocal more.
+template <bool kCapped>
 __device__ __forceinline__ float score_row(const PrefillParams &p, float (&x)[64], float slope2, int dist0) {
-    if (p.cap_out > 0.f) {
-        float big = fmaxf(fabsf(x[0]), fabsf(x[1]));
-#pragma unroll
-        for (int i = 2; i < 64; i += 2) big = fmax3(big, fabsf(x[i]), fabsf(x[i + 1]));
-        big *= fabsf(p.cap_in);
-        if (__all_sync(0xffffffffu, big <= 0.25f && p.cap_short)) {
-            cap_poly<3>(p, kTanh3, x);
-        } else if (__all_sync(0xffffffffu, big <= 0.45f && p.cap_short)) {
-            cap_poly<4>(p, kTanh4, x);
-        } else if (__all_sync(0xffffffffu, big <= 0.75f)) {
-            cap_poly<6>(p, kTanh6, x);
-        } else {
-            const float k = p.cap_in * 2.885390081777927f;  // 2 log2(e) / cap
-#pragma unroll
-            for (int i = 0; i < 64; ++i) x[i] = p.cap_out - 2.f * p.cap_out * fast_rcp(1.f + fast_exp2(x[i] * k));
-        }
+    if constexpr (kCapped) {
+        cap_scores(p, x);
         if (!p.slopes) return 1.f;
-    } else if (!p.slopes && p.scale_log2 > 0.f) {
-        return p.scale_log2;  // (a negative scale would turn maxima into minima: applied below)
+    } else {
+        if (!p.slopes && p.scale_log2 > 0.f) return p.scale_log2;  // (a negative scale would turn maxima into minima)
     }
     // bias: a pair of columns after the other adds two slopes; started afresh every 16
     // columns, so that the sum's rounding stays within a few steps
-    const F32x2 one = pack_f32(1.f, 1.f), scale = pack_f32(p.scale_log2, p.scale_log2);
-    const F32x2 f = p.cap_out > 0.f ? one : scale, step = pack_f32(2.f * slope2, 2.f * slope2);
+    const float by = kCapped ? 1.f : p.scale_log2;
+    const F32x2 f = pack_f32(by, by), step = pack_f32(2.f * slope2, 2.f * slope2);
     F32x2 bias = 0ull;
 #pragma unroll
     for (int i = 0; i < 64; i += 2) {
@@ -487,9 +507,14 @@ __device__ __forceinline__ float score_row(const PrefillParams &p, float (&x)[64
     return 1.f;
 }
 
-// kScored: scores capped, biased and masked to an interval of tokens per row; a form of
-// its own, so that the plain one carries none of it.
-template <typename T, int BS, int ORDER, bool kScored = false>
+// kForm: the plain softmax; the scored one (scores capped, biased and masked to an interval
+// of tokens per row); the same without a cap; or the scored one of capped bf16 scores without a bias and with
+// cap_out <= kFixedRefMax, whose rows need no maximum.  There |score| <= cap_out, so
+// cap_out / 2 serves as every row's reference: the weights lie in 2^-120 .. 2^40, which
+// bf16 and fp32 hold as exactly as 1 (fp16 does not), and the maximum, its exchange between
+// the two warps and the rescaling fall away.  Each form is compiled apart: the softmax loop
+// fills the register file, and code that a form does not run would slow it.
+template <typename T, int BS, int ORDER, int kForm = kPlainForm>
 __global__ void __launch_bounds__(384, 1)
     paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                             const __grid_constant__ CUtensorMap tmap_k,
@@ -498,6 +523,9 @@ __global__ void __launch_bounds__(384, 1)
     using L = PrefillLayout;
     constexpr int TILE = L::kTile, D = 128;
     constexpr bool kBF16 = !std::is_same<T, __half>::value;
+    constexpr bool kScored = kForm != kPlainForm, kFixed = kForm == kFixedForm;
+    constexpr bool kCapped = kForm == kScoredForm || kFixed;
+    static_assert(!kFixed || kBF16, "the fixed reference needs bf16's range");
     static_assert(TILE / BS <= 32, "one table entry per producer lane");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -762,6 +790,21 @@ __global__ void __launch_bounds__(384, 1)
                     ok = false;
                     break;
                 }
+                if constexpr (kCapped) {
+                    // K rows past the tile's tokens -> 0, so that their scores are 0 (cap_scores);
+                    // here, where S buffers wait filled, rather than in the softmax warps (15 us of
+                    // 263 on 17-tile items there)
+                    const int valid = it.tok_hi - (it.tok_lo + j * TILE);
+                    if (valid < TILE) {
+                        __syncwarp();
+                        unsigned char *slot = sm + L::kOffK + (jt % KS) * L::kPanel;
+                        for (int i = valid * 16 + lane; i < TILE * 16; i += 32)
+                            *reinterpret_cast<uint4 *>(slot + ((i >> 3) & 1) * L::kHalf + (i >> 4) * 128 + (i & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();  // visible to the MMA
+                        __syncwarp();
+                    }
+                }
                 if (lane == 0) {
                     const int b = jt % SB;
                     tc::fence_after_sync();
@@ -881,7 +924,7 @@ __global__ void __launch_bounds__(384, 1)
         // through shared memory; a slot is rewritten only after the next tile's
         // exchange, which the partner reaches after reading it.
         // Scored form: half 1 keeps its P in its own columns, 64 .. 95, and exchanges through
-        // column 96, so that a tile without an exchange (fixed_ref below) needs no order
+        // column 96, so that a tile without an exchange (the fixed form) needs no order
         // between the two warps.
         constexpr int kX1 = kScored ? 96 : 64;  // half 1's exchange column
         auto pair_sync = [&](int step) -> bool {
@@ -932,11 +975,7 @@ __global__ void __launch_bounds__(384, 1)
             if constexpr (kScored && !kPlanned) view = prefill_row(p, it, r);
             const int row_lo = view.lo, row_hi = view.hi;  // ... in the scored form [row_lo, row_hi)
             const float slope2 = view.slope2;
-            // Scored form, bf16, capped and not biased: |score| <= cap_out, so 0 serves as every
-            // row's reference: bf16 and fp32 hold 2^-80 .. 2^80 as exactly as 1 (fp16 does not),
-            // and the maximum, its exchange between the two warps and the rescaling fall away
-            const bool fixed_ref = kScored && kBF16 && p.fixed_ref;
-            float m_ref = fixed_ref ? 0.f : -INFINITY, l = 0.f;
+            float m_ref = kFixed ? p.shift : -INFINITY, l = 0.f;
             for (int j = 0; j < it.ntiles && ok; ++j, ++jt) {
                 const int b = jt % SB;
                 const int t0 = it.tok_lo + j * TILE;
@@ -963,14 +1002,11 @@ __global__ void __launch_bounds__(384, 1)
                 float pmax = -INFINITY, factor = 1.f;
                 if constexpr (kScored) {
                     // the scores themselves replace the raw ones: capped, biased, masked to -inf
-                    factor = score_row(p, x, slope2, t0 + c0 - pos);
-                    if (!full) {
-                        // one bit per column: a select and a bit test each
-                        const uint32_t seen[2] = {below(chi) & ~below(clo), below(chi - 32) & ~below(clo - 32)};
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) x[i] = (seen[i / 32] >> (i % 32)) & 1u ? x[i] : -INFINITY;
-                    }
-                    if (!fixed_ref) {
+                    const uint32_t seen0 = below(chi) & ~below(clo), seen1 = below(chi - 32) & ~below(clo - 32);
+                    if constexpr (kFixed) cap_scores(p, x);
+                    else factor = score_row<kCapped>(p, x, slope2, t0 + c0 - pos);
+                    if (!full) hide(x, seen0, seen1);
+                    if constexpr (!kFixed) {
                         pmax = fmaxf(x[0], x[63]);
 #pragma unroll
                         for (int i = 1; i + 1 < 63; i += 2) pmax = fmax3(pmax, x[i], x[i + 1]);
@@ -991,7 +1027,7 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     pmax = ext * p.scale_log2;
                 }
-                if (!fixed_ref) {
+                if constexpr (!kFixed) {
                     float pmax_other;
                     if (!exchange_max(xs++, b, pmax, pmax_other)) {
                         ok = false;
@@ -1012,13 +1048,13 @@ __global__ void __launch_bounds__(384, 1)
                                 break;
                             }
                             tc::fence_after_sync();
-    #pragma unroll
+#pragma unroll
                             for (int c = 0; c < 64; c += 16) {
                                 float o[16];
                                 tc::tmem_ld_x16(lane_base + L::kOCol + c0 + c, o);
                                 tc::tmem_ld_wait();
                                 uint32_t w[16];
-    #pragma unroll
+#pragma unroll
                                 for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * alpha);
                                 asm volatile(
                                     "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, "
@@ -1069,7 +1105,7 @@ __global__ void __launch_bounds__(384, 1)
                         tc::tmem_st_x16(pcol + 16 * c16, packed);
                     }
                 };
-                if (kScored && fixed_ref) weights(std::false_type{}, std::false_type{});
+                if (kFixed) weights(std::false_type{}, std::false_type{});
                 else if (kScored || full) weights(std::false_type{}, std::true_type{});
                 else weights(std::true_type{}, std::true_type{});
                 l += l0 + l1;
@@ -1114,7 +1150,7 @@ __global__ void __launch_bounds__(384, 1)
             if (ok) ok = exchange_sum(xs++, l, l_other);
             // without the tiles' exchanges the partner may still be reading when this warp
             // writes the next item's sum
-            if (ok && fixed_ref) ok = pair_sync(xs++);
+            if (kFixed && ok) ok = pair_sync(xs++);
             const float lt = l + l_other;
             if (ok) ok = tc_wait_warp(&o_done[(jt - 1) % SB], ((jt - 1) / SB) & 1, abort_flag, p.status);
             if (ok && prefill_staged(p, it)) {

@@ -63,7 +63,8 @@ class PreparedCall:
     returns the call's output tensor (or None).  It holds the tensors it was
     prepared with; they must keep their storage, while their contents may change
     between calls (new queries and rows, new context lengths within the bound
-    given at preparation)."""
+    given at preparation).  Its output and workspace are its own: calls of one
+    PreparedCall must not overlap on the GPU, and it must stay alive until they are done."""
     __slots__ = ("_fn", "_args", "_dev", "_what", "_tensors", "_result")
 
     @property

@@ -194,22 +194,87 @@ def test_bad_lengths_and_entries_are_flagged():
     assert pkv.get_device_error(dev)[1] == ["context_len"] and (out == 3.0).all()
 
 
-def test_captured_and_replayed():
+@pytest.mark.parametrize("splits", [0, 2])
+def test_captured_and_replayed(splits):
     dev = device()
     c = make([100, 0], [50, 130], 8, 2, 16, BF16, seed=6)
     qs = torch.tensor([0, 50, 180], dtype=torch.int32, device=dev)
     q = c["q"].to(dev)
+    lens = torch.tensor(c["lens"], dtype=torch.int32, device=dev)
     call = pkv.prepare_paged_attention_prefill_scored(
-        q, *pkv.split_pool(c["kv"].to(dev)), c["tables"].to(dev), qs, torch.tensor(c["lens"], dtype=torch.int32, device=dev),
-        max_query_len=130, max_context_len=150, softcap=8.0, window=77, kv_splits=2)
+        q, *pkv.split_pool(c["kv"].to(dev)), c["tables"].to(dev), qs, lens, max_query_len=130, max_context_len=150,
+        softcap=8.0, window=77, kv_splits=splits)
     call()
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         call()
+        call()
     c["q"] = (c["q"].float() * 0.5).to(BF16)
+    c["lens"], c["chunks"] = [149, 130], [50, 130]                      # other lengths at replay
     q.copy_(c["q"])
-    graph.replay()
+    lens.copy_(torch.tensor(c["lens"], dtype=torch.int32))
+    for _ in range(3):
+        graph.replay()
     torch.cuda.synchronize()
     check_no_device_flags(dev)
     check(c, call.result.cpu(), softcap=8.0, window=77, step=7)
+
+
+def test_two_streams_at_once():
+    """Two prepared calls on two streams, each with its own item table."""
+    dev = device()
+    calls, want = [], []
+    for seed, kw in ((1, dict(softcap=20.0)), (2, dict(window=300))):
+        c = make([400, 0, 77], [300, 211, 64], 8, 2, 16, BF16, seed=seed)
+        qs = torch.tensor([0, 300, 511, 575], dtype=torch.int32, device=dev)
+        call = pkv.prepare_paged_attention_prefill_scored(
+            c["q"].to(dev), *pkv.split_pool(c["kv"].to(dev)), c["tables"].clamp(min=0).to(dev), qs,
+            torch.tensor(c["lens"], dtype=torch.int32, device=dev), max_query_len=300, max_context_len=700, **kw)
+        call()
+        torch.cuda.synchronize()
+        check(c, call.result.cpu(), step=50, **kw)
+        want.append(call.result.clone())
+        calls.append(call)
+    streams = [torch.cuda.Stream(dev) for _ in calls]
+    for call in calls:
+        call.result.zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, call in zip(streams, calls):
+            with torch.cuda.stream(s):
+                call()
+    torch.cuda.synchronize()
+    check_no_device_flags(dev)
+    for call, w in zip(calls, want):
+        assert torch.equal(call.result, w)
+
+
+def test_more_row_tiles_than_the_item_table_holds():
+    dev = device()
+    n = 70
+    c = make([3 * i for i in range(n)], [1 + i % 9 for i in range(n)], 2, 2, 16, F16, seed=12)
+    wide = torch.full((n, 512), -7, dtype=torch.int32)
+    wide[:, :c["tables"].shape[1]] = c["tables"]
+    qs = torch.tensor([0] + c["chunks"], dtype=torch.int32).cumsum(0).to(torch.int32)
+    kw = dict(softcap=20.0, window=50)
+    args = (c["q"].to(dev), *pkv.split_pool(c["kv"].to(dev)), wide.to(dev), qs.to(dev),
+            torch.tensor(c["lens"], dtype=torch.int32, device=dev), c["scale"])
+    assert pkv.prefill_scored_workspace_bytes(c["rows"], n, 2, 2, 128, 16, 8192, 8192, 50) == 0
+    out = pkv.paged_attention_prefill_scored(*args, max_query_len=8192, max_context_len=8192, **kw)
+    torch.cuda.synchronize()
+    check_no_device_flags(dev)
+    check(c, out.cpu(), **kw)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("softcap", [55.0, 60.0])
+def test_every_score_at_the_cap(sign, softcap):
+    """All scores at +cap or -cap (the weights' extremes for a fixed reference, and just past it), and large values."""
+    dev = device()
+    c = make([200], [150], 4, 2, 16, BF16, seed=3)
+    c["kv"][:, 0] = torch.rand_like(c["kv"][:, 0].float()).add(1).mul(3).to(BF16)
+    c["q"] = (torch.rand_like(c["q"].float()).add(1) * 20 * sign).to(BF16)
+    c["kv"][:, 1] = (c["kv"][:, 1].float() * 1e18).to(BF16)
+    for splits in (0, 2):
+        check(c, run(dev, c, softcap=softcap, splits=splits), softcap=softcap, step=11)

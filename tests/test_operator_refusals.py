@@ -150,7 +150,7 @@ def test_evict_refusals(lib):
 
     assert select(b=0) == 0
     for kw in (dict(budget=0), dict(sinks=7), dict(sinks=-1), dict(recent=-1), dict(recent=2 ** 31 - 1, budget=2 ** 31 - 1),
-               dict(ws=63), dict(b=-1), dict(b=70000), dict(hkv=0), dict(maxl=-1), dict(w=None), dict(kept=2), dict(kl=None),
+               dict(ws=63), dict(budget=2 ** 30 + 1), dict(ws=2 ** 31, maxl=2 ** 30 + 1), dict(b=-1), dict(b=70000), dict(hkv=0), dict(maxl=-1), dict(w=None), dict(kept=2), dict(kl=None),
                dict(wo=2)):
         assert select(**kw) == INVALID, kw
 
@@ -164,7 +164,7 @@ def test_evict_refusals(lib):
     assert compact(b=0) == 0
     for kw in (dict(d=80), dict(bs=12), dict(dt=3)):
         assert compact(**kw) == UNSUPPORTED, kw
-    for kw in (dict(nb=0), dict(mb=0), dict(budget=0), dict(dmb=0), dict(bt=None), dict(cl=2), dict(kept=None), dict(kl=1),
+    for kw in (dict(nb=0), dict(mb=0), dict(budget=0), dict(budget=2 ** 30 + 1), dict(dmb=0), dict(bt=None), dict(cl=2), dict(kept=None), dict(kl=1),
                dict(dst=18), dict(kc=8), dict(vc=None), dict(stride=64), dict(hkv=0), dict(b=-1), dict(b=70000),
                dict(dst=16, dmb=3)):
         assert compact(**kw) == INVALID, kw
