@@ -153,7 +153,12 @@ pkv_status plan_decode(int num_seqs, int num_q_heads, int num_kv_heads, int head
         const int64_t partial = 2LL * gh * (head_dim + 2) * 4;
         p = std::max<int64_t>(p, kMinAutoPartition);
         p = std::max<int64_t>(p, (kMergeShare * partial + kv_per_token - 1) / kv_per_token);
-        p = (p + block_size - 1) / block_size * block_size;
+        // The scored form counts in rounds of its four warps' tiles: a partition of 17 tiles
+        // takes as long as one of 20.  (64 windows of 1024 tokens, 32 / 8 heads, bf16: 256-token
+        // partitions 51 us, 272-token ones 54.)
+        const int64_t unit = scored ? 4 * std::min(block_size, int8_kv ? 32 : 16) : block_size;
+        const int64_t align = std::max<int64_t>(unit, block_size);
+        p = scored ? std::max<int64_t>(1, (p + align / 2) / align) * align : (p + align - 1) / align * align;
         p = std::min<int64_t>(p, max_partition);
         // When the floors leave fewer than kTargetWaves waves of a form with two
         // resident CTAs per SM, the CTAs of sequences at max_context_len run in a few
@@ -173,7 +178,7 @@ pkv_status plan_decode(int num_seqs, int num_q_heads, int num_kv_heads, int head
                 return static_cast<double>(ctas) / static_cast<double>((ctas + slots - 1) / slots * slots);
             };
             auto part_for = [&](int64_t k) {  // tokens per partition for k partitions
-                return ((len + k - 1) / k + block_size - 1) / block_size * block_size;
+                return ((len + k - 1) / k + align - 1) / align * align;
             };
             double best = fill(n);
             for (int64_t k = (n + 1) / 2; k < n; ++k)

@@ -173,8 +173,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS) evict_sele
             }
             if (lane == 31) warp_sum[warp] = incl;
             __syncthreads();
-            uint32_t above = incl - sum;
-            for (int i = 0; i < warp; ++i) above += warp_sum[i];
+            uint32_t above = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0u);
 #pragma unroll
             for (int i = 0; i < PER_BIN; ++i) {
                 if (above < left && above + mine[i] >= left) {  // one bin of one thread
