@@ -287,11 +287,14 @@ __device__ __forceinline__ int64_t row_offset(const CompactParams &p, int blk, i
 // so a tile's stores (positions [a, b)) can only meet rows that tiles up to this one
 // read, never a later tile's sources -- one barrier between a tile's loads and its
 // stores orders them, and column groups never meet.
-// Bound by memory: rows of 256 bytes gathered at random.  Measured into fresh blocks:
-// 268 MB moved in 50 us, 5.4 TB/s (0.79 of the copy rate of large contiguous arrays).
+// Bound by memory: rows of 256 bytes gathered at random, read and written once
+// (streaming loads and stores: 50 us, plain ones 53).  Measured into fresh blocks: 268 MB
+// moved in 50 us, 5.3 TB/s, 0.79 of the copy rate of large contiguous arrays; eight, two
+// or one row per thread and the heads fastest in the grid: 60 / 51 / 57 / 50.
 template <int ROW_VECS, int VECS, bool IN_PLACE>
 __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const CompactParams p) {
     constexpr int ROWS = kMoveThreads / VECS, TILE = ROWS * kMoveUnroll, GROUPS = ROW_VECS / VECS;
+    pkv::pdl_wait();  // launched ahead of the kernel before it (the choice of what to keep)
     const int h = blockIdx.y, seq = blockIdx.z;
     const int half = blockIdx.x % 2, group = (blockIdx.x / 2) % GROUPS, tile0 = blockIdx.x / (2 * GROUPS);
     int len = p.context_lens[seq], n = p.kept_lens[seq];
@@ -325,27 +328,27 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
                 pkv::raise_flag(p.status, PKV_DEVERR_BLOCK_TABLE);
                 continue;
             }
-            x[u] = *reinterpret_cast<const uint4 *>(base + row_offset(p, sb, h, t, ROW_VECS * 16) + col);
+            x[u] = __ldcs(reinterpret_cast<const uint4 *>(base + row_offset(p, sb, h, t, ROW_VECS * 16) + col));
             to[u] = row_offset(p, db, h, i, ROW_VECS * 16) + col;
         }
         if (IN_PLACE) __syncthreads();
 #pragma unroll
         for (int u = 0; u < kMoveUnroll; ++u)
-            if (to[u] >= 0) *reinterpret_cast<uint4 *>(base + to[u]) = x[u];
+            if (to[u] >= 0) __stcs(reinterpret_cast<uint4 *>(base + to[u]), x[u]);
         if (!IN_PLACE) break;
     }
 }
 
 template <int ROW_VECS>
-void launch_compact(const CompactParams &p, bool in_place, int max_kept, int num_seqs, cudaStream_t s) {
+cudaError_t launch_compact(const CompactParams &p, bool in_place, int max_kept, int num_seqs, cudaStream_t s) {
     if (in_place) {
         constexpr int VECS = ROW_VECS < 4 ? ROW_VECS : 4;  // 64-byte columns: more chains, whole sectors
         const dim3 grid(2 * (ROW_VECS / VECS), p.num_kv_heads, num_seqs);
-        evict_compact_kernel<ROW_VECS, VECS, true><<<grid, kMoveThreads, 0, s>>>(p);
+        return pkv::launch_kernel(evict_compact_kernel<ROW_VECS, VECS, true>, grid, dim3(kMoveThreads), 0, s, true, p);
     } else {
         constexpr int TILE = kMoveThreads / ROW_VECS * kMoveUnroll;
         const dim3 grid(2 * ((max_kept + TILE - 1) / TILE), p.num_kv_heads, num_seqs);
-        evict_compact_kernel<ROW_VECS, ROW_VECS, false><<<grid, kMoveThreads, 0, s>>>(p);
+        return pkv::launch_kernel(evict_compact_kernel<ROW_VECS, ROW_VECS, false>, grid, dim3(kMoveThreads), 0, s, true, p);
     }
 }
 
@@ -440,9 +443,13 @@ PKV_API pkv_status pkv_evict_compact(void *k_cache, void *v_cache, int64_t num_b
     const int max_kept = std::min(budget, std::min(p.src_cap, p.dst_cap));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int row_vecs = head_dim * elem_bytes / 16;
-    if (row_vecs == 16) launch_compact<16>(p, in_place, max_kept, num_seqs, s);
-    else if (row_vecs == 8) launch_compact<8>(p, in_place, max_kept, num_seqs, s);
-    else launch_compact<4>(p, in_place, max_kept, num_seqs, s);
+    const cudaError_t err = row_vecs == 16  ? launch_compact<16>(p, in_place, max_kept, num_seqs, s)
+                            : row_vecs == 8 ? launch_compact<8>(p, in_place, max_kept, num_seqs, s)
+                                            : launch_compact<4>(p, in_place, max_kept, num_seqs, s);
+    if (err != cudaSuccess) {
+        cudaGetLastError();
+        return PKV_ERR_CUDA;
+    }
     pkv::count_launch();
     return pkv::launch_status();
 }
