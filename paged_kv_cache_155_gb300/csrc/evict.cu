@@ -69,7 +69,7 @@ struct SelectParams {
 //
 // Bound by the latency of its passes, not by bytes (4 read and 4 written per token).
 // Measured: 256 rows of 2048-4096 tokens 12 us (24 us when the threshold came from
-// repeated counting against bisecting candidates), 24 rows of 32768 22 us with clusters
+// repeated counting against bisecting candidates), 24 rows of 32768 19 us with clusters
 // of eight (31 us with one CTA a row, which 24 SMs then work on alone).
 template <int THREADS, int EB, int HELD, int CL>
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS) evict_select_kernel(const SelectParams p) {
@@ -146,9 +146,9 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS) evict_sele
             sync_row();
             if constexpr (CL > 1) {
                 // this CTA's share of the bins, summed over the cluster and sent to every CTA
-                if (tid < BINS / CL) {
-                    const uint32_t mine = pkv::smem_addr(&bins[rank * (BINS / CL) + tid]);
-                    const uint32_t sums_at = pkv::smem_addr(&sums[rank * (BINS / CL) + tid]);
+                for (int i = tid; i < BINS / CL; i += THREADS) {
+                    const uint32_t mine = pkv::smem_addr(&bins[rank * (BINS / CL) + i]);
+                    const uint32_t sums_at = pkv::smem_addr(&sums[rank * (BINS / CL) + i]);
                     uint32_t n = 0u;
 #pragma unroll
                     for (int c = 0; c < CL; ++c) n += load_remote(remote(mine, c));
@@ -386,10 +386,23 @@ PKV_API pkv_status pkv_evict_select(const float *weights, int64_t weights_stride
     p.num_kv_heads = num_kv_heads;
     const dim3 grid(static_cast<unsigned>(num_kv_heads), static_cast<unsigned>(num_seqs));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // clusters from 8192 tokens on: one CTA would hold the row on one SM
-    if (max_context_len <= 1024) evict_select_kernel<256, 4, 1, 1><<<grid, 256, 0, s>>>(p);
-    else if (max_context_len <= 8192) evict_select_kernel<512, 8, 2, 1><<<grid, 512, 0, s>>>(p);
-    else evict_select_kernel<512, 8, 2, 8><<<dim3(grid.x * 8, grid.y), 512, 0, s>>>(p);
+    // Rows past 8192 tokens spread over a cluster as large as leaves every cluster resident
+    // at once (two CTAs per SM): one CTA would work through the row on one SM, but a second
+    // wave of clusters would wait for the first.  (Rows of 32768, this rule against always
+    // eight: 72 rows 25 us / 36 us, 152 rows 45 / 73, 512 rows 130 / 223.)
+    if (max_context_len <= 1024) {
+        evict_select_kernel<256, 4, 1, 1><<<grid, 256, 0, s>>>(p);
+    } else if (max_context_len <= 8192) {
+        evict_select_kernel<512, 8, 2, 1><<<grid, 512, 0, s>>>(p);
+    } else {
+        const int sms = pkv::current_sm_count();
+        if (sms <= 0) return PKV_ERR_CUDA;
+        const int64_t rows = static_cast<int64_t>(num_kv_heads) * num_seqs, slots = 2LL * sms;
+        if (rows * 8 <= slots) evict_select_kernel<512, 8, 2, 8><<<dim3(grid.x * 8, grid.y), 512, 0, s>>>(p);
+        else if (rows * 4 <= slots) evict_select_kernel<512, 8, 2, 4><<<dim3(grid.x * 4, grid.y), 512, 0, s>>>(p);
+        else if (rows * 2 <= slots) evict_select_kernel<512, 8, 2, 2><<<dim3(grid.x * 2, grid.y), 512, 0, s>>>(p);
+        else evict_select_kernel<512, 8, 2, 1><<<grid, 512, 0, s>>>(p);
+    }
     pkv::count_launch();
     return pkv::launch_status();
 }

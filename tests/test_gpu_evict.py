@@ -68,6 +68,25 @@ def test_select_over_rows_longer_than_the_registers_hold(kind):
     _select(dev, w, lens, 9000, 16, 1000, in_place=kind == "ties")
 
 
+@pytest.mark.parametrize("rows", [40, 60, 100, 200])
+def test_select_of_many_long_rows(rows):
+    """Enough rows past 8192 tokens for clusters of four and two and for one block each; a few rows are checked."""
+    dev = device()
+    g = torch.Generator().manual_seed(rows)
+    lens = [9000 + 7 * i for i in range(rows // 4)]
+    w = _weights("tail", (len(lens), 4, max(lens)), g)
+    on = w.to(dev)
+    kept, kept_lens = pkv.evict_select(on, torch.tensor(lens, dtype=torch.int32, device=dev), 3000, sinks=2, recent=50,
+                                       weights_out=on)
+    torch.cuda.synchronize()
+    check_no_device_flags(dev)
+    assert (kept_lens.cpu() == 3000).all()
+    for i in (0, len(lens) // 2, len(lens) - 1):
+        ref, _ = refs.select(w[i:i + 1], lens[i:i + 1], 3000, 2, 50)
+        assert torch.equal(kept.cpu()[i], ref[0])
+        assert torch.equal(on.cpu()[i, :, :3000], w[i].gather(1, ref[0].long())) and (on.cpu()[i, :, 3000:lens[i]] == 0).all()
+
+
 def test_select_clamps_and_flags_bad_lengths():
     dev = device()
     w = torch.rand((2, 1, 64))
