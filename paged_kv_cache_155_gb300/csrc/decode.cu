@@ -97,6 +97,15 @@ int resident_ctas_per_sm(bool int8_kv, int heads_per_block) {
     if (heads_per_block == 16) return 2;
     return heads_per_block >= 4 ? 3 : 2;
 }
+// The scored form's warp MMAs take groups of any size from three on: the fewest blocks
+// that cover the group, of 4, 8 or 16 head rows each (8 at most over an INT8 cache), so
+// that its K/V is read once per block and not once per divisor.  (36 contexts of up to
+// 7415 tokens, 20 / 4 heads of 64, fp16: 154 us with one head per block, 37.5 with eight.)
+int scored_heads_per_block_for(int group, bool int8_kv) {
+    if (group <= 2) return group;
+    const int most = int8_kv ? 8 : 16, blocks = (group + most - 1) / most, per = (group + blocks - 1) / blocks;
+    return per <= 4 ? 4 : per <= 8 ? 8 : 16;
+}
 // Query heads per CTA: the largest of 16 (16-bit caches at head_dim 128), 8, 4, 2, 1
 // dividing the group (4 to 16 run the products as warp-level MMAs, 1 or 2 as
 // per-lane loops).
@@ -132,8 +141,8 @@ pkv_status plan_decode(int num_seqs, int num_q_heads, int num_kv_heads, int head
     const int max_partition = pkv::DecodeGeom<128, 16>::kMaxTableEntries * block_size;
     if (partition_size > max_partition) return PKV_ERR_INVALID_ARG;
     const int group = num_q_heads / num_kv_heads;
-    const int gh = heads_per_block_for(group, int8_kv, head_dim);
-    const int64_t grid_y = static_cast<int64_t>(num_kv_heads) * (group / gh);
+    const int gh = scored ? scored_heads_per_block_for(group, int8_kv) : heads_per_block_for(group, int8_kv, head_dim);
+    const int64_t grid_y = static_cast<int64_t>(num_kv_heads) * ((group + gh - 1) / gh);
     if (grid_y > 65535 || num_seqs > 65535) return PKV_ERR_INVALID_ARG;
 
     int part = partition_size;
@@ -345,7 +354,7 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache,
     p.num_seqs = num_seqs;
     p.num_q_heads = num_q_heads;
     p.group = group;
-    p.subgroups = group / gh;
+    p.subgroups = (group + gh - 1) / gh;
     p.items_y = num_kv_heads * p.subgroups;
     p.partition_size = part;
     p.num_partitions = nparts;

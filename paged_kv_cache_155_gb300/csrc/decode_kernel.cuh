@@ -265,7 +265,10 @@ struct DecodeGeom {
 // kScored: scores capped, biased and masked from below (DecodeParams::slopes ..
 // cap_out), and kept for the weights when ws_s is given; a form of its own, so that
 // the plain one carries none of it.
-template <typename T, typename KT, int D, int BS, int GH, bool kScored = false>
+// kPadded (scored warp MMAs): a block may serve fewer than GH heads, so that any group of
+// three heads or more is covered by few blocks rather than read its K/V again for each
+// divisor; compiled apart, as the registers are spent without it.
+template <typename T, typename KT, int D, int BS, int GH, bool kScored = false, bool kPadded = false>
 __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 ? 2 : 3) : (GH >= 4 && kScored) ? 4 : 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                                               const __grid_constant__ CUtensorMap tmap_v,
@@ -307,6 +310,8 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
     const int seq = blockIdx.z;
     const int kvh = blockIdx.y / p.subgroups;
     const int hq0 = kvh * p.group + (blockIdx.y % p.subgroups) * GH;
+    // heads of this block (the rows past them are zero)
+    const int nheads = kPadded ? min(GH, p.group - static_cast<int>(blockIdx.y % p.subgroups) * GH) : GH;
 
     // ---- the partition's first table entries are fetched together with the context
     //      length (where the partition starts does not depend on it), so the first
@@ -508,7 +513,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
             float f[D / 4];
 #pragma unroll
             for (int e = 0; e < D / 4; ++e) f[e] = 0.f;
-            if (mg < GH) {
+            if (mg < nheads) {
 #pragma unroll
                 for (int j = 0; j < D / (4 * RUN); ++j) {
 #pragma unroll
@@ -552,13 +557,14 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
 #pragma unroll
             for (int j = 0; j < D / (4 * RUN); ++j) {
                 const int qofs = kSwz ? 64 * (j >> 1) + 8 * (j & 1) : 4 * RUN * j;
-                const uint4 u = mg < GH ? *reinterpret_cast<const uint4 *>(qrow + qofs) : make_uint4(0, 0, 0, 0);
+                const uint4 u = mg < nheads ? *reinterpret_cast<const uint4 *>(qrow + qofs) : make_uint4(0, 0, 0, 0);
                 qa[2 * j][0] = u.x;
                 qa[2 * j][1] = u.y;
                 qa[2 * j + 1][0] = u.z;
                 qa[2 * j + 1][1] = u.w;
                 if constexpr (kRows16) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(qrow + 8 * D + qofs);  // head mg + 8
+                    uint4 w = make_uint4(0, 0, 0, 0);  // head mg + 8
+                    if (!kPadded || mg + 8 < nheads) w = *reinterpret_cast<const uint4 *>(qrow + 8 * D + qofs);
                     qb[2 * j][0] = w.x;
                     qb[2 * j][1] = w.y;
                     qb[2 * j + 1][0] = w.z;
@@ -595,7 +601,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
         for (int e = 0; e < kSlopes; ++e) {
             // INT8 MMA: heads 2 mt, 2 mt + 1; 16-bit MMA: mg, mg + 8; lanes: head e
             const int h = kMma ? (kQuant ? 2 * mt + e : mg + 8 * e) : e;
-            slope2[e] = p.slopes && h < GH ? p.slopes[hq0 + h] * 1.4426950408889634f : 0.f;
+            slope2[e] = p.slopes && h < nheads ? p.slopes[hq0 + h] * 1.4426950408889634f : 0.f;
         }
     }
     const int qpos = len - 1;  // the query's position
@@ -848,11 +854,13 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
 #pragma unroll
                             for (int h = 0; h < STEP / 8; ++h) {
                                 const int at = c * TILE + tb + 8 * h + 2 * mt;
-                                if (mg < GH)
+                                if (mg < nheads)
                                     *reinterpret_cast<float2 *>(score_row(mg) + at) = make_float2(sc[2 * h], sc[2 * h + 1]);
-                                if constexpr (kRows16)
-                                    *reinterpret_cast<float2 *>(score_row(mg + 8) + at) =
-                                        make_float2(sc2[2 * h], sc2[2 * h + 1]);
+                                if constexpr (kRows16) {
+                                    if (!kPadded || mg + 8 < nheads)
+                                        *reinterpret_cast<float2 *>(score_row(mg + 8) + at) =
+                                            make_float2(sc2[2 * h], sc2[2 * h + 1]);
+                                }
                             }
                         }
                     }
@@ -1110,7 +1118,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
         if constexpr (kScored && !kQuant) {
             // a flagged table entry's tokens get no weight
             if (p.ws_s && tbl[(c * TILE) / BS] < 0) {
-                for (int k = lane; k < GH * TILE; k += 32) score_row(k / TILE)[c * TILE + k % TILE] = -INFINITY;
+                for (int k = lane; k < nheads * TILE; k += 32) score_row(k / TILE)[c * TILE + k % TILE] = -INFINITY;
             }
         }
         __syncwarp();
@@ -1228,7 +1236,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
     __syncthreads();
 
     const bool single = nparts == 1 && !p.always_partial;
-    for (int idx = threadIdx.x; idx < GH * D; idx += blockDim.x) {
+    for (int idx = threadIdx.x; idx < nheads * D; idx += blockDim.x) {
         const int g = idx / D;
         const int j = idx - g * D;
         float mw[NW];

@@ -14,7 +14,7 @@
 
 namespace pkv {
 
-template <typename T, typename KT, int D, int BS, int GH, bool kScored>
+template <typename T, typename KT, int D, int BS, int GH, bool kScored, bool kPadded = false>
 pkv_status launch_decode_one(const DecodeParams &p, const DecodeMaps &maps, dim3 grid, cudaStream_t stream,
                              bool overlap) {
     using G = DecodeGeom<D, BS, sizeof(KT), decode_lane_values<KT, GH>(), (GH >= 4), (GH == 16)>;
@@ -23,13 +23,13 @@ pkv_status launch_decode_one(const DecodeParams &p, const DecodeMaps &maps, dim3
     if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
     if (!bit || !(configured_devices.load(std::memory_order_acquire) & bit)) {
-        if (cudaFuncSetAttribute(paged_decode_kernel<T, KT, D, BS, GH, kScored>,
+        if (cudaFuncSetAttribute(paged_decode_kernel<T, KT, D, BS, GH, kScored, kPadded>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  G::kSmemBytes) != cudaSuccess)
             return PKV_ERR_CUDA;
         configured_devices.fetch_or(bit, std::memory_order_acq_rel);
     }
-    if (launch_kernel(paged_decode_kernel<T, KT, D, BS, GH, kScored>, grid, dim3(G::kWarps * 32),
+    if (launch_kernel(paged_decode_kernel<T, KT, D, BS, GH, kScored, kPadded>, grid, dim3(G::kWarps * 32),
                       G::kSmemBytes, stream, overlap, maps.k, maps.v, p) != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
@@ -41,14 +41,26 @@ pkv_status launch_decode_one(const DecodeParams &p, const DecodeMaps &maps, dim3
 template <typename T, typename KT, int D, int BS, bool kScored>
 pkv_status launch_decode_gh(const DecodeParams &p, const DecodeMaps &m, int gh, dim3 grid,
                             cudaStream_t s, bool overlap) {
+    if constexpr (kScored) {
+        if (gh >= 4 && p.group % gh != 0) {
+            switch (gh) {
+                case 4: return launch_decode_one<T, KT, D, BS, 4, true, true>(p, m, grid, s, overlap);
+                case 8: return launch_decode_one<T, KT, D, BS, 8, true, true>(p, m, grid, s, overlap);
+                case 16:
+                    if constexpr (sizeof(KT) == 2) return launch_decode_one<T, KT, D, BS, 16, true, true>(p, m, grid, s, overlap);
+                    break;
+            }
+            return PKV_ERR_UNSUPPORTED;
+        }
+    }
     switch (gh) {
         case 1: return launch_decode_one<T, KT, D, BS, 1, kScored>(p, m, grid, s, overlap);
         case 2: return launch_decode_one<T, KT, D, BS, 2, kScored>(p, m, grid, s, overlap);
         case 4: return launch_decode_one<T, KT, D, BS, 4, kScored>(p, m, grid, s, overlap);
         case 8: return launch_decode_one<T, KT, D, BS, 8, kScored>(p, m, grid, s, overlap);
         case 16:
-            // 16 heads per block: the 16-bit warp-MMA form at head_dim 128
-            if constexpr (sizeof(KT) == 2 && D == 128) return launch_decode_one<T, KT, D, BS, 16, kScored>(p, m, grid, s, overlap);
+            // 16 heads per block: the 16-bit warp-MMA form at head_dim 128 (the scored one at 64 too)
+            if constexpr (sizeof(KT) == 2 && (D == 128 || kScored)) return launch_decode_one<T, KT, D, BS, 16, kScored>(p, m, grid, s, overlap);
             break;
     }
     return PKV_ERR_UNSUPPORTED;

@@ -112,7 +112,10 @@ def check(c, out, wout=None, softcap=0.0, slopes=None, window=0, starts=None, we
 SLOPES = lambda hq: torch.exp2(-8.0 * torch.arange(1, hq + 1) / hq).float()
 SHAPES = [  # hq, hkv, d, bs: one, two, four, eight, sixteen and odd heads per KV head
     (4, 4, 64, 16), (6, 2, 128, 8), (4, 2, 128, 32), (8, 2, 128, 16), (8, 1, 128, 8), (32, 2, 128, 32), (16, 1, 128, 8),
-    (8, 2, 64, 32), (16, 2, 64, 8), (10, 5, 64, 32)]
+    (8, 2, 64, 32), (16, 2, 64, 8), (10, 5, 64, 32),
+    # groups that fill no whole block: three, five, six, twelve, twenty, thirty-four heads
+    (6, 2, 128, 16), (10, 2, 128, 16), (15, 3, 64, 8), (12, 2, 128, 8), (24, 2, 64, 16), (24, 2, 128, 32), (20, 1, 128, 16),
+    (40, 2, 64, 32), (34, 1, 128, 8), (16, 1, 64, 16)]
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
@@ -223,6 +226,31 @@ def test_a_long_context_split_many_ways_and_its_weights():
     c = make([20011], 4, 1, 128, 16, F16, seed=31)
     out, wout = run(dev, c, 20.0, SLOPES(4) / 64, 0, None, None, True, 16 * 16)
     check(c, out, wout, 20.0, SLOPES(4) / 64)
+
+
+@pytest.mark.parametrize("odd", [0, 1], ids=["vectors", "odd_stride"])
+def test_weights_of_a_large_batch(odd):
+    """Enough tokens for several steps per block of the weights; the first and last sequences are checked in full, the others'
+    weights by their sums (each query head's weights sum to 1)."""
+    dev = device()
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(1, 2600, (64,), generator=g).tolist()
+    lens[0], lens[-1] = 2600, 2599
+    c = make(lens, 16, 8, 64, 16, F16, seed=9)
+    kv = c["kv"].to(dev)
+    w = torch.full((64, 8, 2600 + odd), 5.0, device=dev)
+    old = torch.rand((64, 8, 2600 + odd), generator=g).to(dev)
+    dl = torch.tensor(lens, dtype=torch.int32, device=dev)
+    out = pkv.paged_attention_decode_scored(c["q"].to(dev), *pkv.split_pool(kv), c["tables"].to(dev), dl, c["scale"], weights=old,
+                                            weights_out=w, max_context_len=2600)
+    torch.cuda.synchronize()
+    check_no_device_flags(dev)
+    inside = torch.arange(2600 + odd, device=dev) < dl[:, None]
+    assert (w[~inside[:, None].expand_as(w)] == 5.0).all()
+    added = torch.where(inside[:, None], w.double() - old.double(), 0.0).sum(2).cpu()
+    assert (added - 2.0).abs().max() <= 2600 * 2.0 ** -23 + 1e-3          # roundings of w + the scores' slack (below 5e-4)
+    ends = dict(c, lens=[lens[0], lens[-1]], tables=c["tables"][[0, -1]], q=c["q"][[0, -1]])
+    check(ends, out.cpu()[[0, -1]], w.cpu()[[0, -1]], weights=old.cpu()[[0, -1]])
 
 
 def test_bad_lengths_and_entries_are_flagged():
