@@ -98,6 +98,31 @@ def test_one_axis_in_place_and_skipped_tokens():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("int8", [False, True], ids=["16bit", "int8"])
+@pytest.mark.parametrize("d,interleaved", [(64, False), (128, True)])
+def test_an_odd_chunk_of_many_tokens(d, interleaved, int8):
+    """Enough tokens for two per block, the last block with one."""
+    dev = device()
+    c = _case(dev, 2049, 3, 1, d, 16, torch.bfloat16, 2, d, seed=10, int8=int8)
+    if not int8:
+        slots = c["slots"].clone()
+        slots[5::11] = -1
+        _check(c, dev, interleaved, axis=c["axis"], slots=slots)
+        return
+    sc = torch.full((1, d), 0.03)
+    kv = c["kv"].to(dev)
+    out = pkv.rope_reshape_and_cache_int8(c["q"], c["k"], c["v"], c["pos"].to(dev), c["inv"].to(dev), c["slots"].to(dev),
+                                          *pkv.split_pool(kv), sc.to(dev), sc.to(dev), axis_of_pair=c["axis"].to(dev),
+                                          interleaved=interleaved)
+    torch.cuda.synchronize()
+    check_no_device_flags(dev)
+    ref, mag = refs.rotate(c["host"][0], c["pos"], c["axis"], c["inv"], interleaved)
+    refs.rounded_close(out.cpu(), ref, mag * SLACK, "q")
+    ref, mag = refs.rotate(c["host"][1], c["pos"], c["axis"], c["inv"], interleaved)
+    code = kv.cpu()[c["slots"] // 16, 0, :, c["slots"] % 16].double()
+    assert ((code - (ref / 0.03).clamp(-127, 127)).abs() <= 0.5 + mag * SLACK / 0.03 + 127 * 2.0 ** -22).all()
+
+
 def test_rows_longer_than_one_step_and_no_tokens():
     dev = device()
     c = _case(dev, 3, 200, 100, 128, 8, torch.bfloat16, 2, 64, seed=6)
