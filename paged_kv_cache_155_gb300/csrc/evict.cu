@@ -53,6 +53,7 @@ struct SelectParams {
     unsigned int *status;
     int64_t weights_stride;
     int len_cap, budget, sinks, recent, num_kv_heads;
+    int vectors;           // rows of weights start 16-byte aligned
 };
 
 // CL CTAs (a cluster) per (KV head, sequence).  The kept tokens are the first `sinks`,
@@ -62,27 +63,30 @@ struct SelectParams {
 // digit in shared memory, find the digit at which the count from above passes `need`,
 // and descend; done as soon as the keys from some digit on are exactly `need`.  In a
 // cluster every CTA counts its share and reads the others' counts.  A row's tokens go
-// in batches of CL x EB x THREADS, CTA after CTA; the keys of the first HELD batches
-// stay in registers, a longer row's others are read again (from L2) in each pass.  The
-// kept positions then leave in ascending order, batch by batch, by a prefix count over
-// the block and the cluster.
+// in batches of CL x EB x THREADS, CTA after CTA, EB consecutive ones per thread; the
+// first HELD batches stay in registers, a longer row's others are read again (from L2)
+// in each pass.  The kept positions then leave in ascending order, batch by batch, by
+// one prefix count of the threads over the block and the cluster, gathered in shared
+// memory so that the stores are whole lines.
 //
 // Bound by the latency of its passes, not by bytes (4 read and 4 written per token).
-// Measured: 256 rows of 2048-4096 tokens 12 us (24 us when the threshold came from
-// repeated counting against bisecting candidates), 24 rows of 32768 19 us with clusters
-// of eight (31 us with one CTA a row, which 24 SMs then work on alone).
+// Measured: 256 rows of 2048-4096 tokens 11 us (24 us when the threshold came from
+// repeated counting against bisecting candidates), 24 rows of 32768 18 us with clusters
+// of eight (31 us with one CTA a row, which 24 SMs then work on alone), 512 rows of 32768
+// 80 us (130 us with strided tokens, a ballot per 32 of them and stores straight to the
+// row).
 template <int THREADS, int EB, int HELD, int CL>
-__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS) evict_select_kernel(const SelectParams p) {
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(const SelectParams p) {
     constexpr int WARPS = THREADS / 32, PART = EB * THREADS, BATCH = CL * PART;
     constexpr int BINS = 2048, PER_BIN = BINS / THREADS;
-    static_assert(BINS % THREADS == 0 && CL <= 32 && EB * HELD <= 32, "whole bins per thread, masks of 32 bits");
-    __shared__ uint32_t bins[BINS];
-    __shared__ uint32_t sums[CL > 1 ? BINS : 1];  // the bins summed over the cluster
+    constexpr int COUNTS = CL > 1 ? 2 * BINS : BINS;
+    static_assert(BINS % THREADS == 0 && WARPS <= 32 && EB % 4 == 0 && PART < 65536, "whole bins per thread, counts of 16 bits");
+    // the threshold's counts, then a batch's kept positions and their weights
+    __shared__ uint32_t shared[COUNTS > 2 * PART ? COUNTS : 2 * PART];
+    uint32_t *const bins = shared, *const sums = shared + (CL > 1 ? BINS : 0);  // sums: the bins over the cluster
     __shared__ uint32_t warp_sum[WARPS];
-    __shared__ uint32_t found[3];            // the digit, the keys above it, the keys in it
-    __shared__ uint32_t totals[EB * WARPS];  // (kept outright, ties) of each 32 tokens, 16 bits each
-    __shared__ uint32_t bases[EB * WARPS];   // their exclusive prefix
-    __shared__ uint32_t part_total;          // their sum
+    __shared__ uint32_t found[3];       // the digit, the keys above it, the keys in it
+    __shared__ uint32_t totals[2][CL];  // (kept outright, ties) of each CTA's part of a batch, 16 bits each
     const int rank = blockIdx.x % CL;
     const auto sync_row = [] {
         if constexpr (CL > 1) cluster_sync();
@@ -102,27 +106,41 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS) evict_sele
     float *wout = p.weights_out ? p.weights_out + row * p.weights_stride : nullptr;
     int32_t *kept = p.kept + row * p.budget;
     const int rtid = rank * THREADS + tid;  // thread of the row
+    // a thread's EB tokens of a batch, from first_of on
+    const auto first_of = [&](int batch) { return batch * BATCH + rank * PART + tid * EB; };
+    const auto load = [&](int batch, float (&v)[EB]) {
+        const int t0 = first_of(batch);
+        if (p.vectors && t0 + EB <= len) {
+#pragma unroll
+            for (int e = 0; e < EB; e += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(w + t0 + e);
+                v[e] = x.x, v[e + 1] = x.y, v[e + 2] = x.z, v[e + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < EB; ++e) v[e] = t0 + e < len ? w[t0 + e] : 0.f;
+        }
+    };
+    const auto below = [](int n) { return (1u << max(0, min(n, EB))) - 1u; };  // the lowest n of EB bits
+    float val[HELD][EB];
+#pragma unroll
+    for (int b = 0; b < HELD; ++b) load(b, val[b]);
     for (int i = keep + rtid; i < p.budget; i += CL * THREADS) kept[i] = -1;
+    // the tokens [mid0, mid1) compete for `need` places, the others stay
     const bool all = len <= p.budget;
-    const int mid0 = p.sinks, mid1 = len - p.recent;  // the tokens that compete, when !all
     const uint32_t need = all ? 0u : static_cast<uint32_t>(p.budget - p.sinks - p.recent);
-    const auto token = [&](int batch, int e) { return batch * BATCH + rank * PART + e * THREADS + tid; };
+    const int mid0 = all ? 0 : p.sinks, mid1 = all ? 0 : len - p.recent;
+    const auto competing = [&](int batch) {
+        const int t0 = first_of(batch);
+        return below(mid1 - t0) & ~below(mid0 - t0);
+    };
 
     // the keys >= thr stay, or (not exact) those > thr and the first `ties` that equal it
-    uint32_t thr = 0u, ties = 0u;
-    bool exact = false;
+    uint32_t thr = 0xffffffffu, ties = 0u;  // (need 0: no key is that large)
+    bool exact = true;
     if (need > 0) {
-        uint32_t key[EB * HELD];
-        uint32_t held = 0u;  // bit i: key i's token competes
-#pragma unroll
-        for (int i = 0; i < EB * HELD; ++i) {
-            const int t = token(i / EB, i % EB);
-            const bool competes = t >= mid0 && t < mid1;
-            key[i] = competes ? __float_as_uint(w[t]) : 0u;
-            held |= static_cast<uint32_t>(competes) << i;
-        }
-#pragma unroll
-        for (int i = 0; i < EB * HELD; ++i) key[i] = weight_key(__uint_as_float(key[i]));
+        thr = 0u;
+        exact = false;
         uint32_t left = need;  // of the keys that share thr's digits so far
         // digits: bits 31..21, 20..10, 9..0
         for (int shift = 21, width = 11; width > 0 && !exact; width = shift == 21 ? 11 : shift == 10 ? 10 : 0,
@@ -130,19 +148,23 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS) evict_sele
             for (int i = tid; i < BINS; i += THREADS) bins[i] = 0u;
             __syncthreads();
             const uint32_t mask = (1u << width) - 1u;
-            auto count = [&](uint32_t k) {
-                // the digits above are thr's (all of a key's, in the first pass)
-                if (shift == 21 || (k >> (shift + width)) == (thr >> (shift + width)))
-                    atomicAdd(&bins[(k >> shift) & mask], 1u);
+            const auto count = [&](int batch, const float (&v)[EB]) {
+                const uint32_t comp = competing(batch);
+#pragma unroll
+                for (int e = 0; e < EB; ++e) {
+                    const uint32_t k = weight_key(v[e]);
+                    // the digits above are thr's (all of a key's, in the first pass)
+                    if (((comp >> e) & 1u) && (shift == 21 || (k >> (shift + width)) == (thr >> (shift + width))))
+                        atomicAdd(&bins[(k >> shift) & mask], 1u);
+                }
             };
 #pragma unroll
-            for (int i = 0; i < EB * HELD; ++i)
-                if ((held >> i) & 1u) count(key[i]);
-            for (int b = HELD; b * BATCH < mid1; ++b)
-                for (int e = 0; e < EB; ++e) {
-                    const int t = token(b, e);
-                    if (t >= mid0 && t < mid1) count(weight_key(w[t]));
-                }
+            for (int b = 0; b < HELD; ++b) count(b, val[b]);
+            for (int b = HELD; b * BATCH < mid1; ++b) {
+                float v[EB];
+                load(b, v);
+                count(b, v);
+            }
             sync_row();
             if constexpr (CL > 1) {
                 // this CTA's share of the bins, summed over the cluster and sent to every CTA
@@ -161,8 +183,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS) evict_sele
             uint32_t mine[PER_BIN], sum = 0u;
 #pragma unroll
             for (int i = 0; i < PER_BIN; ++i) {
-                const int at = BINS - 1 - (tid * PER_BIN + i);
-                mine[i] = CL > 1 ? sums[at] : bins[at];
+                mine[i] = sums[BINS - 1 - (tid * PER_BIN + i)];
                 sum += mine[i];
             }
             uint32_t incl = sum;
@@ -190,72 +211,82 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS) evict_sele
         }
         ties = exact ? 0u : left;
     }
+    // what stays outright has a key from `from` on (no weight has the key 2^32 - 1)
+    const uint32_t from = exact ? thr : thr + 1u;
 
+    if (CL > 1 && need == 0) sync_row();  // the other CTAs run, and so can be stored to
+    uint32_t *const out_pos = shared, *const out_weight = shared + PART;
     uint32_t done = 0u, ties_done = 0u;  // tokens kept outright / equal to the threshold, before this batch
-    for (int b = 0; b * BATCH < len; ++b) {
-        float val[EB];
-#pragma unroll
-        for (int e = 0; e < EB; ++e) val[e] = token(b, e) < len ? w[token(b, e)] : 0.f;
-        uint32_t in_mask[EB], tie_mask[EB];  // the warp's tokens e: stays outright / equals the threshold
+    const auto emit = [&](int b, const float (&v)[EB]) {
+        const int t0 = first_of(b);
+        const uint32_t comp = competing(b);
+        uint32_t in = below(len - t0) & ~comp, tie = 0u;
 #pragma unroll
         for (int e = 0; e < EB; ++e) {
-            const int t = token(b, e);
-            const uint32_t k = weight_key(val[e]);
-            const bool fixed = t < len && (all || t < mid0 || t >= mid1);
-            const bool competes = need > 0 && t >= mid0 && t < mid1;
-            in_mask[e] = __ballot_sync(0xffffffffu, fixed || (competes && (exact ? k >= thr : k > thr)));
-            tie_mask[e] = __ballot_sync(0xffffffffu, competes && !exact && k == thr);
-            if (lane == 0) totals[e * WARPS + warp] = __popc(in_mask[e]) | (__popc(tie_mask[e]) << 16);
+            const uint32_t k = weight_key(v[e]);
+            in |= static_cast<uint32_t>(k >= from) << e & comp;
+            tie |= static_cast<uint32_t>(k == thr) << e & comp;
         }
+        if (exact) tie = 0u;
+        // (outright, ties) before this thread's tokens: each half of a sum stays below 2^16
+        const uint32_t own = __popc(in) | (__popc(tie) << 16);
+        uint32_t incl = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        if (lane == 31) warp_sum[warp] = incl;
         __syncthreads();
-        if (warp == 0) {  // each half of a sum stays below 2^16
-            constexpr int PER = (EB * WARPS + 31) / 32;
-            uint32_t local[PER], sum = 0u;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int at = lane * PER + i;
-                local[i] = sum;
-                sum += at < EB * WARPS ? totals[at] : 0u;
-            }
-            uint32_t incl = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int at = lane * PER + i;
-                if (at < EB * WARPS) bases[at] = incl - sum + local[i];
-            }
-            if (lane == 31) part_total = incl;
+        const uint32_t ws = lane < WARPS ? warp_sum[lane] : 0u;
+        const uint32_t before = incl - own + __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0u);
+        const uint32_t part = __reduce_add_sync(0xffffffffu, ws);
+        // (two sets of totals in turn: a CTA may be a batch ahead, never two)
+        if constexpr (CL > 1) {
+            if (tid < CL) store_remote(remote(pkv::smem_addr(&totals[b & 1][rank]), tid), part);
         }
         // every weight of this batch is in registers behind this barrier, and ranks only
         // move tokens down: weights_out may be weights
         sync_row();
-        uint32_t in_base = done, tie_base = ties_done;
+        uint32_t in_base = done, tie_base = ties_done;  // before this CTA's part
 #pragma unroll
         for (int c = 0; c < CL; ++c) {
-            const uint32_t v = CL > 1 ? load_remote(remote(pkv::smem_addr(&part_total), c)) : part_total;
+            const uint32_t n = CL > 1 ? totals[b & 1][c] : part;
             if (c < rank) {
-                in_base += v & 0xffffu;
-                tie_base += v >> 16;
+                in_base += n & 0xffffu;
+                tie_base += n >> 16;
             }
-            done += v & 0xffffu;
-            ties_done += v >> 16;
+            done += n & 0xffffu;
+            ties_done += n >> 16;
         }
+        const uint32_t ties_out = min(tie_base, ties);  // of the ties before the part, those that stay
+        const uint32_t base = in_base + ties_out;
+        const uint32_t kept_here = (part & 0xffffu) + min(tie_base + (part >> 16), ties) - ties_out;
+        uint32_t tie_at = tie_base + (before >> 16);
+        uint32_t at = (before & 0xffffu) + min(tie_at, ties) - ties_out;
 #pragma unroll
         for (int e = 0; e < EB; ++e) {
-            const uint32_t before = bases[e * WARPS + warp], mask = (1u << lane) - 1u;
-            const uint32_t in_before = in_base + (before & 0xffffu) + __popc(in_mask[e] & mask);
-            const uint32_t tie_before = tie_base + (before >> 16) + __popc(tie_mask[e] & mask);
-            if (((in_mask[e] >> lane) & 1u) || (((tie_mask[e] >> lane) & 1u) && tie_before < ties)) {
-                const uint32_t rank_of = in_before + min(tie_before, ties);
-                kept[rank_of] = token(b, e);
-                if (wout) wout[rank_of] = val[e];
+            const bool is_tie = (tie >> e) & 1u;
+            if (((in >> e) & 1u) || (is_tie && tie_at < ties)) {
+                out_pos[at] = t0 + e;
+                if (wout) out_weight[at] = __float_as_uint(v[e]);
+                ++at;
             }
+            tie_at += is_tie;
         }
-        sync_row();  // before the shared counts change, or a CTA whose counts are read exits
+        __syncthreads();
+        for (uint32_t i = tid; i < kept_here; i += THREADS) {
+            kept[base + i] = static_cast<int32_t>(out_pos[i]);
+            if (wout) wout[base + i] = __uint_as_float(out_weight[i]);
+        }
+    };
+#pragma unroll
+    for (int b = 0; b < HELD; ++b)
+        if (b * BATCH < len) emit(b, val[b]);
+    for (int b = HELD; b * BATCH < len; ++b) {
+        float v[EB];
+        load(b, v);
+        emit(b, v);
     }
     if (wout)
         for (int i = keep + rtid; i < len; i += CL * THREADS) wout[i] = 0.f;  // slots the next tokens take
@@ -384,12 +415,13 @@ PKV_API pkv_status pkv_evict_select(const float *weights, int64_t weights_stride
     p.sinks = sinks;
     p.recent = recent;
     p.num_kv_heads = num_kv_heads;
+    p.vectors = weights_stride % 4 == 0 && pkv::aligned16(weights);
     const dim3 grid(static_cast<unsigned>(num_kv_heads), static_cast<unsigned>(num_seqs));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // Rows past 8192 tokens spread over a cluster as large as leaves every cluster resident
     // at once (two CTAs per SM): one CTA would work through the row on one SM, but a second
     // wave of clusters would wait for the first.  (Rows of 32768, this rule against always
-    // eight: 72 rows 25 us / 36 us, 152 rows 45 / 73, 512 rows 130 / 223.)
+    // eight: 72 rows 20 us / 34 us, 152 rows 29 / 61, 512 rows 80 / 191.)
     if (max_context_len <= 1024) {
         evict_select_kernel<256, 4, 1, 1><<<grid, 256, 0, s>>>(p);
     } else if (max_context_len <= 8192) {

@@ -68,6 +68,30 @@ def test_select_over_rows_longer_than_the_registers_hold(kind):
     _select(dev, w, lens, 9000, 16, 1000, in_place=kind == "ties")
 
 
+@pytest.mark.parametrize("budget,sinks,recent", [(40000, 3, 100), (39999, 0, 0), (12000, 5000, 7000), (12000, 0, 12000)])
+@pytest.mark.parametrize("width", [40000, 40003])
+def test_select_of_long_rows_that_stay_whole_or_leave_no_choice(budget, sinks, recent, width):
+    dev = device()
+    lens = [40000, 39999, 33000, 3]
+    w = _weights("tail", (4, 2, width), torch.Generator().manual_seed(budget))
+    for in_place in (False, True):
+        _select(dev, w, lens, budget, sinks, recent, in_place=in_place)
+
+
+@pytest.mark.parametrize("n", [9, 1000, 5001, 20000])
+def test_select_of_weights_at_any_alignment(n):
+    dev = device()
+    flat = _weights("signed", (3 * n + 4,), torch.Generator().manual_seed(n)).to(dev)
+    lens = torch.tensor([n], dtype=torch.int32, device=dev)
+    for at in range(4):
+        w = flat[at:at + 3 * n].view(1, 3, n)
+        kept, _ = pkv.evict_select(w, lens, n // 2, sinks=1, recent=2)
+        torch.cuda.synchronize()
+        ref, _ = refs.select(w.cpu(), [n], n // 2, 1, 2)
+        assert torch.equal(kept.cpu(), ref)
+    check_no_device_flags(dev)
+
+
 @pytest.mark.parametrize("rows", [40, 60, 100, 200])
 def test_select_of_many_long_rows(rows):
     """Enough rows past 8192 tokens for clusters of four and two and for one block each; a few rows are checked."""
