@@ -21,14 +21,19 @@
 
 namespace {
 
-constexpr int kThreads = 256;
-// Steps of a thread whose loads are in flight together, and CTAs per SM (48 registers,
+// Threads of a CTA: few tokens, whose CTAs all run at once, take kWide threads each (a
+// token's rows in fewer steps); more take kNarrow, whose CTAs start and end in finer
+// turns.  Measured, wide / narrow: 64 tokens of 32 + 2 x 8 heads of 128 3.1 us / 3.6, 800
+// tokens 6.6 / 5.7, 8192 tokens 38 / 35; 8192 tokens into an INT8 cache 53 / 43.
+constexpr int kWide = 256, kNarrow = 128;
+// Steps of a thread whose loads are in flight together, and threads per SM (48 registers,
 // 64 with the quantiser): the bytes in flight.  Measured on 8192 tokens of 64 + 2 x 8
-// heads: 59 us; four steps and three CTAs 68, one step and six CTAs 70.
+// heads, wide CTAs: 59 us; four steps and 768 threads 68, one step and 1536 threads 70.
 constexpr int kDepth = 2;
-constexpr int kBlocks16 = 5, kBlocksInt8 = 4;
+constexpr int kResident16 = 1280, kResidentInt8 = 1024;
 // Tokens per CTA from kManyTokens tokens on: two share the angles' latency (59.0 us
-// against 59.8 with one, 61.9 with four); below, one, so that the SMs share the work.
+// against 59.8 with one, 61.9 with four, wide CTAs); below, one, so that the SMs share
+// the work.
 constexpr int kTok = 2, kManyTokens = 2048;
 
 // quantize_int8 (pkv_device.cuh) without a division in most cases: the quotient by an
@@ -76,11 +81,11 @@ __device__ __forceinline__ int turn_fraction(double inv_freq, int64_t position) 
 // angles are the same in every row of a token and a rotation never crosses threads.
 // The rows are the q heads, then K, then V; a thread's first rows are loaded before
 // the angles are computed, one pair of one token per thread.
-template <typename T, bool QUANT, int D, bool ADJACENT, int TOK>
-__global__ void __launch_bounds__(kThreads, QUANT ? kBlocksInt8 : kBlocks16) rope_reshape_and_cache_kernel(const RopeParams p) {
+template <typename T, bool QUANT, int D, bool ADJACENT, int THREADS, int TOK>
+__global__ void __launch_bounds__(THREADS, (QUANT ? kResidentInt8 : kResident16) / THREADS) rope_reshape_and_cache_kernel(const RopeParams p) {
     constexpr int LANES = D / 16;
-    constexpr int ROWS = kThreads / LANES;  // rows in flight per step
-    static_assert(TOK * (D / 2) <= kThreads, "one thread per angle");
+    constexpr int ROWS = THREADS / LANES;  // rows in flight per step
+    static_assert(TOK * (D / 2) <= THREADS, "one thread per angle");
     __shared__ float2 turn[TOK][D / 2];     // (cos, sin)
     __shared__ int64_t slots[TOK];          // -1: skip
     const int64_t n0 = static_cast<int64_t>(blockIdx.x) * TOK;
@@ -224,24 +229,24 @@ __global__ void __launch_bounds__(kThreads, QUANT ? kBlocksInt8 : kBlocks16) rop
 }
 
 template <typename T, bool QUANT, int D, bool ADJACENT>
-void launch_rope_form(const RopeParams &p, cudaStream_t s) {
-    if (p.num_tokens >= kManyTokens) {
-        const unsigned grid = static_cast<unsigned>((p.num_tokens + kTok - 1) / kTok);
-        rope_reshape_and_cache_kernel<T, QUANT, D, ADJACENT, kTok><<<grid, kThreads, 0, s>>>(p);
-    } else {
-        rope_reshape_and_cache_kernel<T, QUANT, D, ADJACENT, 1>
-            <<<static_cast<unsigned>(p.num_tokens), kThreads, 0, s>>>(p);
-    }
+void launch_rope_form(const RopeParams &p, int sms, cudaStream_t s) {
+    const unsigned tokens = static_cast<unsigned>(p.num_tokens);
+    if (p.num_tokens <= static_cast<int64_t>(sms) * (QUANT ? kResidentInt8 : kResident16) / kWide)
+        rope_reshape_and_cache_kernel<T, QUANT, D, ADJACENT, kWide, 1><<<tokens, kWide, 0, s>>>(p);
+    else if (p.num_tokens < kManyTokens)
+        rope_reshape_and_cache_kernel<T, QUANT, D, ADJACENT, kNarrow, 1><<<tokens, kNarrow, 0, s>>>(p);
+    else
+        rope_reshape_and_cache_kernel<T, QUANT, D, ADJACENT, kNarrow, kTok><<<(tokens + kTok - 1) / kTok, kNarrow, 0, s>>>(p);
 }
 
 template <typename T, bool QUANT>
-void launch_rope(const RopeParams &p, int head_dim, bool adjacent, cudaStream_t s) {
+void launch_rope(const RopeParams &p, int head_dim, bool adjacent, int sms, cudaStream_t s) {
     if (head_dim == 128) {
-        if (adjacent) launch_rope_form<T, QUANT, 128, true>(p, s);
-        else launch_rope_form<T, QUANT, 128, false>(p, s);
+        if (adjacent) launch_rope_form<T, QUANT, 128, true>(p, sms, s);
+        else launch_rope_form<T, QUANT, 128, false>(p, sms, s);
     } else {
-        if (adjacent) launch_rope_form<T, QUANT, 64, true>(p, s);
-        else launch_rope_form<T, QUANT, 64, false>(p, s);
+        if (adjacent) launch_rope_form<T, QUANT, 64, true>(p, sms, s);
+        else launch_rope_form<T, QUANT, 64, false>(p, sms, s);
     }
 }
 
@@ -278,7 +283,8 @@ pkv_status rope_impl(const void *q, int64_t q_stride, const void *k_new, int64_t
         (reinterpret_cast<uintptr_t>(axis_of_pair) & 3u))
         return PKV_ERR_INVALID_ARG;
     unsigned int *status = pkv::status_word_ptr();
-    if (!status) return PKV_ERR_CUDA;
+    const int sms = pkv::current_sm_count();
+    if (!status || sms <= 0) return PKV_ERR_CUDA;
     RopeParams p{};
     p.q = static_cast<const char *>(q);
     p.k_new = static_cast<const char *>(k_new);
@@ -308,11 +314,11 @@ pkv_status rope_impl(const void *q, int64_t q_stride, const void *k_new, int64_t
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool adjacent = interleaved != 0;
     if (dtype == PKV_F16) {
-        if (int8_kv) launch_rope<__half, true>(p, head_dim, adjacent, s);
-        else launch_rope<__half, false>(p, head_dim, adjacent, s);
+        if (int8_kv) launch_rope<__half, true>(p, head_dim, adjacent, sms, s);
+        else launch_rope<__half, false>(p, head_dim, adjacent, sms, s);
     } else {
-        if (int8_kv) launch_rope<__nv_bfloat16, true>(p, head_dim, adjacent, s);
-        else launch_rope<__nv_bfloat16, false>(p, head_dim, adjacent, s);
+        if (int8_kv) launch_rope<__nv_bfloat16, true>(p, head_dim, adjacent, sms, s);
+        else launch_rope<__nv_bfloat16, false>(p, head_dim, adjacent, sms, s);
     }
     pkv::count_launch();
     return pkv::launch_status();

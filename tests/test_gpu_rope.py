@@ -100,10 +100,11 @@ def test_one_axis_in_place_and_skipped_tokens():
 
 @pytest.mark.parametrize("int8", [False, True], ids=["16bit", "int8"])
 @pytest.mark.parametrize("d,interleaved", [(64, False), (128, True)])
-def test_an_odd_chunk_of_many_tokens(d, interleaved, int8):
-    """Enough tokens for two per block, the last block with one."""
+@pytest.mark.parametrize("tokens", [1300, 2049])
+def test_an_odd_chunk_of_many_tokens(tokens, d, interleaved, int8):
+    """Enough tokens for narrow blocks, and for two tokens per block with one in the last."""
     dev = device()
-    c = _case(dev, 2049, 3, 1, d, 16, torch.bfloat16, 2, d, seed=10, int8=int8)
+    c = _case(dev, tokens, 3, 1, d, 16, torch.bfloat16, 2, d, seed=10, int8=int8)
     if not int8:
         slots = c["slots"].clone()
         slots[5::11] = -1
