@@ -1222,8 +1222,7 @@ __global__ void __launch_bounds__(384, 1)
 
 // The item table of the planned order: one entry per row tile that holds work, sorted by
 // KV tiles, most first (a counting sort; the order among equals is free).  One block: a
-// row tile's first visible token is the minimum over its rows' starts, gathered row by
-// row in shared memory.  A sequence out of contract is flagged and gets no entry.
+// row tile's first visible token is the minimum over its rows' starts, by a warp.  A sequence out of contract is flagged and gets no entry.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBuckets = 1024;
 inline __global__ void __launch_bounds__(kPlanThreads) paged_prefill_plan_kernel(const PrefillParams p, PrefillPlan *plan) {
@@ -1234,26 +1233,28 @@ inline __global__ void __launch_bounds__(kPlanThreads) paged_prefill_plan_kernel
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int count = p.num_seqs * p.row_tiles;  // <= kMaxPlanEntries
-    for (int e = tid; e < count; e += kPlanThreads) first[e] = p.starts ? 0x7fffffff : 0;
     bucket[tid] = 0;
-    __syncthreads();
     if (p.starts) {
-        for (int row = tid; row < p.num_rows; row += kPlanThreads) {
-            int a = 0, b = p.num_seqs - 1;  // the last sequence whose chunk starts at or before the row
-            while (a < b) {
-                const int m = (a + b + 1) / 2;
-                if (p.query_start[m] <= row) a = m;
-                else b = m - 1;
+        // a warp per row tile (several in flight)
+#pragma unroll 4
+        for (int e = warp; e < count; e += kPlanThreads / 32) {
+            const int seq = fast_div(e, p.div_row_tiles), rt = e - seq * p.row_tiles;
+            const PrefillSeqVals sv{p.query_start[seq], p.query_start[seq + 1], p.context_lens[seq]};
+            int q0, chunk, len, least = 0x7fffffff;
+            if (prefill_seq(p, sv, q0, chunk, len)) {
+                const int j1 = min(chunk, (rt + 1) * p.tile_tokens);
+                for (int j = rt * p.tile_tokens + lane; j < j1; j += 32) least = min(least, p.starts[q0 + j]);
             }
-            const int j = row - p.query_start[a];
-            if (j >= 0 && row < p.query_start[a + 1] && j < p.qlen_cap)
-                atomicMin(&first[a * p.row_tiles + j / p.tile_tokens], p.starts[row]);
+            least = __reduce_min_sync(0xffffffffu, least);
+            if (lane == 0) first[e] = least;
         }
-        __syncthreads();
+    } else {
+        for (int e = tid; e < count; e += kPlanThreads) first[e] = 0;
     }
+    __syncthreads();
     // entry e of this thread: its range, and its bucket by KV tiles
     const auto make = [&](int e, PrefillEntry &v) -> int {  // KV tiles, or -1: no entry
-        const int seq = e / p.row_tiles, rt = e - seq * p.row_tiles;
+        const int seq = fast_div(e, p.div_row_tiles), rt = e - seq * p.row_tiles;
         const PrefillSeqVals sv{p.query_start[seq], p.query_start[seq + 1], p.context_lens[seq]};
         int q0, chunk, len;
         if (!prefill_seq(p, sv, q0, chunk, len)) return -1;
@@ -1268,10 +1269,15 @@ inline __global__ void __launch_bounds__(kPlanThreads) paged_prefill_plan_kernel
         v = PrefillEntry{q0, chunk, len, seq, rt, lo, begin, hi};
         return max(1, (hi - begin + 127) / 128);
     };
-    PrefillEntry v{};
+    PrefillEntry v{}, mine0{};  // mine0: entry tid, kept for the second pass
+    int n0 = -1;
     for (int e = tid; e < count; e += kPlanThreads) {
-        const int seq = e / p.row_tiles;
+        const int seq = fast_div(e, p.div_row_tiles);
         const int n = make(e, v);
+        if (e == tid) {
+            mine0 = v;
+            n0 = n;
+        }
         if (n > 0) {
             atomicAdd(&bucket[max(0, kPlanBuckets - n)], 1);  // bucket 0: the most tiles
         } else if (e == seq * p.row_tiles) {
@@ -1291,14 +1297,14 @@ inline __global__ void __launch_bounds__(kPlanThreads) paged_prefill_plan_kernel
     }
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    int before = incl - mine;
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    const int before = incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0);
     bucket[tid] = before;
     if (tid == kPlanThreads - 1) total = before + mine;
     __syncthreads();
     for (int e = tid; e < count; e += kPlanThreads) {
-        const int n = make(e, v);
+        const int n = e == tid ? n0 : make(e, v);
         if (n <= 0) continue;
+        if (e == tid) v = mine0;
         int4 *dst = reinterpret_cast<int4 *>(plan->entry + atomicAdd(&bucket[max(0, kPlanBuckets - n)], 1));
         dst[0] = make_int4(v.q0, v.chunk, v.len, v.seq);
         dst[1] = make_int4(v.row_tile, v.lo, v.tok_lo, v.tok_hi);
