@@ -300,7 +300,8 @@ struct CompactParams {
     const int32_t *context_lens, *kept, *kept_lens;
     unsigned int *status;
     int64_t num_blocks, block_stride;  // bytes
-    int src_stride, dst_stride, budget, num_kv_heads, block_size, src_cap, dst_cap;
+    int src_stride, dst_stride, budget, num_kv_heads, src_cap, dst_cap;
+    int block_shift;  // log2 of the block size
 };
 
 constexpr int kMoveThreads = 256;
@@ -308,7 +309,8 @@ constexpr int kMoveUnroll = 4;
 
 // The bytes of token row (block, head, offset) of one pool half.
 __device__ __forceinline__ int64_t row_offset(const CompactParams &p, int blk, int h, int t, int row_bytes) {
-    return static_cast<int64_t>(blk) * p.block_stride + (static_cast<int64_t>(h) * p.block_size + t % p.block_size) * row_bytes;
+    return static_cast<int64_t>(blk) * p.block_stride +
+           ((static_cast<int64_t>(h) << p.block_shift) + (t & ((1 << p.block_shift) - 1))) * row_bytes;
 }
 
 // Moves token row kept[i] to position i.  VECS 16-byte vectors of a row per CTA
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
                 pkv::raise_flag(p.status, PKV_DEVERR_KEPT);
                 continue;
             }
-            const int sb = src_table[t / p.block_size], db = dst_table[i / p.block_size];
+            const int sb = src_table[t >> p.block_shift], db = dst_table[i >> p.block_shift];
             if (sb < 0 || sb >= p.num_blocks || db < 0 || db >= p.num_blocks) {
                 pkv::raise_flag(p.status, PKV_DEVERR_BLOCK_TABLE);
                 continue;
@@ -482,7 +484,7 @@ PKV_API pkv_status pkv_evict_compact(void *k_cache, void *v_cache, int64_t num_b
     p.dst_stride = in_place ? max_blocks_per_seq : dst_max_blocks_per_seq;
     p.budget = budget;
     p.num_kv_heads = num_kv_heads;
-    p.block_size = block_size;
+    p.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
     p.src_cap = capacity(max_blocks_per_seq);
     p.dst_cap = capacity(p.dst_stride);
     const int max_kept = std::min(budget, std::min(p.src_cap, p.dst_cap));
