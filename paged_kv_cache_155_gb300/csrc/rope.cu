@@ -62,7 +62,8 @@ struct RopeParams {
     int64_t num_tokens;
     int64_t q_stride, k_stride, v_stride, q_out_stride;  // bytes between tokens
     int64_t num_slots, block_stride;                     // block_stride in bytes
-    int num_axes, pairs, num_q_heads, num_kv_heads, block_size;
+    int num_axes, pairs, num_q_heads, num_kv_heads;
+    int block_shift;                                     // log2 of the block size
 };
 
 // Fraction of a turn that pair i of token n has made, as a signed 32-bit fixed-point
@@ -189,10 +190,10 @@ __global__ void __launch_bounds__(THREADS, (QUANT ? kResidentInt8 : kResident16)
         }
         const bool is_v = r >= rows_k;
         const int h = is_v ? r - rows_k : r - rows_q;
-        const int64_t blk = slot / p.block_size;
-        const int off = static_cast<int>(slot - blk * p.block_size);
+        const int64_t blk = slot >> p.block_shift;
+        const int off = static_cast<int>(slot & ((1 << p.block_shift) - 1));
         char *row = (is_v ? p.v_cache : p.k_cache) + blk * p.block_stride +
-                    (static_cast<int64_t>(h) * p.block_size + off) * (D * (QUANT ? 1 : 2));
+                    ((static_cast<int64_t>(h) << p.block_shift) + off) * (D * (QUANT ? 1 : 2));
         if constexpr (QUANT) {
             const float *scale = (is_v ? p.v_scale : p.k_scale) + h * D;
 #pragma unroll
@@ -310,7 +311,7 @@ pkv_status rope_impl(const void *q, int64_t q_stride, const void *k_new, int64_t
     p.pairs = rotary_dim / 2;
     p.num_q_heads = num_q_heads;
     p.num_kv_heads = num_kv_heads;
-    p.block_size = block_size;
+    p.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool adjacent = interleaved != 0;
     if (dtype == PKV_F16) {
