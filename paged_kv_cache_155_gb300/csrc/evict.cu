@@ -304,8 +304,10 @@ struct CompactParams {
     int block_shift;  // log2 of the block size
 };
 
-constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;
+// In place, a CTA's tiles follow one another: larger ones (the same 268 MB: 256 threads 61
+// us, 512 58, 1024 74; 34 MB of four sequences 16.5 / 11.2 / 11.1).
+__host__ __device__ constexpr int move_threads(bool in_place) { return in_place ? 512 : 128; }
 
 // The bytes of token row (block, head, offset) of one pool half.
 __device__ __forceinline__ int64_t row_offset(const CompactParams &p, int blk, int h, int t, int row_bytes) {
@@ -321,12 +323,14 @@ __device__ __forceinline__ int64_t row_offset(const CompactParams &p, int blk, i
 // read, never a later tile's sources -- one barrier between a tile's loads and its
 // stores orders them, and column groups never meet.
 // Bound by memory: rows of 256 bytes gathered at random, read and written once
-// (streaming loads and stores: 50 us, plain ones 53).  Measured into fresh blocks: 268 MB
-// moved in 50 us, 5.3 TB/s, 0.79 of the copy rate of large contiguous arrays; eight, two
-// or one row per thread and the heads fastest in the grid: 60 / 51 / 57 / 50.
+// (plain loads and stores instead of streaming ones: 6% slower).  Measured into fresh
+// blocks: 268 MB moved in 44 us, 6.0 TB/s, 0.89 of the copy rate of large contiguous
+// arrays; eight or two rows per thread 52 / 49, 256 threads instead of 128 44.6, block
+// offsets by division instead of shifts 50 (the kept rows' order hardly matters: adjacent
+// ones 44).
 template <int ROW_VECS, int VECS, bool IN_PLACE>
-__global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const CompactParams p) {
-    constexpr int ROWS = kMoveThreads / VECS, TILE = ROWS * kMoveUnroll, GROUPS = ROW_VECS / VECS;
+__global__ void __launch_bounds__(move_threads(IN_PLACE)) evict_compact_kernel(const CompactParams p) {
+    constexpr int ROWS = move_threads(IN_PLACE) / VECS, TILE = ROWS * kMoveUnroll, GROUPS = ROW_VECS / VECS;
     pkv::pdl_wait();  // launched ahead of the kernel before it (the choice of what to keep)
     const int h = blockIdx.y, seq = blockIdx.z;
     const int half = blockIdx.x % 2, group = (blockIdx.x / 2) % GROUPS, tile0 = blockIdx.x / (2 * GROUPS);
@@ -377,11 +381,11 @@ cudaError_t launch_compact(const CompactParams &p, bool in_place, int max_kept, 
     if (in_place) {
         constexpr int VECS = ROW_VECS < 4 ? ROW_VECS : 4;  // 64-byte columns: more chains, whole sectors
         const dim3 grid(2 * (ROW_VECS / VECS), p.num_kv_heads, num_seqs);
-        return pkv::launch_kernel(evict_compact_kernel<ROW_VECS, VECS, true>, grid, dim3(kMoveThreads), 0, s, true, p);
+        return pkv::launch_kernel(evict_compact_kernel<ROW_VECS, VECS, true>, grid, dim3(move_threads(true)), 0, s, true, p);
     } else {
-        constexpr int TILE = kMoveThreads / ROW_VECS * kMoveUnroll;
+        constexpr int TILE = move_threads(false) / ROW_VECS * kMoveUnroll;
         const dim3 grid(2 * ((max_kept + TILE - 1) / TILE), p.num_kv_heads, num_seqs);
-        return pkv::launch_kernel(evict_compact_kernel<ROW_VECS, ROW_VECS, false>, grid, dim3(kMoveThreads), 0, s, true, p);
+        return pkv::launch_kernel(evict_compact_kernel<ROW_VECS, ROW_VECS, false>, grid, dim3(move_threads(false)), 0, s, true, p);
     }
 }
 
