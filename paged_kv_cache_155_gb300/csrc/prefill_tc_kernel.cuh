@@ -22,7 +22,7 @@
 // per tile); the row's reference maximum moves only when a tile exceeds it by
 // more than kRescaleLog2.  The row sum l adds the fp32 weights whose bf16/fp16
 // roundings feed the PV MMA (unbiased rounding, relative error 2^-9 per weight
-// at most).  With one split the kernel writes the normalised output; with
+// at most; the scored bf16 forms add the rounded ones, add_bf16x2).  With one split the kernel writes the normalised output; with
 // several it writes (o, m, l) partials that paged_prefill_merge_kernel
 // combines.
 //
@@ -422,6 +422,16 @@ __device__ constexpr float kTanh3[3] = {0.9999995827674866f, -0.3332192897796631
 
 // The lowest n bits of a word (n <= 0: none, n >= 32: all).
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// (l0, l1) += two packed bf16 values, in fp32: the scored forms' row sum adds the weights as
+// the PV MMA takes them, so that a row of few tokens, whose roundings do not average out, is
+// divided by what it multiplied -- one visible token returns its V row.  (bf16 only: fp16
+// weights are rounded eight times finer.  The adds take the rounded halves as they are;
+// unpacking them cost 6% on 17-tile items, this 2%.)
+__device__ __forceinline__ void add_bf16x2(float &l0, float &l1, uint32_t v) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.f32.bf16 %0, a, %0;\n\tadd.f32.bf16 %1, b, %1;\n\t}"
+        : "+f"(l0), "+f"(l1) : "r"(v));
+}
 
 // x <- x R(x^2) - shift, R of N terms whose coefficients are scaled to give scale_log2 x at
 // small x.
@@ -1099,8 +1109,9 @@ __global__ void __launch_bounds__(384, 1)
                                 p0 = t < vh ? p0 : 0.f;
                                 p1 = t + 1 < vh ? p1 : 0.f;
                             }
-                            add_f32x2(l0, l1, p0, p1);
                             packed[i] = Elem<T>::pack2(p0, p1);
+                            if constexpr (kScored && kBF16) add_bf16x2(l0, l1, packed[i]);
+                            else add_f32x2(l0, l1, p0, p1);
                         }
                         tc::tmem_st_x16(pcol + 16 * c16, packed);
                     }

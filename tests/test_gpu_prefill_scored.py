@@ -142,6 +142,21 @@ def test_window_borders(hq, hkv, bs, splits, window):
     check(c, run(dev, c, window=window, splits=splits), window=window, step=7)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("softcap,biased", [(5.0, False), (50.0, False), (100.0, False), (50.0, True), (0.0, True)])
+@pytest.mark.parametrize("splits", [0, 2])
+def test_one_visible_token_returns_its_value(splits, softcap, biased, dtype):
+    """The weight's rounding is divided out again: P V / P, off by 2^-22 of itself at most, rounds back to V."""
+    dev = device()
+    c = make([0, 130, 37], [150, 3, 64], 8, 2, 16, dtype, 7)
+    out = run(dev, c, softcap, SLOPES(8) if biased else None, 1, splits=splits).cpu()
+    for i in range(3):
+        for j in range(c["chunks"][i]):
+            row, pos, _, _ = bounds(c, i, j, 1, None, None)
+            v = c["kv"][c["tables"][i, pos // 16], 1, :, pos % 16]
+            assert torch.equal(out[row], v.repeat_interleave(4, 0))
+
+
 def test_documents_with_poison_before_them():
     """One sequence's rows all in its last document, whose start lies inside a block and a tile."""
     dev = device()
