@@ -21,7 +21,7 @@
 // row's softmax is local to one thread pair (its scores are read from TMEM once
 // per tile); the row's reference maximum moves only when a tile exceeds it by
 // more than kRescaleLog2.  The row sum l adds the fp32 weights whose bf16/fp16
-// roundings feed the PV MMA (unbiased rounding, relative error 2^-9 per weight
+// roundings feed the PV MMA (unbiased rounding, relative error 2^-8 per weight
 // at most; the scored bf16 forms add the rounded ones, add_bf16x2).  With one split the kernel writes the normalised output; with
 // several it writes (o, m, l) partials that paged_prefill_merge_kernel
 // combines.
