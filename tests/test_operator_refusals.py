@@ -255,3 +255,13 @@ def test_block_manager_make_private_and_truncate():
     bm.free_sequence(1)
     assert bm.num_free == 10
     assert isinstance(pairs, np.ndarray)
+
+
+def test_a_prepared_call_passes_the_same_values_converted(lib):
+    """From its second call on a prepared call passes the ctypes values of its arguments: a call of no tokens, by both."""
+    args = (1 << 20, 4096, 1 << 21, 1024, 1 << 40, 1024, 1 << 23, 3, None, 1 << 25, 128, True, 1 << 26, 0, 1 << 27, 4096,
+            1 << 28, 1 << 29, 100, 65536, 32, 8, 128, 16, 0)
+    call = pkv.ops.PreparedCall("pkv_rope_reshape_and_cache", args, torch.device("cuda", 0), ())
+    typed = call._typed_args()
+    assert [t.value for t in typed] == list(args)
+    assert lib.pkv_rope_reshape_and_cache(*args, 0) == lib.pkv_rope_reshape_and_cache(*typed, 0) == 0
