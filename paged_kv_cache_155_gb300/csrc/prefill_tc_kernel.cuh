@@ -435,14 +435,17 @@ __device__ __forceinline__ void add_bf16x2(float &l0, float &l1, uint32_t v) {
 
 // x <- x R(x^2) - shift, R of N terms whose coefficients are scaled to give scale_log2 x at
 // small x.
-template <int N>
-__device__ __forceinline__ void cap_poly(const PrefillParams &p, const float (&terms)[N], float (&x)[64]) {
+template <int N, typename F>
+__device__ __forceinline__ void cap_poly(const PrefillParams &p, F &&term, float (&x)[64]) {
     const float k2 = p.cap_in * p.cap_in;
     float k = p.scale_log2;
     const F32x2 shift = pack_f32(-p.shift, -p.shift);
     F32x2 c[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j, k *= k2) c[j] = pack_f32(k * terms[j], k * terms[j]);
+    for (int j = 0; j < N; ++j, k *= k2) {
+        const float t = k * term(j);
+        c[j] = pack_f32(t, t);
+    }
 #pragma unroll
     for (int i = 0; i < 64; i += 2) {
         const F32x2 v = pack_f32(x[i], x[i + 1]);
@@ -457,28 +460,79 @@ __device__ __forceinline__ void cap_poly(const PrefillParams &p, const float (&t
 // Raw scores of a row -> capped scores in log2 units, less the fixed reference (p.shift,
 // else 0): cap * tanh(s / cap) with s = scale * x is x R(x^2), R a polynomial of tanh(z)/z
 // whose coefficients are scaled to take x itself: no exponential, where the softmax
-// already spends one.  A warp takes a short R when its scores stay far below the cap (and
-// the cap is small enough for that fit's error to stay below 2.5e-5 of a score), the
-// six-term one within three quarters, and beyond that the closed form
-// cap (1 - 2 / (1 + e^(2 z))), an exponential and a reciprocal more.  The choice looks at
-// every column: those without a token hold 0 (the QK^T issuer zeroes their K rows), not
-// what an earlier tile left there, or the last bits of a result would depend on it.
-__device__ __forceinline__ void cap_scores(const PrefillParams &p, float (&x)[64]) {
+// already spends one.  A row takes a short R when the scores that it sees stay far below
+// the cap (and the cap is small enough for that fit's error to stay below 2.5e-5 of a
+// score), else the six-term one, and beyond three quarters of the cap the closed form
+// cap (1 - 2 / (1 + e^(2 z))), an exponential and a reciprocal more: for those scores
+// alone, or with a small cap (an absolute error of 2^-22 cap_out <= 5e-5) the whole row.
+// The choice is the row's own, by the columns that it sees (bits of seen0, seen1): a short
+// R is the long one with zeros for its last terms, which changes no bit, so the warp runs
+// what its most demanding row needs and no result depends on the rows beside it, on hidden
+// tokens, or on what an earlier tile left in columns without a token.  The closed form
+// walks the scores again where they lie in TMEM (at `scores`), in a loop: unrolled over the
+// registers it cost the other branches 4 to 9%, by its size alone.
+// Measured (8 chunks of 512 behind 7680 tokens, 64 / 8 heads, window 2048, cap 50; against a
+// choice by all rows and columns of the warp): bf16 265 us / 261, fp16 334 / 324; with cap 3,
+// where most rows take the closed form, 434 / 379.
+__device__ __forceinline__ void cap_scores(const PrefillParams &p, float (&x)[64], bool full, uint32_t seen0,
+                                           uint32_t seen1, uint32_t scores) {
+    if (!full) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) x[i] = ((i < 32 ? seen0 : seen1) >> (i % 32)) & 1u ? x[i] : 0.f;
+    }
     float big = fmaxf(fabsf(x[0]), fabsf(x[1]));
 #pragma unroll
     for (int i = 2; i < 64; i += 2) big = fmax3(big, fabsf(x[i]), fabsf(x[i + 1]));
     big *= fabsf(p.cap_in);
-    if (__all_sync(0xffffffffu, big <= 0.25f && p.cap_short)) {
-        cap_poly<3>(p, kTanh3, x);
-    } else if (__all_sync(0xffffffffu, big <= 0.45f && p.cap_short)) {
-        cap_poly<4>(p, kTanh4, x);
-    } else if (__all_sync(0xffffffffu, big <= 0.75f)) {
-        cap_poly<6>(p, kTanh6, x);
+    const bool three = big <= 0.25f && p.cap_short, four = big <= 0.45f && p.cap_short;
+    if (__all_sync(0xffffffffu, three)) {
+        cap_poly<3>(p, [&](int j) { return kTanh3[j % 3]; }, x);
+    } else if (__all_sync(0xffffffffu, four)) {
+        cap_poly<4>(p, [&](int j) { return three ? (j < 3 ? kTanh3[j % 3] : 0.f) : kTanh4[j % 4]; }, x);
     } else {
-        const float k = p.cap_in * 2.885390081777927f;  // 2 log2(e) / cap
+        const auto term = [&](int j) {
+            return three ? (j < 3 ? kTanh3[j % 3] : 0.f) : four ? (j < 4 ? kTanh4[j % 4] : 0.f) : kTanh6[j];
+        };
+        if (__all_sync(0xffffffffu, big <= 0.75f)) {
+            cap_poly<6>(p, term, x);
+            return;
+        }
+        // (a row that sees nothing takes any form)
+        const bool far = p.cap_short && (big > 0.75f || !(seen0 | seen1));
+        const bool all_far = __all_sync(0xffffffffu, far);
+        float c[6], k = p.scale_log2;
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-            x[i] = (p.cap_out - p.shift) - 2.f * p.cap_out * fast_rcp(1.f + fast_exp2(x[i] * k));
+        for (int j = 0; j < 6; ++j, k *= p.cap_in * p.cap_in) c[j] = k * term(j);
+#pragma unroll 1
+        for (int at = 0; at < 64; at += 16) {
+            float y[16], z[16];
+            uint32_t w[16];
+            tc::tmem_ld_x16(scores + at, y);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                z[i] = y[i] * p.cap_in;
+                w[i] = __float_as_uint((p.cap_out - p.shift) -
+                                       2.f * p.cap_out * fast_rcp(1.f + fast_exp2(z[i] * 2.885390081777927f)));
+            }
+            if (!all_far) {
+                const float most = far ? -1.f : 0.75f;  // the |z| that the polynomial takes
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float u = y[i] * y[i];
+                    float q = fmaf(u, c[5], c[4]);
+#pragma unroll
+                    for (int j = 3; j >= 0; --j) q = fmaf(u, q, c[j]);
+                    q = fmaf(y[i], q, -p.shift);
+                    w[i] = fabsf(z[i]) <= most ? __float_as_uint(q) : w[i];
+                }
+            }
+            tc::tmem_st_x16(scores + at, w);
+        }
+        tc::tmem_st_wait();
+#pragma unroll
+        for (int at = 0; at < 64; at += 16) tc::tmem_ld_x16(scores + at, x + at);
+        tc::tmem_ld_wait();
     }
 }
 
@@ -493,9 +547,10 @@ __device__ __forceinline__ void hide(float (&x)[64], uint32_t seen0, uint32_t se
 // position) -> scores in log2 units, capped and biased; returns the factor that is left
 // to apply (scale_log2, when neither is asked for; else 1).
 template <bool kCapped>
-__device__ __forceinline__ float score_row(const PrefillParams &p, float (&x)[64], float slope2, int dist0) {
+__device__ __forceinline__ float score_row(const PrefillParams &p, float (&x)[64], float slope2, int dist0, bool full,
+                                           uint32_t seen0, uint32_t seen1, uint32_t scores) {
     if constexpr (kCapped) {
-        cap_scores(p, x);
+        cap_scores(p, x, full, seen0, seen1, scores);
         if (!p.slopes) return 1.f;
     } else {
         if (!p.slopes && p.scale_log2 > 0.f) return p.scale_log2;  // (a negative scale would turn maxima into minima)
@@ -800,21 +855,6 @@ __global__ void __launch_bounds__(384, 1)
                     ok = false;
                     break;
                 }
-                if constexpr (kCapped) {
-                    // K rows past the tile's tokens -> 0, so that their scores are 0 (cap_scores);
-                    // here, where S buffers wait filled, rather than in the softmax warps (15 us of
-                    // 263 on 17-tile items there)
-                    const int valid = it.tok_hi - (it.tok_lo + j * TILE);
-                    if (valid < TILE) {
-                        __syncwarp();
-                        unsigned char *slot = sm + L::kOffK + (jt % KS) * L::kPanel;
-                        for (int i = valid * 16 + lane; i < TILE * 16; i += 32)
-                            *reinterpret_cast<uint4 *>(slot + ((i >> 3) & 1) * L::kHalf + (i >> 4) * 128 + (i & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
-                        fence_proxy_async_smem();  // visible to the MMA
-                        __syncwarp();
-                    }
-                }
                 if (lane == 0) {
                     const int b = jt % SB;
                     tc::fence_after_sync();
@@ -1013,8 +1053,9 @@ __global__ void __launch_bounds__(384, 1)
                 if constexpr (kScored) {
                     // the scores themselves replace the raw ones: capped, biased, masked to -inf
                     const uint32_t seen0 = below(chi) & ~below(clo), seen1 = below(chi - 32) & ~below(clo - 32);
-                    if constexpr (kFixed) cap_scores(p, x);
-                    else factor = score_row<kCapped>(p, x, slope2, t0 + c0 - pos);
+                    if constexpr (kFixed) cap_scores(p, x, full, seen0, seen1, lane_base + 128 * b + c0);
+                    else factor = score_row<kCapped>(p, x, slope2, t0 + c0 - pos, full, seen0, seen1,
+                                                          lane_base + 128 * b + c0);
                     if (!full) hide(x, seen0, seen1);
                     if constexpr (!kFixed) {
                         pmax = fmaxf(x[0], x[63]);

@@ -293,3 +293,31 @@ def test_every_score_at_the_cap(sign, softcap):
     c["kv"][:, 1] = (c["kv"][:, 1].float() * 1e18).to(BF16)
     for splits in (0, 2):
         check(c, run(dev, c, softcap=softcap, splits=splits), softcap=softcap, step=11)
+
+
+def _alone(c):
+    """The first sequence of a case by itself, over the same pool."""
+    return dict(c, lens=c["lens"][:1], chunks=c["chunks"][:1], tables=c["tables"][:1], rows=c["chunks"][0],
+                q=c["q"][:c["chunks"][0]])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("softcap", [8.0, 30.0, 1e3, 1e4])
+def test_capped_rows_do_not_depend_on_their_neighbours(softcap, dtype):
+    """Bit for bit: a sequence whose chunk ends inside a row tile, alone and packed before one whose queries are 100 times
+    larger; rows beside a row with large queries; rows before a token with large keys."""
+    dev = device()
+    c = make([200, 0], [37, 64], 8, 2, 16, dtype, seed=13)
+    first = run(dev, _alone(c), softcap=softcap, splits=1)
+    packed = dict(c, q=torch.cat([c["q"][:37], (c["q"][37:].float() * 100).to(dtype)]))
+    assert torch.equal(run(dev, packed, softcap=softcap, splits=1)[:37], first)
+    loud = c["q"].clone()
+    loud[11:20:4] = (loud[11:20:4].float() * 100).to(dtype)
+    others = [j for j in range(37) if j not in range(11, 20, 4)]
+    assert torch.equal(run(dev, _alone(dict(c, q=loud)), softcap=softcap, splits=1)[others], first[others])
+    kv = c["kv"].clone()
+    for t in (215, 230):
+        kv[c["tables"][0, t // 16], 0, :, t % 16] *= 200
+    got = run(dev, _alone(dict(c, kv=kv)), softcap=softcap, splits=1)
+    assert torch.equal(got[:15], first[:15])                                     # positions 200 .. 214
+    check(_alone(dict(c, kv=kv)), got, softcap=softcap, step=5)
