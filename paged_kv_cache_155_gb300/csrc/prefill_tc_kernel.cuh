@@ -433,49 +433,50 @@ __device__ __forceinline__ void add_bf16x2(float &l0, float &l1, uint32_t v) {
         : "+f"(l0), "+f"(l1) : "r"(v));
 }
 
-// x <- x R(x^2) - shift, R of N terms whose coefficients are scaled to give scale_log2 x at
-// small x.
+// z <- z R(z^2) - shift, R of N terms times cap_out.
 template <int N, typename F>
-__device__ __forceinline__ void cap_poly(const PrefillParams &p, F &&term, float (&x)[64]) {
-    const float k2 = p.cap_in * p.cap_in;
-    float k = p.scale_log2;
+__device__ __forceinline__ void cap_poly(const PrefillParams &p, F &&term, float (&z)[64]) {
     const F32x2 shift = pack_f32(-p.shift, -p.shift);
     F32x2 c[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j, k *= k2) {
-        const float t = k * term(j);
+    for (int j = 0; j < N; ++j) {
+        const float t = p.cap_out * term(j);
         c[j] = pack_f32(t, t);
     }
 #pragma unroll
     for (int i = 0; i < 64; i += 2) {
-        const F32x2 v = pack_f32(x[i], x[i + 1]);
+        const F32x2 v = pack_f32(z[i], z[i + 1]);
         const F32x2 u = mul2(v, v);
         F32x2 q = fma2(u, c[N - 1], c[N - 2]);
 #pragma unroll
         for (int j = N - 3; j >= 0; --j) q = fma2(u, q, c[j]);
-        unpack_f32(fma2(v, q, shift), x[i], x[i + 1]);
+        unpack_f32(fma2(v, q, shift), z[i], z[i + 1]);
     }
 }
 
 // Raw scores of a row -> capped scores in log2 units, less the fixed reference (p.shift,
-// else 0): cap * tanh(s / cap) with s = scale * x is x R(x^2), R a polynomial of tanh(z)/z
-// whose coefficients are scaled to take x itself: no exponential, where the softmax
-// already spends one.  A row takes a short R when the scores that it sees stay far below
-// the cap (and the cap is small enough for that fit's error to stay below 2.5e-5 of a
-// score), else the six-term one, and beyond three quarters of the cap the closed form
-// cap (1 - 2 / (1 + e^(2 z))), an exponential and a reciprocal more: for those scores
-// alone, or with a small cap (an absolute error of 2^-22 cap_out <= 5e-5) the whole row.
-// The choice is the row's own, by the columns that it sees (bits of seen0, seen1): a short
-// R is the long one with zeros for its last terms, which changes no bit, so the warp runs
-// what its most demanding row needs and no result depends on the rows beside it, on hidden
-// tokens, or on what an earlier tile left in columns without a token.  The closed form
-// walks the scores again where they lie in TMEM (at `scores`), in a loop: unrolled over the
-// registers it cost the other branches 4 to 9%, by its size alone.
+// else 0): z = s / cap with s = scale * x, and cap * tanh(z) is z R(z^2), R a polynomial of
+// tanh(z)/z times cap_out: no exponential, where the softmax already spends one.  (The
+// division first, a packed multiply per pair: coefficients scaled to take x itself
+// overflowed where the scale is thousands of caps.)  A row takes a short R when the scores
+// that it sees stay far below the cap (and the cap is small enough for that fit's error to
+// stay below 2.5e-5 of a score), else the six-term one, and beyond three quarters of the
+// cap the closed form cap (1 - 2 / (1 + e^(2 z))), an exponential and a reciprocal more: for
+// those scores alone, or with a small cap (an absolute error of 2^-22 cap_out <= 5e-5) the
+// whole row.  The choice is the row's own, by the columns that it sees (bits of seen0,
+// seen1): a short R is the long one with zeros for its last terms, which changes no bit, so
+// the warp runs what its most demanding row needs and no result depends on the rows beside
+// it, on hidden tokens, or on what an earlier tile left in columns without a token.  The
+// closed form walks the scores again where they lie in TMEM (at `scores`), in a loop:
+// unrolled over the registers it cost the other branches 4 to 9%, by its size alone.
 // Measured (8 chunks of 512 behind 7680 tokens, 64 / 8 heads, window 2048, cap 50; against a
-// choice by all rows and columns of the warp): bf16 265 us / 261, fp16 334 / 324; with cap 3,
-// where most rows take the closed form, 434 / 379.
+// choice by all rows and columns of the warp): bf16 266 us / 261, fp16 337 / 325; with cap 3,
+// where most rows take the closed form, 437 / 380.
 __device__ __forceinline__ void cap_scores(const PrefillParams &p, float (&x)[64], bool full, uint32_t seen0,
                                            uint32_t seen1, uint32_t scores) {
+    const F32x2 in = pack_f32(p.cap_in, p.cap_in);
+#pragma unroll
+    for (int i = 0; i < 64; i += 2) unpack_f32(mul2(pack_f32(x[i], x[i + 1]), in), x[i], x[i + 1]);
     if (!full) {
 #pragma unroll
         for (int i = 0; i < 64; ++i) x[i] = ((i < 32 ? seen0 : seen1) >> (i % 32)) & 1u ? x[i] : 0.f;
@@ -483,7 +484,6 @@ __device__ __forceinline__ void cap_scores(const PrefillParams &p, float (&x)[64
     float big = fmaxf(fabsf(x[0]), fabsf(x[1]));
 #pragma unroll
     for (int i = 2; i < 64; i += 2) big = fmax3(big, fabsf(x[i]), fabsf(x[i + 1]));
-    big *= fabsf(p.cap_in);
     const bool three = big <= 0.25f && p.cap_short, four = big <= 0.45f && p.cap_short;
     if (__all_sync(0xffffffffu, three)) {
         cap_poly<3>(p, [&](int j) { return kTanh3[j % 3]; }, x);
@@ -500,18 +500,18 @@ __device__ __forceinline__ void cap_scores(const PrefillParams &p, float (&x)[64
         // (a row that sees nothing takes any form)
         const bool far = p.cap_short && (big > 0.75f || !(seen0 | seen1));
         const bool all_far = __all_sync(0xffffffffu, far);
-        float c[6], k = p.scale_log2;
+        float c[6];
 #pragma unroll
-        for (int j = 0; j < 6; ++j, k *= p.cap_in * p.cap_in) c[j] = k * term(j);
+        for (int j = 0; j < 6; ++j) c[j] = p.cap_out * term(j);
 #pragma unroll 1
         for (int at = 0; at < 64; at += 16) {
-            float y[16], z[16];
+            float z[16];
             uint32_t w[16];
-            tc::tmem_ld_x16(scores + at, y);
+            tc::tmem_ld_x16(scores + at, z);
             tc::tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                z[i] = y[i] * p.cap_in;
+                z[i] *= p.cap_in;
                 w[i] = __float_as_uint((p.cap_out - p.shift) -
                                        2.f * p.cap_out * fast_rcp(1.f + fast_exp2(z[i] * 2.885390081777927f)));
             }
@@ -519,11 +519,11 @@ __device__ __forceinline__ void cap_scores(const PrefillParams &p, float (&x)[64
                 const float most = far ? -1.f : 0.75f;  // the |z| that the polynomial takes
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float u = y[i] * y[i];
+                    const float u = z[i] * z[i];
                     float q = fmaf(u, c[5], c[4]);
 #pragma unroll
                     for (int j = 3; j >= 0; --j) q = fmaf(u, q, c[j]);
-                    q = fmaf(y[i], q, -p.shift);
+                    q = fmaf(z[i], q, -p.shift);
                     w[i] = fabsf(z[i]) <= most ? __float_as_uint(q) : w[i];
                 }
             }

@@ -321,3 +321,27 @@ def test_capped_rows_do_not_depend_on_their_neighbours(softcap, dtype):
     got = run(dev, _alone(dict(c, kv=kv)), softcap=softcap, splits=1)
     assert torch.equal(got[:15], first[:15])                                     # positions 200 .. 214
     check(_alone(dict(c, kv=kv)), got, softcap=softcap, step=5)
+
+
+@pytest.mark.parametrize("scale,softcap", [(-2.0, 0.0), (0.0, 0.0), (8.0, 0.0), (-2.0, 3.0), (0.0, 2.0), (8.0, 3.0), (0.3, 1e6)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_scales_of_any_sign_and_size(scale, softcap, biased):
+    dev = device()
+    kw = dict(softcap=softcap, slopes=SLOPES(4) if biased else None)
+    for dtype in (F16, BF16):
+        c = make([130, 0], [40, 70], 4, 2, 16, dtype, seed=17)
+        c["scale"] = scale
+        check(c, run(dev, c, **kw), step=7, **kw)
+
+
+@pytest.mark.parametrize("part", [0.2, 0.4, 0.6, 0.74, 3.0])
+@pytest.mark.parametrize("scale,softcap", [(8.0, 1e-3), (-8.0, 1e-3), (60.0, 1e-2), (-2.0, 1e-3), (1e-6, 1e6)])
+def test_scores_at_every_part_of_extreme_caps(scale, softcap, part):
+    """The largest |score / softcap| before the cap is `part`, for caps whose ratio to the scale is extreme."""
+    dev = device()
+    c = make([100], [150], 4, 2, 16, BF16, seed=19)
+    c["scale"] = scale
+    k = c["kv"][c["tables"][0].long()][:, 0].double().permute(1, 0, 2, 3).reshape(2, -1, 128)[:, :250]
+    most = torch.einsum("rhgd,htd->rhgt", c["q"].double().view(150, 2, 2, 128), k).abs().max().item()
+    c["q"] = (c["q"].double() * (part * softcap / abs(scale) / most)).to(BF16)
+    check(c, run(dev, c, softcap=softcap), softcap=softcap, step=9)
