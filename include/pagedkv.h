@@ -542,7 +542,11 @@ PKV_API size_t pkv_prefill_scored_workspace_bytes(int num_rows, int num_seqs, in
  * The key range of 128 query rows runs from the smallest lo among them to the
  * largest hi; blocks outside it are not read, so a window's past blocks may be
  * freed.  Inside it, the V rows that some of the 128 rows do not see must be
- * finite.  Other arguments and errors as pkv_paged_attention_prefill.
+ * finite.  A bf16 call with 0 < softcap < 52 and no slopes keeps no maximum per
+ * row (its scores cannot leave [-softcap, softcap]): there |V| times the tokens
+ * that a row sees must stay below 2^78, and where a row's scores all lie near
+ * -softcap, values below 2^-26 count with an absolute error of up to 2^-26.
+ * Other arguments and errors as pkv_paged_attention_prefill.
  */
 PKV_API pkv_status pkv_paged_attention_prefill_scored(
     const void *q, const void *k_cache, const void *v_cache, int64_t num_blocks,

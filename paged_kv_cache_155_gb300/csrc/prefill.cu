@@ -201,7 +201,8 @@ pkv_status prefill_impl(
             p.cap_in = scale / scored->softcap;
             p.cap_out = static_cast<float>(scored->softcap * 1.4426950408889634);
             p.cap_short = p.cap_out <= 200.f;
-            if (dtype == PKV_BF16 && p.cap_out <= pkv::kFixedRefMax && !p.slopes) p.shift = 0.5f * p.cap_out;
+            p.fixed_ref = dtype == PKV_BF16 && p.cap_out <= pkv::kFixedRefMax && !p.slopes;
+            if (p.fixed_ref) p.shift = std::max(0.f, p.cap_out - pkv::kFixedWeightMax);
         }
     }
     // persistent: one CTA per SM (or per item when there are fewer)

@@ -38,7 +38,7 @@ pkv_status launch_prefill_bs(const PrefillParams &p, const CUtensorMap &tq, cons
                              const CUtensorMap &tv, const CUtensorMap &to, int grid, cudaStream_t s) {
     if constexpr (kScored) {
         if constexpr (!std::is_same<T, __half>::value) {
-            if (p.shift > 0.f)
+            if (p.fixed_ref)
                 return p.order == kOrderPlanned ? launch_prefill_one<T, BS, kOrderPlanned, kFixedForm>(p, tq, tk, tv, to, grid, s)
                                                 : launch_prefill_one<T, BS, kOrderRowTiles, kFixedForm>(p, tq, tk, tv, to, grid, s);
         }

@@ -112,9 +112,14 @@ struct PrefillParams {
     float cap_out;               // softcap * log2(e), 0: scores are not capped
     int cap_short;               // the cap is small enough for the short polynomials
     const struct PrefillPlan *plan;  // the item table (planned order)
-    float shift;                 // fixed form: every row's reference, cap_out / 2; else 0
+    int fixed_ref;               // the fixed form
+    float shift;                 // its reference, every row's; else 0
 };
-constexpr float kFixedRefMax = 80.f;
+// The fixed form's largest cap_out, and the exponent that its weights may reach: the reference
+// is what a score of cap_out exceeds that by.  So weights lie in 2^-100 .. 2^50: a product with
+// |V| >= 2^-26 is a normal fp32 number even where every score is at -cap, and O stays finite
+// while |V| times the tokens is below 2^78.
+constexpr float kFixedRefMax = 75.f, kFixedWeightMax = 50.f;
 // see paged_prefill_tc_kernel
 constexpr int kPlainForm = 0, kScoredForm = 1, kFixedForm = 2, kUncappedForm = 3;
 
@@ -573,12 +578,15 @@ __device__ __forceinline__ float score_row(const PrefillParams &p, float (&x)[64
 }
 
 // kForm: the plain softmax; the scored one (scores capped, biased and masked to an interval
-// of tokens per row); the same without a cap; or the scored one of capped bf16 scores without a bias and with
-// cap_out <= kFixedRefMax, whose rows need no maximum.  There |score| <= cap_out, so
-// cap_out / 2 serves as every row's reference: the weights lie in 2^-120 .. 2^40, which
-// bf16 and fp32 hold as exactly as 1 (fp16 does not), and the maximum, its exchange between
-// the two warps and the rescaling fall away.  Each form is compiled apart: the softmax loop
-// fills the register file, and code that a form does not run would slow it.
+// of tokens per row); the same without a cap; or the scored one of capped bf16 scores without
+// a bias and with cap_out <= kFixedRefMax, whose rows need no maximum.  There |score| <=
+// cap_out, so one reference near 0 serves every row: the weights lie in 2^-100 .. 2^50
+// (kFixedWeightMax), which bf16 and fp32 hold as exactly as 1 (fp16 does not) and which leave
+// O the range for any ordinary V, and the maximum, its exchange between the two warps and the
+// rescaling fall away (capped window of 2048, 64 / 8 heads: 266 us; with a maximum,
+// as fp16 takes it, 337).
+// Each form is compiled apart: the softmax loop fills the register file, and code that a form
+// does not run would slow it.
 template <typename T, int BS, int ORDER, int kForm = kPlainForm>
 __global__ void __launch_bounds__(384, 1)
     paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,

@@ -345,3 +345,21 @@ def test_scores_at_every_part_of_extreme_caps(scale, softcap, part):
     most = torch.einsum("rhgd,htd->rhgt", c["q"].double().view(150, 2, 2, 128), k).abs().max().item()
     c["q"] = (c["q"].double() * (part * softcap / abs(scale) / most)).to(BF16)
     check(c, run(dev, c, softcap=softcap), softcap=softcap, step=9)
+
+
+@pytest.mark.parametrize("softcap,sign,size", [(c, *x) for c in (30.0, 50.0, 55.0) for x in (
+    (-1, 1.0), (-1, 1e-4), (-1, 1e-8), (1, 1.0), (1, 1e18))] + [(51.9, -1, 1e-6), (51.9, 1, 1e17)])
+def test_every_score_at_a_cap_and_values_of_any_size(softcap, sign, size):
+    """All scores at -cap: the smallest weights of a fixed reference, whose products with small values still count in full; at
+    +cap the largest, whose products with large values stay finite.  Every token has the same value, and so has the output: the
+    weights' roundings are divided out, and the sums' (350 of 2^-23) round back."""
+    dev = device()
+    c = make([200], [150], 4, 2, 16, BF16, seed=3)
+    c["kv"][:, 0] = torch.rand_like(c["kv"][:, 0].float()).add(1).mul(3).to(BF16)
+    c["q"] = (torch.rand_like(c["q"].float()).add(1) * 20 * sign).to(BF16)
+    value = torch.randn((2, 128), generator=torch.Generator().manual_seed(2))
+    value = (value.sign() * value.abs().clamp(0.5, 2.0) * size).to(BF16)
+    c["kv"][:, 1] = value[None, :, None]
+    for splits in (0, 2):
+        out = run(dev, c, softcap=softcap, splits=splits)
+        assert torch.equal(out[:150], value.repeat_interleave(2, 0).expand(150, 4, 128))
