@@ -256,15 +256,18 @@ int scored_span(int max_context_len, int window, int block_size) {
     if (window <= 0) return max_context_len;
     return static_cast<int>(std::min<int64_t>(max_context_len, static_cast<int64_t>(window) + block_size - 1));
 }
-int64_t score_stride_of(int span) { return (static_cast<int64_t>(span) + 31) / 32 * 32; }
+// A row of scores: the span's whole tiles (up to 16 tokens), then a sum per partition.
+int64_t score_stride_of(int span, int nparts) {
+    return ((static_cast<int64_t>(span) + 15) / 16 * 16 + nparts + 31) / 32 * 32;
+}
 
 // Scored workspace: the partials (also of a single partition when the weights are
-// wanted: their kernel reads m and l), then the scores.
+// wanted: their kernel reads m), then the scores and the sums behind them.
 size_t scored_workspace(int num_seqs, int num_q_heads, int head_dim, int nparts, int span, bool weights) {
     if (!weights) return workspace_for(num_seqs, num_q_heads, head_dim, nparts);
     const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads;
     const size_t partials = rows * nparts * (static_cast<size_t>(head_dim) + 2);
-    return ((partials + 3) / 4 * 4 + rows * static_cast<size_t>(score_stride_of(span))) * sizeof(float);
+    return ((partials + 3) / 4 * 4 + rows * static_cast<size_t>(score_stride_of(span, nparts))) * sizeof(float);
 }
 
 // Decode over a 16-bit cache (k_scale == v_scale == nullptr) or an INT8 cache
@@ -374,7 +377,7 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache,
             merge = 1;
             const size_t partials = rows * (static_cast<size_t>(head_dim) + 2);
             p.ws_s = p.ws_o + (partials + 3) / 4 * 4;
-            p.score_stride = score_stride_of(span);
+            p.score_stride = score_stride_of(span, nparts);
         }
     }
     pkv::WeightParams w{};

@@ -115,7 +115,9 @@ struct DecodeParams {
     const float *slopes;    // [num_q_heads] or null: bias slope * (t - query position)
     const int32_t *starts;  // [num_seqs] or null: first visible token
     float *ws_s;            // or null: every score (log2 units, masked ones -inf), row
-                            // (sequence, query head) at row * score_stride + t - span begin
+                            // (sequence, query head) at row * score_stride + t - span begin;
+                            // a row ends with its partitions' sums of unrounded exponentials,
+                            // the weights' denominators (weight_sums)
     int64_t score_stride;   // a multiple of 32
     int window;             // visible tokens of a sequence, its last ones; 0: all
     int block_size;
@@ -148,6 +150,10 @@ __device__ __forceinline__ DecodeSpan span_of(const DecodeParams &p, int seq, in
     lo = max(lo, 0);
     if (lo >= len) return DecodeSpan{len, len};
     return DecodeSpan{lo, lo & ~(p.block_size - 1)};
+}
+// The row's sums of unrounded exponentials, one per partition.
+__device__ __forceinline__ float *weight_sums(const DecodeParams &p, int64_t row) {
+    return p.ws_s + (row + 1) * p.score_stride - p.num_partitions;
 }
 __device__ __forceinline__ int partitions_of_span(const DecodeParams &p, const DecodeSpan &s, int len) {
     return s.begin < len ? (len - s.begin + p.partition_size - 1) / p.partition_size : 1;
@@ -583,6 +589,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
     float hqs[2] = {1.f, 1.f}, hqb[2] = {0.f, 0.f};            // their score scales / biases
     float mrow = -INFINITY, lrow = 0.f;                        // 16-bit: head mg
     float mrow2 = -INFINITY, lrow2 = 0.f;                      // ... and head mg + 8 (16 heads)
+    float urow = 0.f, urow2 = 0.f;  // scored, with the weights wanted: the sums before rounding
     if constexpr (kMma) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) oacc[j][0] = oacc[j][1] = oacc[j][2] = oacc[j][3] = 0.f;
@@ -881,6 +888,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                     if (__any_sync(0xffffffffu, grow || grow2)) {
                         const float alpha = grow ? fast_exp2(mrow - mx) : 1.f;  // 0 when mrow = -inf
                         lrow *= alpha;
+                        if constexpr (kScored) urow *= alpha;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             oacc[nt][0] *= alpha;
@@ -890,6 +898,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                         if constexpr (kRows16) {
                             const float alpha2 = grow2 ? fast_exp2(mrow2 - mx2) : 1.f;
                             lrow2 *= alpha2;
+                            if constexpr (kScored) urow2 *= alpha2;
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 oacc[nt][2] *= alpha2;
@@ -901,8 +910,8 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                     // the weights meet V rounded to the cache type (as the A fragment of P V,
                     // rows and k indices those of S); the row sum adds the rounded values
                     // (scored: a step may hold no visible token, and then -inf - -inf is kept away;
-                    // with the weights wanted the sum adds the unrounded ones, whose quotients
-                    // they are)
+                    // the accumulated weights are quotients with the unrounded sum, a second one:
+                    // the output is divided by what it multiplied, as without them)
                     const float mb = kScored && mrow == -INFINITY ? 0.f : mrow;
                     const float mb2 = kScored && mrow2 == -INFINITY ? 0.f : mrow2;
                     uint32_t pa[STEP / 8], pb[STEP / 8];
@@ -911,12 +920,14 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                         float r0, r1;
                         const float e0 = fast_exp2(sc[2 * h] - mb), e1 = fast_exp2(sc[2 * h + 1] - mb);
                         pa[h] = pack_mma2<kMmaBF16>(e0, e1, r0, r1);
-                        lrow += kScored && p.ws_s ? e0 + e1 : r0 + r1;
+                        lrow += r0 + r1;
+                        if constexpr (kScored) urow += e0 + e1;
                         pb[h] = 0u;
                         if constexpr (kRows16) {
                             const float f0 = fast_exp2(sc2[2 * h] - mb2), f1 = fast_exp2(sc2[2 * h + 1] - mb2);
                             pb[h] = pack_mma2<kMmaBF16>(f0, f1, r0, r1);
-                            lrow2 += kScored && p.ws_s ? f0 + f1 : r0 + r1;
+                            lrow2 += r0 + r1;
+                            if constexpr (kScored) urow2 += f0 + f1;
                         }
                     }
                     // O += P V: B column mg of n-tile nt is channel (D / 8) mg + nt; lane
@@ -1145,9 +1156,15 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
         lrow += __shfl_xor_sync(0xffffffffu, lrow, 2);
         lrow2 += __shfl_xor_sync(0xffffffffu, lrow2, 1);
         lrow2 += __shfl_xor_sync(0xffffffffu, lrow2, 2);
+        if constexpr (kScored) {
+            urow += __shfl_xor_sync(0xffffffffu, urow, 1);
+            urow += __shfl_xor_sync(0xffffffffu, urow, 2);
+            urow2 += __shfl_xor_sync(0xffffffffu, urow2, 1);
+            urow2 += __shfl_xor_sync(0xffffffffu, urow2, 2);
+        }
         if (aborted) {
             mrow = mrow2 = -INFINITY;
-            lrow = lrow2 = 0.f;
+            lrow = lrow2 = urow = urow2 = 0.f;
         }
     } else {
 #pragma unroll
@@ -1201,6 +1218,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
             if (mt == 0) {
                 row[D] = mrow;
                 row[D + 1] = lrow;
+                if constexpr (kScored) row[D + 2] = urow;
             }
         }
         if constexpr (kRows16) {
@@ -1213,6 +1231,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
             if (mt == 0) {
                 row[D] = mrow2;
                 row[D + 1] = lrow2;
+                if constexpr (kScored) row[D + 2] = urow2;
             }
         }
     } else {
@@ -1230,6 +1249,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
             for (int g = 0; g < GH; ++g) {
                 mine[g * (D + 4) + D] = m[g];
                 mine[g * (D + 4) + D + 1] = l[g];
+                if constexpr (kScored) mine[g * (D + 4) + D + 2] = l[g];  // (16-bit: not rounded here)
             }
         }
     }
@@ -1268,6 +1288,17 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
             if (j == 0) {
                 p.ws_m[pr] = mmax;
                 p.ws_l[pr] = lsum;
+                if constexpr (kScored && !kQuant) {
+                    if (p.ws_s) {
+                        float usum = 0.f;
+#pragma unroll
+                        for (int w = 0; w < NW; ++w) {
+                            const float *src = reinterpret_cast<const float *>(stages + w * S * G::kStageBytes);
+                            usum += (mw[w] == -INFINITY ? 0.f : fast_exp2(mw[w] - mmax)) * src[g * (D + 4) + D + 2];
+                        }
+                        weight_sums(p, row)[part] = usum;
+                    }
+                }
             }
         }
     }

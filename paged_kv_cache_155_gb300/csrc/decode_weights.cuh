@@ -8,7 +8,8 @@ namespace pkv {
 
 // weights_out[b][h][t] = weights[b][h][t] + the sum over KV head h's query heads of their
 // softmax weights 2^(s - M) / L at token t, for every t of the context (masked tokens
-// keep their weight).  The decode kernel left the scores s and each partition's (m, l).
+// keep their weight).  The decode kernel left the scores s, each partition's maximum and its
+// sum of unrounded exponentials.
 struct WeightParams {
     const float *weights;  // or null: zeros
     float *weights_out;    // null: the merge alone
@@ -27,12 +28,14 @@ constexpr int kWeightBlocksPerSm = 8;
 constexpr int kMaxWeightHeads = 128;  // query heads per KV head
 
 // Maximum and sum of one row over its partitions, by a warp: every lane gets M and L.
-__device__ __forceinline__ void join_row(const DecodeParams &p, int64_t base, int nparts, float &m, float &l) {
+__device__ __forceinline__ void join_row(const DecodeParams &p, int64_t row, int nparts, float &m, float &l) {
     const int lane = threadIdx.x & 31;
+    const int64_t base = row * p.num_partitions;
+    const float *sums = weight_sums(p, row);
     float mq = -INFINITY, lq = 0.f;
     if (lane < nparts) {
         mq = p.ws_m[base + lane];
-        lq = p.ws_l[base + lane];
+        lq = sums[lane];
     }
     m = mq;
     for (int q = lane + 32; q < nparts; q += 32) m = fmaxf(m, p.ws_m[base + q]);
@@ -41,7 +44,7 @@ __device__ __forceinline__ void join_row(const DecodeParams &p, int64_t base, in
     l = mq == -INFINITY ? 0.f : fast_exp2(mq - m) * lq;
     for (int q = lane + 32; q < nparts; q += 32) {
         const float mo = p.ws_m[base + q];
-        if (mo != -INFINITY) l += fast_exp2(mo - m) * p.ws_l[base + q];
+        if (mo != -INFINITY) l += fast_exp2(mo - m) * sums[q];
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -98,7 +101,7 @@ __device__ __forceinline__ void weights_chunk(const DecodeParams &p, const Weigh
     load(first, 0);
     for (int g = warp; g < p.group; g += kWeightThreads / 32) {
         float m, l;
-        join_row(p, (row0 + g) * p.num_partitions, nparts, m, l);
+        join_row(p, row0 + g, nparts, m, l);
         if ((threadIdx.x & 31) == 0) {
             head_max[g] = m == -INFINITY ? 0.f : m;  // an empty row: every score is -inf, every weight 0
             head_inv[g] = l > 0.f ? 1.f / l : 0.f;

@@ -310,3 +310,26 @@ def test_two_graphs_and_two_streams_do_not_share_a_workspace():
         for (call, w), (out, ref_w) in zip(calls, refs_):
             assert torch.equal(call.result, out) and torch.equal(w, ref_w)
     check_no_device_flags(dev)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("hq,hkv,d,bs", [(4, 4, 64, 16), (4, 2, 128, 32), (8, 2, 128, 16), (8, 1, 128, 8), (32, 2, 128, 32),
+                                         (15, 3, 64, 8), (24, 2, 128, 32)])
+def test_outputs_do_not_change_when_the_weights_are_wanted(hq, hkv, d, bs, dtype):
+    """Bit for bit; and where every visible token has one value, the output is that value (the weights' roundings are divided
+    out again: off by a few 2^-24 of itself, which rounds back)."""
+    dev = device()
+    c = make([1, 2, 3, 5, 40, 700], hq, hkv, d, bs, dtype, seed=23)
+    value = torch.randn((hkv, d), generator=torch.Generator().manual_seed(2)).to(dtype)
+    for same in (True, False):
+        if same:
+            kv = c["kv"].clone()
+            kv[:, 1] = value[None, :, None]
+        else:
+            kv = c["kv"]
+        for kw in (dict(), dict(softcap=3.0), dict(window=4)):
+            plain, _ = run(dev, c, kv=kv, **kw)
+            out, _ = run(dev, c, kv=kv, want=True, **kw)
+            assert torch.equal(out, plain)
+            if same:
+                assert torch.equal(out, value.repeat_interleave(hq // hkv, 0).expand(6, hq, d))
