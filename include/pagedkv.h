@@ -431,7 +431,8 @@ PKV_API pkv_status pkv_paged_attention_decode_scored_int8(
  *                  `weights` itself, else must not overlap it.
  *   kept           [num_seqs][num_kv_heads][budget] int32: the kept positions,
  *                  ascending, then -1.
- *   kept_lens      [num_seqs] int32: n, the context lengths after eviction.
+ *   kept_lens      [num_seqs] int32: n, the context lengths after eviction; must
+ *                  not overlap context_lens (PKV_ERR_INVALID_ARG).
  */
 PKV_API pkv_status pkv_evict_select(const float *weights, int64_t weights_stride,
                                     const int32_t *context_lens, int max_context_len,

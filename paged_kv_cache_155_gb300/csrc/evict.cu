@@ -406,6 +406,8 @@ PKV_API pkv_status pkv_evict_select(const float *weights, int64_t weights_stride
     if (bad(weights) || bad(context_lens) || bad(kept) || bad(kept_lens) ||
         (reinterpret_cast<uintptr_t>(weights_out) & 3u))
         return PKV_ERR_INVALID_ARG;
+    // one KV head's CTA writes a sequence's new length while the others' may still read the old one
+    if (kept_lens < context_lens + num_seqs && context_lens < kept_lens + num_seqs) return PKV_ERR_INVALID_ARG;
     unsigned int *status = pkv::status_word_ptr();
     if (!status) return PKV_ERR_CUDA;
     SelectParams p{};

@@ -829,7 +829,8 @@ def evict_select(weights: torch.Tensor, context_lens: torch.Tensor, budget: int,
     the tokens between (equal weights: the lower position).  weights: fp32 [B, Hkv, W],
     W >= max_context_len, as paged_attention_decode_scored accumulates them;
     ``weights_out`` (may be ``weights``) gets the kept weights in their new places and
-    zeros up to the old length."""
+    zeros up to the old length.  ``kept_lens`` must not be ``context_lens``: evict_compact
+    needs both."""
     return prepare_evict_select(weights, context_lens, budget, sinks=sinks, recent=recent,
                                 max_context_len=max_context_len, weights_out=weights_out, kept=kept,
                                 kept_lens=kept_lens)()
@@ -863,6 +864,8 @@ def prepare_evict_select(weights: torch.Tensor, context_lens: torch.Tensor, budg
         kept_lens = torch.empty(b, dtype=torch.int32, device=weights.device)
     elif kept_lens.dtype != torch.int32 or kept_lens.numel() != b or not kept_lens.is_contiguous():
         raise ValueError("kept_lens must be a contiguous int32 [num_seqs]")
+    if abs(kept_lens.data_ptr() - context_lens.data_ptr()) < 4 * b:
+        raise ValueError("kept_lens must not overlap context_lens")
     _one_device(weights, context_lens=context_lens, weights_out=weights_out, kept=kept, kept_lens=kept_lens)
     args = (weights.data_ptr(), width, context_lens.data_ptr(), int(max_context_len), b, hkv, int(budget), int(sinks),
             int(recent), None if weights_out is None else weights_out.data_ptr(), kept.data_ptr(),

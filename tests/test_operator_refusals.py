@@ -212,6 +212,20 @@ def test_binding_refuses_before_the_library():
         pkv.evict_compact(k, v, bt, n, kept, n, dst_block_tables=bt[:1])
 
 
+def test_new_lengths_over_the_old_ones_are_refused(lib):
+    """One KV head writes a sequence's new length while the others may still read the old one."""
+    buf = np.zeros(64, dtype=np.int32)
+    at = buf.ctypes.data
+    call = lambda cl, kl, b=4: lib.pkv_evict_select(at, 64, cl, 64, b, 2, 8, 1, 2, None, at + 128, kl, None)
+    for cl, kl in ((at, at), (at, at + 12), (at + 12, at)):
+        assert call(cl, kl) == INVALID
+    assert call(at, at, b=0) == 0
+    w, n = torch.zeros((2, 2, 64)), torch.tensor([5, 64, 7], dtype=torch.int32)
+    for lens, kept_lens in ((n[:2], n[:2]), (n[:2], n[1:])):
+        with pytest.raises(ValueError, match="overlap"):
+            pkv.evict_select(w, lens, 8, kept_lens=kept_lens)
+
+
 def test_block_manager_make_private_and_truncate():
     bm = BlockManager(10, 4, 8)
     bm.add_sequence(1)
