@@ -111,6 +111,26 @@ def test_select_of_many_long_rows(rows):
         assert torch.equal(on.cpu()[i, :, :3000], w[i].gather(1, ref[0].long())) and (on.cpu()[i, :, 3000:lens[i]] == 0).all()
 
 
+@pytest.mark.parametrize("kind", ["tail", "ties"])
+@pytest.mark.parametrize("seqs,heads,longest", [(10, 4, 41000), (10, 6, 33500), (20, 4, 25000), (50, 3, 17000)])
+def test_select_in_place_of_rows_that_clusters_read_again(seqs, heads, longest, kind):
+    """Clusters of four hold 32768 tokens of a row in registers, clusters of two 16384: longer rows, whose later batches are
+    read again in each pass and as they are written; equal weights on both sides of the batches' borders."""
+    dev = device()
+    lens = [longest - 37 * i for i in range(seqs)]
+    w = _weights(kind, (seqs, heads, longest), torch.Generator().manual_seed(longest))
+    on = w.to(dev)
+    kept, kept_lens = pkv.evict_select(on, torch.tensor(lens, dtype=torch.int32, device=dev), 12000, sinks=4, recent=300,
+                                       weights_out=on)
+    torch.cuda.synchronize()
+    check_no_device_flags(dev)
+    assert (kept_lens.cpu() == 12000).all()
+    for i in (0, seqs // 2, seqs - 1):
+        ref, _ = refs.select(w[i:i + 1], lens[i:i + 1], 12000, 4, 300)
+        assert torch.equal(kept.cpu()[i], ref[0])
+        assert torch.equal(on.cpu()[i, :, :12000], w[i].gather(1, ref[0].long())) and (on.cpu()[i, :, 12000:lens[i]] == 0).all()
+
+
 def test_select_clamps_and_flags_bad_lengths():
     dev = device()
     w = torch.rand((2, 1, 64))
