@@ -705,7 +705,8 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                         }
                     }
                     // per head, the maximum over the step's tokens (the eight lanes with this
-                    // mt hold them): finite, as token tb is in the context
+                    // mt hold them): finite in the plain form, as token tb is in the context; -inf
+                    // in the scored one when the step holds no visible token
                     float mx[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -877,7 +878,8 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                         mx = fmaxf(mx, sc[e]);
                         if constexpr (kRows16) mx2 = fmaxf(mx2, sc2[e]);
                     }
-                    // over the row's four lanes: finite, as token tb is in the context
+                    // over the row's four lanes: finite in the plain form, as token tb is in the
+                    // context; -inf in the scored one when the step holds no visible token
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                     if constexpr (kRows16) {

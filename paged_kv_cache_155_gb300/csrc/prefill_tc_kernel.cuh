@@ -98,7 +98,7 @@ struct PrefillParams {
     int num_items;     // row_tiles * num_kv_heads * num_seqs * splits
     int splits;        // KV splits per row tile
     int split_tokens;  // tokens per split, a multiple of 128
-    int order;         // item order: kOrderRowTiles, kOrderPairs or kOrderSortedGroups
+    int order;         // item order: kOrderRowTiles, kOrderPairs, kOrderSortedGroups or kOrderPlanned
     FastDiv div_row_tiles, div_kv_heads, div_group, div_splits, div_per_tile;  // make_fast_div of
                        // row_tiles, num_kv_heads, group, splits, num_kv_heads * num_seqs * splits
     float scale_log2;
