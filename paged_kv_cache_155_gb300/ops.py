@@ -479,6 +479,13 @@ def _one_device(anchor: torch.Tensor, **tensors) -> None:
         raise ValueError("tensors must be on a CUDA device")
 
 
+def _int32(**values) -> None:
+    """The C ABI's int arguments: ctypes would cut a larger value to its low 32 bits."""
+    for name, v in values.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name} must fit 32 bits")
+
+
 def _token_rows(t: torch.Tensor, name: str, tokens: int, heads: Optional[int], d: int) -> Tuple[int, int]:
     """(heads, elements between tokens) of a [tokens, heads, d] tensor dense within a token."""
     if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
@@ -635,6 +642,7 @@ def _prepare_decode_scored(what, q, k_cache, v_cache, scales, block_tables, cont
     if context_lens.dtype != torch.int32 or context_lens.numel() != b or not context_lens.is_contiguous():
         raise ValueError("context_lens must be a contiguous int32 [num_seqs]")
     _check_scores(softcap, slopes, window, hq)
+    _int32(window=window, partition_size=partition_size, max_context_len=max_context_len or 0)
     if starts is not None and (starts.dtype != torch.int32 or starts.numel() != b or not starts.is_contiguous()):
         raise ValueError("starts must be a contiguous int32 [num_seqs]")
     if scale is None:
@@ -788,6 +796,7 @@ def prepare_paged_attention_prefill_scored(q: torch.Tensor, k_cache: torch.Tenso
     if context_lens.dtype != torch.int32 or not context_lens.is_contiguous():
         raise ValueError("context_lens must be a contiguous int32 [num_seqs]")
     _check_scores(softcap, slopes, window, hq)
+    _int32(window=window, kv_splits=kv_splits, max_query_len=max_query_len, max_context_len=max_context_len)
     for name, t, n in (("starts", starts, rows), ("prefix_lens", prefix_lens, b)):
         if t is not None and (t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous int32 [{n}]")
@@ -850,6 +859,7 @@ def prepare_evict_select(weights: torch.Tensor, context_lens: torch.Tensor, budg
     if weights_out is not None and (weights_out.dtype != torch.float32 or weights_out.shape != weights.shape
                                     or not weights_out.is_contiguous()):
         raise ValueError("weights_out must match weights")
+    _int32(budget=budget, max_context_len=max_context_len or 0)
     if budget <= 0 or sinks < 0 or recent < 0 or sinks + recent > budget:
         raise ValueError("budget must be positive and cover sinks + recent")
     if max_context_len is None:

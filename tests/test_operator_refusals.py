@@ -226,6 +226,22 @@ def test_new_lengths_over_the_old_ones_are_refused(lib):
             pkv.evict_select(w, lens, 8, kept_lens=kept_lens)
 
 
+def test_integers_past_32_bits_are_refused_not_cut():
+    k, v = pkv.split_pool(torch.zeros((8, 2, 2, 16, 128), dtype=torch.float16))
+    q, bt, n = torch.zeros((2, 4, 128), dtype=torch.float16), torch.zeros((2, 4), dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    qs = torch.tensor([0, 1, 2], dtype=torch.int32)
+    far = 2 ** 32 + 5
+    for kw in (dict(window=far), dict(partition_size=2 ** 32), dict(max_context_len=far)):
+        with pytest.raises(ValueError, match="32 bits"):
+            pkv.paged_attention_decode_scored(q, k, v, bt, n, **{"max_context_len": 64, **kw})
+    for kw in (dict(window=far), dict(kv_splits=2 ** 32 + 1), dict(max_context_len=far), dict(max_query_len=far)):
+        with pytest.raises(ValueError, match="32 bits"):
+            pkv.paged_attention_prefill_scored(q, k, v, bt, qs, n, **{"max_context_len": 64, "max_query_len": 1, **kw})
+    for kw in (dict(budget=far), dict(budget=8, max_context_len=far)):
+        with pytest.raises(ValueError, match="32 bits"):
+            pkv.evict_select(torch.zeros((2, 2, 64)), n, **kw)
+
+
 def test_block_manager_make_private_and_truncate():
     bm = BlockManager(10, 4, 8)
     bm.add_sequence(1)
