@@ -297,6 +297,15 @@ PKV_API pkv_status pkv_paged_attention_decode_shared_prefix(
  * Operators that a model's layers run around plain attention.  The pages have
  * no counterpart for them: rotary positions, score forms and masks belong to
  * the model, and eviction bounds a context that the pages let grow.
+ *
+ * Token t and position p of a score (distance bias, window, starts,
+ * prefix_lens) are rows of the cached context.  After
+ * pkv_evict_compact they are no longer the tokens' positions: the kept tokens
+ * have moved together, each KV head its own.  A distance bias then measures the
+ * shortened distance, a window counts kept tokens, and starts and prefix_lens
+ * have to be given anew.  Rotary positions are not affected: K is stored
+ * rotated by the position that the caller gave, and the next token's is still
+ * the caller's to count.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -372,7 +381,7 @@ PKV_API size_t pkv_decode_scored_workspace_bytes(int num_seqs, int num_q_heads, 
  *     lo = max(0, p + 1 - window  (window > 0),  starts[i]  (starts given)).
  *
  *   softcap        0 (none) or in [1e-3, 1e6].
- *   slopes         [num_q_heads] fp32, device, or NULL.
+ *   slopes         [num_q_heads] fp32, finite, device, or NULL.
  *   window         0: the whole context.
  *   starts         [num_seqs] int32, device, or NULL: the first visible token,
  *                  e.g. of the sequence's last document.  A sequence that sees
@@ -384,8 +393,14 @@ PKV_API size_t pkv_decode_scored_workspace_bytes(int num_seqs, int num_q_heads, 
  *                  (weights NULL: plus nothing); columns past the context are
  *                  left as they are.  The same array may be both; else they
  *                  must not overlap.  weights_stride >= max_context_len.
- *                  weights_out NULL: not wanted.
- *   workspace      >= pkv_decode_scored_workspace_bytes(...).
+ *                  weights_out NULL: not wanted.  At most 128 query heads per
+ *                  KV head (else PKV_ERR_UNSUPPORTED).
+ *   workspace      >= pkv_decode_scored_workspace_bytes(...).  With weights_out
+ *                  it holds every score in fp32, for each sequence as many as
+ *                  the bound allows: 4 * num_seqs * num_q_heads * (the smaller
+ *                  of max_context_len and window + block_size - 1) bytes and a
+ *                  few per cent (256 sequences of 64 heads bounded by 131072
+ *                  tokens: 8.6 GB), however short the contexts are.
  * Tokens before lo are not read: table entries of blocks that lie before lo
  * are never dereferenced (a window's past blocks may be freed), and what lo's
  * block holds before it does not matter, NaN or infinities included.  Other

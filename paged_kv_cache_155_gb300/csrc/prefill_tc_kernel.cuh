@@ -208,6 +208,10 @@ struct PrefillPlan {
     int entries, pad[3];
     PrefillEntry entry[1];
 };
+// Row tiles, by the host's bounds, up to which the plan's one block makes the table; more take
+// the row-tile order.  Measured past the limit, a sequence of 2048 tokens (32 / 8 heads, 64
+// sequences with the table, 66 without): causal 36.8 / 47.3 us, documents of 700 21.5 / 24.6,
+// window 512 24.0 / 24.7.
 constexpr int kMaxPlanEntries = 4096;
 __device__ __forceinline__ PrefillEntry load_entry(const PrefillParams &p, int item, int num_items) {
     PrefillEntry e{};
