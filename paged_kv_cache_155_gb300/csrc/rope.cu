@@ -31,9 +31,11 @@ constexpr int kWide = 256, kNarrow = 128;
 // heads, wide CTAs: 59 us; four steps and 768 threads 68, one step and 1536 threads 70.
 constexpr int kDepth = 2;
 constexpr int kResident16 = 1280, kResidentInt8 = 1024;
-// Tokens per CTA from kManyTokens tokens on: two share the angles' latency (59.0 us
-// against 59.8 with one, 61.9 with four, wide CTAs); below, one, so that the SMs share
-// the work.
+// Tokens per CTA from kManyTokens tokens on: two share the angles' latency; below, one, so
+// that the SMs share the work.  Chosen with wide CTAs (8192 tokens of 64 + 2 x 8 heads: 59.0 us,
+// with one token 59.8, with four 61.9).  Narrow ones, which this range takes now, one token /
+// two: the same 53.1 / 54.8, 4096 tokens 28.7 / 31.9; INT8 cache, 32 + 2 x 32 heads of 64, 8192
+// tokens 52.2 / 50.2, 4096 25.6 / 24.7, 3000 19.9 / 21.5.
 constexpr int kTok = 2, kManyTokens = 2048;
 
 // quantize_int8 (pkv_device.cuh) without a division in most cases: the quotient by an
