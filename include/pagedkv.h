@@ -68,9 +68,10 @@ typedef enum pkv_status {
     PKV_ERR_OUT_OF_BLOCKS = 6  /* block manager: the free pool cannot cover the request */
 } pkv_status;
 
-/* PKV_INT8 names an INT8 cache; only pkv_copy_blocks takes it as `dtype` (the
- * INT8 entry points below take the query / new-row dtype, fp16 or bf16). */
-typedef enum pkv_dtype { PKV_F16 = 0, PKV_BF16 = 1, PKV_INT8 = 2 } pkv_dtype;
+/* PKV_INT8 names an INT8 cache, PKV_INT4 a 4-bit one; only pkv_copy_blocks takes
+ * PKV_INT4 as `dtype`, and it and pkv_evict_compact PKV_INT8 (the entry points of
+ * these caches below take the query / new-row dtype, fp16 or bf16). */
+typedef enum pkv_dtype { PKV_F16 = 0, PKV_BF16 = 1, PKV_INT8 = 2, PKV_INT4 = 3 } pkv_dtype;
 
 /* Flags of the device status word (bitwise OR of what the kernels saw). */
 #define PKV_DEVERR_SLOT        0x1u  /* slot_mapping entry >= num_blocks*block_size  */
@@ -190,7 +191,8 @@ PKV_API pkv_status pkv_paged_attention_decode(
  * pkv_copy_blocks -- copy-on-write block copies (P1 §8.3; P3 §2.3 and §5.5).
  * For each pair p, the K half and the V half of block src_dst_pairs[2p] are
  * copied bit-exactly over those of block src_dst_pairs[2p+1].  dtype is the
- * cache's: PKV_F16, PKV_BF16 or PKV_INT8.
+ * cache's: PKV_F16, PKV_BF16, PKV_INT8 or PKV_INT4 (whose block_stride_elems counts
+ * bytes).
  *
  *   src_dst_pairs  [num_pairs][2] int64, device.  Destinations must be
  *                  distinct and must not also appear as sources (otherwise the
@@ -255,6 +257,73 @@ PKV_API pkv_status pkv_paged_attention_decode_int8(
     int max_context_len, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
     int block_size, float scale, void *out, void *workspace, size_t workspace_bytes,
     int partition_size, pkv_dtype dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * 4-bit KV cache with scales of its own: every row carries them, so nothing is
+ * calibrated.  The 32 channels of group j of one token and KV head are stored as
+ *     zero z  = their smallest value (exact in the rows' type),
+ *     scale s = (largest - smallest) / 15, rounded up to the rows' type,
+ *     codes c = the integer nearest to (x - z) / s, ties to even, 0 when s = 0,
+ * and read back as s * c + z: a value is off by s / 2 at most.  Values must be
+ * finite (a NaN gets code 0, a group with an infinity reads back as NaN).
+ * The pool is bytes, [num_blocks][2][num_kv_heads][block_size * head_dim * 5 / 8]:
+ * a head's record of a block holds the codes of its tokens, head_dim / 2 bytes
+ * each, then head_dim / 32 (scale, zero) pairs for each of its tokens.  With
+ * NG = head_dim / 32, channel 32 j + 4 u + e of a token is nibble e (low first) of
+ * its 16-bit word u * NG + j.  Block strides count bytes, a multiple of 16.
+ * dtype is the rows' type, fp16 or bf16, the same in every call on a pool.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * pkv_reshape_and_cache_int4 -- pkv_reshape_and_cache into a 4-bit cache: the rows
+ * k_new, v_new ([num_tokens][num_kv_heads][head_dim], dtype) quantised as above
+ * and stored at their slots.  Slot rules and errors as pkv_reshape_and_cache;
+ * num_kv_heads <= 65535.
+ */
+PKV_API pkv_status pkv_reshape_and_cache_int4(const void *k_new, const void *v_new,
+                                              const int64_t *slot_mapping, int64_t num_tokens,
+                                              void *k_cache, void *v_cache, int64_t num_blocks,
+                                              int64_t block_stride_bytes, int num_kv_heads,
+                                              int head_dim, int block_size, pkv_dtype dtype,
+                                              void *stream);
+
+/*
+ * pkv_dequantise_blocks_int4 -- read blocks back: for each pair p, block
+ * src_dst_pairs[2p] of the 4-bit pool is written as 16-bit values (s * c + z, one
+ * rounding) over block src_dst_pairs[2p+1] of a 16-bit pool of the same shape, e.g.
+ * for a chunked prefill behind a cached context.  Every row of the block is read,
+ * unwritten ones included.
+ *   src_dst_pairs  [num_pairs][2] int64, device; destinations must be distinct.  An
+ *                  entry outside its pool raises PKV_DEVERR_COPY_PAIR and its pair
+ *                  is skipped.
+ */
+PKV_API pkv_status pkv_dequantise_blocks_int4(const void *k_cache4, const void *v_cache4,
+                                              int64_t num_blocks4, int64_t block_stride_bytes4,
+                                              const int64_t *src_dst_pairs, int64_t num_pairs,
+                                              void *k_cache, void *v_cache, int64_t num_blocks,
+                                              int64_t block_stride_elems, int num_kv_heads,
+                                              int head_dim, int block_size, pkv_dtype dtype,
+                                              void *stream);
+
+/* Workspace of pkv_paged_attention_decode_int4 (same contract as
+ * pkv_decode_workspace_bytes). */
+PKV_API size_t pkv_decode_int4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
+                                               int head_dim, int block_size, int max_context_len,
+                                               int partition_size);
+
+/*
+ * pkv_paged_attention_decode_int4 -- pkv_paged_attention_decode over a 4-bit cache.
+ * partition_size is 0 or a multiple of 32.  Tokens past a context, in its last block,
+ * may hold anything.  A query is held to 2^-24 of its largest channel, and V's groups
+ * should have scales of at least 2^-50.  Other arguments and errors as
+ * pkv_paged_attention_decode.
+ */
+PKV_API pkv_status pkv_paged_attention_decode_int4(
+    const void *q, const void *k_cache, const void *v_cache, int64_t num_blocks,
+    int64_t block_stride_bytes, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *context_lens, int max_context_len, int num_seqs, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, float scale, void *out, void *workspace,
+    size_t workspace_bytes, int partition_size, pkv_dtype dtype, void *stream);
 
 /*
  * pkv_shared_prefix_workspace_bytes -- workspace of

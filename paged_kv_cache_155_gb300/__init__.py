@@ -16,6 +16,8 @@ thin PyTorch binding.
   paged_attention_prefill_scored  the chunked prefill with the same score forms,
                           document starts and a prefix that every row sees
   evict_select / evict_compact   keep the heaviest tokens of each KV head's context
+  reshape_and_cache_int4 / dequantise_blocks_int4 / paged_attention_decode_int4   a cache
+                          of 4-bit codes with scales of its own: written, read back, decoded
 
 Each call has a ``prepare_*`` twin that checks and marshals its arguments once
 and returns a callable (``PreparedCall``) for loops that reuse their buffers.
@@ -23,7 +25,7 @@ and returns a callable (``PreparedCall``) for loops that reuse their buffers.
 The library must be built first (``__graft_entry__.build()``); the calls raise
 if it is missing.  There is no CPU implementation in this package.
 """
-from .ops import (F16, BF16, INT8, copy_blocks, debug_wait_timeout,  # noqa: F401
+from .ops import (F16, BF16, INT8, INT4, copy_blocks, debug_wait_timeout,  # noqa: F401
                   decode_int8_workspace_bytes, decode_plan, decode_workspace_bytes,
                   get_device_error, launch_count, paged_attention_decode,
                   paged_attention_decode_int8, paged_attention_decode_shared_prefix,
@@ -40,7 +42,10 @@ from .ops import (F16, BF16, INT8, copy_blocks, debug_wait_timeout,  # noqa: F40
                   paged_attention_decode_scored_int8,
                   prepare_paged_attention_decode_scored_int8,
                   prefill_scored_workspace_bytes, paged_attention_prefill_scored,
-                  prepare_paged_attention_prefill_scored)
+                  prepare_paged_attention_prefill_scored, int4_pool, reshape_and_cache_int4,
+                  prepare_reshape_and_cache_int4, dequantise_blocks_int4,
+                  prepare_dequantise_blocks_int4, decode_int4_workspace_bytes,
+                  paged_attention_decode_int4, prepare_paged_attention_decode_int4)
 from .block_table import slot_mapping  # noqa: F401
 from ._lib import PagedKVError  # noqa: F401
 
@@ -58,4 +63,8 @@ __all__ = ["reshape_and_cache", "paged_attention_decode", "paged_attention_decod
            "decode_scored_workspace_bytes", "paged_attention_decode_scored",
            "prepare_paged_attention_decode_scored", "paged_attention_decode_scored_int8",
            "prepare_paged_attention_decode_scored_int8", "prefill_scored_workspace_bytes",
-           "paged_attention_prefill_scored", "prepare_paged_attention_prefill_scored"]
+           "paged_attention_prefill_scored", "prepare_paged_attention_prefill_scored",
+           "int4_pool", "reshape_and_cache_int4", "prepare_reshape_and_cache_int4",
+           "dequantise_blocks_int4", "prepare_dequantise_blocks_int4",
+           "decode_int4_workspace_bytes", "paged_attention_decode_int4",
+           "prepare_paged_attention_decode_int4"]

@@ -75,6 +75,11 @@ SIGNATURES = {
     "pkv_evict_select": (I32, [P, I64, P, I32, I32, I32, I32, I32, I32, P, P, P, P]),
     "pkv_evict_compact": (I32, [P, P, I64, I64, I32, I32, I32, P, I32, P, I32, P, P, I32, P, I32,
                                 I32, P]),
+    "pkv_reshape_and_cache_int4": (I32, [P, P, P, I64, P, P, I64, I64, I32, I32, I32, I32, P]),
+    "pkv_dequantise_blocks_int4": (I32, [P, P, I64, I64, P, I64, P, P, I64, I64, I32, I32, I32, I32, P]),
+    "pkv_decode_int4_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32, I32]),
+    "pkv_paged_attention_decode_int4": (I32, [P, P, P, I64, I64, P, I32, P, I32, I32, I32, I32, I32,
+                                              I32, ctypes.c_float, P, P, SZ, I32, I32, P]),
     "pkv_bm_create": (P, [I64, I32, I32]),
     "pkv_bm_destroy": (None, [P]),
     "pkv_bm_num_free": (I64, [P]),

@@ -11,7 +11,7 @@
 // INT8 write's codes are those of the quantiser in pkv_device.cuh.
 // Device-resident indices are range-checked before use; a bad one raises a
 // status flag and is skipped.
-#include "pkv_device.cuh"
+#include "int4.cuh"
 #include "pkv_host.h"
 
 namespace {
@@ -289,12 +289,14 @@ PKV_API pkv_status pkv_copy_blocks(void *k_cache, void *v_cache, int64_t num_blo
                                    int64_t block_stride_elems, int num_kv_heads, int head_dim,
                                    int block_size, const int64_t *src_dst_pairs,
                                    int64_t num_pairs, pkv_dtype dtype, void *stream) {
-    if (dtype != PKV_F16 && dtype != PKV_BF16 && dtype != PKV_INT8) return PKV_ERR_UNSUPPORTED;
+    if (dtype != PKV_F16 && dtype != PKV_BF16 && dtype != PKV_INT8 && dtype != PKV_INT4) return PKV_ERR_UNSUPPORTED;
     if (!supported_shape(head_dim, block_size)) return PKV_ERR_UNSUPPORTED;
     if (num_pairs < 0 || num_kv_heads <= 0 || num_blocks <= 0) return PKV_ERR_INVALID_ARG;
     if (num_pairs > 0x7fffffffLL) return PKV_ERR_INVALID_ARG;
-    const int elem_bytes = dtype == PKV_INT8 ? 1 : 2;
-    const int64_t half_elems = static_cast<int64_t>(num_kv_heads) * block_size * head_dim;
+    const int elem_bytes = dtype == PKV_INT8 || dtype == PKV_INT4 ? 1 : 2;
+    const int64_t half_elems = dtype == PKV_INT4
+                                   ? static_cast<int64_t>(num_kv_heads) * pkv::int4_record_bytes(head_dim, block_size)
+                                   : static_cast<int64_t>(num_kv_heads) * block_size * head_dim;
     if (block_stride_elems < half_elems || (block_stride_elems * elem_bytes) % 16)
         return PKV_ERR_INVALID_ARG;
     if (!k_cache || !v_cache || !pkv::aligned16(k_cache) || !pkv::aligned16(v_cache))

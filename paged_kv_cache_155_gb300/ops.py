@@ -24,7 +24,7 @@ import torch
 
 from ._lib import DEVERR, PagedKVError, lib
 
-F16, BF16, INT8 = 0, 1, 2
+F16, BF16, INT8, INT4 = 0, 1, 2, 3
 _workspaces = {}
 
 
@@ -347,8 +347,12 @@ def paged_attention_prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
 
 
 def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, src_dst_pairs: torch.Tensor) -> None:
-    """Copy K and V of block src over block dst for each row (src, dst) of an int64 [n, 2]."""
-    nb, hkv, bs, d, stride = _cache_geometry(k_cache, v_cache)
+    """Copy K and V of block src over block dst for each row (src, dst) of an int64 [n, 2]
+    (16-bit, INT8 and 4-bit caches)."""
+    if k_cache.dtype == torch.uint8:
+        nb, hkv, bs, d, stride = _int4_geometry(k_cache, v_cache)
+    else:
+        nb, hkv, bs, d, stride = _cache_geometry(k_cache, v_cache)
     if src_dst_pairs.dtype != torch.int64 or src_dst_pairs.dim() != 2 or src_dst_pairs.shape[1] != 2 \
             or not src_dst_pairs.is_contiguous():
         raise ValueError("src_dst_pairs must be a contiguous int64 [n, 2]")
@@ -356,7 +360,7 @@ def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, src_dst_pairs: tor
         raise ValueError("src_dst_pairs must be on the device")
     st = lib().pkv_copy_blocks(k_cache.data_ptr(), v_cache.data_ptr(), nb, stride, hkv, d, bs,
                                src_dst_pairs.data_ptr(), int(src_dst_pairs.shape[0]),
-                               _cache_dtype_code(k_cache), _stream(k_cache))
+                               INT4 if k_cache.dtype == torch.uint8 else _cache_dtype_code(k_cache), _stream(k_cache))
     _check(st, "pkv_copy_blocks")
 
 
@@ -821,6 +825,139 @@ def prepare_paged_attention_prefill_scored(q: torch.Tensor, k_cache: torch.Tenso
     return PreparedCall("pkv_paged_attention_prefill_scored", args, q.device,
                         (q, k_cache, v_cache, block_tables, query_start, context_lens, out, slopes, starts,
                          prefix_lens, workspace), out)
+
+
+# ---------------------------------------------------------------------------
+# 4-bit cache with a scale and a zero per 32 channels of each row
+# ---------------------------------------------------------------------------
+
+def int4_pool(num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int, device=None) -> torch.Tensor:
+    """An empty 4-bit pool: uint8 [num_blocks, 2, num_kv_heads, block_size, head_dim * 5 / 8].
+    ``split_pool`` gives its K and V halves.  The last two dimensions are a head's record of a
+    block: the codes of its tokens, then their scales and zeros."""
+    if head_dim not in (64, 128):
+        raise ValueError("head_dim must be 64 or 128")
+    return torch.empty((num_blocks, 2, num_kv_heads, block_size, head_dim * 5 // 8), dtype=torch.uint8, device=device)
+
+
+def _int4_geometry(k_cache, v_cache):
+    """(num_blocks, num_kv_heads, block_size, head_dim, block stride in bytes) of a 4-bit cache's halves."""
+    nb, hkv, bs, width, stride = _cache_geometry(k_cache, v_cache)
+    if k_cache.dtype != torch.uint8 or width not in (40, 80):
+        raise ValueError("k_cache/v_cache must be uint8 [num_blocks, num_kv_heads, block_size, head_dim * 5 / 8]")
+    return nb, hkv, bs, width * 8 // 5, stride
+
+
+def reshape_and_cache_int4(k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
+                           k_cache: torch.Tensor, v_cache: torch.Tensor) -> None:
+    """Quantise new K/V rows [T, Hkv, d] (fp16/bf16) to 4-bit codes with a scale and a zero per
+    32 channels, and write them into their slots of a 4-bit cache (``int4_pool``); slot < 0 skips."""
+    prepare_reshape_and_cache_int4(k_new, v_new, slot_mapping, k_cache, v_cache)()
+
+
+def prepare_reshape_and_cache_int4(k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
+                                   k_cache: torch.Tensor, v_cache: torch.Tensor) -> PreparedCall:
+    """reshape_and_cache_int4, checked and marshalled once (see PreparedCall)."""
+    nb, hkv, bs, d, stride = _int4_geometry(k_cache, v_cache)
+    t = int(k_new.shape[0])
+    if k_new.shape != (t, hkv, d) or v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
+        raise ValueError(f"k_new/v_new must be [T, {hkv}, {d}] of one dtype")
+    if not (k_new.is_contiguous() and v_new.is_contiguous() and slot_mapping.is_contiguous()):
+        raise ValueError("k_new, v_new and slot_mapping must be contiguous")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != t:
+        raise ValueError("slot_mapping must be int64 [T]")
+    _one_device(k_cache, v_cache=v_cache, k_new=k_new, v_new=v_new, slot_mapping=slot_mapping)
+    args = (k_new.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr(), t, k_cache.data_ptr(), v_cache.data_ptr(), nb,
+            stride, hkv, d, bs, _dtype_code(k_new))
+    return PreparedCall("pkv_reshape_and_cache_int4", args, k_cache.device, (k_new, v_new, slot_mapping, k_cache, v_cache))
+
+
+def dequantise_blocks_int4(k_cache4: torch.Tensor, v_cache4: torch.Tensor, src_dst_pairs: torch.Tensor,
+                           k_cache: torch.Tensor, v_cache: torch.Tensor) -> None:
+    """Read blocks of a 4-bit cache back: block src of it, as 16-bit values, over block dst of
+    the 16-bit cache for each row (src, dst) of an int64 [n, 2].  The 16-bit cache's dtype is that
+    of the rows that were quantised."""
+    prepare_dequantise_blocks_int4(k_cache4, v_cache4, src_dst_pairs, k_cache, v_cache)()
+
+
+def prepare_dequantise_blocks_int4(k_cache4: torch.Tensor, v_cache4: torch.Tensor, src_dst_pairs: torch.Tensor,
+                                   k_cache: torch.Tensor, v_cache: torch.Tensor) -> PreparedCall:
+    """dequantise_blocks_int4, checked and marshalled once (see PreparedCall)."""
+    nb4, hkv, bs, d, stride4 = _int4_geometry(k_cache4, v_cache4)
+    nb, *shape, stride = _cache_geometry(k_cache, v_cache)
+    if shape != [hkv, bs, d]:
+        raise ValueError(f"k_cache/v_cache must be [num_blocks, {hkv}, {bs}, {d}]")
+    if src_dst_pairs.dtype != torch.int64 or src_dst_pairs.dim() != 2 or src_dst_pairs.shape[1] != 2 \
+            or not src_dst_pairs.is_contiguous():
+        raise ValueError("src_dst_pairs must be a contiguous int64 [n, 2]")
+    _one_device(k_cache4, v_cache4=v_cache4, src_dst_pairs=src_dst_pairs, k_cache=k_cache, v_cache=v_cache)
+    args = (k_cache4.data_ptr(), v_cache4.data_ptr(), nb4, stride4, src_dst_pairs.data_ptr(),
+            int(src_dst_pairs.shape[0]), k_cache.data_ptr(), v_cache.data_ptr(), nb, stride, hkv, d, bs, _dtype_code(k_cache))
+    return PreparedCall("pkv_dequantise_blocks_int4", args, k_cache4.device,
+                        (k_cache4, v_cache4, src_dst_pairs, k_cache, v_cache))
+
+
+def decode_int4_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                                partition_size=0) -> int:
+    n = lib().pkv_decode_int4_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                              max_context_len, partition_size)
+    if n == ctypes.c_size_t(-1).value:
+        raise PagedKVError("pkv_decode_int4_workspace_bytes", 1)
+    return int(n)
+
+
+def paged_attention_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                scale: Optional[float] = None, out: Optional[torch.Tensor] = None, *,
+                                max_context_len: Optional[int] = None, partition_size: int = 0,
+                                workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_attention_decode over a 4-bit cache (``int4_pool``); q and out have the dtype of the
+    rows that were quantised.  partition_size: 0 or a multiple of 32."""
+    return prepare_paged_attention_decode_int4(q, k_cache, v_cache, block_tables, context_lens, scale, out,
+                                               max_context_len=max_context_len, partition_size=partition_size,
+                                               workspace=workspace)()
+
+
+def prepare_paged_attention_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                        block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                        scale: Optional[float] = None, out: Optional[torch.Tensor] = None, *,
+                                        max_context_len: Optional[int] = None, partition_size: int = 0,
+                                        workspace: Optional[torch.Tensor] = None) -> PreparedCall:
+    """paged_attention_decode_int4, checked and marshalled once (see PreparedCall); the call
+    returns ``out``.  Without ``workspace`` it holds one of its own."""
+    nb, hkv, bs, d, stride = _int4_geometry(k_cache, v_cache)
+    b, hq, scale, max_context_len, out = _decode_args(q, d, block_tables, context_lens, scale, out, max_context_len)
+    _int32(partition_size=partition_size)
+    _one_device(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens, out=out)
+    with torch.cuda.device(q.device):
+        need = decode_int4_workspace_bytes(b, hq, hkv, d, bs, max_context_len, partition_size)
+    workspace = _own_workspace(q.device, need, workspace)
+    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, stride, block_tables.data_ptr(),
+            int(block_tables.shape[1]), context_lens.data_ptr(), max_context_len, b, hq, hkv, d, bs, scale, out.data_ptr(),
+            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), int(partition_size), _dtype_code(q))
+    return PreparedCall("pkv_paged_attention_decode_int4", args, q.device,
+                        (q, k_cache, v_cache, block_tables, context_lens, out, workspace), out)
+
+
+def _decode_args(q, d, block_tables, context_lens, scale, out, max_context_len):
+    """The checks that decode calls share: (num_seqs, num_q_heads, scale, max_context_len, out)."""
+    if q.dim() != 3 or q.shape[2] != d or not q.is_contiguous():
+        raise ValueError(f"q must be a contiguous [num_seqs, num_q_heads, {d}]")
+    b, hq = int(q.shape[0]), int(q.shape[1])
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != b \
+            or not block_tables.is_contiguous():
+        raise ValueError("block_tables must be a contiguous int32 [num_seqs, max_blocks_per_seq]")
+    if context_lens.dtype != torch.int32 or context_lens.numel() != b or not context_lens.is_contiguous():
+        raise ValueError("context_lens must be a contiguous int32 [num_seqs]")
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item()) if b else 0
+    _int32(max_context_len=max_context_len)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out must match q")
+    return b, hq, 1.0 / math.sqrt(d) if scale is None else float(scale), int(max_context_len), out
 
 
 # ---------------------------------------------------------------------------
