@@ -495,6 +495,121 @@ PKV_API pkv_status pkv_paged_attention_decode_scored_int8(
     const int32_t *starts, void *out, void *workspace, size_t workspace_bytes,
     int partition_size, pkv_dtype dtype, void *stream);
 
+/* ------------------------------------------------------------------------
+ * A sliding window with a few first tokens that stay visible (attention sinks): a
+ * query at position p sees the tokens t <= p with
+ *     t < sinks   or   t > p - window        (window >= 1, sinks >= 0),
+ * so an endless stream keeps a bounded cache.  Blocks that lie wholly between the
+ * first tokens and the window are not read and their table entries are never
+ * dereferenced: they may be freed.  What their remaining rows hold does not
+ * matter for the decode (NaN and infinities included).
+ * ------------------------------------------------------------------------ */
+
+/* Workspace of pkv_paged_attention_decode_sinks (int8_cache 0) or its INT8-cache
+ * form; the contract of pkv_decode_scored_workspace_bytes. */
+PKV_API size_t pkv_decode_sinks_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
+                                                int head_dim, int block_size, int max_context_len,
+                                                int window, int sinks, int int8_cache,
+                                                int partition_size);
+
+/* pkv_paged_attention_decode_sinks -- pkv_paged_attention_decode with that mask: the
+ * query of sequence i sits at position context_lens[i] - 1.  Other arguments and
+ * errors as pkv_paged_attention_decode. */
+PKV_API pkv_status pkv_paged_attention_decode_sinks(
+    const void *q, const void *k_cache, const void *v_cache, int64_t num_blocks,
+    int64_t block_stride_elems, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *context_lens, int max_context_len, int num_seqs, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, float scale, int window, int sinks, void *out,
+    void *workspace, size_t workspace_bytes, int partition_size, pkv_dtype dtype, void *stream);
+
+/* pkv_paged_attention_decode_sinks over an INT8 cache (pkv_paged_attention_decode_int8). */
+PKV_API pkv_status pkv_paged_attention_decode_sinks_int8(
+    const void *q, const int8_t *k_cache, const int8_t *v_cache, const float *k_scale,
+    const float *v_scale, int64_t num_blocks, int64_t block_stride_elems,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+    int max_context_len, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, float scale, int window, int sinks, void *out, void *workspace,
+    size_t workspace_bytes, int partition_size, pkv_dtype dtype, void *stream);
+
+/* Workspace of pkv_paged_attention_prefill_sinks; the contract of
+ * pkv_prefill_scored_workspace_bytes. */
+PKV_API size_t pkv_prefill_sinks_workspace_bytes(int num_rows, int num_seqs, int num_q_heads,
+                                                 int num_kv_heads, int head_dim, int block_size,
+                                                 int max_query_len, int max_context_len, int window,
+                                                 int sinks, int kv_splits);
+
+/* pkv_paged_attention_prefill_sinks -- pkv_paged_attention_prefill with that mask, each
+ * chunk row at its own position.  The V rows that some of a row tile's rows see and
+ * others do not must be finite.  workspace >= pkv_prefill_sinks_workspace_bytes(...).
+ * Other arguments and errors as pkv_paged_attention_prefill. */
+PKV_API pkv_status pkv_paged_attention_prefill_sinks(
+    const void *q, const void *k_cache, const void *v_cache, int64_t num_blocks,
+    int64_t block_stride_elems, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *query_start, const int32_t *context_lens, int num_rows, int max_query_len,
+    int max_context_len, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, float scale, int window, int sinks, void *out, void *workspace,
+    size_t workspace_bytes, int kv_splits, pkv_dtype dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * A tree of drafted tokens (speculative decoding): the drafted tokens of a sequence
+ * are its chunk, written behind its context like any chunk; the verification's
+ * attention lets each see the context and its own ancestors, and the path that is
+ * accepted is then moved together.
+ * ------------------------------------------------------------------------ */
+
+/* Workspace of pkv_paged_attention_tree on the current device: it depends on its SMs
+ * alone ((size_t)-1 without a device). */
+PKV_API size_t pkv_tree_workspace_bytes(void);
+
+/*
+ * pkv_paged_attention_tree -- attention of the chunk rows of pkv_paged_attention_prefill
+ * with a mask of their own: row j of sequence i's chunk (C tokens behind L - C context
+ * tokens) sees every token t < L - C, and chunk token c where bit c is set in the
+ * row's words of tree_mask (c < C; bit c % 64 of word c / 64).  A row usually sees
+ * itself and its ancestors, but any bits will do; a row that sees nothing gets zeros.
+ *
+ *   tree_mask     [num_rows][mask_words] int64, device; 64 * mask_words >=
+ *                 max_query_len.
+ *   workspace     >= pkv_tree_workspace_bytes(); calls that may overlap need one
+ *                 each.  Contents need no initialisation.
+ * Every chunk token's V row must be finite.  All other arguments and errors as
+ * pkv_paged_attention_prefill (head_dim 128, up to 128 query heads per KV head).
+ */
+PKV_API pkv_status pkv_paged_attention_tree(
+    const void *q, const void *k_cache, const void *v_cache, int64_t num_blocks,
+    int64_t block_stride_elems, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *query_start, const int32_t *context_lens, const int64_t *tree_mask,
+    int mask_words, int num_rows, int max_query_len, int max_context_len, int num_seqs,
+    int num_q_heads, int num_kv_heads, int head_dim, int block_size, float scale, void *out,
+    void *workspace, size_t workspace_bytes, pkv_dtype dtype, void *stream);
+
+/*
+ * pkv_tree_commit -- keep the accepted path of each sequence's drafted tokens: with
+ * base = L - C, the K and V rows of chunk token accepted[i][j] move to position
+ * base + j, for j < accepted_lens[i] (bit-exact, in place).  Afterwards the context
+ * is base + accepted_lens[i] tokens long, and the blocks past it can be freed
+ * (pkv_bm_truncate).  dtype is the cache's: PKV_F16, PKV_BF16 or PKV_INT8.
+ *
+ *   accepted       [num_seqs][max_accepted] int32, device: chunk tokens in ascending
+ *                  order.  One that does not ascend or lies outside the chunk raises
+ *                  PKV_DEVERR_KEPT and is skipped (the rows behind it are then
+ *                  unspecified); a length that does not fit raises it too and moves nothing.
+ *   query_start, context_lens, max_query_len, max_context_len   as
+ *                  pkv_paged_attention_tree; a sequence out of contract raises
+ *                  PKV_DEVERR_CONTEXT_LEN and is left as it is.
+ *   new_context_lens   [num_seqs] int32, device, or NULL: the lengths afterwards; must
+ *                  not overlap context_lens (PKV_ERR_INVALID_ARG).
+ * The blocks that get rows must belong to their sequence alone (pkv_bm_make_private).
+ */
+PKV_API pkv_status pkv_tree_commit(void *k_cache, void *v_cache, int64_t num_blocks,
+                                   int64_t block_stride_elems, int num_kv_heads, int head_dim,
+                                   int block_size, const int32_t *block_tables,
+                                   int max_blocks_per_seq, const int32_t *query_start,
+                                   const int32_t *context_lens, int max_query_len,
+                                   int max_context_len, int num_seqs, const int32_t *accepted,
+                                   const int32_t *accepted_lens, int max_accepted,
+                                   int32_t *new_context_lens, pkv_dtype dtype, void *stream);
+
 /*
  * pkv_evict_select -- which tokens of each (sequence, KV head) stay in the
  * cache.  A context of L = context_lens[i] tokens keeps n = min(L, budget):

@@ -18,6 +18,10 @@ thin PyTorch binding.
   evict_select / evict_compact   keep the heaviest tokens of each KV head's context
   reshape_and_cache_int4 / dequantise_blocks_int4 / paged_attention_decode_int4   a cache
                           of 4-bit codes with scales of its own: written, read back, decoded
+  paged_attention_decode_sinks / paged_attention_prefill_sinks   a sliding window and a few
+                          first tokens that stay visible; decode _int8
+  paged_attention_tree / tree_commit   a tree of drafted tokens: the verification's
+                          attention, and the accepted path's rows moved together
 
 Each call has a ``prepare_*`` twin that checks and marshals its arguments once
 and returns a callable (``PreparedCall``) for loops that reuse their buffers.
@@ -45,7 +49,13 @@ from .ops import (F16, BF16, INT8, INT4, copy_blocks, debug_wait_timeout,  # noq
                   prepare_paged_attention_prefill_scored, int4_pool, reshape_and_cache_int4,
                   prepare_reshape_and_cache_int4, dequantise_blocks_int4,
                   prepare_dequantise_blocks_int4, decode_int4_workspace_bytes,
-                  paged_attention_decode_int4, prepare_paged_attention_decode_int4)
+                  paged_attention_decode_int4, prepare_paged_attention_decode_int4,
+                  decode_sinks_workspace_bytes, paged_attention_decode_sinks,
+                  prepare_paged_attention_decode_sinks, paged_attention_decode_sinks_int8,
+                  prepare_paged_attention_decode_sinks_int8, prefill_sinks_workspace_bytes,
+                  paged_attention_prefill_sinks, prepare_paged_attention_prefill_sinks,
+                  tree_workspace_bytes, paged_attention_tree, prepare_paged_attention_tree,
+                  tree_commit, prepare_tree_commit)
 from .block_table import slot_mapping  # noqa: F401
 from ._lib import PagedKVError  # noqa: F401
 
@@ -67,4 +77,10 @@ __all__ = ["reshape_and_cache", "paged_attention_decode", "paged_attention_decod
            "int4_pool", "reshape_and_cache_int4", "prepare_reshape_and_cache_int4",
            "dequantise_blocks_int4", "prepare_dequantise_blocks_int4",
            "decode_int4_workspace_bytes", "paged_attention_decode_int4",
-           "prepare_paged_attention_decode_int4"]
+           "prepare_paged_attention_decode_int4", "decode_sinks_workspace_bytes",
+           "paged_attention_decode_sinks", "prepare_paged_attention_decode_sinks",
+           "paged_attention_decode_sinks_int8", "prepare_paged_attention_decode_sinks_int8",
+           "prefill_sinks_workspace_bytes", "paged_attention_prefill_sinks",
+           "prepare_paged_attention_prefill_sinks", "tree_workspace_bytes",
+           "paged_attention_tree", "prepare_paged_attention_tree", "tree_commit",
+           "prepare_tree_commit"]

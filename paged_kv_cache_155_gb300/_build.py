@@ -20,7 +20,8 @@ LIB_PATH = os.path.join(PKG_DIR, "libpagedkv.so")
 
 SOURCES = ["api.cu", "cache_ops.cu", "decode.cu", "decode_f16.cu", "decode_bf16.cu", "decode_i8.cu", "prefill.cu",
            "decode_scored_f16.cu", "decode_scored_bf16.cu", "decode_scored_i8.cu", "prefill_scored_f16.cu", "prefill_scored_bf16.cu",
-           "int4_cache.cu", "decode_int4.cu", "decode_int4_f16.cu", "decode_int4_bf16.cu",
+           "prefill_sinks_f16.cu", "prefill_sinks_bf16.cu", "tree.cu", "tree_f16.cu", "tree_bf16.cu",
+           "decode_sinks_f16.cu", "decode_sinks_bf16.cu", "decode_sinks_i8.cu", "int4_cache.cu", "decode_int4.cu", "decode_int4_f16.cu", "decode_int4_bf16.cu",
            "decode_noalloc.cu", "rope.cu", "evict.cu", "block_manager.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",

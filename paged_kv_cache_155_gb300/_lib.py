@@ -80,6 +80,21 @@ SIGNATURES = {
     "pkv_decode_int4_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32, I32]),
     "pkv_paged_attention_decode_int4": (I32, [P, P, P, I64, I64, P, I32, P, I32, I32, I32, I32, I32,
                                               I32, ctypes.c_float, P, P, SZ, I32, I32, P]),
+    "pkv_decode_sinks_workspace_bytes": (SZ, [I32] * 10),
+    "pkv_paged_attention_decode_sinks": (I32, [P, P, P, I64, I64, P, I32, P, I32, I32, I32, I32, I32,
+                                               I32, ctypes.c_float, I32, I32, P, P, SZ, I32, I32, P]),
+    "pkv_paged_attention_decode_sinks_int8": (I32, [P, P, P, P, P, I64, I64, P, I32, P, I32, I32, I32,
+                                                    I32, I32, I32, ctypes.c_float, I32, I32, P, P, SZ,
+                                                    I32, I32, P]),
+    "pkv_prefill_sinks_workspace_bytes": (SZ, [I32] * 11),
+    "pkv_paged_attention_prefill_sinks": (I32, [P, P, P, I64, I64, P, I32, P, P, I32, I32, I32, I32,
+                                                I32, I32, I32, I32, ctypes.c_float, I32, I32, P, P, SZ,
+                                                I32, I32, P]),
+    "pkv_tree_workspace_bytes": (SZ, []),
+    "pkv_paged_attention_tree": (I32, [P, P, P, I64, I64, P, I32, P, P, P, I32, I32, I32, I32, I32, I32,
+                                       I32, I32, I32, ctypes.c_float, P, P, SZ, I32, P]),
+    "pkv_tree_commit": (I32, [P, P, I64, I64, I32, I32, I32, P, I32, P, P, I32, I32, I32, P, P, I32, P,
+                              I32, P]),
     "pkv_bm_create": (P, [I64, I32, I32]),
     "pkv_bm_destroy": (None, [P]),
     "pkv_bm_num_free": (I64, [P]),

@@ -248,13 +248,17 @@ struct ScoredArgs {
     const float *weights;
     float *weights_out;
     int64_t weights_stride;
+    bool sink_form = false;  // a window and first tokens, nothing else
+    int sinks = 0;
 };
 
 // The longest token range a scored sequence attends over, from the block of its
-// first visible token on.
-int scored_span(int max_context_len, int window, int block_size) {
+// first visible token on (and the blocks of the first `sinks` tokens before it).
+int scored_span(int max_context_len, int window, int block_size, int sinks = 0) {
     if (window <= 0) return max_context_len;
-    return static_cast<int>(std::min<int64_t>(max_context_len, static_cast<int64_t>(window) + block_size - 1));
+    return static_cast<int>(std::min<int64_t>(max_context_len,
+                                              static_cast<int64_t>(window) + block_size - 1 +
+                                                  (static_cast<int64_t>(sinks) + block_size - 1) / block_size * block_size));
 }
 // A row of scores: the span's whole tiles (up to 16 tokens), then a sum per partition.
 int64_t score_stride_of(int span, int nparts) {
@@ -302,6 +306,7 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache,
         const ScoredArgs &a = *scored;
         // a cap far outside the scores' range would overflow score / softcap
         if (a.softcap != 0.f && !(a.softcap >= 1e-3f && a.softcap <= 1e6f)) return PKV_ERR_INVALID_ARG;
+        if (a.sink_form && (a.window < 1 || a.sinks < 0)) return PKV_ERR_INVALID_ARG;
         if (a.window < 0 || (a.weights && !a.weights_out) ||
             (a.weights_out && a.weights_stride < max_context_len) ||
             ((reinterpret_cast<uintptr_t>(a.slopes) | reinterpret_cast<uintptr_t>(a.starts) |
@@ -316,7 +321,7 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache,
 
     int part = 0, nparts = 0, gh = 0, merge = 0;
     const bool want_weights = scored && scored->weights_out;
-    const int span = scored ? scored_span(max_context_len, scored->window, block_size) : max_context_len;
+    const int span = scored ? scored_span(max_context_len, scored->window, block_size, scored->sinks) : max_context_len;
     // Validate the shape first (no CUDA call), then plan for the real SM count.
     pkv_status plan = plan_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                                   span, partition_size, 1, int8_kv, &part, &nparts, &gh,
@@ -368,6 +373,7 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache,
         p.starts = scored->starts;
         p.window = scored->window;
         p.block_size = block_size;
+        p.sinks = std::min(scored->sinks, max_context_len);  // (rounded up to blocks in 32 bits)
         if (scored->softcap > 0.f) {
             p.cap_in = static_cast<float>(0.6931471805599453 / scored->softcap);
             p.cap_out = static_cast<float>(scored->softcap * 1.4426950408889634);
@@ -410,6 +416,11 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache,
         !encode_decode_maps(&maps, k_cache, v_cache, int8_kv, num_blocks, block_stride_elems,
                             num_kv_heads, block_size, dtype))
         return PKV_ERR_CUDA;
+    if (scored && scored->sink_form) {
+        auto launch = int8_kv ? (dtype == PKV_F16 ? pkv::launch_sinks_i8_f16 : pkv::launch_sinks_i8_bf16)
+                              : (dtype == PKV_F16 ? pkv::launch_sinks_f16 : pkv::launch_sinks_bf16);
+        return launch(p, maps, head_dim, block_size, gh, grid, merge_rows, s);
+    }
     if (scored) {
         auto launch = int8_kv ? (dtype == PKV_F16 ? pkv::launch_scored_i8_f16 : pkv::launch_scored_i8_bf16)
                               : (dtype == PKV_F16 ? pkv::launch_scored_f16 : pkv::launch_scored_bf16);
@@ -500,6 +511,42 @@ PKV_API size_t pkv_decode_scored_workspace_bytes(int num_seqs, int num_q_heads, 
                     int8_cache != 0, &part, &nparts, nullptr, nullptr, 0, true) != PKV_OK)
         return static_cast<size_t>(-1);
     return scored_workspace(num_seqs, num_q_heads, head_dim, nparts, span, want_weights != 0);
+}
+
+PKV_API size_t pkv_decode_sinks_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                                int block_size, int max_context_len, int window, int sinks,
+                                                int int8_cache, int partition_size) {
+    const int sm = partition_size > 0 ? 1 : pkv::current_sm_count();
+    if (sm <= 0 || window < 1 || sinks < 0 || block_size <= 0) return static_cast<size_t>(-1);
+    int part = 0, nparts = 0, gh = 0, merge = 0;
+    const int span = scored_span(max_context_len, window, block_size, sinks);
+    if (plan_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, span, partition_size, sm, int8_cache != 0,
+                    &part, &nparts, &gh, &merge, 0, true) != PKV_OK)
+        return static_cast<size_t>(-1);
+    return scored_workspace(num_seqs, num_q_heads, head_dim, nparts, span, false);
+}
+
+PKV_API pkv_status pkv_paged_attention_decode_sinks(
+    const void *q, const void *k_cache, const void *v_cache, int64_t num_blocks, int64_t block_stride_elems,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens, int max_context_len, int num_seqs,
+    int num_q_heads, int num_kv_heads, int head_dim, int block_size, float scale, int window, int sinks, void *out,
+    void *workspace, size_t workspace_bytes, int partition_size, pkv_dtype dtype, void *stream) {
+    const ScoredArgs a{0.f, nullptr, window, nullptr, nullptr, nullptr, 0, true, sinks};
+    return decode_impl(q, k_cache, v_cache, nullptr, nullptr, false, num_blocks, block_stride_elems, block_tables,
+                       max_blocks_per_seq, context_lens, max_context_len, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                       block_size, scale, out, workspace, workspace_bytes, partition_size, dtype, stream, &a);
+}
+
+PKV_API pkv_status pkv_paged_attention_decode_sinks_int8(
+    const void *q, const int8_t *k_cache, const int8_t *v_cache, const float *k_scale, const float *v_scale,
+    int64_t num_blocks, int64_t block_stride_elems, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *context_lens, int max_context_len, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, float scale, int window, int sinks, void *out, void *workspace, size_t workspace_bytes,
+    int partition_size, pkv_dtype dtype, void *stream) {
+    const ScoredArgs a{0.f, nullptr, window, nullptr, nullptr, nullptr, 0, true, sinks};
+    return decode_impl(q, k_cache, v_cache, k_scale, v_scale, true, num_blocks, block_stride_elems, block_tables,
+                       max_blocks_per_seq, context_lens, max_context_len, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                       block_size, scale, out, workspace, workspace_bytes, partition_size, dtype, stream, &a);
 }
 
 PKV_API pkv_status pkv_paged_attention_decode_scored(

@@ -123,6 +123,7 @@ struct DecodeParams {
     int block_size;
     float cap_in;           // ln 2 / softcap: a score in log2 units -> score / softcap
     float cap_out;          // softcap * log2(e); 0: scores are not capped
+    int sinks;              // sink form: first tokens that stay visible besides the window
 };
 
 // Tensor maps of the two pool halves for the forms that stage by tiled TMA
@@ -150,6 +151,19 @@ __device__ __forceinline__ DecodeSpan span_of(const DecodeParams &p, int seq, in
     lo = max(lo, 0);
     if (lo >= len) return DecodeSpan{len, len};
     return DecodeSpan{lo, lo & ~(p.block_size - 1)};
+}
+// Sink form: a sequence sees its first `sinks` tokens and its last `window`.  The whole blocks
+// between them are left out (the gap, in blocks), and what is left is counted through: token t of
+// the context is token t, or t - gap * block_size behind the gap, of the len tokens that the
+// partitions cut.  Of those, [sinks, lo) are hidden (none when lo <= sinks).
+struct SinkSpan {
+    int lo, len, first_blocks, gap;
+};
+__device__ __forceinline__ SinkSpan sink_span_of(const DecodeParams &p, int len) {
+    const int lo = max(0, len - p.window);
+    const int first = (p.sinks + p.block_size - 1) / p.block_size;
+    const int gap = max(0, lo / p.block_size - first);
+    return SinkSpan{lo - gap * p.block_size, len - gap * p.block_size, first, gap};
 }
 // The row's sums of unrounded exponentials, one per partition.
 __device__ __forceinline__ float *weight_sums(const DecodeParams &p, int64_t row) {
@@ -274,7 +288,8 @@ struct DecodeGeom {
 // kPadded (scored warp MMAs): a block may serve fewer than GH heads, so that any group of
 // three heads or more is covered by few blocks rather than read its K/V again for each
 // divisor; compiled apart, as the registers are spent without it.
-template <typename T, typename KT, int D, int BS, int GH, bool kScored = false, bool kPadded = false>
+// kSinks (with kScored): the window and the first tokens (sink_span_of), no other score form.
+template <typename T, typename KT, int D, int BS, int GH, bool kScored = false, bool kPadded = false, bool kSinks = false>
 __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 ? 2 : 3) : (GH >= 4 && kScored) ? 4 : 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                                               const __grid_constant__ CUtensorMap tmap_v,
@@ -340,21 +355,37 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
         len = len < 0 ? 0 : p.len_cap;
     }
     DecodeSpan span{0, 0};
+    SinkSpan sinks{0, 0, 0, 0};
     int nparts;
-    if constexpr (kScored) {
+    if constexpr (kSinks) {
+        sinks = sink_span_of(p, len);
+        len = sinks.len;  // from here on tokens are counted without the gap
+        span = DecodeSpan{sinks.lo, 0};
+        nparts = partitions_of(p, len);
+    } else if constexpr (kScored) {
         span = span_of(p, seq, len);
         nparts = partitions_of_span(p, span, len);
     } else {
         nparts = partitions_of(p, len);
     }
     if (part >= nparts) return;  // uniform over the CTA
+    // entry i of this partition's slice of the table
+    auto table_entry = [&](int i) {
+        if constexpr (kSinks) return trow[i + (blk0 + i >= sinks.first_blocks ? sinks.gap : 0)];
+        else return trow[i];
+    };
     if constexpr (kScored) {
         tok0 = span.begin + part * p.partition_size;
         blk0 = tok0 / BS;
         trow = p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq + blk0;
-        if (static_cast<int>(threadIdx.x) < min(p.max_blocks_per_seq - blk0, p.partition_size / BS))
-            first_entry = trow[threadIdx.x];
+        if (static_cast<int>(threadIdx.x) < min((kSinks ? (len + BS - 1) / BS : p.max_blocks_per_seq) - blk0, p.partition_size / BS))
+            first_entry = table_entry(threadIdx.x);
     }
+    // scored: whether token t (counted from the partition's first) is hidden below the visible range
+    auto below_span = [&](int t) {
+        if constexpr (kSinks) return tok0 + t < span.lo && tok0 + t >= p.sinks;
+        else return tok0 + t < span.lo;
+    };
     const int tok1 = min(len, tok0 + p.partition_size);
     const int ntok = max(0, tok1 - tok0);
     const int nchunks = (ntok + TILE - 1) / TILE;
@@ -362,7 +393,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
 
     // ---- table slice of this partition -> shared memory (bad entries -> -1)
     for (int i = threadIdx.x; i < nblk; i += blockDim.x) {
-        int b = i < static_cast<int>(blockDim.x) ? first_entry : trow[i];
+        int b = i < static_cast<int>(blockDim.x) ? first_entry : table_entry(i);
         if (b < 0 || b >= p.num_blocks) {
             raise_flag(p.status, PKV_DEVERR_BLOCK_TABLE);
             b = -1;
@@ -608,7 +639,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
         for (int e = 0; e < kSlopes; ++e) {
             // INT8 MMA: heads 2 mt, 2 mt + 1; 16-bit MMA: mg, mg + 8; lanes: head e
             const int h = kMma ? (kQuant ? 2 * mt + e : mg + 8 * e) : e;
-            slope2[e] = p.slopes && h < nheads ? p.slopes[hq0 + h] * 1.4426950408889634f : 0.f;
+            slope2[e] = !kSinks && p.slopes && h < nheads ? p.slopes[hq0 + h] * 1.4426950408889634f : 0.f;
         }
     }
     const int qpos = len - 1;  // the query's position
@@ -648,7 +679,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
         // scored form: the chunk's distance from the query (converted once; the lanes add
         // small constants), and whether any of its rows is masked
         const float dist0 = kScored ? static_cast<float>(tok0 + c * TILE - qpos) : 0.f;
-        const bool masked = kScored && (valid < TILE || tok0 + c * TILE < span.lo);
+        const bool masked = kScored && (valid < TILE || (tok0 + c * TILE < span.lo && (!kSinks || tok0 + (c + 1) * TILE > p.sinks)));
         if (tbl[(c * TILE) / BS] >= 0) {
             const KT *ks = reinterpret_cast<const KT *>(my_stages + s * G::kStageBytes);
             const KT *vs = ks + TILE * D;
@@ -698,10 +729,11 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int t = tb + mg + 8 * (e >> 1);
-                            sc[e] = score_modified(p, sc[e], slope2[e & 1],
-                                                   (dist0 + static_cast<float>(tb + 8 * (e >> 1))) + lane_dist);
+                            if constexpr (!kSinks)
+                                sc[e] = score_modified(p, sc[e], slope2[e & 1],
+                                                       (dist0 + static_cast<float>(tb + 8 * (e >> 1))) + lane_dist);
                             if (STEP == 8 && e >= 2) sc[e] = -INFINITY;  // a step of 8 tokens has no rows mg + 8
-                            else if (masked && (t >= valid || tok0 + c * TILE + t < span.lo)) sc[e] = -INFINITY;
+                            else if (masked && (t >= valid || below_span(c * TILE + t))) sc[e] = -INFINITY;
                         }
                     }
                     // per head, the maximum over the step's tokens (the eight lanes with this
@@ -850,15 +882,15 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                         for (int e = 0; e < STEP / 4; ++e) {
                             const int t = tb + 8 * (e >> 1) + 2 * mt + (e & 1);
                             const float dist = (dist0 + static_cast<float>(tb + 8 * (e >> 1) + (e & 1))) + lane_dist;
-                            const bool hidden = masked && (t >= valid || tok0 + c * TILE + t < span.lo);
-                            sc[e] = score_modified(p, sc[e], slope2[0], dist);
+                            const bool hidden = masked && (t >= valid || below_span(c * TILE + t));
+                            if constexpr (!kSinks) sc[e] = score_modified(p, sc[e], slope2[0], dist);
                             if (hidden) sc[e] = -INFINITY;
                             if constexpr (kRows16) {
-                                sc2[e] = score_modified(p, sc2[e], slope2[1], dist);
+                                if constexpr (!kSinks) sc2[e] = score_modified(p, sc2[e], slope2[1], dist);
                                 if (hidden) sc2[e] = -INFINITY;
                             }
                         }
-                        if (p.ws_s) {
+                        if (!kSinks && p.ws_s) {
 #pragma unroll
                             for (int h = 0; h < STEP / 8; ++h) {
                                 const int at = c * TILE + tb + 8 * h + 2 * mt;
@@ -980,7 +1012,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
 #pragma unroll
                         for (int r = 0; r < STEP / 4; ++r) {
                             const int vt_row = tb + (r >> 1) * 8 + 2 * mt + (r & 1);
-                            if (vt_row >= valid || (kScored && vt_row < vlo)) {
+                            if (vt_row >= valid || (kScored && vt_row < vlo && below_span(c * TILE + vt_row))) {
 #pragma unroll
                                 for (int w = 0; w < VW; ++w) x[r][w] = 0u;
                             }
@@ -1053,14 +1085,14 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                         for (int it = 0; it < IT_STEP; ++it) {
                             const int t = (it0 + it) * TPG + grp;
                             const float dist = (dist0 + static_cast<float>((it0 + it) * TPG)) + lane_dist;
-                            const bool hidden = masked && (t >= valid || tok0 + c * TILE + t < span.lo);
+                            const bool hidden = masked && (t >= valid || below_span(c * TILE + t));
 #pragma unroll
                             for (int g = 0; g < GH; ++g) {
-                                sc[it][g] = score_modified(p, sc[it][g], slope2[g], dist);
+                                if constexpr (!kSinks) sc[it][g] = score_modified(p, sc[it][g], slope2[g], dist);
                                 if (hidden) sc[it][g] = -INFINITY;
                             }
                         }
-                        if (!kQuant && p.ws_s) {
+                        if (!kQuant && !kSinks && p.ws_s) {
                             // every lane of a token row holds its score: lane `sub` writes the row of
                             // step it0 + sub, so a store covers IT_STEP * TPG tokens
 #pragma unroll
@@ -1102,7 +1134,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
 #pragma unroll
                     for (int it = 0; it < IT_STEP; ++it) {
                         const int t = (it0 + it) * TPG + grp;
-                        if (t < valid && (!masked || tok0 + c * TILE + t >= span.lo)) {
+                        if (t < valid && (!masked || !below_span(c * TILE + t))) {
                             if constexpr (kQuant) {
                                 uint32_t vh[VL / 2];
                                 load_codes_f16<VL>(vs + t * D + sub * VL, vh);
@@ -1128,7 +1160,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
                 }
             }
         }
-        if constexpr (kScored && !kQuant) {
+        if constexpr (kScored && !kQuant && !kSinks) {
             // a flagged table entry's tokens get no weight
             if (p.ws_s && tbl[(c * TILE) / BS] < 0) {
                 for (int k = lane; k < nheads * TILE; k += 32) score_row(k / TILE)[c * TILE + k % TILE] = -INFINITY;
@@ -1290,7 +1322,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
             if (j == 0) {
                 p.ws_m[pr] = mmax;
                 p.ws_l[pr] = lsum;
-                if constexpr (kScored && !kQuant) {
+                if constexpr (kScored && !kQuant && !kSinks) {
                     if (p.ws_s) {
                         float usum = 0.f;
 #pragma unroll
@@ -1321,7 +1353,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
 constexpr int kMergeUnroll = 8;
 constexpr int kMergeWideFrom = 32;  // partitions per row from which four warps share a row
 
-template <typename T, int D, int WPR, bool kScored>
+template <typename T, int D, int WPR, bool kScored, bool kSinks = false>
 __device__ __forceinline__ void merge_rows(const DecodeParams &p, int num_rows, int block) {
     static_assert(WPR == 1 || WPR == 4, "one or four warps per row");
     constexpr int PER_LANE = D / 32;
@@ -1339,7 +1371,8 @@ __device__ __forceinline__ void merge_rows(const DecodeParams &p, int num_rows, 
     if (len < 0) len = 0;
     if (len > p.len_cap) len = p.len_cap;
     int nparts;  // slots holding partials
-    if constexpr (kScored) nparts = partitions_of_span(p, span_of(p, seq, len), len);
+    if constexpr (kSinks) nparts = partitions_of(p, sink_span_of(p, len).len);
+    else if constexpr (kScored) nparts = partitions_of_span(p, span_of(p, seq, len), len);
     else nparts = p.slot_base + partitions_of(p, len);
     if (nparts <= 1 && !p.always_partial) return;           // written by the decode kernel
     const int mine = nparts > share ? (nparts - share + WPR - 1) / WPR : 0;  // this warp's partitions
@@ -1412,10 +1445,10 @@ __device__ __forceinline__ void merge_rows(const DecodeParams &p, int num_rows, 
     for (int e = 0; e < PER_LANE; ++e) dst[e] = Elem<T>::from_f32(lsum > 0.f ? o[e] / lsum : 0.f);
 }
 
-template <typename T, int D, int WPR>
+template <typename T, int D, int WPR, bool kSinks = false>
 __global__ void __launch_bounds__(128) paged_decode_merge_kernel(const DecodeParams p, int num_rows) {
     pdl_wait();
-    merge_rows<T, D, WPR, false>(p, num_rows, blockIdx.x);
+    merge_rows<T, D, WPR, false, kSinks>(p, num_rows, blockIdx.x);
 }
 
 }  // namespace pkv

@@ -22,7 +22,7 @@ struct PrefillShape {
 
 pkv_status plan_prefill(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                         int block_size, int max_query_len, int max_context_len, int kv_splits,
-                        int sm_count, PrefillShape *pp, int window = 0, bool has_prefix = false) {
+                        int sm_count, PrefillShape *pp, int window = 0, bool has_prefix = false, int sinks = 0) {
     if (head_dim != 128) return PKV_ERR_UNSUPPORTED;
     if (block_size != 8 && block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads ||
@@ -35,10 +35,11 @@ pkv_status plan_prefill(int num_seqs, int num_q_heads, int num_kv_heads, int hea
     const int64_t row_tiles = (static_cast<int64_t>(max_query_len) + pp->tile_tokens - 1) / pp->tile_tokens;
     pp->row_tiles = static_cast<int>(row_tiles);
     // the longest token range of a row tile: with a window (and no prefix behind it) its
-    // rows' windows, from the block that holds the first
+    // rows' windows, from the block that holds the first, behind the blocks of the first tokens
     if (window > 0 && !has_prefix)
         max_context_len = static_cast<int>(std::min<int64_t>(
-            max_context_len, static_cast<int64_t>(window) + pp->tile_tokens - 1 + block_size - 1));
+            max_context_len, static_cast<int64_t>(window) + pp->tile_tokens - 1 + block_size - 1 +
+                                 (static_cast<int64_t>(sinks) + block_size - 1) / block_size * block_size));
     const int64_t ctx_tiles = std::max<int64_t>(1, (max_context_len + 127) / 128);
     int64_t want = kv_splits;
     if (want == 0) {
@@ -80,6 +81,8 @@ struct ScoredPrefillArgs {
     int window;
     const int32_t *starts;
     const int32_t *prefix_lens;
+    bool sink_form = false;  // a window and first tokens, nothing else
+    int sinks = 0;
 };
 
 pkv_status prefill_impl(
@@ -104,6 +107,9 @@ pkv_status prefill_impl(
         return PKV_ERR_INVALID_ARG;
     const int window = scored ? scored->window : 0;
     const bool has_prefix = scored && scored->prefix_lens;
+    const bool sink_form = scored && scored->sink_form;
+    const int sinks = scored ? scored->sinks : 0;
+    if (sink_form && (window < 1 || sinks < 0)) return PKV_ERR_INVALID_ARG;
     if (scored) {
         // a cap far outside the scores' range would overflow score / softcap
         if (scored->softcap != 0.f && !(scored->softcap >= 1e-3f && scored->softcap <= 1e6f))
@@ -119,14 +125,14 @@ pkv_status prefill_impl(
     PrefillShape pp;
     // shape first (no CUDA call), then the plan for the real SM count
     pkv_status st = plan_prefill(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
-                                 max_query_len, max_context_len, kv_splits, 1, &pp, window, has_prefix);
+                                 max_query_len, max_context_len, kv_splits, 1, &pp, window, has_prefix, sinks);
     if (st != PKV_OK) return st;
     int sm = 0;
     if (kv_splits == 0) {
         sm = pkv::current_sm_count();
         if (sm <= 0) return PKV_ERR_CUDA;
         st = plan_prefill(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_query_len,
-                          max_context_len, 0, sm, &pp, window, has_prefix);
+                          max_context_len, 0, sm, &pp, window, has_prefix, sinks);
         if (st != PKV_OK) return st;
     }
     const bool plan_items = scored && planned(pp, num_seqs);
@@ -197,6 +203,7 @@ pkv_status prefill_impl(
         p.prefix_lens = scored->prefix_lens;
         p.window = window;
         p.block_size = block_size;
+        p.sinks = std::min(sinks, max_context_len);  // (rounded up to blocks in 32 bits)
         if (scored->softcap > 0.f) {
             p.cap_in = scale / scored->softcap;
             p.cap_out = static_cast<float>(scored->softcap * 1.4426950408889634);
@@ -212,10 +219,14 @@ pkv_status prefill_impl(
         auto *plan = static_cast<pkv::PrefillPlan *>(workspace);
         p.plan = plan;
         p.order = pkv::kOrderPlanned;
-        pkv::paged_prefill_plan_kernel<<<1, pkv::kPlanThreads, 0, s>>>(p, plan);
+        (sink_form ? pkv::paged_prefill_plan_kernel<true> : pkv::paged_prefill_plan_kernel<false>)<<<1, pkv::kPlanThreads, 0, s>>>(p, plan);
         pkv::count_launch();
         if (st = pkv::launch_status(); st != PKV_OK) return st;
     }
+    if (sink_form)
+        return dtype == PKV_F16
+                   ? pkv::launch_prefill_sinks_f16(p, tq, tk, tv, to, block_size, grid, max_query_len, s)
+                   : pkv::launch_prefill_sinks_bf16(p, tq, tk, tv, to, block_size, grid, max_query_len, s);
     if (scored)
         return dtype == PKV_F16
                    ? pkv::launch_prefill_scored_f16(p, tq, tk, tv, to, block_size, grid, max_query_len, s)
@@ -266,6 +277,32 @@ PKV_API size_t pkv_prefill_scored_workspace_bytes(int num_rows, int num_seqs, in
         return static_cast<size_t>(-1);
     if (planned(pp, num_seqs)) return plan_bytes(pp, num_seqs);
     return prefill_workspace(num_rows, num_q_heads, pp.splits);
+}
+
+PKV_API size_t pkv_prefill_sinks_workspace_bytes(int num_rows, int num_seqs, int num_q_heads, int num_kv_heads,
+                                                 int head_dim, int block_size, int max_query_len, int max_context_len,
+                                                 int window, int sinks, int kv_splits) {
+    const int sm = kv_splits > 0 ? 1 : pkv::current_sm_count();
+    if (sm <= 0 || num_rows < 0 || window < 1 || sinks < 0) return static_cast<size_t>(-1);
+    PrefillShape pp;
+    if (plan_prefill(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_query_len, max_context_len, kv_splits,
+                     sm, &pp, window, false, sinks) != PKV_OK)
+        return static_cast<size_t>(-1);
+    if (planned(pp, num_seqs)) return plan_bytes(pp, num_seqs);
+    return prefill_workspace(num_rows, num_q_heads, pp.splits);
+}
+
+PKV_API pkv_status pkv_paged_attention_prefill_sinks(
+    const void *q, const void *k_cache, const void *v_cache, int64_t num_blocks, int64_t block_stride_elems,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *query_start, const int32_t *context_lens,
+    int num_rows, int max_query_len, int max_context_len, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, float scale, int window, int sinks, void *out, void *workspace, size_t workspace_bytes, int kv_splits,
+    pkv_dtype dtype, void *stream) {
+    const ScoredPrefillArgs a{0.f, nullptr, window, nullptr, nullptr, true, sinks};
+    return prefill_impl(q, k_cache, v_cache, num_blocks, block_stride_elems, block_tables, max_blocks_per_seq,
+                        query_start, context_lens, num_rows, max_query_len, max_context_len, num_seqs, num_q_heads,
+                        num_kv_heads, head_dim, block_size, scale, out, workspace, workspace_bytes, kv_splits, dtype,
+                        stream, &a);
 }
 
 PKV_API pkv_status pkv_paged_attention_prefill_scored(

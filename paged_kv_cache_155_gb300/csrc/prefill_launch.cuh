@@ -70,6 +70,45 @@ pkv_status launch_prefill(const PrefillParams &p, const CUtensorMap &tq, const C
     return launch_status();
 }
 
+// The sink form (a window and first tokens): planned items, or row tiles when the KV ranges are split.
+template <typename T>
+pkv_status launch_prefill_sinks(const PrefillParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
+                                const CUtensorMap &tv, const CUtensorMap &to, int block_size, int grid,
+                                int max_query_len, cudaStream_t s) {
+    auto launch = [&](auto bs) -> pkv_status {
+        constexpr int BS = decltype(bs)::value;
+        return p.order == kOrderPlanned ? launch_prefill_one<T, BS, kOrderPlanned, kSinkForm>(p, tq, tk, tv, to, grid, s)
+                                        : launch_prefill_one<T, BS, kOrderRowTiles, kSinkForm>(p, tq, tk, tv, to, grid, s);
+    };
+    const pkv_status st = block_size == 8    ? launch(std::integral_constant<int, 8>{})
+                          : block_size == 16 ? launch(std::integral_constant<int, 16>{})
+                                             : launch(std::integral_constant<int, 32>{});
+    if (st != PKV_OK || p.splits == 1) return st;
+    const int64_t rows = static_cast<int64_t>(max_query_len) * p.num_q_heads;
+    const dim3 mgrid(static_cast<unsigned>((rows + 3) / 4), static_cast<unsigned>(p.num_seqs));
+    paged_prefill_merge_kernel<T, true, true><<<mgrid, 128, 0, s>>>(p);
+    count_launch();
+    return launch_status();
+}
+
+// The tree form: the stream order over all SMs, then the merge of the units that it cut.
+template <typename T>
+pkv_status launch_tree(const PrefillParams &p, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                       const CUtensorMap &to, int block_size, int grid, cudaStream_t s) {
+    const pkv_status st =
+        block_size == 8    ? launch_prefill_one<T, 8, kOrderStream, kTreeForm>(p, tq, tk, tv, to, grid, s)
+        : block_size == 16 ? launch_prefill_one<T, 16, kOrderStream, kTreeForm>(p, tq, tk, tv, to, grid, s)
+                           : launch_prefill_one<T, 32, kOrderStream, kTreeForm>(p, tq, tk, tv, to, grid, s);
+    if (st != PKV_OK) return st;
+    const dim3 mgrid(static_cast<unsigned>(grid), static_cast<unsigned>((p.tile_rows + kTreeMergeWarps - 1) / kTreeMergeWarps));
+    if (launch_kernel(paged_tree_merge_kernel<T>, mgrid, dim3(32 * kTreeMergeWarps), 0, s, true, p) != cudaSuccess) {
+        cudaGetLastError();
+        return PKV_ERR_CUDA;
+    }
+    count_launch();
+    return launch_status();
+}
+
 // Defined in prefill_scored_f16.cu / prefill_scored_bf16.cu.
 pkv_status launch_prefill_scored_f16(const PrefillParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
                                      const CUtensorMap &tv, const CUtensorMap &to, int block_size, int grid,
@@ -77,5 +116,17 @@ pkv_status launch_prefill_scored_f16(const PrefillParams &p, const CUtensorMap &
 pkv_status launch_prefill_scored_bf16(const PrefillParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
                                       const CUtensorMap &tv, const CUtensorMap &to, int block_size, int grid,
                                       int max_query_len, cudaStream_t s);
+
+// Defined in prefill_sinks_f16.cu / _bf16.cu and tree_f16.cu / _bf16.cu.
+pkv_status launch_prefill_sinks_f16(const PrefillParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
+                                    const CUtensorMap &tv, const CUtensorMap &to, int block_size, int grid,
+                                    int max_query_len, cudaStream_t s);
+pkv_status launch_prefill_sinks_bf16(const PrefillParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
+                                     const CUtensorMap &tv, const CUtensorMap &to, int block_size, int grid,
+                                     int max_query_len, cudaStream_t s);
+pkv_status launch_tree_f16(const PrefillParams &p, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                           const CUtensorMap &to, int block_size, int grid, cudaStream_t s);
+pkv_status launch_tree_bf16(const PrefillParams &p, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                            const CUtensorMap &to, int block_size, int grid, cudaStream_t s);
 
 }  // namespace pkv

@@ -114,6 +114,12 @@ struct PrefillParams {
     const struct PrefillPlan *plan;  // the item table (planned order)
     int fixed_ref;               // the fixed form
     float shift;                 // its reference, every row's; else 0
+    int sinks;                   // sink form: first tokens that every row sees besides its window
+    // Tree form: which tokens of the chunk a row sees, and the shared work (stream order).
+    const int64_t *tree_mask;    // [num_rows][mask_words], bit c: chunk token c
+    int mask_words;
+    float *seg_o, *seg_m, *seg_l;      // partials of cut units: [2 CTA + slot][128 rows][128], [..][128]
+    struct TreeSplit *tree_splits;     // [grid]: the unit that begins in a CTA's share and goes on past it
 };
 // The fixed form's largest cap_out, and the exponent that its weights may reach: the reference
 // is what a score of cap_out exceeds that by.  So weights lie in 2^-100 .. 2^50: a product with
@@ -121,10 +127,10 @@ struct PrefillParams {
 // while |V| times the tokens is below 2^78.
 constexpr float kFixedRefMax = 75.f, kFixedWeightMax = 50.f;
 // see paged_prefill_tc_kernel
-constexpr int kPlainForm = 0, kScoredForm = 1, kFixedForm = 2, kUncappedForm = 3;
+constexpr int kPlainForm = 0, kScoredForm = 1, kFixedForm = 2, kUncappedForm = 3, kSinkForm = 4, kTreeForm = 5;
 
 // Item orders (PrefillParams::order), see prefill_item.
-constexpr int kOrderRowTiles = 0, kOrderPairs = 1, kOrderSortedGroups = 2, kOrderPlanned = 3;
+constexpr int kOrderRowTiles = 0, kOrderPairs = 1, kOrderSortedGroups = 2, kOrderPlanned = 3, kOrderStream = 4;
 constexpr int kSortedGroupsMaxSeqs = 32;  // sequences a block ranks by length itself
 
 // One sequence's chunk start, chunk end and context length, as read from the
@@ -180,6 +186,7 @@ __device__ __forceinline__ bool prefill_seq(const PrefillParams &p, const Prefil
 // warps (the minimum of the starts is a warp reduction).
 struct PrefillRange {
     int lo, hi, begin;
+    int gap = 0;  // sink form: tokens left out behind the first ones (whole blocks)
 };
 __device__ __forceinline__ PrefillRange prefill_range(const PrefillParams &p, int seq, int q0, int len, int base_pos,
                                                       int j0, int j1) {
@@ -193,6 +200,23 @@ __device__ __forceinline__ PrefillRange prefill_range(const PrefillParams &p, in
     if (p.prefix_lens) hi = max(hi, min(len, p.prefix_lens[seq]));
     if (lo >= hi) return PrefillRange{hi, hi, hi};
     return PrefillRange{lo, hi, lo & ~(p.block_size - 1)};
+}
+
+// Sink form: rows whose first window begins at token lo see nothing between the first
+// `sinks` tokens and lo, and the whole blocks there are left out: the gap.  What is left is
+// counted through -- token t of the context is token t, or t - gap behind the gap, of the
+// range that the tiles walk -- and only the producers' block lookup goes back.
+__device__ __forceinline__ int sink_blocks(const PrefillParams &p) { return (p.sinks + p.block_size - 1) / p.block_size; }
+__device__ __forceinline__ int sink_gap(const PrefillParams &p, int lo) {
+    return max(0, lo / p.block_size - sink_blocks(p)) * p.block_size;
+}
+// The same range for chunk tokens j0 .. j1, in counted tokens: [0, hi), of which those from
+// `sinks` to lo are seen by no row.
+__device__ __forceinline__ PrefillRange sink_range(const PrefillParams &p, int base_pos, int j0, int j1) {
+    const int lo = max(0, base_pos + j0 + 1 - p.window), gap = sink_gap(p, lo);
+    PrefillRange r{lo - gap, base_pos + j1 + 1 - gap, 0};
+    r.gap = gap;
+    return r;
 }
 
 // Planned order (scored form, one split): the row tiles of all sequences that hold work,
@@ -233,6 +257,8 @@ struct PrefillItem {
     int ntiles;          // 128-token KV tiles
     int seq;
     int lo;              // scored form: the row tile's first visible token (tokens before it are masked)
+    int gap;             // sink form: tokens left out (lo, tok_lo and tok_hi count without them)
+    bool partial;        // tree form: a piece of the unit's KV tiles; its partials go to slot `split` of this CTA
 };
 
 // Item i of the static order.
@@ -252,9 +278,11 @@ struct PrefillItem {
 // (sequence, KV head) pairs in L2.  False when the item holds no work: a row tile
 // past the chunk, a split past the tile's causal limit, or a sequence out of
 // contract (flagged once when `flag`).
-template <int ORDER, bool kScored = false>
+template <int ORDER, bool kScored = false, bool kSinks = false>
 __device__ __forceinline__ bool prefill_item(const PrefillParams &p, int i, const PrefillSeqVals &sv,
                                              bool flag, PrefillItem &it, const unsigned char *by_len) {
+    it.gap = 0;
+    it.partial = false;
     if constexpr (ORDER == kOrderSortedGroups) {
         const int g = fast_div(i, p.div_row_tiles);
         const int pos = i - g * p.row_tiles;
@@ -290,6 +318,15 @@ __device__ __forceinline__ bool prefill_item(const PrefillParams &p, int i, cons
     if (it.row0 >= it.rows) return false;
     const int last_row = min(it.rows, it.row0 + p.tile_rows) - 1;
     it.base_pos = it.len - it.chunk;
+    if constexpr (kSinks) {
+        const PrefillRange r = sink_range(p, it.base_pos, fast_div(it.row0, p.div_group), fast_div(last_row, p.div_group));
+        it.lo = r.lo;
+        it.gap = r.gap;
+        it.tok_lo = it.split * p.split_tokens;
+        it.tok_hi = min(r.hi, it.tok_lo + p.split_tokens);
+        it.ntiles = (it.tok_hi - it.tok_lo + 127) / 128;
+        return it.tok_hi > it.tok_lo;
+    }
     if constexpr (kScored) {
         const PrefillRange r = prefill_range(p, it.seq, it.q0, it.len, it.base_pos, fast_div(it.row0, p.div_group),
                                              fast_div(last_row, p.div_group));
@@ -310,7 +347,10 @@ __device__ __forceinline__ bool prefill_item(const PrefillParams &p, int i, cons
     return it.tok_hi > it.tok_lo;
 }
 
+// (sink form: an entry's tok_lo is its gap, the tiles begin at 0)
+template <bool kSinks>
 __device__ __forceinline__ void planned_item(const PrefillParams &p, int i, const PrefillEntry &e, PrefillItem &it) {
+    it.partial = false;
     it.q0 = e.q0;
     it.chunk = e.chunk;
     it.len = e.len;
@@ -322,10 +362,122 @@ __device__ __forceinline__ void planned_item(const PrefillParams &p, int i, cons
     it.row0 = e.row_tile * p.tile_rows;
     it.base_pos = e.len - e.chunk;
     it.lo = e.lo;
-    it.tok_lo = e.tok_lo;
+    it.gap = kSinks ? e.tok_lo : 0;
+    it.tok_lo = kSinks ? 0 : e.tok_lo;
     it.tok_hi = e.tok_hi;
-    it.ntiles = max(1, (e.tok_hi - e.tok_lo + 127) / 128);  // rows that see nothing: a tile without tokens
+    it.ntiles = max(1, (it.tok_hi - it.tok_lo + 127) / 128);  // rows that see nothing: a tile without tokens
 }
+
+// Stream order (tree form): the KV tiles of all units -- a row tile of a sequence and a KV head -- in one
+// row, sequence by sequence, KV head by KV head, cut into equal shares, one per CTA.  Every CTA then
+// streams the same number of tiles whatever the contexts' lengths; it takes at most two pieces of
+// units that are cut (its first and its last), whose partials are merged, and whole units between.
+// A draft's few rows per context leave this kernel bound by the context's bytes, so an even share of
+// them is what a split has to give.
+struct StreamShare {
+    int seq, pos;  // the first unit's sequence, and the share's first tile counted in that sequence
+    int left;      // tiles of the share
+    int quota;     // tiles of every share (the last ones' may be shorter)
+};
+struct TreeSplit {
+    int pieces;    // CTAs that hold pieces of the unit, this one first; 0: none begins here
+    int slot;      // this CTA's piece
+    int q0, chunk; // the unit's sequence
+    int kvh, row_tile;
+    int pad[2];
+};
+constexpr int kMinShare = 2;  // tiles of a share, at least
+// KV tiles of one unit and units of a sequence (no tiles: an empty or bad sequence)
+__device__ __forceinline__ int stream_tiles(const PrefillParams &p, const PrefillSeqVals &v, int &units) {
+    int q0, chunk, len;
+    units = 0;
+    if (!prefill_seq(p, v, q0, chunk, len) || chunk == 0) return 0;
+    units = (chunk + p.tile_tokens - 1) / p.tile_tokens * p.num_kv_heads;
+    return (len + 127) / 128;
+}
+// This CTA's share, by one warp.
+__device__ __forceinline__ StreamShare stream_share(const PrefillParams &p, int lane) {
+    auto tiles_of = [&](int seq) {
+        if (seq >= p.num_seqs) return 0;
+        int units;
+        const int n = stream_tiles(p, PrefillSeqVals{p.query_start[seq], p.query_start[seq + 1], p.context_lens[seq]}, units);
+        return n * units;
+    };
+    const int mine0 = tiles_of(lane);  // sequences 0 .. 31, kept for the second pass
+    int total = mine0;
+    for (int seq = 32 + lane; seq < p.num_seqs; seq += 32) total += tiles_of(seq);
+    total = __reduce_add_sync(0xffffffffu, total);
+    StreamShare s{0, 0, 0, max(kMinShare, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x))};
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * s.quota;
+    if (first >= total) return s;
+    s.left = min(s.quota, total - static_cast<int>(first));
+    int before = 0;
+    for (int s0 = 0;; s0 += 32) {
+        const int mine = s0 == 0 ? mine0 : tiles_of(s0 + lane);
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + incl > first);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            s.seq = s0 + l;
+            s.pos = static_cast<int>(first) - (before + __shfl_sync(0xffffffffu, incl - mine, l));
+            return s;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+}
+// A role's walk over the share's items.
+struct StreamWalk {
+    StreamShare s;
+    PrefillSeqVals v;
+    int tiles, units;  // of sequence s.seq
+    bool first;
+    __device__ __forceinline__ void start(const PrefillParams &p, const StreamShare &share) {
+        s = share;
+        first = true;
+        if (s.left > 0) load(p);
+    }
+    __device__ __forceinline__ void load(const PrefillParams &p) {
+        v = PrefillSeqVals{p.query_start[s.seq], p.query_start[s.seq + 1], p.context_lens[s.seq]};
+        tiles = stream_tiles(p, v, units);
+    }
+    // the next item; false at the end.  last: the tiles of its unit behind it (0: the unit ends here)
+    __device__ __forceinline__ bool next(const PrefillParams &p, PrefillItem &it, int &behind) {
+        if (s.left <= 0) return false;
+        while (s.pos >= tiles * units) {  // (the share's tiles lie in later sequences)
+            ++s.seq;
+            s.pos = 0;
+            load(p);
+        }
+        const int unit = s.pos / tiles, tile = s.pos - unit * tiles;
+        const int n = min(tiles - tile, s.left);
+        it.seq = s.seq;
+        it.q0 = v.q0;
+        it.chunk = v.q1 - v.q0;
+        it.len = v.len;
+        const int row_tiles = (it.chunk + p.tile_tokens - 1) / p.tile_tokens;
+        it.kvh = unit / row_tiles;
+        it.row_tile = unit - it.kvh * row_tiles;
+        it.rows = it.chunk * p.group;
+        it.row0 = it.row_tile * p.tile_rows;
+        it.base_pos = it.len - it.chunk;
+        it.tok_lo = tile * 128;
+        it.tok_hi = min(it.len, (tile + n) * 128);
+        it.ntiles = n;
+        it.lo = it.gap = 0;
+        it.partial = n < tiles;
+        it.split = first ? 0 : 1;
+        behind = tiles - tile - n;
+        first = false;
+        s.pos += n;
+        s.left -= n;
+        return true;
+    }
+};
 
 // Scored form: what thread r's row of an item sees, [lo, hi), and its bias per token in
 // log2 units; a row past the item's rows sees nothing.
@@ -356,6 +508,7 @@ __device__ __forceinline__ int prefill_slot_item(const PrefillParams &p, int k) 
     if constexpr (ORDER == kOrderSortedGroups || ORDER == kOrderPlanned)
         return k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     if constexpr (ORDER == kOrderPairs) return 2 * (blockIdx.x + (k >> 1) * gridDim.x) + (k & 1);
+    if constexpr (ORDER == kOrderStream) return k;  // (the walk says when the share ends)
     return blockIdx.x + k * gridDim.x;
 }
 
@@ -363,7 +516,7 @@ __device__ __forceinline__ int prefill_slot_item(const PrefillParams &p, int k) 
 // last V slot (one split, and every row of the row tile inside the chunk, so the
 // box holds no other sequence's rows); the others store row by row.
 __device__ __forceinline__ bool prefill_staged(const PrefillParams &p, const PrefillItem &it) {
-    return p.splits == 1 && it.row0 + p.tile_rows <= it.rows;
+    return p.splits == 1 && !it.partial && it.row0 + p.tile_rows <= it.rows;
 }
 
 // Shared memory: the Q tile(s) of consecutive items, K and V rings of
@@ -386,6 +539,7 @@ struct PrefillLayout {
     static constexpr int kOffSum = kOffMisc + 16;     // row-sum exchange: [2 halves][128 rows] fp32
     static constexpr int kOffByLen = kOffSum + 2 * 128 * 4;  // sequences by length (sorted-groups order)
     static constexpr int kBytes = kOffByLen + kSortedGroupsMaxSeqs;
+    static_assert(sizeof(StreamShare) <= kSortedGroupsMaxSeqs, "stream order: the share takes the table's place");
     static constexpr int kSmemBytes = kBytes + 1024;  // + alignment slack
     static constexpr uint32_t kTmemCols = 512;        // S[3] at 0 / 128 / 256 (P[b] over S[b]), O at 384
     static constexpr uint32_t kOCol = 384;
@@ -601,6 +755,8 @@ __global__ void __launch_bounds__(384, 1)
     constexpr int TILE = L::kTile, D = 128;
     constexpr bool kBF16 = !std::is_same<T, __half>::value;
     constexpr bool kScored = kForm != kPlainForm, kFixed = kForm == kFixedForm;
+    constexpr bool kSinks = kForm == kSinkForm, kTree = kForm == kTreeForm;
+    static_assert(kTree == (ORDER == kOrderStream), "trees, and they alone, take the stream order");
     constexpr bool kCapped = kForm == kScoredForm || kFixed;
     static_assert(!kFixed || kBF16, "the fixed reference needs bf16's range");
     static_assert(TILE / BS <= 32, "one table entry per producer lane");
@@ -675,6 +831,22 @@ __global__ void __launch_bounds__(384, 1)
         }
         if (lane < p.num_seqs) by_len[rank] = static_cast<unsigned char>(lane);
     }
+    StreamShare *share_slot = reinterpret_cast<StreamShare *>(sm + L::kOffByLen);
+    if constexpr (kTree) {
+        pdl_trigger();  // the merge behind this grid may be placed
+        if (warp == 2) {
+            const StreamShare mine = stream_share(p, lane);
+            if (lane == 0) *share_slot = mine;
+        }
+        if (blockIdx.x == 0 && warp == 3) {
+            // sequences out of contract
+            for (int seq = lane; seq < p.num_seqs; seq += 32) {
+                int q0, chunk, len;
+                if (!prefill_seq(p, PrefillSeqVals{p.query_start[seq], p.query_start[seq + 1], p.context_lens[seq]}, q0, chunk, len))
+                    raise_flag(p.status, PKV_DEVERR_CONTEXT_LEN);
+            }
+        }
+    }
     if (warp == 0 && lane == 0) {
         tc::prefetch_tensormap(&tmap_q);
         tc::prefetch_tensormap(&tmap_k);
@@ -688,6 +860,12 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t tmem = *tmem_slot;
     constexpr bool kPlanned = ORDER == kOrderPlanned;
     int num_items = p.num_items;
+    StreamWalk walk;  // stream order: this role's walk
+    int behind = 0;
+    if constexpr (kTree) {
+        num_items = 0x7fffffff;
+        walk.start(p, *share_slot);
+    }
     if constexpr (kPlanned) {
         pdl_wait();  // for the item table, written by the kernel before this one
         num_items = p.plan->entries * p.num_kv_heads;
@@ -716,10 +894,12 @@ __global__ void __launch_bounds__(384, 1)
         if constexpr (kPlanned) ahead = load_entry(p, prefill_slot_item<ORDER>(p, 0), num_items);
         for (int ki = 0, item = prefill_slot_item<ORDER>(p, 0); item < num_items && ok; item = prefill_slot_item<ORDER>(p, ++ki)) {
             PrefillItem it;
-            if constexpr (kPlanned) {
-                planned_item(p, item, ahead, it);
+            if constexpr (kTree) {
+                if (!walk.next(p, it, behind)) break;
+            } else if constexpr (kPlanned) {
+                planned_item<kSinks>(p, item, ahead, it);
                 ahead = load_entry(p, prefill_slot_item<ORDER>(p, ki + 1), num_items);
-            } else if (!prefill_item<ORDER, kScored>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), kv == 0, it, by_len)) {
+            } else if (!prefill_item<ORDER, kScored, kSinks>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), kv == 0, it, by_len)) {
                 continue;
             }
             const int32_t *trow = p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks_per_seq;
@@ -728,7 +908,9 @@ __global__ void __launch_bounds__(384, 1)
                 const int nblk = (min(TILE, it.tok_hi - t0) + BS - 1) / BS;
                 int e = -1;
                 if (lane < nblk) {
-                    e = trow[t0 / BS + lane];
+                    int at = t0 / BS + lane;
+                    if constexpr (kSinks) at += at >= sink_blocks(p) ? it.gap / BS : 0;
+                    e = trow[at];
                     if (e < 0 || e >= p.num_blocks) {
                         if (kv == 0) raise_flag(p.status, PKV_DEVERR_BLOCK_TABLE);
                         e = -1;
@@ -757,10 +939,20 @@ __global__ void __launch_bounds__(384, 1)
                 // the next item's Q box into L2 now, so its load does not wait for HBM (lane 0
                 // alone: the scored form's token range, a warp's work, is not needed for it)
                 PrefillItem nx;
+                if constexpr (kTree) {
+                    StreamWalk peek = walk;
+                    int unused;
+                    if (peek.next(p, nx, unused)) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            tc::tma_prefetch_3d(&tmap_q, c * 64, nx.kvh * p.group, nx.q0 + nx.row_tile * p.tile_tokens);
+                    }
+                    return;
+                }
                 if constexpr (kPlanned) {
                     const int i2 = prefill_slot_item<ORDER>(p, ki + 1);
                     if (i2 < num_items) {
-                        planned_item(p, i2, ahead, nx);
+                        planned_item<kSinks>(p, i2, ahead, nx);
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
                             tc::tma_prefetch_3d(&tmap_q, c * 64, nx.kvh * p.group, nx.q0 + nx.row_tile * p.tile_tokens);
@@ -849,10 +1041,12 @@ __global__ void __launch_bounds__(384, 1)
         if constexpr (kPlanned) ahead = load_entry(p, prefill_slot_item<ORDER>(p, 0), num_items);
         for (int ki = 0, item = prefill_slot_item<ORDER>(p, 0); item < num_items && ok; item = prefill_slot_item<ORDER>(p, ++ki)) {
             PrefillItem it;
-            if constexpr (kPlanned) {
-                planned_item(p, item, ahead, it);
+            if constexpr (kTree) {
+                if (!walk.next(p, it, behind)) break;
+            } else if constexpr (kPlanned) {
+                planned_item<kSinks>(p, item, ahead, it);
                 ahead = load_entry(p, prefill_slot_item<ORDER>(p, ki + 1), num_items);
-            } else if (!prefill_item<ORDER, kScored>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) {
+            } else if (!prefill_item<ORDER, kScored, kSinks>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) {
                 continue;
             }
             const int qb = n % QB;
@@ -901,10 +1095,12 @@ __global__ void __launch_bounds__(384, 1)
         if constexpr (kPlanned) ahead = load_entry(p, prefill_slot_item<ORDER>(p, 0), num_items);
         for (int ki = 0, item = prefill_slot_item<ORDER>(p, 0); item < num_items && ok; item = prefill_slot_item<ORDER>(p, ++ki)) {
             PrefillItem it;
-            if constexpr (kPlanned) {
-                planned_item(p, item, ahead, it);
+            if constexpr (kTree) {
+                if (!walk.next(p, it, behind)) break;
+            } else if constexpr (kPlanned) {
+                planned_item<kSinks>(p, item, ahead, it);
                 ahead = load_entry(p, prefill_slot_item<ORDER>(p, ki + 1), num_items);
-            } else if (!prefill_item<ORDER, kScored>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) {
+            } else if (!prefill_item<ORDER, kScored, kSinks>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) {
                 continue;
             }
             const bool staged = prefill_staged(p, it);
@@ -1013,21 +1209,24 @@ __global__ void __launch_bounds__(384, 1)
             return true;
         };
         PrefillRow view{0, 0, 0.f};
+        TreeSplit split{};  // tree form
         PrefillEntry ahead{};  // planned order: the next item's entry
         if constexpr (kPlanned) ahead = load_entry(p, prefill_slot_item<ORDER>(p, 0), num_items);
         if constexpr (kPlanned) {
             if (prefill_slot_item<ORDER>(p, 0) < num_items) {
                 PrefillItem first;
-                planned_item(p, prefill_slot_item<ORDER>(p, 0), ahead, first);
+                planned_item<kSinks>(p, prefill_slot_item<ORDER>(p, 0), ahead, first);
                 view = prefill_row(p, first, r);
             }
         }
         for (int ki = 0, item = prefill_slot_item<ORDER>(p, 0); item < num_items && ok; item = prefill_slot_item<ORDER>(p, ++ki)) {
             PrefillItem it;
-            if constexpr (kPlanned) {
-                planned_item(p, item, ahead, it);
+            if constexpr (kTree) {
+                if (!walk.next(p, it, behind)) break;
+            } else if constexpr (kPlanned) {
+                planned_item<kSinks>(p, item, ahead, it);
                 ahead = load_entry(p, prefill_slot_item<ORDER>(p, ki + 1), num_items);
-            } else if (!prefill_item<ORDER, kScored>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) {
+            } else if (!prefill_item<ORDER, kScored, kSinks>(p, item, prefill_seq_vals<ORDER>(p, item, by_len), false, it, by_len)) {
                 continue;
             }
             const int row = it.row0 + r;
@@ -1038,12 +1237,31 @@ __global__ void __launch_bounds__(384, 1)
             const int row_lo = view.lo, row_hi = view.hi;  // ... in the scored form [row_lo, row_hi)
             const float slope2 = view.slope2;
             float m_ref = kFixed ? p.shift : -INFINITY, l = 0.f;
+            const int64_t *tree_row = nullptr;  // this row's words
+            if constexpr (kTree) {
+                if (live) tree_row = p.tree_mask + static_cast<int64_t>(it.q0 + jtok) * p.mask_words;
+                if (behind > 0 && (it.tok_lo == 0)) {
+                    // the unit begins in this share and goes on: its pieces, in this CTA and the next ones
+                    split = TreeSplit{1 + (behind + walk.s.quota - 1) / walk.s.quota, it.split, it.q0, it.chunk, it.kvh, it.row_tile, {0, 0}};
+                }
+            }
             for (int j = 0; j < it.ntiles && ok; ++j, ++jt) {
                 const int b = jt % SB;
                 const int t0 = it.tok_lo + j * TILE;
                 const int valid = min(TILE, it.tok_hi - t0);                    // columns loaded
                 const int vr = live ? max(0, min(valid, pos + 1 - t0)) : 0;  // columns this row sees
                 const int vh = max(0, min(64, vr - c0));                     // ... in this half
+                // tree form: the columns seen of the chunk, its words read while S is made
+                uint64_t tree_bits = 0;
+                if constexpr (kTree) {
+                    const int at = t0 + c0 - it.base_pos;  // the half's first column as a chunk token
+                    if (tree_row && at > -64 && at < it.chunk) {
+                        const int w = at >> 6, sh = at & 63;  // (at < 0: word -1)
+                        const uint64_t low = w >= 0 && w < p.mask_words ? static_cast<uint64_t>(tree_row[w]) : 0ull;
+                        const uint64_t high = sh && w + 1 < p.mask_words ? static_cast<uint64_t>(tree_row[w + 1]) : 0ull;
+                        tree_bits = (low >> sh) | (sh ? high << (64 - sh) : 0ull);
+                    }
+                }
                 if (!tc_wait_warp(&s_full[b], (jt / SB) & 1, abort_flag, p.status)) {
                     ok = false;
                     break;
@@ -1056,15 +1274,29 @@ __global__ void __launch_bounds__(384, 1)
                 tc::tmem_ld_wait();
                 // tiles every row of the warp sees completely skip the per-column masks
                 // (scored: columns [clo, chi) of this half)
-                const int clo = kScored ? min(64, max(0, row_lo - t0 - c0)) : 0;
-                const int chi = kScored ? min(64, max(0, min(valid, row_hi - t0) - c0)) : 0;
-                const bool full = __all_sync(0xffffffffu, kScored ? clo == 0 && chi == 64 : vr == TILE);
+                const int clo = kScored ? min(64, max(0, row_lo - it.gap - t0 - c0)) : 0;
+                const int chi = kScored ? min(64, max(0, min(valid, row_hi - it.gap - t0) - c0)) : 0;
+                // ... and in the sink form the first tokens, in the tree form the context and the row's words
+                uint32_t seen0 = 0, seen1 = 0;
+                if constexpr (kScored) seen0 = below(chi) & ~below(clo), seen1 = below(chi - 32) & ~below(clo - 32);
+                if constexpr (kSinks) {
+                    const int first = min(p.sinks, row_hi - it.gap) - t0 - c0;
+                    seen0 |= below(first);
+                    seen1 |= below(first - 32);
+                }
+                if constexpr (kTree) {
+                    const int ctx = live ? it.base_pos - t0 - c0 : 0, in = valid - c0;
+                    seen0 = (below(ctx) | static_cast<uint32_t>(tree_bits)) & below(in);
+                    seen1 = (below(ctx - 32) | static_cast<uint32_t>(tree_bits >> 32)) & below(in - 32);
+                }
+                const bool full = __all_sync(0xffffffffu, kSinks || kTree ? (seen0 & seen1) == 0xffffffffu
+                                                          : kScored      ? clo == 0 && chi == 64
+                                                                         : vr == TILE);
                 // partial maximum of the visible scaled scores: the extreme raw score times
                 // the scale (the maximum for a positive scale, the minimum otherwise)
                 float pmax = -INFINITY, factor = 1.f;
                 if constexpr (kScored) {
                     // the scores themselves replace the raw ones: capped, biased, masked to -inf
-                    const uint32_t seen0 = below(chi) & ~below(clo), seen1 = below(chi - 32) & ~below(clo - 32);
                     if constexpr (kFixed) cap_scores(p, x, full, seen0, seen1, lane_base + 128 * b + c0);
                     else factor = score_row<kCapped>(p, x, slope2, t0 + c0 - pos, full, seen0, seen1,
                                                           lane_base + 128 * b + c0);
@@ -1174,7 +1406,8 @@ __global__ void __launch_bounds__(384, 1)
                 else weights(std::true_type{}, std::true_type{});
                 l += l0 + l1;
                 const int skip = kScored ? it.lo - t0 : 0;  // rows before the row tile's first visible token
-                if (valid < TILE || (kScored && skip > 0)) {
+                const int keep = kSinks ? p.sinks - t0 : 0;   // ... but for the first ones
+                if (valid < TILE || (kScored && skip > 0 && (!kSinks || keep < TILE))) {
                     // V rows past the loaded range: zero this half so 0 * stale never reaches
                     // the MMA.  The parity wait cannot alias an older phase of the slot: S(jt)
                     // exists only once PV(jt - kSB) has completed, so V(jt - kVS), the slot's
@@ -1186,7 +1419,7 @@ __global__ void __launch_bounds__(384, 1)
                         ok = false;
                         break;
                     }
-                    if (r >= valid || (kScored && r < skip)) {
+                    if (r >= valid || (kScored && r < skip && (!kSinks || r >= keep))) {
                         uint4 *vrow = reinterpret_cast<uint4 *>(sm + L::kOffV + (jt % VS) * L::kPanel + half * L::kHalf +
                                                                 r * 128);
 #pragma unroll
@@ -1204,7 +1437,7 @@ __global__ void __launch_bounds__(384, 1)
                 const int i2 = prefill_slot_item<ORDER>(p, ki + 1);
                 if (i2 < num_items) {
                     PrefillItem nx;
-                    planned_item(p, i2, ahead, nx);
+                    planned_item<kSinks>(p, i2, ahead, nx);
                     view = prefill_row(p, nx, r);
                 }
             }
@@ -1245,7 +1478,9 @@ __global__ void __launch_bounds__(384, 1)
                 tc::fence_after_sync();
                 const int g = live ? row - jtok * p.group : 0;
                 const int64_t orow = (static_cast<int64_t>(it.q0) + jtok) * p.num_q_heads + it.kvh * p.group + g;
-                const bool direct = p.splits == 1;
+                const bool direct = p.splits == 1 && !it.partial;
+                // tree form: the rows of a piece go to its slot
+                const int64_t seg = kTree ? (2 * static_cast<int64_t>(blockIdx.x) + it.split) * 128 + r : 0;
                 const float inv_l = lt > 0.f ? 1.f / lt : 0.f;
 #pragma unroll
                 for (int c = 0; c < 64; c += 16) {
@@ -1261,17 +1496,25 @@ __global__ void __launch_bounds__(384, 1)
                         dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
                         dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
                     } else {
-                        float *dst = p.ws_o + (orow * p.splits + it.split) * D + c0 + c;
+                        float *dst = (kTree ? p.seg_o + seg * D : p.ws_o + (orow * p.splits + it.split) * D) + c0 + c;
 #pragma unroll
                         for (int i = 0; i < 16; i += 4)
                             *reinterpret_cast<float4 *>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                     }
                 }
                 if (live && !direct && half == 0) {
-                    p.ws_m[orow * p.splits + it.split] = m_ref;
-                    p.ws_l[orow * p.splits + it.split] = lt;
+                    if constexpr (kTree) {
+                        p.seg_m[seg] = m_ref;
+                        p.seg_l[seg] = lt;
+                    } else {
+                        p.ws_m[orow * p.splits + it.split] = m_ref;
+                        p.ws_l[orow * p.splits + it.split] = lt;
+                    }
                 }
             }
+        }
+        if constexpr (kTree) {
+            if (warp == 2 && lane == 0) p.tree_splits[blockIdx.x] = split;
         }
     }
 
@@ -1289,7 +1532,8 @@ __global__ void __launch_bounds__(384, 1)
 // row tile's first visible token is the minimum over its rows' starts, by a warp.  A sequence out of contract is flagged and gets no entry.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBuckets = 1024;
-inline __global__ void __launch_bounds__(kPlanThreads) paged_prefill_plan_kernel(const PrefillParams p, PrefillPlan *plan) {
+template <bool kSinks>
+__global__ void __launch_bounds__(kPlanThreads) paged_prefill_plan_kernel(const PrefillParams p, PrefillPlan *plan) {
     __shared__ int first[kMaxPlanEntries];
     __shared__ int bucket[kPlanBuckets];
     __shared__ int warp_sum[kPlanThreads / 32];
@@ -1325,6 +1569,11 @@ inline __global__ void __launch_bounds__(kPlanThreads) paged_prefill_plan_kernel
         const int j0 = rt * p.tile_tokens, j1 = min(chunk, j0 + p.tile_tokens) - 1;
         if (j0 >= chunk) return -1;
         const int base_pos = len - chunk;
+        if constexpr (kSinks) {
+            const PrefillRange r = sink_range(p, base_pos, j0, j1);
+            v = PrefillEntry{q0, chunk, len, seq, rt, r.lo, r.gap, r.hi};
+            return (r.hi + 127) / 128;
+        }
         int lo = max(p.window > 0 ? max(0, base_pos + j0 + 1 - p.window) : 0, first[e]);
         int hi = base_pos + j1 + 1;
         if (p.prefix_lens) hi = max(hi, min(len, p.prefix_lens[seq]));
@@ -1379,7 +1628,7 @@ inline __global__ void __launch_bounds__(kPlanThreads) paged_prefill_plan_kernel
 // Log-sum-exp merge of a prefill's KV splits: one warp per (chunk row, query
 // head); the row at position pos has partials in splits 0 .. pos / split_tokens.
 // (scored form: the splits that the row's tile spans).
-template <typename T, bool kScored = false>
+template <typename T, bool kScored = false, bool kSinks = false>
 __global__ void __launch_bounds__(128) paged_prefill_merge_kernel(const PrefillParams p) {
     constexpr int D = 128, PER_LANE = D / 32;
     const int seq = blockIdx.y;
@@ -1394,7 +1643,9 @@ __global__ void __launch_bounds__(128) paged_prefill_merge_kernel(const PrefillP
     int nsp = min(p.splits, pos / p.split_tokens + 1);
     if constexpr (kScored) {
         const int j0 = jtok / p.tile_tokens * p.tile_tokens, j1 = min(chunk, j0 + p.tile_tokens) - 1;
-        const PrefillRange r = prefill_range(p, seq, q0, len, len - chunk, j0, j1);
+        PrefillRange r;
+        if constexpr (kSinks) r = sink_range(p, len - chunk, j0, j1);
+        else r = prefill_range(p, seq, q0, len, len - chunk, j0, j1);
         nsp = (r.hi - r.begin + p.split_tokens - 1) / p.split_tokens;
     }
     const int64_t orow = (static_cast<int64_t>(q0) + jtok) * p.num_q_heads + hq;
@@ -1413,6 +1664,42 @@ __global__ void __launch_bounds__(128) paged_prefill_merge_kernel(const PrefillP
     T *dst = static_cast<T *>(p.out) + orow * D + lane * PER_LANE;
 #pragma unroll
     for (int e = 0; e < PER_LANE; ++e) dst[e] = Elem<T>::from_f32(lsum > 0.f ? o[e] / lsum : 0.f);
+}
+
+// Log-sum-exp merge of the tree form's cut units: the unit that begins in CTA blockIdx.x's share and
+// goes on past it, from that CTA's slot and slot 0 of the CTAs behind.  One warp per row.
+constexpr int kTreeMergeWarps = 8;
+template <typename T>
+__global__ void __launch_bounds__(32 * kTreeMergeWarps) paged_tree_merge_kernel(const PrefillParams p) {
+    constexpr int D = 128;
+    pdl_wait();
+    const TreeSplit s = p.tree_splits[blockIdx.x];
+    if (s.pieces == 0) return;
+    const int lane = threadIdx.x & 31, r = blockIdx.y * kTreeMergeWarps + (threadIdx.x >> 5);
+    const int row = s.row_tile * p.tile_rows + r;
+    if (r >= p.tile_rows || row >= s.chunk * p.group) return;
+    auto seg = [&](int i) { return (2 * static_cast<int64_t>(blockIdx.x + i) + (i == 0 ? s.slot : 0)) * 128 + r; };
+    float mmax = -INFINITY;
+    for (int i = lane; i < s.pieces; i += 32) mmax = fmaxf(mmax, p.seg_m[seg(i)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mmax = fmaxf(mmax, __shfl_xor_sync(0xffffffffu, mmax, o));
+    float lsum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = 0; i < s.pieces; ++i) {
+        const int64_t at = seg(i);
+        const float m = p.seg_m[at], w = m == -INFINITY ? 0.f : fast_exp2(m - mmax);
+        const float4 v = *reinterpret_cast<const float4 *>(p.seg_o + at * D + 4 * lane);
+        lsum = fmaf(w, p.seg_l[at], lsum);
+        o[0] = fmaf(w, v.x, o[0]);
+        o[1] = fmaf(w, v.y, o[1]);
+        o[2] = fmaf(w, v.z, o[2]);
+        o[3] = fmaf(w, v.w, o[3]);
+    }
+    const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+    const int jtok = fast_div(row, p.div_group), g = row - jtok * p.group;
+    const int64_t orow = (static_cast<int64_t>(s.q0) + jtok) * p.num_q_heads + s.kvh * p.group + g;
+    *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + orow * D + 4 * lane) =
+        make_uint2(Elem<T>::pack2(o[0] * inv, o[1] * inv), Elem<T>::pack2(o[2] * inv, o[3] * inv));
 }
 
 }  // namespace pkv

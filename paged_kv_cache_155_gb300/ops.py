@@ -961,6 +961,260 @@ def _decode_args(q, d, block_tables, context_lens, scale, out, max_context_len):
 
 
 # ---------------------------------------------------------------------------
+# A sliding window with a few first tokens that stay visible
+# ---------------------------------------------------------------------------
+
+def _check_sinks(window, sinks):
+    _int32(window=window, sinks=sinks)
+    if window < 1 or sinks < 0:
+        raise ValueError("window must be at least 1 and sinks not negative")
+
+
+def decode_sinks_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len, window,
+                                 sinks, int8=False, partition_size=0) -> int:
+    n = lib().pkv_decode_sinks_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                               max_context_len, window, sinks, int(int8), partition_size)
+    if n == ctypes.c_size_t(-1).value:
+        raise PagedKVError("pkv_decode_sinks_workspace_bytes", 1)
+    return int(n)
+
+
+def _prepare_decode_sinks(what, q, k_cache, v_cache, scales, block_tables, context_lens, scale, out, window, sinks,
+                          max_context_len, partition_size, workspace):
+    nb, hkv, bs, d, stride = _check_int8_cache(k_cache, v_cache, *scales) if scales else _cache_geometry(k_cache, v_cache)
+    if not scales and q.dtype != k_cache.dtype:
+        raise ValueError("q dtype must match the cache")
+    _check_sinks(window, sinks)
+    _int32(partition_size=partition_size)
+    b, hq, scale, max_context_len, out = _decode_args(q, d, block_tables, context_lens, scale, out, max_context_len)
+    _one_device(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens, out=out)
+    with torch.cuda.device(q.device):
+        need = decode_sinks_workspace_bytes(b, hq, hkv, d, bs, max_context_len, window, sinks, bool(scales), partition_size)
+    workspace = _own_workspace(q.device, need, workspace)
+    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *(t.data_ptr() for t in scales), nb, stride,
+            block_tables.data_ptr(), int(block_tables.shape[1]), context_lens.data_ptr(), max_context_len, b, hq, hkv, d, bs,
+            scale, int(window), int(sinks), out.data_ptr(), None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), int(partition_size), _dtype_code(q))
+    return PreparedCall(what, args, q.device,
+                        (q, k_cache, v_cache, scales, block_tables, context_lens, out, workspace), out)
+
+
+def paged_attention_decode_sinks(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                 block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                 scale: Optional[float] = None, out: Optional[torch.Tensor] = None, *, window: int,
+                                 sinks: int, max_context_len: Optional[int] = None, partition_size: int = 0,
+                                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_attention_decode over the last ``window`` tokens of each context and its first
+    ``sinks`` ones; the blocks between are not read and may be freed."""
+    return prepare_paged_attention_decode_sinks(q, k_cache, v_cache, block_tables, context_lens, scale, out,
+                                                window=window, sinks=sinks, max_context_len=max_context_len,
+                                                partition_size=partition_size, workspace=workspace)()
+
+
+def prepare_paged_attention_decode_sinks(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                         block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                         scale: Optional[float] = None, out: Optional[torch.Tensor] = None, *,
+                                         window: int, sinks: int, max_context_len: Optional[int] = None,
+                                         partition_size: int = 0,
+                                         workspace: Optional[torch.Tensor] = None) -> PreparedCall:
+    """paged_attention_decode_sinks, checked and marshalled once (see PreparedCall); the call
+    returns ``out``.  Without ``workspace`` it holds one of its own."""
+    return _prepare_decode_sinks("pkv_paged_attention_decode_sinks", q, k_cache, v_cache, (), block_tables, context_lens,
+                                 scale, out, window, sinks, max_context_len, partition_size, workspace)
+
+
+def paged_attention_decode_sinks_int8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                      k_scale: torch.Tensor, v_scale: torch.Tensor, block_tables: torch.Tensor,
+                                      context_lens: torch.Tensor, scale: Optional[float] = None,
+                                      out: Optional[torch.Tensor] = None, *, window: int, sinks: int,
+                                      max_context_len: Optional[int] = None, partition_size: int = 0,
+                                      workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_attention_decode_sinks over an INT8 cache with per-channel scales [Hkv, d]."""
+    return prepare_paged_attention_decode_sinks_int8(
+        q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, out, window=window, sinks=sinks,
+        max_context_len=max_context_len, partition_size=partition_size, workspace=workspace)()
+
+
+def prepare_paged_attention_decode_sinks_int8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                              k_scale: torch.Tensor, v_scale: torch.Tensor,
+                                              block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                              scale: Optional[float] = None, out: Optional[torch.Tensor] = None, *,
+                                              window: int, sinks: int, max_context_len: Optional[int] = None,
+                                              partition_size: int = 0,
+                                              workspace: Optional[torch.Tensor] = None) -> PreparedCall:
+    """paged_attention_decode_sinks_int8, checked and marshalled once (see PreparedCall)."""
+    return _prepare_decode_sinks("pkv_paged_attention_decode_sinks_int8", q, k_cache, v_cache, (k_scale, v_scale),
+                                 block_tables, context_lens, scale, out, window, sinks, max_context_len, partition_size,
+                                 workspace)
+
+
+def _chunk_args(q, d, dtype, block_tables, query_start, context_lens, scale, out, max_query_len, max_context_len):
+    """The checks that calls over chunks share: (num_rows, num_q_heads, num_seqs, scale, out)."""
+    if q.dim() != 3 or q.shape[2] != d or not q.is_contiguous() or q.dtype != dtype:
+        raise ValueError(f"q must be a contiguous [num_rows, num_q_heads, {d}] of the cache dtype")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out must match q")
+    b = _chunk_tables(block_tables, query_start, context_lens, max_query_len, max_context_len)
+    return int(q.shape[0]), int(q.shape[1]), b, 1.0 / math.sqrt(d) if scale is None else float(scale), out
+
+
+def _chunk_tables(block_tables, query_start, context_lens, max_query_len, max_context_len):
+    b = int(context_lens.numel())
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != b \
+            or not block_tables.is_contiguous():
+        raise ValueError("block_tables must be a contiguous int32 [num_seqs, max_blocks_per_seq]")
+    if query_start.dtype != torch.int32 or query_start.numel() != b + 1 or not query_start.is_contiguous():
+        raise ValueError("query_start must be a contiguous int32 [num_seqs + 1]")
+    if context_lens.dtype != torch.int32 or not context_lens.is_contiguous():
+        raise ValueError("context_lens must be a contiguous int32 [num_seqs]")
+    _int32(max_query_len=max_query_len, max_context_len=max_context_len)
+    return b
+
+
+def prefill_sinks_workspace_bytes(num_rows, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_query_len,
+                                  max_context_len, window, sinks, kv_splits=0) -> int:
+    n = lib().pkv_prefill_sinks_workspace_bytes(num_rows, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                                max_query_len, max_context_len, window, sinks, kv_splits)
+    if n == ctypes.c_size_t(-1).value:
+        raise PagedKVError("pkv_prefill_sinks_workspace_bytes", 1)
+    return int(n)
+
+
+def paged_attention_prefill_sinks(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                  block_tables: torch.Tensor, query_start: torch.Tensor, context_lens: torch.Tensor,
+                                  scale: Optional[float] = None, out: Optional[torch.Tensor] = None, *,
+                                  max_query_len: int, max_context_len: int, window: int, sinks: int,
+                                  kv_splits: int = 0, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_attention_prefill where each row sees the last ``window`` tokens up to its position
+    and the first ``sinks`` ones."""
+    return prepare_paged_attention_prefill_sinks(
+        q, k_cache, v_cache, block_tables, query_start, context_lens, scale, out, max_query_len=max_query_len,
+        max_context_len=max_context_len, window=window, sinks=sinks, kv_splits=kv_splits, workspace=workspace)()
+
+
+def prepare_paged_attention_prefill_sinks(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                          block_tables: torch.Tensor, query_start: torch.Tensor,
+                                          context_lens: torch.Tensor, scale: Optional[float] = None,
+                                          out: Optional[torch.Tensor] = None, *, max_query_len: int,
+                                          max_context_len: int, window: int, sinks: int, kv_splits: int = 0,
+                                          workspace: Optional[torch.Tensor] = None) -> PreparedCall:
+    """paged_attention_prefill_sinks, checked and marshalled once (see PreparedCall); the call
+    returns ``out``.  Without ``workspace`` it holds one of its own."""
+    nb, hkv, bs, d, stride = _cache_geometry(k_cache, v_cache)
+    _check_sinks(window, sinks)
+    _int32(kv_splits=kv_splits)
+    rows, hq, b, scale, out = _chunk_args(q, d, k_cache.dtype, block_tables, query_start, context_lens, scale, out,
+                                          max_query_len, max_context_len)
+    _one_device(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, query_start=query_start,
+                context_lens=context_lens, out=out)
+    with torch.cuda.device(q.device):
+        need = prefill_sinks_workspace_bytes(rows, b, hq, hkv, d, bs, max_query_len, max_context_len, window, sinks,
+                                             kv_splits)
+    workspace = _own_workspace(q.device, need, workspace)
+    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, stride, block_tables.data_ptr(),
+            int(block_tables.shape[1]), query_start.data_ptr(), context_lens.data_ptr(), rows, int(max_query_len),
+            int(max_context_len), b, hq, hkv, d, bs, scale, int(window), int(sinks), out.data_ptr(),
+            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), int(kv_splits), _dtype_code(q))
+    return PreparedCall("pkv_paged_attention_prefill_sinks", args, q.device,
+                        (q, k_cache, v_cache, block_tables, query_start, context_lens, out, workspace), out)
+
+
+# ---------------------------------------------------------------------------
+# A tree of drafted tokens
+# ---------------------------------------------------------------------------
+
+def tree_workspace_bytes() -> int:
+    n = lib().pkv_tree_workspace_bytes()
+    if n == ctypes.c_size_t(-1).value:
+        raise PagedKVError("pkv_tree_workspace_bytes", 3)
+    return int(n)
+
+
+def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                         query_start: torch.Tensor, context_lens: torch.Tensor, tree_mask: torch.Tensor,
+                         scale: Optional[float] = None, out: Optional[torch.Tensor] = None, *, max_query_len: int,
+                         max_context_len: int, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of drafted tokens, the chunks of paged_attention_prefill: row j of a chunk sees the
+    tokens before the chunk, and chunk token c where bit c of its tree_mask words is set.
+
+    tree_mask: int64 [num_rows, words], bit c % 64 of word c // 64; 64 * words >= max_query_len.
+    A row that sees nothing gets zeros."""
+    return prepare_paged_attention_tree(q, k_cache, v_cache, block_tables, query_start, context_lens, tree_mask, scale,
+                                        out, max_query_len=max_query_len, max_context_len=max_context_len,
+                                        workspace=workspace)()
+
+
+def prepare_paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                 block_tables: torch.Tensor, query_start: torch.Tensor, context_lens: torch.Tensor,
+                                 tree_mask: torch.Tensor, scale: Optional[float] = None,
+                                 out: Optional[torch.Tensor] = None, *, max_query_len: int, max_context_len: int,
+                                 workspace: Optional[torch.Tensor] = None) -> PreparedCall:
+    """paged_attention_tree, checked and marshalled once (see PreparedCall); the call returns
+    ``out``.  Without ``workspace`` it holds one of its own."""
+    nb, hkv, bs, d, stride = _cache_geometry(k_cache, v_cache)
+    rows, hq, b, scale, out = _chunk_args(q, d, k_cache.dtype, block_tables, query_start, context_lens, scale, out,
+                                          max_query_len, max_context_len)
+    if tree_mask.dtype != torch.int64 or tree_mask.dim() != 2 or tree_mask.shape[0] != rows or not tree_mask.is_contiguous():
+        raise ValueError("tree_mask must be a contiguous int64 [num_rows, words]")
+    if 64 * int(tree_mask.shape[1]) < max_query_len:
+        raise ValueError("tree_mask must have a bit for every chunk token")
+    _one_device(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, query_start=query_start,
+                context_lens=context_lens, out=out, tree_mask=tree_mask)
+    with torch.cuda.device(q.device):
+        need = tree_workspace_bytes()
+    workspace = _own_workspace(q.device, need, workspace)
+    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, stride, block_tables.data_ptr(),
+            int(block_tables.shape[1]), query_start.data_ptr(), context_lens.data_ptr(), tree_mask.data_ptr(),
+            int(tree_mask.shape[1]), rows, int(max_query_len), int(max_context_len), b, hq, hkv, d, bs, scale,
+            out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _dtype_code(q))
+    return PreparedCall("pkv_paged_attention_tree", args, q.device,
+                        (q, k_cache, v_cache, block_tables, query_start, context_lens, tree_mask, out, workspace), out)
+
+
+def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor, query_start: torch.Tensor,
+                context_lens: torch.Tensor, accepted: torch.Tensor, accepted_lens: torch.Tensor,
+                new_context_lens: Optional[torch.Tensor] = None, *, max_query_len: int,
+                max_context_len: int) -> torch.Tensor:
+    """Move the K and V rows of each sequence's accepted path (chunk tokens, ascending: accepted
+    int32 [B, n], accepted_lens int32 [B]) to the front of its chunk, in place; returns the
+    context lengths afterwards (``new_context_lens``, which must not be ``context_lens``).
+    16-bit and INT8 caches; the blocks that get rows must belong to their sequence alone."""
+    return prepare_tree_commit(k_cache, v_cache, block_tables, query_start, context_lens, accepted, accepted_lens,
+                               new_context_lens, max_query_len=max_query_len, max_context_len=max_context_len)()
+
+
+def prepare_tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                        query_start: torch.Tensor, context_lens: torch.Tensor, accepted: torch.Tensor,
+                        accepted_lens: torch.Tensor, new_context_lens: Optional[torch.Tensor] = None, *,
+                        max_query_len: int, max_context_len: int) -> PreparedCall:
+    """tree_commit, checked and marshalled once (see PreparedCall); the call returns the new
+    context lengths."""
+    nb, hkv, bs, d, stride = _cache_geometry(k_cache, v_cache)
+    b = _chunk_tables(block_tables, query_start, context_lens, max_query_len, max_context_len)
+    if accepted.dtype != torch.int32 or accepted.dim() != 2 or accepted.shape[0] != b or not accepted.is_contiguous():
+        raise ValueError("accepted must be a contiguous int32 [num_seqs, n]")
+    if new_context_lens is None:
+        new_context_lens = torch.empty_like(context_lens)
+    for name, t in (("accepted_lens", accepted_lens), ("new_context_lens", new_context_lens)):
+        if t.dtype != torch.int32 or t.numel() != b or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 [num_seqs]")
+    if abs(new_context_lens.data_ptr() - context_lens.data_ptr()) < 4 * b:
+        raise ValueError("new_context_lens must not overlap context_lens")
+    _one_device(k_cache, v_cache=v_cache, block_tables=block_tables, query_start=query_start, context_lens=context_lens,
+                accepted=accepted, accepted_lens=accepted_lens, new_context_lens=new_context_lens)
+    args = (k_cache.data_ptr(), v_cache.data_ptr(), nb, stride, hkv, d, bs, block_tables.data_ptr(),
+            int(block_tables.shape[1]), query_start.data_ptr(), context_lens.data_ptr(), int(max_query_len),
+            int(max_context_len), b, accepted.data_ptr(), accepted_lens.data_ptr(), int(accepted.shape[1]),
+            new_context_lens.data_ptr(), _cache_dtype_code(k_cache))
+    return PreparedCall("pkv_tree_commit", args, k_cache.device,
+                        (k_cache, v_cache, block_tables, query_start, context_lens, accepted, accepted_lens,
+                         new_context_lens), new_context_lens)
+
+
+# ---------------------------------------------------------------------------
 # Eviction by accumulated attention weight
 # ---------------------------------------------------------------------------
 

@@ -84,3 +84,35 @@ def attend(q, k, v, scale, seen):
         if size.shape[1]:
             most[:, h, 0] = size.amax(1) * abs(scale)
     return out, mag, most
+
+
+def place(lens, bs, g, spare=2):
+    """Random tables for contexts of these lengths (entries past a context are bad ones), and the pool's blocks."""
+    need = [-(-n // bs) for n in lens]
+    perm, at = torch.randperm(sum(need) + spare, generator=g).to(torch.int32), 0
+    tables = torch.full((len(lens), max(need + [1]) + 1), -7, dtype=torch.int32)
+    for i, n in enumerate(need):
+        tables[i, :n] = perm[at:at + n]
+        at += n
+    return tables, len(perm)
+
+
+def poison(kv, tables, tokens):
+    """NaN and infinities into every row of the pool but the given tokens (a list per sequence)."""
+    bs = kv.shape[3]
+    covered = torch.zeros(kv.shape[0], bs, dtype=torch.bool)
+    for i, ts in enumerate(tokens):
+        for t in ts:
+            covered[tables[i, t // bs], t % bs] = True
+    bad = torch.tensor([float("nan"), float("inf"), -float("inf")], dtype=kv.dtype)
+    for k, (b, o) in enumerate((~covered).nonzero().tolist()):
+        kv[b, :, :, o] = bad[k % 3]
+
+
+def attention_bound(mag, most, d, p_half, int8_q=0.0):
+    """How far an output may be from exact before its last rounding: every product and partial sum of a score rounds once at
+    2^-23 (tensor cores truncate) of the summed magnitudes, scaling adds a few of its size; both sides of the softmax's
+    quotient carry that; each weight is rounded once to the MMA's type, as is the row sum (p_half each).  int8_q: the
+    relative error of an INT8 cache's fp16 query."""
+    slack = most * ((d + 8) * 2.0 ** -23 + 2.0 ** -20 + int8_q)
+    return mag * (2 * slack + 2 * p_half + 2.0 ** -18)
