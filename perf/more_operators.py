@@ -291,10 +291,13 @@ def _handle(s, make):
 
 def _own_int4(s):
     import paged_kv_cache_155_gb300 as pkv
-    k4, v4 = s["pool"][:, 0], s["pool"][:, 1]
-    write, read = _handle(s, lambda: (
-        pkv.prepare_reshape_and_cache_int4(s["k"], s["v"], s["slots"], k4, v4),
-        pkv.prepare_dequantise_blocks_int4(k4, v4, s["pairs"], s["kv"][:, 0], s["kv"][:, 1])))
+
+    def make():  # the halves are cut once, when the calls are prepared
+        k4, v4 = s["pool"][:, 0], s["pool"][:, 1]
+        return (pkv.prepare_reshape_and_cache_int4(s["k"], s["v"], s["slots"], k4, v4),
+                pkv.prepare_dequantise_blocks_int4(k4, v4, s["pairs"], s["kv"][:, 0], s["kv"][:, 1]))
+
+    write, read = _handle(s, make)
     write()
     read()
     return dict(kv=s["kv"])
@@ -310,13 +313,16 @@ def _own_decode4(s):
 
 def _own_tree(s):
     import paged_kv_cache_155_gb300 as pkv
-    k, v = s["kv"][:, 0], s["kv"][:, 1]
-    write, attend, commit = _handle(s, lambda: (
-        pkv.prepare_reshape_and_cache(s["k"], s["v"], s["slots"], k, v),
-        pkv.prepare_paged_attention_tree(s["q"], k, v, s["tables"], s["query_start"], s["lens"], s["mask"], s["scale"],
-                                         s["out"], max_query_len=s["max_chunk"], max_context_len=s["max_len"]),
-        pkv.prepare_tree_commit(k, v, s["tables"], s["query_start"], s["lens"], s["path"], s["path_lens"], s["new_lens"],
-                                max_query_len=s["max_chunk"], max_context_len=s["max_len"])))
+
+    def make():
+        k, v = s["kv"][:, 0], s["kv"][:, 1]
+        rest = (s["tables"], s["query_start"], s["lens"])
+        bound = dict(max_query_len=s["max_chunk"], max_context_len=s["max_len"])
+        return (pkv.prepare_reshape_and_cache(s["k"], s["v"], s["slots"], k, v),
+                pkv.prepare_paged_attention_tree(s["q"], k, v, *rest, s["mask"], s["scale"], s["out"], **bound),
+                pkv.prepare_tree_commit(k, v, *rest, s["path"], s["path_lens"], s["new_lens"], **bound))
+
+    write, attend, commit = _handle(s, make)
     write()
     out = attend()
     commit()
