@@ -305,25 +305,27 @@ PKV_API pkv_status pkv_dequantise_blocks_int4(const void *k_cache4, const void *
                                               int head_dim, int block_size, pkv_dtype dtype,
                                               void *stream);
 
-/* Workspace of pkv_paged_attention_decode_int4 (same contract as
- * pkv_decode_workspace_bytes). */
+/* Workspace of pkv_paged_attention_decode_int4 on the current device: it depends on its
+ * SMs, the head counts and head_dim ((size_t)-1 for arguments out of contract). */
 PKV_API size_t pkv_decode_int4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
-                                               int head_dim, int block_size, int max_context_len,
-                                               int partition_size);
+                                               int head_dim, int block_size, int max_context_len);
 
 /*
  * pkv_paged_attention_decode_int4 -- pkv_paged_attention_decode over a 4-bit cache.
- * partition_size is 0 or a multiple of 32.  Tokens past a context, in its last block,
- * may hold anything.  A query is held to 2^-24 of its largest channel, and V's groups
- * should have scales of at least 2^-50.  Other arguments and errors as
- * pkv_paged_attention_decode.
+ * The contexts' work is cut evenly on the device, whatever their lengths, so there is
+ * no partition size; workspace >= pkv_decode_int4_workspace_bytes(...) is always
+ * needed, and calls that may overlap need one each.  Tokens past a context, in its last
+ * block, may hold anything.  A query is held to 2^-24 of its largest channel, and V's
+ * groups should have scales of at least 2^-50.  Other arguments and errors as
+ * pkv_paged_attention_decode; the result depends on the batch's lengths within the
+ * roundings (they decide where a context is cut), not on the blocks' places.
  */
 PKV_API pkv_status pkv_paged_attention_decode_int4(
     const void *q, const void *k_cache, const void *v_cache, int64_t num_blocks,
     int64_t block_stride_bytes, const int32_t *block_tables, int max_blocks_per_seq,
     const int32_t *context_lens, int max_context_len, int num_seqs, int num_q_heads,
     int num_kv_heads, int head_dim, int block_size, float scale, void *out, void *workspace,
-    size_t workspace_bytes, int partition_size, pkv_dtype dtype, void *stream);
+    size_t workspace_bytes, pkv_dtype dtype, void *stream);
 
 /*
  * pkv_shared_prefix_workspace_bytes -- workspace of

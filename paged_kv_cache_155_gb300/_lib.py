@@ -77,9 +77,9 @@ SIGNATURES = {
                                 I32, P]),
     "pkv_reshape_and_cache_int4": (I32, [P, P, P, I64, P, P, I64, I64, I32, I32, I32, I32, P]),
     "pkv_dequantise_blocks_int4": (I32, [P, P, I64, I64, P, I64, P, P, I64, I64, I32, I32, I32, I32, P]),
-    "pkv_decode_int4_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32, I32]),
+    "pkv_decode_int4_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32]),
     "pkv_paged_attention_decode_int4": (I32, [P, P, P, I64, I64, P, I32, P, I32, I32, I32, I32, I32,
-                                              I32, ctypes.c_float, P, P, SZ, I32, I32, P]),
+                                              I32, ctypes.c_float, P, P, SZ, I32, P]),
     "pkv_decode_sinks_workspace_bytes": (SZ, [I32] * 10),
     "pkv_paged_attention_decode_sinks": (I32, [P, P, P, I64, I64, P, I32, P, I32, I32, I32, I32, I32,
                                                I32, ctypes.c_float, I32, I32, P, P, SZ, I32, I32, P]),

@@ -1,5 +1,5 @@
-// decode_int4.cu -- the pkv_paged_attention_decode_int4 entry point: argument checks, the
-// split-context plan, workspace layout, and the launch.
+// decode_int4.cu -- the pkv_paged_attention_decode_int4 entry point: argument checks, the plan,
+// workspace layout, and the launch.
 #include <algorithm>
 #include <cmath>
 
@@ -7,65 +7,38 @@
 
 namespace {
 
-constexpr int kMinPartition = 256;  // tokens
-// What starting and ending a CTA costs, in tokens of its main loop.
-constexpr int kCtaTokens = 128;
-constexpr int kMaxWaves = 8;        // waves of resident CTAs that a split may make
+constexpr int kWorkersPerCta = 4;
 
 struct Int4Plan {
-    int partition = 0, partitions = 1, tiles = 1, blocks = 1;  // tiles of 8 heads per block, blocks per KV head
+    int tiles = 1;     // column tiles of eight heads per block
+    int blocks = 1;    // blocks of heads per KV head
+    int resident = 3;  // CTAs per SM (DecodeInt4Geom::kResident)
 };
 
 pkv_status plan_int4(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size, int max_context_len,
-                     int partition_size, int sm_count, Int4Plan *plan) {
+                     Int4Plan *plan) {
     if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
     if (block_size != 8 && block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
-    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || max_context_len < 0 ||
-        partition_size < 0 || sm_count <= 0 || partition_size % 32)
+    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || max_context_len < 0)
         return PKV_ERR_INVALID_ARG;
-    constexpr int kEntries = pkv::DecodeInt4Geom<128, 16, 1>::kMaxTableEntries;
-    const int most = kEntries * block_size;
-    if (partition_size > most) return PKV_ERR_INVALID_ARG;
     // the fewest blocks of at most 16 heads that cover the group, of 8 heads where these do
     const int group = num_q_heads / num_kv_heads;
     plan->blocks = (group + 15) / 16;
     plan->tiles = (group + plan->blocks - 1) / plan->blocks <= 8 ? 1 : 2;
     plan->blocks = (group + 8 * plan->tiles - 1) / (8 * plan->tiles);
-    const int64_t grid_y = static_cast<int64_t>(num_kv_heads) * plan->blocks;
-    if (grid_y > 65535 || num_seqs > 65535) return PKV_ERR_INVALID_ARG;
-    const int64_t len = std::max(1, max_context_len);
-    auto part_for = [&](int64_t n) { return ((len + n - 1) / n + 31) / 32 * 32; };
-    int64_t part = partition_size;
-    if (part == 0) {
-        // The split whose rounds of resident CTAs take the least time for sequences of the
-        // longest length: rounds x (a partition's tokens + a CTA's fixed cost).
-        const int64_t units = std::max<int64_t>(1, num_seqs * grid_y);
-        const int64_t slots = static_cast<int64_t>(sm_count) * (plan->tiles == 1 ? 3 : 2);
-        const int64_t fewest = (len + most - 1) / most;
-        const int64_t most_parts = std::max(fewest, std::min((len + kMinPartition - 1) / kMinPartition,
-                                                             (kMaxWaves * slots + units - 1) / units));
-        // (for w rounds, the most partitions that still take w)
-        int64_t best = -1;
-        for (int w = 0; w <= kMaxWaves + 1; ++w) {
-            const int64_t n = w == 0 ? fewest : w > kMaxWaves ? most_parts : std::max(fewest, std::min(most_parts, w * slots / units));
-            const int64_t p = part_for(n), parts = (len + p - 1) / p;
-            if (p > most) continue;
-            const int64_t cost = (units * parts + slots - 1) / slots * (p + kCtaTokens);
-            if (best < 0 || cost < best) {
-                best = cost;
-                part = p;
-            }
-        }
-        if (part == 0) part = most;
-    }
-    plan->partition = static_cast<int>(part);
-    plan->partitions = static_cast<int>((len + part - 1) / part);
+    plan->resident = plan->tiles == 1 ? (head_dim == 64 ? 4 : 3) : (head_dim == 64 ? 3 : 2);
+    // all units' chunks fit the kernel's 32-bit count
+    const int64_t units = static_cast<int64_t>(num_kv_heads) * plan->blocks;
+    const int64_t chunks = std::max<int64_t>(1, (max_context_len + 31LL) / 32);
+    if (units > 0x3fffffff || units * chunks > 0x3fffffff || units * chunks * std::max(num_seqs, 1) > 0x3fffffff)
+        return PKV_ERR_INVALID_ARG;
     return PKV_OK;
 }
 
-size_t workspace_of(int num_seqs, int num_q_heads, int head_dim, int partitions) {
-    if (partitions <= 1) return 0;
-    return static_cast<size_t>(num_seqs) * num_q_heads * partitions * (static_cast<size_t>(head_dim) + 2) * sizeof(float);
+// Workspace: the partials of two pieces per worker, then what the merge has to know per worker.
+size_t workspace_of(const Int4Plan &plan, int head_dim, int sm_count) {
+    const size_t workers = static_cast<size_t>(sm_count) * plan.resident * kWorkersPerCta;
+    return workers * (2 * 8 * plan.tiles * (static_cast<size_t>(head_dim) + 2) * sizeof(float) + sizeof(pkv::Int4Split));
 }
 
 }  // namespace
@@ -73,13 +46,12 @@ size_t workspace_of(int num_seqs, int num_q_heads, int head_dim, int partitions)
 extern "C" {
 
 PKV_API size_t pkv_decode_int4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
-                                               int block_size, int max_context_len, int partition_size) {
-    const int sm = partition_size > 0 ? 1 : pkv::current_sm_count();
-    if (sm <= 0) return static_cast<size_t>(-1);
+                                               int block_size, int max_context_len) {
     Int4Plan plan;
-    if (plan_int4(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len, partition_size, sm, &plan) != PKV_OK)
+    if (plan_int4(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len, &plan) != PKV_OK)
         return static_cast<size_t>(-1);
-    return workspace_of(num_seqs, num_q_heads, head_dim, plan.partitions);
+    const int sm = pkv::current_sm_count();
+    return sm > 0 ? workspace_of(plan, head_dim, sm) : static_cast<size_t>(-1);
 }
 
 PKV_API pkv_status pkv_paged_attention_decode_int4(const void *q, const void *k_cache, const void *v_cache,
@@ -88,11 +60,10 @@ PKV_API pkv_status pkv_paged_attention_decode_int4(const void *q, const void *k_
                                                    const int32_t *context_lens, int max_context_len, int num_seqs,
                                                    int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                                                    float scale, void *out, void *workspace, size_t workspace_bytes,
-                                                   int partition_size, pkv_dtype dtype, void *stream) {
+                                                   pkv_dtype dtype, void *stream) {
     if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
     Int4Plan plan;
-    // shape first (no CUDA call), then the plan for the real SM count
-    pkv_status st = plan_int4(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len, partition_size, 1, &plan);
+    const pkv_status st = plan_int4(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len, &plan);
     if (st != PKV_OK) return st;
     if (num_blocks <= 0 || num_blocks > 0x7fffffffLL || max_blocks_per_seq <= 0 ||
         static_cast<int64_t>(max_context_len) > static_cast<int64_t>(max_blocks_per_seq) * block_size || !std::isfinite(scale))
@@ -101,30 +72,26 @@ PKV_API pkv_status pkv_paged_attention_decode_int4(const void *q, const void *k_
     if (block_stride_bytes < half || block_stride_bytes % 16) return PKV_ERR_INVALID_ARG;
     if (!k_cache || !v_cache || !pkv::aligned16(k_cache) || !pkv::aligned16(v_cache)) return PKV_ERR_INVALID_ARG;
     if (num_seqs == 0) return PKV_OK;
-    if (!q || !out || !block_tables || !context_lens || !pkv::aligned16(q) || !pkv::aligned16(out) ||
+    if (!q || !out || !block_tables || !context_lens || !workspace || !pkv::aligned16(q) || !pkv::aligned16(out) ||
+        !pkv::aligned16(workspace) ||
         ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens)) & 3u))
         return PKV_ERR_INVALID_ARG;
-    if (partition_size == 0) {
-        const int sm = pkv::current_sm_count();
-        if (sm <= 0) return PKV_ERR_CUDA;
-        st = plan_int4(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len, 0, sm, &plan);
-        if (st != PKV_OK) return st;
-    }
-    const size_t need = workspace_of(num_seqs, num_q_heads, head_dim, plan.partitions);
-    if (need > 0 && (!workspace || workspace_bytes < need || !pkv::aligned16(workspace))) return PKV_ERR_INVALID_ARG;
-    if (plan.partitions > 1 && static_cast<int64_t>(num_seqs) * num_q_heads > 0x7fffffff) return PKV_ERR_INVALID_ARG;
+    const int sm = pkv::current_sm_count();
+    if (sm <= 0) return PKV_ERR_CUDA;
+    if (workspace_bytes < workspace_of(plan, head_dim, sm)) return PKV_ERR_INVALID_ARG;
     unsigned int *status = pkv::status_word_ptr();
     if (!status) return PKV_ERR_CUDA;
 
-    pkv::DecodeParams p{};
+    pkv::Int4Params p{};
     p.q = q;
     p.k_cache = k_cache;
     p.v_cache = v_cache;
     p.out = out;
-    const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads * plan.partitions;
-    p.ws_o = need ? static_cast<float *>(workspace) : nullptr;
-    p.ws_m = need ? p.ws_o + rows * head_dim : nullptr;
-    p.ws_l = need ? p.ws_m + rows : nullptr;
+    const size_t rows = static_cast<size_t>(sm) * plan.resident * kWorkersPerCta * 2 * 8 * plan.tiles;
+    p.seg_o = static_cast<float *>(workspace);
+    p.seg_m = p.seg_o + rows * head_dim;
+    p.seg_l = p.seg_m + rows;
+    p.splits = reinterpret_cast<pkv::Int4Split *>(p.seg_l + rows);
     p.block_tables = block_tables;
     p.context_lens = context_lens;
     p.status = status;
@@ -135,17 +102,17 @@ PKV_API pkv_status pkv_paged_attention_decode_int4(const void *q, const void *k_
     p.num_seqs = num_seqs;
     p.num_q_heads = num_q_heads;
     p.group = num_q_heads / num_kv_heads;
-    p.subgroups = plan.blocks;
-    p.items_y = num_kv_heads * plan.blocks;
-    p.partition_size = plan.partition;
-    p.num_partitions = plan.partitions;
+    p.blocks = plan.blocks;
+    p.units = num_kv_heads * plan.blocks;
     p.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
-    const int merge_rows = plan.partitions > 1 ? num_seqs * num_q_heads : 0;
-    p.trigger_dependents = merge_rows > 0;
-    const dim3 grid(static_cast<unsigned>(plan.partitions), static_cast<unsigned>(p.items_y), static_cast<unsigned>(num_seqs));
+    // every SM's resident CTAs, or fewer where the contexts' bound leaves no more shares
+    const int64_t chunks = std::max<int64_t>(1, (max_context_len + 31LL) / 32) * p.units * num_seqs;
+    const int64_t most = (chunks + pkv::kInt4MinShare * kWorkersPerCta - 1) / (pkv::kInt4MinShare * kWorkersPerCta);
+    const int grid = static_cast<int>(std::min<int64_t>(most, static_cast<int64_t>(sm) * plan.resident));
+    p.by_unit = static_cast<int64_t>(num_seqs) * p.units <= static_cast<int64_t>(grid) * kWorkersPerCta;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return dtype == PKV_F16 ? pkv::launch_int4_f16(p, head_dim, block_size, plan.tiles, grid, merge_rows, s)
-                            : pkv::launch_int4_bf16(p, head_dim, block_size, plan.tiles, grid, merge_rows, s);
+    return dtype == PKV_F16 ? pkv::launch_int4_f16(p, head_dim, block_size, plan.tiles, grid, s)
+                            : pkv::launch_int4_bf16(p, head_dim, block_size, plan.tiles, grid, s);
 }
 
 }  // extern "C"

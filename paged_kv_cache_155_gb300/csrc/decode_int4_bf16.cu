@@ -2,8 +2,7 @@
 #include "decode_int4_launch.cuh"
 
 namespace pkv {
-pkv_status launch_int4_bf16(const DecodeParams &p, int head_dim, int block_size, int tiles, dim3 grid, int merge_rows,
-                           cudaStream_t s) {
-    return launch_int4_typed<__nv_bfloat16>(p, head_dim, block_size, tiles, grid, merge_rows, s);
+pkv_status launch_int4_bf16(const Int4Params &p, int head_dim, int block_size, int tiles, int grid, cudaStream_t s) {
+    return launch_int4_typed<__nv_bfloat16>(p, head_dim, block_size, tiles, grid, s);
 }
 }  // namespace pkv

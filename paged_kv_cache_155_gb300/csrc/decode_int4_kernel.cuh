@@ -1,5 +1,4 @@
-// decode_int4_kernel.cuh -- paged decode attention over the 4-bit cache (format: int4.cuh),
-// one CTA per (partition of the context, KV head [x block of query heads], sequence).
+// decode_int4_kernel.cuh -- paged decode attention over the 4-bit cache (format: int4.cuh).
 //
 // What it computes: the decode's softmax attention (decode_kernel.cuh) with the values that the
 // codes stand for, K_t = sK c + zK and V_t = sV c + zV per group j of 32 channels:
@@ -7,28 +6,35 @@
 //     o   = sum_t p_t ( sV[t,j] c[t,j] + zV[t,j] ),       p_t = exp(s_t - ref).
 // The codes meet the query and the weights as exact small integers, and a token's scales
 // enter once per group: q_j . c is one group's MMA accumulator, the V scale multiplies the
-// weight (p_t sV[t,j], rounded once to fp16), and the zeros are plain fp32 sums.
+// weight (p_t sV[t,j], rounded once to fp16); the zeros are one more MMA for K (against sum(q_j),
+// split in two or three 16-bit numbers) and plain fp32 sums for V.
 //
 // What bounds it: 5/8 byte a value, a quarter of what a 16-bit cache reads, against the same
-// number of codes to widen; so per code the kernel spends 0.9 integer operations and half an
+// number of codes to widen; so per code the kernel spends 0.75 integer operations and half an
 // MMA slot, and little else.
 //  * Both products run as warp-level MMAs (m16n8k16, fp16 operands, fp32 accumulators) with the
 //    tokens (S^T = K Q^T) or the channels (O^T = V^T P^T) as the 16 rows and eight query heads as the
 //    columns, for any group of heads: unused columns are zero.  Groups of more than eight heads take
 //    two column tiles on the same K and V fragments, so their codes are widened once.
-//  * Widening: four codes of a 16-bit word become fp16 numbers without a conversion: shifted so
-//    that a nibble falls on mantissa bits 2 .. 5 or 6 .. 9 of 1024.0, it reads 1024 + 4 c or
-//    1024 + 64 c (codes_f16).  (At bits 0 .. 3, without a shift, the offset would be 68 times the
-//    largest code and cost the sums that many roundings; here it is 17 times at most.)  K's factor 1/4
-//    or 1/64 is in the query, V's is applied to the output channel, whose accumulator holds one nibble
-//    position only.  K's offset is the accumulator's start, -1024 sum(q); V's is 1024 times the sum of
-//    the weights as they were rounded, which one more MMA against ones makes.
+//  * Widening costs a mask: a nibble at bits 0 .. 3 or 4 .. 7 of a 16-bit word is a subnormal fp16
+//    number, exactly c 2^-24 or c 2^-20, and MMAs take those as they are (codes_f16).  K's factor 16
+//    between the two is in the query, V's is applied to the output channel, whose accumulator holds
+//    one nibble position only.  (With the exponent of 1024.0 set above the nibbles, as an offset to be
+//    taken away again, and 16 tokens a step, 64 x 4096 tokens of 32 / 8 heads took 106 us; so 83.)
 //  * The weights' reference is the running maximum of s_t + log2(max_j sV[t,j]), not of s_t, so that
 //    p_t sV[t,j], what fp16 has to hold, is at most 2^6 and near 1 where it counts, whatever V's scale is.
-//  * Each warp streams its own ring of 32-token stages by bulk copies (a block's record of one head is
-//    contiguous: codes and scales arrive together) and shares nothing with the other warps until the end.
+//  * Every warp is a worker of its own: the 32-token chunks of all (sequence, KV head) units stand in one
+//    row and are cut into equal shares, so that any mix of lengths keeps all warps busy to the end and
+//    none waits for another (CTAs as workers, whose warps join their sums, measured the same on long contexts
+//    and 1.5 us slower on a few).  A worker holds at most two pieces of cut units (its first and last);
+//    their partials are merged by paged_decode_int4_merge_kernel, whole units are written at once.
+//  * A worker streams its share through its own ring of stages by bulk copies (a block's record of one head
+//    is contiguous: codes and scales arrive together), one copy per lane, the table entries read a chunk
+//    ahead; the ring runs on from one unit to the next.  A stage is one softmax step.
 //  * The token of an MMA row is chosen so that V's four token rows of a load lie side by side
 //    (token_of_row): two-way instead of four-way shared-memory conflicts.
+// Measured: 64 x 4096 tokens of 32 / 8 heads of 128, fp16: 76 us (0.65 of measured HBM; 0.77 per further
+// token, 11 us fixed); without the arithmetic 55 us, without the copies 68.
 #pragma once
 
 #include "decode_kernel.cuh"
@@ -45,28 +51,59 @@ struct DecodeInt4Geom {
     static constexpr int kRecord = int4_record_bytes(D, BS);       // a block's K (or V) rows of one head
     static constexpr int kHalfBytes = kBlocks * kRecord;           // 2560 at head_dim 128
     static constexpr int kStageBytes = 2 * kHalfBytes;
-    static constexpr int kResident = NT == 1 ? 3 : 2;              // CTAs per SM, by registers
+    static constexpr int kResident = NT == 1 ? (D == 64 ? 4 : 3) : (D == 64 ? 3 : 2);  // CTAs per SM, by registers
     // about 180 KB of stages per SM: several times the bytes that cover the memory latency
-    static constexpr int kStages = (NT == 1 ? 15360 : 20480) / kStageBytes;
-    static constexpr int kMaxTableEntries = 1024;
+    static constexpr int kStages = 46080 / kResident / kStageBytes;
     static constexpr int kHeads = 8 * NT;
-    static constexpr int kSmemBytes = kWarps * kStages * (kStageBytes + 8) + kMaxTableEntries * 4;
-    static_assert(kHeads * (D + 4) * 4 <= kStages * kStageBytes, "merge scratch must fit a warp's stages");
+    static constexpr int kSmemBytes = kWarps * kStages * (kStageBytes + 8 + 4);
 };
+
+// A cut unit.  The table of them is indexed by unit (seq * units + unit) when there are no more units
+// than workers, else by the worker in whose share it begins (at most one goes on past a share).
+struct Int4Split {
+    int pieces;  // workers that hold pieces of it; 0: not cut, or none begins in this share
+    int worker;  // the first of them, whose piece is in its slot `slot` (the others' in slot 0)
+    int slot;
+    int seq, unit;
+};
+struct Int4Params {
+    const void *q;                // [num_seqs][num_q_heads][D]
+    const void *k_cache, *v_cache;
+    void *out;
+    float *seg_o, *seg_m, *seg_l; // partials [2 worker + slot][heads of a block][D], [..][heads]
+    Int4Split *splits;            // [min(workers, num_seqs * units)]
+    int by_unit;                  // its index
+    const int32_t *block_tables, *context_lens;
+    unsigned int *status;
+    int64_t num_blocks, block_stride;  // bytes
+    int max_blocks_per_seq, len_cap, num_seqs, num_q_heads, group;
+    int blocks;                   // blocks of heads per KV head
+    int units;                    // units of a sequence: num_kv_heads * blocks
+    float scale_log2;
+};
+constexpr int kInt4MinShare = 2;  // chunks of a share, at least
 
 // The token (0 .. 7) of MMA row r: rows 2 t, which one lane load of V takes for t = 0 .. 3, are
 // tokens 0 .. 3, and rows 2 t + 1 tokens 5, 4, 7, 6.
 __host__ __device__ constexpr int token_of_row(int r) { return r & 1 ? 4 + ((r >> 1) ^ 1) : r >> 1; }
 
-// Four codes in each half of a word -> fp16 pairs: r[0], r[2] = 1024 + 4 c, r[1], r[3] = 1024 + 64 c.
+// Four codes in each half of a word -> fp16 pairs: r[0], r[2] = c 2^-24, r[1], r[3] = c 2^-20.
 __device__ __forceinline__ void codes_f16(uint32_t x, uint32_t (&r)[4]) {
-    const uint32_t a = x << 2, b = x >> 6;
-    r[0] = (a & 0x003c003cu) | 0x64006400u;
-    r[1] = (a & 0x03c003c0u) | 0x64006400u;
-    r[2] = (b & 0x003c003cu) | 0x64006400u;
-    r[3] = (b & 0x03c003c0u) | 0x64006400u;
+    const uint32_t y = x >> 8;
+    r[0] = x & 0x000f000fu;
+    r[1] = x & 0x00f000f0u;
+    r[2] = y & 0x000f000fu;
+    r[3] = y & 0x00f000f0u;
 }
-constexpr float kInt4Offset = 1024.f;
+
+// ... for V, whose output channels have accumulators of their own: r[2] is the whole byte, c + 16 c' with the
+// next code c', whose channel's accumulator takes its share away at the end (one operation less).
+__device__ __forceinline__ void codes_f16_bytes(uint32_t x, uint32_t (&r)[4]) {
+    r[0] = x & 0x000f000fu;
+    r[1] = x & 0x00f000f0u;
+    r[2] = __byte_perm(x, 0u, 0x4341);
+    r[3] = r[2] & 0x00f000f0u;
+}
 
 // The words of two units (of one token, or of one unit in two tokens) -> per group j the four
 // codes of the first in the low half and of the second in the high half.
@@ -81,280 +118,356 @@ __device__ __forceinline__ float fast_log2(float x) {
     return y;
 }
 
+// The larger scale (low half) of two (scale, zero) words, in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t max_scale(uint32_t a, uint32_t b) {
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 m = __hmax2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&m);
+    } else {
+        const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&m);
+    }
+}
+
+// A sequence's length as the kernels take it, and its chunks (at least one, possibly empty: an
+// empty context's zeros are written too).
+__device__ __forceinline__ int int4_len(const Int4Params &p, int seq) {
+    return min(max(p.context_lens[seq], 0), p.len_cap);
+}
+__device__ __forceinline__ int int4_chunks(int len) { return max(1, (len + 31) / 32); }
+
+// The chunks of every worker's share, and of all units together (total); by one warp.
+__device__ __forceinline__ int int4_share(const Int4Params &p, int workers, int &total) {
+    const int lane = threadIdx.x & 31;
+    total = 0;
+    for (int seq = lane; seq < p.num_seqs; seq += 32) total += int4_chunks(int4_len(p, seq));
+    total = __reduce_add_sync(0xffffffffu, total) * p.units;
+    return max(kInt4MinShare, (total + workers - 1) / workers);
+}
+
 template <typename T, int D, int BS, int NT>
-__global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) paged_decode_int4_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) paged_decode_int4_kernel(const Int4Params p) {
     using G = DecodeInt4Geom<D, BS, NT>;
-    constexpr int NW = G::kWarps, S = G::kStages, NG = G::kGroups, ST = G::kStageTokens, SB = G::kBlocks;
+    constexpr int NW = G::kWarps, S = G::kStages, NG = G::kGroups, SB = G::kBlocks, HEADS = G::kHeads;
     constexpr int ROW = int4_row_bytes(D), PAR = int4_param_bytes(D);
-    if (p.trigger_dependents) pdl_trigger();
+    constexpr bool kBF16 = !std::is_same<T, __half>::value;
+    pdl_trigger();  // the merge behind this grid may be placed
 
     extern __shared__ __align__(128) unsigned char smem[];
-    unsigned char *stages = smem;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + NW * S * G::kStageBytes);
-    int32_t *tbl = reinterpret_cast<int32_t *>(smem + NW * S * (G::kStageBytes + 8));
-
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int part = blockIdx.x, seq = blockIdx.z;
-    const int kvh = blockIdx.y / p.subgroups, sub = blockIdx.y - kvh * p.subgroups;
-    const int hq0 = kvh * p.group + sub * G::kHeads;
-    const int nheads = min(G::kHeads, p.group - sub * G::kHeads);
-
-    // ---- the partition's table entries, fetched together with the context length
-    const int tok0 = part * p.partition_size;
-    const int32_t *trow = p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq + tok0 / BS;
-    int first_entry = 0;
-    if (static_cast<int>(threadIdx.x) < min(p.max_blocks_per_seq - tok0 / BS, p.partition_size / BS))
-        first_entry = trow[threadIdx.x];
-    int len = p.context_lens[seq];
-    if (len < 0 || len > p.len_cap) {
-        if (threadIdx.x == 0 && part == 0 && blockIdx.y == 0) raise_flag(p.status, PKV_DEVERR_CONTEXT_LEN);
-        len = len < 0 ? 0 : p.len_cap;
-    }
-    const int nparts = partitions_of(p, len);
-    if (part >= nparts) return;  // uniform over the CTA
-    const int ntok = max(0, min(len, tok0 + p.partition_size) - tok0);
-    const int nchunks = (ntok + ST - 1) / ST;
-    const int nblk = (ntok + BS - 1) / BS;
-    for (int i = threadIdx.x; i < nblk; i += blockDim.x) {
-        int b = i < static_cast<int>(blockDim.x) ? first_entry : trow[i];
-        if (b < 0 || b >= p.num_blocks) {
-            raise_flag(p.status, PKV_DEVERR_BLOCK_TABLE);
-            b = -1;
-        }
-        tbl[i] = b;
-    }
-    unsigned char *my_stages = stages + warp * S * G::kStageBytes;
-    uint64_t *my_bars = bars + warp * S;
+    const int mg = lane >> 2, mt = lane & 3;
+    unsigned char *my_stages = smem + warp * S * G::kStageBytes;
+    uint64_t *my_bars = reinterpret_cast<uint64_t *>(smem + NW * S * G::kStageBytes) + warp * S;
+    uint32_t *my_good = reinterpret_cast<uint32_t *>(smem + NW * S * (G::kStageBytes + 8)) + warp * S;  // blocks of a stage that were copied
     if (lane == 0) {
         for (int s = 0; s < S; ++s) mbar_init(&my_bars[s], 1);
         fence_mbar_init();
     }
-    __syncthreads();
+    __syncwarp();
 
-    // chunk c (32 tokens) -> stage s of this warp; flagged blocks are not copied
-    const uint64_t policy = l2_policy_evict_first();
-    const char *kc = static_cast<const char *>(p.k_cache) + static_cast<int64_t>(kvh) * G::kRecord;
-    const char *vc = static_cast<const char *>(p.v_cache) + static_cast<int64_t>(kvh) * G::kRecord;
-    auto issue = [&](int c, int s) {
-        const int b0 = c * SB, nb = min(SB, nblk - b0);
-        uint32_t bytes = 0;
+    // ---- this worker's share: chunks [first, first + left) of the row
+    const int worker = blockIdx.x * NW + warp;
+    int total;
+    const int share = int4_share(p, gridDim.x * NW, total);
+    const int64_t first = static_cast<int64_t>(worker) * share;
+    int left = first < total ? min(share, total - static_cast<int>(first)) : 0;
+    if (left == 0) {
+        if (lane == 0 && !p.by_unit) p.splits[worker].pieces = 0;
+        return;
+    }
+    int seq = 0, unit = 0, chunk = 0;  // where the share begins
+    for (int s0 = 0, before = 0;; s0 += 32) {
+        const int mine = s0 + lane < p.num_seqs ? int4_chunks(int4_len(p, s0 + lane)) : 0;
+        int incl = mine;
 #pragma unroll
-        for (int i = 0; i < SB; ++i)
-            if (i < nb && tbl[b0 + i] >= 0) bytes += 2 * G::kRecord;
-        if (bytes == 0) {
-            mbar_arrive(&my_bars[s]);
-            return;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
         }
-        mbar_arrive_expect_tx(&my_bars[s], bytes);
-        unsigned char *dst = my_stages + s * G::kStageBytes;
-#pragma unroll
-        for (int i = 0; i < SB; ++i) {
-            if (i >= nb || tbl[b0 + i] < 0) continue;
-            const int64_t at = static_cast<int64_t>(tbl[b0 + i]) * p.block_stride;
-            bulk_copy_g2s(dst + i * G::kRecord, kc + at, G::kRecord, &my_bars[s], policy);
-            bulk_copy_g2s(dst + G::kHalfBytes + i * G::kRecord, vc + at, G::kRecord, &my_bars[s], policy);
+        const unsigned past = __ballot_sync(0xffffffffu, static_cast<int64_t>(before + incl) * p.units > first);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            const int n = __shfl_sync(0xffffffffu, mine, l);
+            const int pos = static_cast<int>(first - static_cast<int64_t>(before + __shfl_sync(0xffffffffu, incl - mine, l)) * p.units);
+            seq = s0 + l;
+            unit = pos / n;
+            chunk = pos - unit * n;
+            break;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+
+    // ---- the copies' walk, up to S chunks ahead: lanes 2 i and 2 i + 1 copy block i's K and V records of
+    //      a chunk.  A lane's table entry of the next chunk is read while the one before it is copied.
+    const uint64_t policy = l2_policy_evict_first();
+    const char *const cache0 = static_cast<const char *>(lane & 1 ? p.v_cache : p.k_cache);
+    const char *cache = cache0 + static_cast<int64_t>(unit / p.blocks) * G::kRecord;  // of the unit's KV head
+    int i_seq = seq, i_unit = unit, i_chunk = chunk, i_left = left, i_len = int4_len(p, seq), i_entry = -1;
+    auto fetch = [&]() {
+        i_entry = -1;
+        const int at = i_chunk * SB + (lane >> 1);
+        if (i_left > 0 && lane < 2 * SB && at * BS < i_len) {
+            i_entry = p.block_tables[static_cast<int64_t>(i_seq) * p.max_blocks_per_seq + at];
+            if (i_entry < 0 || i_entry >= p.num_blocks) {
+                raise_flag(p.status, PKV_DEVERR_BLOCK_TABLE);
+                i_entry = -1;
+            }
         }
     };
-    const int my_chunks = nchunks > warp ? (nchunks - warp + NW - 1) / NW : 0;
-    if (lane == 0) {
-        for (int i = 0; i < S && i < my_chunks; ++i) issue(warp + i * NW, i);
-    }
+    auto issue = [&](int s) {
+        const uint32_t good = __ballot_sync(0xffffffffu, i_entry >= 0);
+        if (lane == 0) {
+            my_good[s] = good;
+            if (good) mbar_arrive_expect_tx(&my_bars[s], __popc(good) * G::kRecord);
+            else mbar_arrive(&my_bars[s]);
+        }
+        __syncwarp();
+        if (i_entry >= 0)
+            bulk_copy_g2s(my_stages + s * G::kStageBytes + (lane & 1) * G::kHalfBytes + (lane >> 1) * G::kRecord,
+                          cache + i_entry * p.block_stride, G::kRecord, &my_bars[s], policy);
+        --i_left;
+        if (++i_chunk == int4_chunks(i_len)) {
+            i_chunk = 0;
+            if (++i_unit == p.units) {
+                i_unit = 0;
+                ++i_seq;
+                if (i_left > 0) i_len = int4_len(p, i_seq);
+            }
+            cache = cache0 + static_cast<int64_t>(i_unit / p.blocks) * G::kRecord;
+        }
+        fetch();
+    };
+    fetch();
+    for (int s = 0; s < S && i_left > 0; ++s) issue(s);
 
-    // ---- the query: lane (mg, mt) holds column (head) mg of every column tile at channels
-    //      32 j + 8 mt + 0 .. 7, the channels of a K row's units 2 mt and 2 mt + 1.  Scaled by a
-    //      power of two (its largest magnitude into [2^5, 2^6)), then nibble e's by 1/4 or 1/64.
-    const int mg = lane >> 2, mt = lane & 3;
-    uint32_t qb[NT][NG][4];
-    float off[NT][NG][2], qs[NT][NG][2];  // -1024 sum(q'), sum(q) of heads 2 mt, 2 mt + 1 per group
-    float hs[NT][2];                      // their score scale, log2 units
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        float f[NG][8];
-        const int h = 8 * n + mg;
-        const T *qrow = static_cast<const T *>(p.q) + (static_cast<int64_t>(seq) * p.num_q_heads + hq0 + h) * D + 8 * mt;
-        float amax = 0.f;
-#pragma unroll
-        for (int j = 0; j < NG; ++j) {
-            const uint4 u = h < nheads ? *reinterpret_cast<const uint4 *>(qrow + 32 * j) : make_uint4(0, 0, 0, 0);
-            Elem<T>::to_f32x8(u, f[j]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[j][e]));
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const int qe = row_exponent(amax);
-        const float down = exp2_int(-qe) * 64.f;
-        const float up = exp2_int(qe) * (p.scale_log2 / 64.f);
-#pragma unroll
-        for (int j = 0; j < NG; ++j) {
-            float sum_q = 0.f, sum_r = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float fe = e & 1 ? 1.f / 64.f : 0.25f;
-                const float a = f[j][e] * down, b = f[j][4 + e] * down;
-                float ra, rb;
-                qb[n][j][e] = pack_mma2<false>(a * fe, b * fe, ra, rb);
-                sum_q += a + b;
-                sum_r += ra + rb;
-            }
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                sum_q += __shfl_xor_sync(0xffffffffu, sum_q, o);
-                sum_r += __shfl_xor_sync(0xffffffffu, sum_r, o);
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                qs[n][j][e] = __shfl_sync(0xffffffffu, sum_q, 4 * (2 * mt + e));
-                off[n][j][e] = -kInt4Offset * __shfl_sync(0xffffffffu, sum_r, 4 * (2 * mt + e));
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) hs[n][e] = __shfl_sync(0xffffffffu, up, 4 * (2 * mt + e));
-    }
-
-    // ---- accumulators: O^T m-tile (j, half) holds channels 32 j + 4 mg + 2 half (d0, d1) and + 1
-    //      (d2, d3) of heads 2 mt (d0, d2) and 2 mt + 1; ones: 1024 times the sums of the rounded weights
-    float oacc[NT][NG][2][4], ones[NT][NG][4], zacc[NT][NG][2], m[NT][2], l[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        m[n][0] = m[n][1] = -INFINITY;
-        l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-        for (int j = 0; j < NG; ++j) {
-            zacc[n][j][0] = zacc[n][j][1] = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) oacc[n][j][0][e] = oacc[n][j][1][e] = ones[n][j][e] = 0.f;
-        }
-    }
     constexpr float kGrow = 6.f;  // the reference moves when a maximum exceeds it by more (log2 units)
     const int tau = token_of_row(mg);
     const int va = mt, vb = 4 + (mt ^ 1);  // V's tokens of a lane: rows 2 mt and 2 mt + 1
+    auto load_units = [](const unsigned char *src, uint32_t (&u0)[NG / 2], uint32_t (&u1)[NG / 2]) {
+        if constexpr (NG == 4) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(src);
+            u0[0] = u.x;
+            u0[1] = u.y;
+            u1[0] = u.z;
+            u1[1] = u.w;
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2 *>(src);
+            u0[0] = u.x;
+            u1[0] = u.y;
+        }
+    };
+    auto load_params = [](const unsigned char *src, uint32_t (&w)[NG]) {
+        if constexpr (NG == 4) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(src);
+            w[0] = u.x;
+            w[1] = u.y;
+            w[2] = u.z;
+            w[3] = u.w;
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2 *>(src);
+            w[0] = u.x;
+            w[1] = u.y;
+        }
+    };
+    // the eight tokens 8 i .. 8 i + 7 of a stage's half: their block's record and their first row in it
+    auto octet = [](const unsigned char *half, int i) { return half + 8 * i / BS * G::kRecord; };
+    auto first_row = [](int i) { return 8 * i % BS; };
 
-    bool aborted = false;
-    for (int i = 0; i < my_chunks; ++i) {
-        const int s = i % S;
-        const bool ok = mbar_wait_bounded(&my_bars[s], (i / S) & 1, kWaitTimeoutNs);
-        if (__any_sync(0xffffffffu, !ok)) {
-            // give up: flag it, let this warp's copies still in flight land, stop
-            if (lane == 0) {
-                raise_flag(p.status, PKV_DEVERR_TIMEOUT);
-                for (int k = i; k < my_chunks && k < i + S; ++k)
-                    mbar_wait_bounded(&my_bars[k % S], (k / S) & 1, kDrainTimeoutNs);
-            }
-            __syncwarp();
-            aborted = true;
-            break;
-        }
-        const int c = warp + i * NW;
-        const int valid = min(ST, ntok - c * ST);  // >= 1
-        // tokens of the stage that count: in the context, and their block's entry not flagged
-        uint32_t vis = valid < 32 ? (1u << valid) - 1u : 0xffffffffu;
+    int s = 0;  // the next chunk's stage and its barrier's phase
+    uint32_t phase = 0;
+    Int4Split split{0, 0, 0, 0, 0};
+    for (bool first_piece = true; left > 0; first_piece = false) {
+        const int ctx = p.context_lens[seq], len = min(max(ctx, 0), p.len_cap);
+        const int chunks = int4_chunks(len), end = min(chunks, chunk + left);
+        if (chunk == 0 && unit == 0 && ctx != len && lane == 0) raise_flag(p.status, PKV_DEVERR_CONTEXT_LEN);
+        const int kvh = unit / p.blocks, sub = unit - kvh * p.blocks;
+        const int hq0 = kvh * p.group + sub * HEADS;
+        const int nheads = min(HEADS, p.group - sub * HEADS);
+
+        // ---- the query: lane (mg, mt) holds column (head) mg of every column tile at channels
+        //      32 j + 8 mt + 0 .. 7, the channels of a K row's units 2 mt and 2 mt + 1.  Scaled by a
+        //      power of two (its largest magnitude into [2^9, 2^10)), then odd nibbles' by 1/16.
+        uint32_t qb[NT][NG][4], zb[NT][2];  // zb: sum(q) per group, in 16-bit pieces along k
+        float hs[NT][2];                    // score scale of heads 2 mt, 2 mt + 1, log2 units
 #pragma unroll
-        for (int b = 0; b < SB; ++b) {
-            if (b * BS < valid && tbl[c * SB + b] < 0) vis &= BS == 32 ? 0u : ~(((1u << (BS & 31)) - 1u) << (b * BS & 31));
-        }
-        const unsigned char *kst = my_stages + s * G::kStageBytes, *vst = kst + G::kHalfBytes;
-#pragma unroll
-        for (int tb = 0; tb < ST; tb += 16) {
-            if (tb >= valid) break;  // warp-uniform: the step holds no context token
-            const bool partial = ((vis >> tb) & 0xffffu) != 0xffffu;
-            // rows mg and mg + 8 of the tile: tokens tb + tau and tb + 8 + tau
-            constexpr int B = BS;
-            const int ba = tb / B, oa = tb % B, bb = (tb + 8) / B, ob = (tb + 8) % B;
-            const unsigned char *ka = kst + ba * G::kRecord, *kb = kst + bb * G::kRecord;
-            const unsigned char *wa = vst + ba * G::kRecord, *wb = vst + bb * G::kRecord;
-            // ---- S^T = K Q^T: per group its own accumulator, from the offset on
-            uint32_t k0[2][NG / 2], k1[2][NG / 2];  // [row half][words of units 2 mt, 2 mt + 1]
-            uint32_t kp[2][NG], vp[2][NG];          // (scale, zero) words of the two tokens
-            auto load_units = [&](const unsigned char *src, uint32_t (&u0)[NG / 2], uint32_t (&u1)[NG / 2]) {
-                if constexpr (NG == 4) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(src);
-                    u0[0] = u.x;
-                    u0[1] = u.y;
-                    u1[0] = u.z;
-                    u1[1] = u.w;
-                } else {
-                    const uint2 u = *reinterpret_cast<const uint2 *>(src);
-                    u0[0] = u.x;
-                    u1[0] = u.y;
-                }
-            };
-            auto load_params = [&](const unsigned char *src, uint32_t (&w)[NG]) {
-                if constexpr (NG == 4) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(src);
-                    w[0] = u.x;
-                    w[1] = u.y;
-                    w[2] = u.z;
-                    w[3] = u.w;
-                } else {
-                    const uint2 u = *reinterpret_cast<const uint2 *>(src);
-                    w[0] = u.x;
-                    w[1] = u.y;
-                }
-            };
-            load_units(ka + (oa + tau) * ROW + mt * (ROW / 4), k0[0], k1[0]);
-            load_units(kb + (ob + tau) * ROW + mt * (ROW / 4), k0[1], k1[1]);
-            load_params(ka + B * ROW + (oa + tau) * PAR, kp[0]);
-            load_params(kb + B * ROW + (ob + tau) * PAR, kp[1]);
-            load_params(wa + B * ROW + (oa + tau) * PAR, vp[0]);
-            load_params(wb + B * ROW + (ob + tau) * PAR, vp[1]);
-            float sc[NT][4];  // tokens (0, 1: tau, 2, 3: 8 + tau) x heads 2 mt, 2 mt + 1
-#pragma unroll
-            for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+        for (int n = 0; n < NT; ++n) {
+            float f[NG][8];
+            const int h = 8 * n + mg;
+            const T *qrow = static_cast<const T *>(p.q) + (static_cast<int64_t>(seq) * p.num_q_heads + hq0 + h) * D + 8 * mt;
+            float amax = 0.f;
 #pragma unroll
             for (int j = 0; j < NG; ++j) {
-                uint32_t ra[4], rb[4];
-                codes_f16(group_word<NG>(k0[0], k1[0], j), ra);
-                codes_f16(group_word<NG>(k0[1], k1[1], j), rb);
-                const float2 pa = Int4Param<T>::unpack(kp[0][j]), pb = Int4Param<T>::unpack(kp[1][j]);
+                const uint4 u = h < nheads ? *reinterpret_cast<const uint4 *>(qrow + 32 * j) : make_uint4(0, 0, 0, 0);
+                Elem<T>::to_f32x8(u, f[j]);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float a[4] = {off[n][j][0], off[n][j][1], off[n][j][0], off[n][j][1]};
-                    mma_16816<false>(a, ra[0], rb[0], ra[1], rb[1], qb[n][j][0], qb[n][j][1]);
-                    mma_16816<false>(a, ra[2], rb[2], ra[3], rb[3], qb[n][j][2], qb[n][j][3]);
-                    fma_f32x2(sc[n][0], sc[n][1], a[0], a[1], pa.x, pa.x);
-                    fma_f32x2(sc[n][2], sc[n][3], a[2], a[3], pb.x, pb.x);
-                    fma_f32x2(sc[n][0], sc[n][1], qs[n][j][0], qs[n][j][1], pa.y, pa.y);
-                    fma_f32x2(sc[n][2], sc[n][3], qs[n][j][0], qs[n][j][1], pb.y, pb.y);
-                }
+                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[j][e]));
             }
-            float2 sv[2][NG];  // V's (scale, zero)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            const int qe = row_exponent(amax);
+            const float down = exp2_int(-qe) * 1024.f;
+            const float up = exp2_int(qe) * (p.scale_log2 / 1024.f);
+            float sum[NG];
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int j = 0; j < NG; ++j) {
+                sum[j] = 0.f;
 #pragma unroll
-                for (int j = 0; j < NG; ++j) sv[r][j] = Int4Param<T>::unpack(vp[r][j]);
-            bool seen[2] = {true, true};
-            if (partial) {
-                // hidden tokens: what their rows hold (stale bytes, NaN scales) does not count
+                for (int e = 0; e < 4; ++e) {
+                    const float fe = e & 1 ? 0.0625f : 1.f;
+                    const float a = f[j][e] * down, b = f[j][4 + e] * down;
+                    float ra, rb;
+                    qb[n][j][e] = pack_mma2<false>(a * fe, b * fe, ra, rb);
+                    sum[j] += a + b;
+                }
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
+            }
+            // k of the zeros' MMA: group pair (k / 2) % (NG / 2) of piece k / NG; the pieces of a sum are its
+            // rounding to the MMA's type, that of the remainder, and (bf16) of what then remains
+            const int pair = NG == 4 ? mt & 1 : 0, piece = NG == 4 ? mt >> 1 : mt;
+            float a = pair ? sum[NG - 2] : sum[0], b = pair ? sum[NG - 1] : sum[1];
+            constexpr int PIECES = kBF16 ? 3 : 2;
+            zb[n][0] = zb[n][1] = 0u;
+#pragma unroll
+            for (int k = 0; k < PIECES; ++k) {
+                float ra, rb;
+                const uint32_t w = pack_mma2<kBF16>(a, b, ra, rb);
+                if (piece == k) zb[n][0] = w;
+                if (NG == 4 && k == 2 && piece == 0) zb[n][1] = w;
+                a -= ra;
+                b -= rb;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) hs[n][e] = __shfl_sync(0xffffffffu, up, 4 * (2 * mt + e));
+        }
+
+        // ---- accumulators: O^T m-tile (j, half) holds channels 32 j + 4 mg + 2 half (d0, d1) and + 1
+        //      (d2, d3) of heads 2 mt (d0, d2) and 2 mt + 1
+        float oacc[NT][NG][2][4], zacc[NT][NG][2], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                zacc[n][j][0] = zacc[n][j][1] = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) oacc[n][j][0][e] = oacc[n][j][1][e] = 0.f;
+            }
+        }
+        for (int c = chunk; c < end; ++c) {
+            const bool ok = mbar_wait_bounded(&my_bars[s], phase, kWaitTimeoutNs);
+            if (__any_sync(0xffffffffu, !ok)) {
+                // give up: flag it, let this warp's copies still in flight land, stop
+                if (lane == 0) {
+                    raise_flag(p.status, PKV_DEVERR_TIMEOUT);
+                    for (int k = 0; k < S && k < left - (c - chunk); ++k) {
+                        const int at = s + k < S ? s + k : s + k - S;
+                        mbar_wait_bounded(&my_bars[at], s + k < S ? phase : phase ^ 1u, kDrainTimeoutNs);
+                    }
+                    if (!p.by_unit) p.splits[worker].pieces = 0;
+                }
+                __syncwarp();
+                return;
+            }
+            // tokens of the stage that count: in the context, and their block copied
+            const int valid = len - c * 32;  // >= 1, but 0 for an empty context
+            const uint32_t good = my_good[s];
+            uint32_t vis = valid < 32 ? (1u << valid) - 1u : 0xffffffffu;
+            if (good != (SB == 4 ? 0xffu : SB == 2 ? 0xfu : 0x3u)) {
+#pragma unroll
+                for (int b = 0; b < SB; ++b)
+                    if (!(good >> (2 * b) & 1u)) vis &= BS == 32 ? 0u : ~(((1u << (BS & 31)) - 1u) << (b * BS & 31));
+            }
+            const bool partial = vis != 0xffffffffu;
+            const unsigned char *kst = my_stages + s * G::kStageBytes, *vst = kst + G::kHalfBytes;
+            // ---- S^T = K Q^T, tokens 8 i + tau (octets i): per group its own accumulator, then the scales
+            float sc[4][NT][2];  // [octet][column tile][heads 2 mt, 2 mt + 1]
+#pragma unroll
+            for (int i2 = 0; i2 < 4; i2 += 2) {
+                uint32_t u0[2][NG / 2], u1[2][NG / 2], kp[2][NG];  // words of units 2 mt, 2 mt + 1; (scale, zero)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    seen[r] = (vis >> (tb + 8 * r + tau)) & 1u;
+                    const unsigned char *rec = octet(kst, i2 + r);
+                    load_units(rec + (first_row(i2 + r) + tau) * ROW + mt * (ROW / 4), u0[r], u1[r]);
+                    load_params(rec + BS * ROW + (first_row(i2 + r) + tau) * PAR, kp[r]);
+                }
+                // the zeros of this lane's group pair
+                uint32_t z[2];
 #pragma unroll
-                    for (int j = 0; j < NG; ++j)
-                        if (!seen[r]) sv[r][j] = make_float2(0.f, 0.f);
+                for (int r = 0; r < 2; ++r) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(octet(kst, i2 + r) + BS * ROW + (first_row(i2 + r) + tau) * PAR +
+                                                                     (NG == 4 ? 8 * (mt & 1) : 0));
+                    z[r] = __byte_perm(w.x, w.y, 0x7632);
+                }
+                float sz[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    sz[n][0] = sz[n][1] = sz[n][2] = sz[n][3] = 0.f;
+                    mma_16816<kBF16>(sz[n], z[0], z[1], z[0], z[1], zb[n][0], zb[n][1]);
+                }
+                float ss[NT][4];
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    uint32_t ra[4], rb[4];
+                    codes_f16(group_word<NG>(u0[0], u1[0], j), ra);
+                    codes_f16(group_word<NG>(u0[1], u1[1], j), rb);
+                    const float pa = Int4Param<T>::unpack(kp[0][j]).x, pb = Int4Param<T>::unpack(kp[1][j]).x;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float a[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma_16816<false>(a, ra[0], rb[0], ra[1], rb[1], qb[n][j][0], qb[n][j][1]);
+                        mma_16816<false>(a, ra[2], rb[2], ra[3], rb[3], qb[n][j][2], qb[n][j][3]);
+                        // (scalar products here and below: packed ones would take a second copy of the scale, a
+                        // move on the busier integer pipe each)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float by = e < 2 ? pa : pb;
+                            ss[n][e] = j == 0 ? a[e] * by : fmaf(a[e], by, ss[n][e]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    constexpr float kUnit = 16777216.f;  // 2^24: the codes' unit
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[i2 + e / 2][n][e & 1] = fmaf(ss[n][e], kUnit, sz[n][e]);
                 }
             }
-            // log2 of the token's largest V scale; the clamp keeps p (at most 2^-e) in range
-            float ev[2];
+            // ---- V's (scale, zero) pairs; hidden tokens' do not count, whatever their rows hold (stale
+            //      bytes, NaN scales)
+            uint32_t vp[4][NG];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float most = sv[r][0].x;
+            for (int i = 0; i < 4; ++i) load_params(octet(vst, i) + BS * ROW + (first_row(i) + tau) * PAR, vp[i]);
+            // log2 of each token's largest V scale; the clamp keeps p (at most 2^-e) in range
+            float ev[4];
 #pragma unroll
-                for (int j = 1; j < NG; ++j) most = fmaxf(most, sv[r][j].x);
-                ev[r] = fmaxf(fast_log2(most), -40.f);
+            for (int i = 0; i < 4; ++i) {
+                uint32_t most = max_scale<T>(vp[i][0], vp[i][1]);
+                if constexpr (NG == 4) most = max_scale<T>(most, max_scale<T>(vp[i][2], vp[i][3]));
+                ev[i] = fmaxf(fast_log2(Int4Param<T>::unpack(most).x), -40.f);
+            }
+            if (partial) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if ((vis >> (8 * i + tau)) & 1u) continue;
+                    ev[i] = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < NG; ++j) vp[i][j] = 0u;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) sc[i][n][0] = sc[i][n][1] = 0.f;
+                }
             }
             float mx[NT][2];
             bool grow = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    sc[n][e] *= hs[n][e & 1];
-                    if (partial && !seen[e >> 1]) sc[n][e] = -INFINITY;
-                }
-#pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float v = fmaxf(sc[n][e] + ev[0], sc[n][2 + e] + ev[1]);
+                    float v = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v = fmaxf(v, fmaf(sc[i][n][e], hs[n][e], ev[i]));
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
                     mx[n][e] = v;
@@ -380,122 +493,214 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
                         zacc[n][j][1] *= a[1];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            ones[n][j][e] *= a[e & 1];
                             oacc[n][j][0][e] *= a[e & 1];
                             oacc[n][j][1][e] *= a[e & 1];
                         }
                     }
                 }
             }
-            // ---- weights, and their products with V's scales in the B layout of O^T
-            uint32_t pb0[NT][NG], pb1[NT][NG];
+            // ---- weights
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-                const float w[4] = {fast_exp2(sc[n][0] - r0), fast_exp2(sc[n][1] - r1), fast_exp2(sc[n][2] - r0),
-                                    fast_exp2(sc[n][3] - r1)};
-                l[n][0] += w[0] + w[2];
-                l[n][1] += w[1] + w[3];
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float ref = m[n][e] == -INFINITY ? 0.f : m[n][e];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc[i][n][e] = fast_exp2(fmaf(sc[i][n][e], hs[n][e], -ref));
+                }
+            if (partial) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!((vis >> (8 * i + tau)) & 1u)) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) sc[i][n][0] = sc[i][n][1] = 0.f;
+                    }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) l[n][e] += (sc[0][n][e] + sc[1][n][e]) + (sc[2][n][e] + sc[3][n][e]);
+            // ---- O^T += V^T P^T, 16 tokens at a time: the weights times a group's scales in the B layout,
+            //      unit mg of tokens va, vb of both octets as the A fragments
+#pragma unroll
+            for (int i2 = 0; i2 < 4; i2 += 2) {
+                uint32_t v[4][NG / 2];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = i2 + r / 2;
+                    const unsigned char *src = octet(vst, i) + (first_row(i) + (r & 1 ? vb : va)) * ROW + mg * (ROW / 8);
+                    if constexpr (NG == 4) {
+                        const uint2 u = *reinterpret_cast<const uint2 *>(src);
+                        v[r][0] = u.x;
+                        v[r][1] = u.y;
+                    } else {
+                        v[r][0] = *reinterpret_cast<const uint32_t *>(src);
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < NG; ++j) {
-                    const __half2 ha = __floats2half2_rn(w[0] * sv[0][j].x, w[1] * sv[0][j].x);
-                    const __half2 hb = __floats2half2_rn(w[2] * sv[1][j].x, w[3] * sv[1][j].x);
-                    pb0[n][j] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&ha));
-                    pb1[n][j] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&hb));
-                    fma_f32x2(zacc[n][j][0], zacc[n][j][1], w[0], w[1], sv[0][j].y, sv[0][j].y);
-                    fma_f32x2(zacc[n][j][0], zacc[n][j][1], w[2], w[3], sv[1][j].y, sv[1][j].y);
+                    uint32_t ra[4], rb[4];
+                    codes_f16_bytes(group_word<NG>(v[0], v[1], j), ra);
+                    codes_f16_bytes(group_word<NG>(v[2], v[3], j), rb);
+                    const float2 s0 = Int4Param<T>::unpack(vp[i2][j]), s1 = Int4Param<T>::unpack(vp[i2 + 1][j]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const __half2 ha = __floats2half2_rn(sc[i2][n][0] * s0.x, sc[i2][n][1] * s0.x);
+                        const __half2 hb = __floats2half2_rn(sc[i2 + 1][n][0] * s1.x, sc[i2 + 1][n][1] * s1.x);
+                        const uint32_t b0 = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&ha));
+                        const uint32_t b1 = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&hb));
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            zacc[n][j][e] = fmaf(sc[i2 + 1][n][e], s1.y, fmaf(sc[i2][n][e], s0.y, zacc[n][j][e]));
+                        mma_16816<false>(oacc[n][j][0], ra[0], ra[1], rb[0], rb[1], b0, b1);
+                        mma_16816<false>(oacc[n][j][1], ra[2], ra[3], rb[2], rb[3], b0, b1);
+                    }
                 }
             }
-            // ---- O^T += V^T P^T: unit mg of tokens va, vb and 8 + va, 8 + vb
-            uint32_t v[4][NG / 2];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const unsigned char *src = (r < 2 ? wa + oa * ROW : wb + ob * ROW) + (r & 1 ? vb : va) * ROW + mg * (ROW / 8);
-                if constexpr (NG == 4) {
-                    const uint2 u = *reinterpret_cast<const uint2 *>(src);
-                    v[r][0] = u.x;
-                    v[r][1] = u.y;
-                } else {
-                    v[r][0] = *reinterpret_cast<const uint32_t *>(src);
-                }
+            __syncwarp();
+            if (i_left > 0) {
+                fence_proxy_async_smem();
+                issue(s);
             }
-#pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                uint32_t ra[4], rb[4];
-                codes_f16(group_word<NG>(v[0], v[1], j), ra);
-                codes_f16(group_word<NG>(v[2], v[3], j), rb);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    mma_16816<false>(oacc[n][j][0], ra[0], ra[1], rb[0], rb[1], pb0[n][j], pb1[n][j]);
-                    mma_16816<false>(oacc[n][j][1], ra[2], ra[3], rb[2], rb[3], pb0[n][j], pb1[n][j]);
-                    mma_16816<false>(ones[n][j], 0x64006400u, 0x64006400u, 0x64006400u, 0x64006400u, pb0[n][j], pb1[n][j]);
-                }
+            if (++s == S) {
+                s = 0;
+                phase ^= 1u;
             }
         }
-        __syncwarp();
-        if (lane == 0 && i + S < my_chunks) {
-            fence_proxy_async_smem();
-            issue(warp + (i + S) * NW, s);
-        }
-    }
 
-    // ---- a head's row sums over its lanes, then the warps merged through shared memory (each
-    //      warp reuses its own stages: all of its copies have landed)
-    float *mine = reinterpret_cast<float *>(my_stages);  // [heads][D + 4]
-    __syncwarp();
+        // ---- the unit's piece is done: a head's sums over its lanes, then out or into its slot
+        const bool whole = chunk == 0 && end == chunks;
+        const int64_t slot = (2 * static_cast<int64_t>(worker) + (first_piece ? 0 : 1)) * HEADS;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < 2; ++e) {
+                const int h = 8 * n + 2 * mt + e;
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
-            float *row = mine + (8 * n + 2 * mt + e) * (D + 4);
+                for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
+                const float norm = !whole ? 1.f : l[n][e] > 0.f ? 1.f / l[n][e] : 0.f;
+                const int64_t row = static_cast<int64_t>(seq) * p.num_q_heads + hq0 + h;
 #pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                float z = zacc[n][j][e];
+                for (int j = 0; j < NG; ++j) {
+                    float z = zacc[n][j][e];
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-                const float w = ones[n][j][e];
-                *reinterpret_cast<float4 *>(row + 32 * j + 4 * mg) =
-                    make_float4(fmaf(oacc[n][j][0][e] - w, 0.25f, z), fmaf(oacc[n][j][0][2 + e] - w, 1.f / 64.f, z),
-                                fmaf(oacc[n][j][1][e] - w, 0.25f, z), fmaf(oacc[n][j][1][2 + e] - w, 1.f / 64.f, z));
+                    for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+                    constexpr float kEven = 16777216.f, kOdd = 1048576.f;  // 2^24, 2^20: the nibbles' places
+                    const float r0 = fmaf(oacc[n][j][0][e], kEven, z) * norm, r1 = fmaf(oacc[n][j][0][2 + e], kOdd, z) * norm;
+                    // (the third nibble's accumulator holds the fourth's too)
+                    const float r2 = fmaf(oacc[n][j][1][e] - oacc[n][j][1][2 + e], kEven, z) * norm, r3 = fmaf(oacc[n][j][1][2 + e], kOdd, z) * norm;
+                    if (h >= nheads) continue;
+                    if (whole)
+                        *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + row * D + 32 * j + 4 * mg) =
+                            make_uint2(Elem<T>::pack2(r0, r1), Elem<T>::pack2(r2, r3));
+                    else
+                        *reinterpret_cast<float4 *>(p.seg_o + (slot + h) * D + 32 * j + 4 * mg) = make_float4(r0, r1, r2, r3);
+                }
+                if (!whole && mg == 0 && h < nheads) {
+                    p.seg_m[slot + h] = m[n][e];
+                    p.seg_l[slot + h] = l[n][e];
+                }
             }
-            if (mg == 0) {
-                row[D] = aborted ? -INFINITY : m[n][e];
-                row[D + 1] = aborted ? 0.f : l[n][e];
-            }
+        }
+        left -= end - chunk;
+        if (chunk == 0) {  // (end < chunks: left is 0, and the pieces behind are those of the next workers)
+            split = Int4Split{end < chunks ? 1 + (chunks - end + share - 1) / share : 0, worker, first_piece ? 0 : 1, seq, unit};
+            if (p.by_unit && lane == 0) p.splits[seq * p.units + unit] = split;
+        }
+        chunk = 0;
+        if (++unit == p.units) {
+            unit = 0;
+            ++seq;
         }
     }
-    __syncthreads();
-    const bool single = nparts == 1;
-    for (int idx = threadIdx.x; idx < nheads * D; idx += blockDim.x) {
-        const int h = idx / D, j = idx - h * D;
-        float mw[NW], mmax = -INFINITY;
+    if (lane == 0 && !p.by_unit) p.splits[worker] = split;
+}
+
+// Log-sum-exp merge of the cut units: entry blockIdx.x of their table.  WPH warps share a head's pieces:
+// four where units are few and cut into many (grid.y: the heads), else one (grid.y: the heads' fours, or
+// all in turn).
+template <typename T, int D, int WPH>
+__global__ void __launch_bounds__(128) paged_decode_int4_merge_kernel(const Int4Params p, int heads) {
+    static_assert(WPH == 1 || WPH == 4, "one or four warps per head");
+    constexpr int PER = D / 32;
+    using Part = typename std::conditional<PER == 4, float4, float2>::type;
+    __shared__ float comb[WPH == 4 ? 4 : 1][D + 2];  // the four warps' (o, m, l) of a head
+    pdl_wait();
+    const Int4Split s = p.splits[blockIdx.x];
+    if (s.pieces == 0) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int kvh = s.unit / p.blocks, sub = s.unit - kvh * p.blocks;
+    const int nheads = min(heads, p.group - sub * heads);
+    auto slot = [&](int i, int h) { return (2 * static_cast<int64_t>(s.worker + i) + (i == 0 ? s.slot : 0)) * heads + h; };
+    const int share = WPH == 4 ? warp : 0;
+    const int mine = s.pieces > share ? (s.pieces - share + WPH - 1) / WPH : 0;  // pieces share, share + WPH, ...
+    for (int h = WPH == 4 ? blockIdx.y : blockIdx.y * 4 + warp; h < nheads; h += WPH == 4 ? gridDim.y : 4 * gridDim.y) {
+        // the first pieces' rows are on their way while the maxima are compared
+        Part v[8];
+        auto rows = [&](int i0) {
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            mw[w] = reinterpret_cast<const float *>(stages + w * S * G::kStageBytes)[h * (D + 4) + D];
-            mmax = fmaxf(mmax, mw[w]);
-        }
-        float lsum = 0.f, osum = 0.f;
+            for (int u = 0; u < 8; ++u)
+                if (i0 + u < mine) v[u] = reinterpret_cast<const Part *>(p.seg_o + slot(share + WPH * (i0 + u), h) * D)[lane];
+        };
+        rows(0);
+        float mmax = -INFINITY;
+        for (int i = lane; i < mine; i += 32) mmax = fmaxf(mmax, p.seg_m[slot(share + WPH * i, h)]);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float *src = reinterpret_cast<const float *>(stages + w * S * G::kStageBytes) + h * (D + 4);
-            if (mw[w] == -INFINITY) continue;
-            const float wgt = fast_exp2(mw[w] - mmax);
-            lsum += wgt * src[D + 1];
-            osum += wgt * src[j];
-        }
-        const int64_t row = static_cast<int64_t>(seq) * p.num_q_heads + hq0 + h;
-        if (single) {
-            static_cast<T *>(p.out)[row * D + j] = Elem<T>::from_f32(lsum > 0.f ? osum / lsum : 0.f);
-        } else {
-            const int64_t pr = row * p.num_partitions + part;
-            p.ws_o[pr * D + j] = osum;
-            if (j == 0) {
-                p.ws_m[pr] = mmax;
-                p.ws_l[pr] = lsum;
+        for (int o = 16; o > 0; o >>= 1) mmax = fmaxf(mmax, __shfl_xor_sync(0xffffffffu, mmax, o));
+        float lsum = 0.f, o[PER] = {};
+        for (int i0 = 0; i0 < mine; i0 += 32) {
+            const int cnt = min(32, mine - i0);
+            float w = 0.f;  // this lane's piece
+            if (lane < cnt) {
+                const int64_t at = slot(share + WPH * (i0 + lane), h);
+                const float mi = p.seg_m[at];
+                w = mi == -INFINITY ? 0.f : fast_exp2(mi - mmax);
+                lsum = fmaf(w, p.seg_l[at], lsum);
+            }
+            for (int j0 = 0; j0 < cnt; j0 += 8) {
+                if (i0 + j0 > 0) rows(i0 + j0);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float wu = __shfl_sync(0xffffffffu, w, (j0 + u) & 31);
+                    if (j0 + u < cnt) {
+                        const float *f = reinterpret_cast<const float *>(&v[u]);
+#pragma unroll
+                        for (int e = 0; e < PER; ++e) o[e] = fmaf(wu, f[e], o[e]);
+                    }
+                }
             }
         }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, off);
+        if constexpr (WPH == 4) {
+            // the four warps' results, relative to their own maxima, combined in warp 0
+            __syncthreads();  // (the head before is read)
+#pragma unroll
+            for (int e = 0; e < PER; ++e) comb[warp][lane * PER + e] = o[e];
+            if (lane == 0) {
+                comb[warp][D] = mmax;
+                comb[warp][D + 1] = lsum;
+            }
+            __syncthreads();
+            if (warp != 0) continue;
+            float mall = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) mall = fmaxf(mall, comb[w][D]);
+            lsum = 0.f;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) o[e] = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float sw = comb[w][D] == -INFINITY ? 0.f : fast_exp2(comb[w][D] - mall);
+                lsum = fmaf(sw, comb[w][D + 1], lsum);
+#pragma unroll
+                for (int e = 0; e < PER; ++e) o[e] = fmaf(sw, comb[w][lane * PER + e], o[e]);
+            }
+        }
+        const float norm = lsum > 0.f ? 1.f / lsum : 0.f;
+        T *dst = static_cast<T *>(p.out) + (static_cast<int64_t>(s.seq) * p.num_q_heads + kvh * p.group + sub * heads + h) * D + PER * lane;
+#pragma unroll
+        for (int e = 0; e < PER; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = Elem<T>::pack2(o[e] * norm, o[e + 1] * norm);
     }
 }
 

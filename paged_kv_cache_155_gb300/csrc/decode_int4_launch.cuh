@@ -2,6 +2,7 @@
 // element type (decode_int4_f16.cu, decode_int4_bf16.cu).
 #pragma once
 
+#include <algorithm>
 #include <atomic>
 
 #include "decode_int4_kernel.cuh"
@@ -10,7 +11,7 @@
 namespace pkv {
 
 template <typename T, int D, int BS, int NT>
-pkv_status launch_int4_one(const DecodeParams &p, dim3 grid, cudaStream_t stream) {
+pkv_status launch_int4_one(const Int4Params &p, int grid, cudaStream_t stream) {
     using G = DecodeInt4Geom<D, BS, NT>;
     static std::atomic<uint64_t> configured_devices{0};  // bit per device ordinal
     int dev = 0;
@@ -22,7 +23,7 @@ pkv_status launch_int4_one(const DecodeParams &p, dim3 grid, cudaStream_t stream
             return PKV_ERR_CUDA;
         configured_devices.fetch_or(bit, std::memory_order_acq_rel);
     }
-    if (launch_kernel(paged_decode_int4_kernel<T, D, BS, NT>, grid, dim3(G::kWarps * 32), G::kSmemBytes, stream, false,
+    if (launch_kernel(paged_decode_int4_kernel<T, D, BS, NT>, dim3(static_cast<unsigned>(grid)), dim3(G::kWarps * 32), G::kSmemBytes, stream, false,
                       p) != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
@@ -32,7 +33,7 @@ pkv_status launch_int4_one(const DecodeParams &p, dim3 grid, cudaStream_t stream
 }
 
 template <typename T, int D, int NT>
-pkv_status launch_int4_bs(const DecodeParams &p, int block_size, dim3 grid, cudaStream_t s) {
+pkv_status launch_int4_bs(const Int4Params &p, int block_size, int grid, cudaStream_t s) {
     switch (block_size) {
         case 8: return launch_int4_one<T, D, 8, NT>(p, grid, s);
         case 16: return launch_int4_one<T, D, 16, NT>(p, grid, s);
@@ -41,21 +42,25 @@ pkv_status launch_int4_bs(const DecodeParams &p, int block_size, dim3 grid, cuda
     return PKV_ERR_UNSUPPORTED;
 }
 
-// tiles: column tiles of eight heads per block (1 or 2); merge_rows > 0: the merge follows.
+// tiles: column tiles of eight heads per block (1 or 2); grid CTAs, then the merge of the units that
+// their workers cut.
 template <typename T>
-pkv_status launch_int4_typed(const DecodeParams &p, int head_dim, int block_size, int tiles, dim3 grid, int merge_rows,
-                             cudaStream_t s) {
+pkv_status launch_int4_typed(const Int4Params &p, int head_dim, int block_size, int tiles, int grid, cudaStream_t s) {
     pkv_status st;
     if (head_dim == 128)
         st = tiles == 1 ? launch_int4_bs<T, 128, 1>(p, block_size, grid, s) : launch_int4_bs<T, 128, 2>(p, block_size, grid, s);
     else
         st = tiles == 1 ? launch_int4_bs<T, 64, 1>(p, block_size, grid, s) : launch_int4_bs<T, 64, 2>(p, block_size, grid, s);
-    if (st != PKV_OK || merge_rows == 0) return st;
-    const bool wide = p.num_partitions >= kMergeWideFrom;
-    const dim3 blocks(static_cast<unsigned>(wide ? merge_rows : (merge_rows + 3) / 4));
-    auto merge = head_dim == 128 ? (wide ? paged_decode_merge_kernel<T, 128, 4> : paged_decode_merge_kernel<T, 128, 1>)
-                                 : (wide ? paged_decode_merge_kernel<T, 64, 4> : paged_decode_merge_kernel<T, 64, 1>);
-    if (launch_kernel(merge, blocks, dim3(128), 0, s, true, p, merge_rows) != cudaSuccess) {
+    if (st != PKV_OK) return st;
+    // units cut into many pieces: four warps share a head's
+    const int64_t units = static_cast<int64_t>(p.num_seqs) * p.units;
+    const bool shared = p.by_unit && grid * 4 >= 16 * units;
+    auto merge = head_dim == 128 ? (shared ? paged_decode_int4_merge_kernel<T, 128, 4> : paged_decode_int4_merge_kernel<T, 128, 1>)
+                                 : (shared ? paged_decode_int4_merge_kernel<T, 64, 4> : paged_decode_int4_merge_kernel<T, 64, 1>);
+    const int heads = std::min(p.group, 8 * tiles);
+    const dim3 blocks(static_cast<unsigned>(p.by_unit ? units : grid * 4),
+                      static_cast<unsigned>(shared ? heads : p.by_unit ? (heads + 3) / 4 : 1));
+    if (launch_kernel(merge, blocks, dim3(128), 0, s, true, p, 8 * tiles) != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
     }
@@ -63,9 +68,7 @@ pkv_status launch_int4_typed(const DecodeParams &p, int head_dim, int block_size
     return launch_status();
 }
 
-pkv_status launch_int4_f16(const DecodeParams &p, int head_dim, int block_size, int tiles, dim3 grid, int merge_rows,
-                           cudaStream_t s);
-pkv_status launch_int4_bf16(const DecodeParams &p, int head_dim, int block_size, int tiles, dim3 grid, int merge_rows,
-                            cudaStream_t s);
+pkv_status launch_int4_f16(const Int4Params &p, int head_dim, int block_size, int tiles, int grid, cudaStream_t s);
+pkv_status launch_int4_bf16(const Int4Params &p, int head_dim, int block_size, int tiles, int grid, cudaStream_t s);
 
 }  // namespace pkv

@@ -897,10 +897,8 @@ def prepare_dequantise_blocks_int4(k_cache4: torch.Tensor, v_cache4: torch.Tenso
                         (k_cache4, v_cache4, src_dst_pairs, k_cache, v_cache))
 
 
-def decode_int4_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
-                                partition_size=0) -> int:
-    n = lib().pkv_decode_int4_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
-                                              max_context_len, partition_size)
+def decode_int4_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len) -> int:
+    n = lib().pkv_decode_int4_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len)
     if n == ctypes.c_size_t(-1).value:
         raise PagedKVError("pkv_decode_int4_workspace_bytes", 1)
     return int(n)
@@ -909,33 +907,30 @@ def decode_int4_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, b
 def paged_attention_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                                 block_tables: torch.Tensor, context_lens: torch.Tensor,
                                 scale: Optional[float] = None, out: Optional[torch.Tensor] = None, *,
-                                max_context_len: Optional[int] = None, partition_size: int = 0,
+                                max_context_len: Optional[int] = None,
                                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """paged_attention_decode over a 4-bit cache (``int4_pool``); q and out have the dtype of the
-    rows that were quantised.  partition_size: 0 or a multiple of 32."""
+    rows that were quantised."""
     return prepare_paged_attention_decode_int4(q, k_cache, v_cache, block_tables, context_lens, scale, out,
-                                               max_context_len=max_context_len, partition_size=partition_size,
-                                               workspace=workspace)()
+                                               max_context_len=max_context_len, workspace=workspace)()
 
 
 def prepare_paged_attention_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                                         block_tables: torch.Tensor, context_lens: torch.Tensor,
                                         scale: Optional[float] = None, out: Optional[torch.Tensor] = None, *,
-                                        max_context_len: Optional[int] = None, partition_size: int = 0,
+                                        max_context_len: Optional[int] = None,
                                         workspace: Optional[torch.Tensor] = None) -> PreparedCall:
     """paged_attention_decode_int4, checked and marshalled once (see PreparedCall); the call
     returns ``out``.  Without ``workspace`` it holds one of its own."""
     nb, hkv, bs, d, stride = _int4_geometry(k_cache, v_cache)
     b, hq, scale, max_context_len, out = _decode_args(q, d, block_tables, context_lens, scale, out, max_context_len)
-    _int32(partition_size=partition_size)
     _one_device(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens, out=out)
     with torch.cuda.device(q.device):
-        need = decode_int4_workspace_bytes(b, hq, hkv, d, bs, max_context_len, partition_size)
+        need = decode_int4_workspace_bytes(b, hq, hkv, d, bs, max_context_len)
     workspace = _own_workspace(q.device, need, workspace)
     args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, stride, block_tables.data_ptr(),
             int(block_tables.shape[1]), context_lens.data_ptr(), max_context_len, b, hq, hkv, d, bs, scale, out.data_ptr(),
-            None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), int(partition_size), _dtype_code(q))
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _dtype_code(q))
     return PreparedCall("pkv_paged_attention_decode_int4", args, q.device,
                         (q, k_cache, v_cache, block_tables, context_lens, out, workspace), out)
 

@@ -167,17 +167,30 @@ def s_max(pool, table, n, dtype):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("hq,hkv,d,bs", [(1, 1, 64, 8), (4, 4, 128, 16), (8, 1, 128, 8), (32, 4, 128, 32), (12, 4, 64, 16),
                                          (16, 1, 128, 16), (40, 2, 64, 32), (36, 1, 128, 8), (13, 1, 64, 8), (128, 8, 128, 16)])
-@pytest.mark.parametrize("part", [0, 64])
-def test_decode(hq, hkv, d, bs, dtype, part):
+@pytest.mark.parametrize("more", [0, 1500])
+def test_decode(hq, hkv, d, bs, dtype, more):
     dev, g = device(), torch.Generator().manual_seed(hq * 7 + d + bs)
-    lens = [0, 1, 31, 32, 33, 65, 200, 311]
+    lens = [0, 1, 31, 32, 33, 65, 200, 311] + [more] * (more > 0)  # a long context's units are cut by several workers
     pool, tables = _pool_of(lens, hkv, bs, d, dtype, g)
     q = (torch.randn((len(lens), hq, d), generator=g) * 2).to(dtype)
     out = pkv.paged_attention_decode_int4(q.to(dev), *pkv.split_pool(pool.to(dev)), tables.to(dev),
-                                          torch.tensor(lens, dtype=torch.int32, device=dev), max_context_len=311,
-                                          partition_size=part)
+                                          torch.tensor(lens, dtype=torch.int32, device=dev), max_context_len=max(lens))
     check_no_device_flags(dev)
-    _check_decode(out.cpu(), q, pool, tables, lens, dtype, 1 / math.sqrt(d), f"part {part}")
+    _check_decode(out.cpu(), q, pool, tables, lens, dtype, 1 / math.sqrt(d), f"more {more}")
+
+
+def test_decode_of_many_and_of_few_tokens():
+    """More sequences than a warp reads at once, and batches whose workers outnumber their chunks."""
+    dev = device()
+    for hq, hkv, lens in ((4, 2, [i * 53 % 300 for i in range(100)]), (8, 8, [3]), (16, 1, [0, 0]), (1, 1, [4000, 0, 1])):
+        g = torch.Generator().manual_seed(len(lens))
+        pool, tables = _pool_of(lens, hkv, 16, 64, torch.float16, g)
+        q = (torch.randn((len(lens), hq, 64), generator=g) * 2).to(torch.float16)
+        out = torch.full_like(q, 7.0).to(dev)
+        pkv.paged_attention_decode_int4(q.to(dev), *pkv.split_pool(pool.to(dev)), tables.to(dev),
+                                        torch.tensor(lens, dtype=torch.int32, device=dev), out=out, max_context_len=max(lens))
+        check_no_device_flags(dev)
+        _check_decode(out.cpu(), q, pool, tables, lens, torch.float16, 0.125, f"{len(lens)} sequences")
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -221,7 +234,7 @@ def test_prepared_calls_on_another_stream_and_in_a_graph():
     pool, tables = _pool_of(lens, 2, 16, 128, torch.bfloat16, g)
     q = torch.randn((3, 8, 128), generator=g).to(torch.bfloat16).to(dev)
     dl, dt, dp = torch.tensor(lens, dtype=torch.int32, device=dev), tables.to(dev), pool.to(dev)
-    calls = [pkv.prepare_paged_attention_decode_int4(q, *pkv.split_pool(dp), dt, dl, max_context_len=910, partition_size=64)
+    calls = [pkv.prepare_paged_attention_decode_int4(q, *pkv.split_pool(dp), dt, dl, max_context_len=910)
              for _ in range(2)]  # two workspaces: their graphs may run together
     want = calls[0]().clone()
     torch.cuda.synchronize()
