@@ -30,7 +30,7 @@ struct Int4Param;  // a (scale, zero) pair as one 32-bit word, the scale in the 
 
 template <>
 struct Int4Param<__half> {
-    static __device__ __forceinline__ uint32_t scale_up(float x) { return __half_as_ushort(__float2half_ru(x)); }
+    static __device__ __forceinline__ uint32_t scale_down(float x) { return __half_as_ushort(__float2half_rd(x)); }
     static __device__ __forceinline__ uint32_t bits(float x) { return __half_as_ushort(__float2half_rn(x)); }
     static __device__ __forceinline__ float value(uint32_t b) { return __half2float(__ushort_as_half(static_cast<unsigned short>(b))); }
     static __device__ __forceinline__ float2 unpack(uint32_t w) {
@@ -40,7 +40,7 @@ struct Int4Param<__half> {
 
 template <>
 struct Int4Param<__nv_bfloat16> {
-    static __device__ __forceinline__ uint32_t scale_up(float x) { return __bfloat16_as_ushort(__float2bfloat16_ru(x)); }
+    static __device__ __forceinline__ uint32_t scale_down(float x) { return __bfloat16_as_ushort(__float2bfloat16_rd(x)); }
     static __device__ __forceinline__ uint32_t bits(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
     static __device__ __forceinline__ float value(uint32_t b) { return __uint_as_float(b << 16); }
     static __device__ __forceinline__ float2 unpack(uint32_t w) {
