@@ -109,6 +109,7 @@ PKV_API pkv_status pkv_paged_attention_decode_int4(const void *q, const void *k_
     const int64_t chunks = std::max<int64_t>(1, (max_context_len + 31LL) / 32) * p.units * num_seqs;
     const int64_t most = (chunks + pkv::kInt4MinShare * kWorkersPerCta - 1) / (pkv::kInt4MinShare * kWorkersPerCta);
     const int grid = static_cast<int>(std::min<int64_t>(most, static_cast<int64_t>(sm) * plan.resident));
+    p.seg_workers = sm * plan.resident * kWorkersPerCta;
     p.by_unit = static_cast<int64_t>(num_seqs) * p.units <= static_cast<int64_t>(grid) * kWorkersPerCta;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return dtype == PKV_F16 ? pkv::launch_int4_f16(p, head_dim, block_size, plan.tiles, grid, s)

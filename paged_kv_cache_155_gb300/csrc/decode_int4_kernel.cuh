@@ -72,7 +72,7 @@ struct Int4Params {
     void *out;
     float *seg_o, *seg_m, *seg_l; // partials [2 worker + slot][heads of a block][D], [..][heads]
     Int4Split *splits;            // [min(workers, num_seqs * units)]
-    int by_unit;                  // its index
+    int by_unit, seg_workers;     // its index; workers that the partials have room for
     const int32_t *block_tables, *context_lens;
     unsigned int *status;
     int64_t num_blocks, block_stride;  // bytes
@@ -626,8 +626,13 @@ __global__ void __launch_bounds__(128) paged_decode_int4_merge_kernel(const Int4
     using Part = typename std::conditional<PER == 4, float4, float2>::type;
     __shared__ float comb[WPH == 4 ? 4 : 1][D + 2];  // the four warps' (o, m, l) of a head
     pdl_wait();
-    const Int4Split s = p.splits[blockIdx.x];
-    if (s.pieces == 0) return;
+    Int4Split s = p.splits[blockIdx.x];
+    if (p.by_unit) {
+        s.seq = blockIdx.x / p.units;
+        s.unit = blockIdx.x - s.seq * p.units;
+    }
+    // (a kernel that gave up on a wait leaves entries unwritten)
+    if (s.pieces <= 0 || s.worker < 0 || s.worker >= p.seg_workers || s.pieces > p.seg_workers - s.worker || (s.slot & ~1)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int kvh = s.unit / p.blocks, sub = s.unit - kvh * p.blocks;
     const int nheads = min(heads, p.group - sub * heads);

@@ -100,8 +100,10 @@ pkv_status launch_tree(const PrefillParams &p, const CUtensorMap &tq, const CUte
         : block_size == 16 ? launch_prefill_one<T, 16, kOrderStream, kTreeForm>(p, tq, tk, tv, to, grid, s)
                            : launch_prefill_one<T, 32, kOrderStream, kTreeForm>(p, tq, tk, tv, to, grid, s);
     if (st != PKV_OK) return st;
-    const dim3 mgrid(static_cast<unsigned>(grid), static_cast<unsigned>((p.tile_rows + kTreeMergeWarps - 1) / kTreeMergeWarps));
-    if (launch_kernel(paged_tree_merge_kernel<T>, mgrid, dim3(32 * kTreeMergeWarps), 0, s, true, p) != cudaSuccess) {
+    const int entries = p.by_unit ? p.num_seqs * p.num_kv_heads * p.row_tiles : grid;
+    const bool shared = p.by_unit && entries * 8 <= grid;  // units cut into eight pieces or more
+    if (launch_kernel(shared ? paged_tree_merge_kernel<T, 4> : paged_tree_merge_kernel<T, 1>, dim3(static_cast<unsigned>(entries), 16),
+                      dim3(shared ? 512 : 128), 0, s, true, p) != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
     }

@@ -118,8 +118,10 @@ struct PrefillParams {
     // Tree form: which tokens of the chunk a row sees, and the shared work (stream order).
     const int64_t *tree_mask;    // [num_rows][mask_words], bit c: chunk token c
     int mask_words;
-    float *seg_o, *seg_m, *seg_l;      // partials of cut units: [2 CTA + slot][128 rows][128], [..][128]
-    struct TreeSplit *tree_splits;     // [grid]: the unit that begins in a CTA's share and goes on past it
+    float *seg_o, *seg_m, *seg_l;      // partials of cut units: [2 CTA + slot][32 channel fours][128 rows][4],
+                                       // so that a warp's rows store side by side, and [..][128 rows]
+    struct TreeSplit *tree_splits;     // the cut units, see TreeSplit
+    int by_unit, seg_ctas;             // its index; CTAs that the partials have room for
 };
 // The fixed form's largest cap_out, and the exponent that its weights may reach: the reference
 // is what a score of cap_out exceeds that by.  So weights lie in 2^-100 .. 2^50: a product with
@@ -379,12 +381,16 @@ struct StreamShare {
     int left;      // tiles of the share
     int quota;     // tiles of every share (the last ones' may be shorter)
 };
+// A cut unit.  The table is indexed by unit -- (sequence, KV head, row tile), with row tiles by the host's
+// bound -- when there are no more of them than CTAs, else by the CTA in whose share it begins (at most
+// one goes on past a share).  Few units, cut into many pieces, then have a few merging blocks: one per
+// CTA, most of which find nothing, ran in several waves behind the kernel, whose registers leave them no room.
 struct TreeSplit {
-    int pieces;    // CTAs that hold pieces of the unit, this one first; 0: none begins here
-    int slot;      // this CTA's piece
-    int q0, chunk; // the unit's sequence
+    int pieces;     // CTAs that hold pieces of the unit; 0: not cut (or none begins in this share)
+    int cta, slot;  // the first of them, and its piece's slot (0 in the others)
+    int q0, chunk;  // the unit's sequence
     int kvh, row_tile;
-    int pad[2];
+    int pad;
 };
 constexpr int kMinShare = 2;  // tiles of a share, at least
 // KV tiles of one unit and units of a sequence (no tiles: an empty or bad sequence)
@@ -1240,9 +1246,12 @@ __global__ void __launch_bounds__(384, 1)
             const int64_t *tree_row = nullptr;  // this row's words
             if constexpr (kTree) {
                 if (live) tree_row = p.tree_mask + static_cast<int64_t>(it.q0 + jtok) * p.mask_words;
-                if (behind > 0 && (it.tok_lo == 0)) {
-                    // the unit begins in this share and goes on: its pieces, in this CTA and the next ones
-                    split = TreeSplit{1 + (behind + walk.s.quota - 1) / walk.s.quota, it.split, it.q0, it.chunk, it.kvh, it.row_tile, {0, 0}};
+                if (it.tok_lo == 0) {
+                    // the unit begins in this share; if it goes on, its pieces are in this CTA and the next ones
+                    split = TreeSplit{behind > 0 ? 1 + (behind + walk.s.quota - 1) / walk.s.quota : 0, static_cast<int>(blockIdx.x),
+                                      it.split, it.q0, it.chunk, it.kvh, it.row_tile, 0};
+                    if (p.by_unit && warp == 2 && lane == 0)
+                        p.tree_splits[(it.seq * p.num_kv_heads + it.kvh) * p.row_tiles + it.row_tile] = split;
                 }
             }
             for (int j = 0; j < it.ntiles && ok; ++j, ++jt) {
@@ -1480,7 +1489,7 @@ __global__ void __launch_bounds__(384, 1)
                 const int64_t orow = (static_cast<int64_t>(it.q0) + jtok) * p.num_q_heads + it.kvh * p.group + g;
                 const bool direct = p.splits == 1 && !it.partial;
                 // tree form: the rows of a piece go to its slot
-                const int64_t seg = kTree ? (2 * static_cast<int64_t>(blockIdx.x) + it.split) * 128 + r : 0;
+                const int64_t slot = kTree ? 2 * static_cast<int64_t>(blockIdx.x) + it.split : 0;
                 const float inv_l = lt > 0.f ? 1.f / lt : 0.f;
 #pragma unroll
                 for (int c = 0; c < 64; c += 16) {
@@ -1496,16 +1505,17 @@ __global__ void __launch_bounds__(384, 1)
                         dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
                         dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
                     } else {
-                        float *dst = (kTree ? p.seg_o + seg * D : p.ws_o + (orow * p.splits + it.split) * D) + c0 + c;
+                        float *dst = kTree ? p.seg_o + ((slot * 32 + (c0 + c) / 4) * 128 + r) * 4
+                                           : p.ws_o + (orow * p.splits + it.split) * D + c0 + c;
 #pragma unroll
                         for (int i = 0; i < 16; i += 4)
-                            *reinterpret_cast<float4 *>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                            *reinterpret_cast<float4 *>(dst + (kTree ? i * 128 : i)) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                     }
                 }
                 if (live && !direct && half == 0) {
                     if constexpr (kTree) {
-                        p.seg_m[seg] = m_ref;
-                        p.seg_l[seg] = lt;
+                        p.seg_m[slot * 128 + r] = m_ref;
+                        p.seg_l[slot * 128 + r] = lt;
                     } else {
                         p.ws_m[orow * p.splits + it.split] = m_ref;
                         p.ws_l[orow * p.splits + it.split] = lt;
@@ -1514,7 +1524,7 @@ __global__ void __launch_bounds__(384, 1)
             }
         }
         if constexpr (kTree) {
-            if (warp == 2 && lane == 0) p.tree_splits[blockIdx.x] = split;
+            if (!p.by_unit && warp == 2 && lane == 0) p.tree_splits[blockIdx.x] = split;
         }
     }
 
@@ -1666,40 +1676,111 @@ __global__ void __launch_bounds__(128) paged_prefill_merge_kernel(const PrefillP
     for (int e = 0; e < PER_LANE; ++e) dst[e] = Elem<T>::from_f32(lsum > 0.f ? o[e] / lsum : 0.f);
 }
 
-// Log-sum-exp merge of the tree form's cut units: the unit that begins in CTA blockIdx.x's share and
-// goes on past it, from that CTA's slot and slot 0 of the CTAs behind.  One warp per row.
-constexpr int kTreeMergeWarps = 8;
-template <typename T>
-__global__ void __launch_bounds__(32 * kTreeMergeWarps) paged_tree_merge_kernel(const PrefillParams p) {
+// Log-sum-exp merge of the tree form's cut units, entry blockIdx.x of their table: a thread takes one row
+// and the eight channels 8 y (the loads of a warp's rows lie side by side; the sixteen blocks of a unit each
+// weigh the pieces for themselves).  Where units are few and cut into many, SHARES threads share a row's
+// pieces, so that their loads are one or two rounds, and join their sums in shared memory.  Measured with the
+// kernel before it, SHARES 4 / 1, 16 nodes of 32 / 8 heads, 4096 tokens: 1 context (17 pieces a unit) 15.1 /
+// 21.0 us, 2 contexts 18.9 / 20.5, 8 contexts (2.4 pieces) 43.2 / 35.7.
+template <typename T, int SHARES>
+__global__ void __launch_bounds__(128 * SHARES) paged_tree_merge_kernel(const PrefillParams p) {
     constexpr int D = 128;
-    pdl_wait();
-    const TreeSplit s = p.tree_splits[blockIdx.x];
-    if (s.pieces == 0) return;
-    const int lane = threadIdx.x & 31, r = blockIdx.y * kTreeMergeWarps + (threadIdx.x >> 5);
-    const int row = s.row_tile * p.tile_rows + r;
-    if (r >= p.tile_rows || row >= s.chunk * p.group) return;
-    auto seg = [&](int i) { return (2 * static_cast<int64_t>(blockIdx.x + i) + (i == 0 ? s.slot : 0)) * 128 + r; };
-    float mmax = -INFINITY;
-    for (int i = lane; i < s.pieces; i += 32) mmax = fmaxf(mmax, p.seg_m[seg(i)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mmax = fmaxf(mmax, __shfl_xor_sync(0xffffffffu, mmax, o));
-    float lsum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int i = 0; i < s.pieces; ++i) {
-        const int64_t at = seg(i);
-        const float m = p.seg_m[at], w = m == -INFINITY ? 0.f : fast_exp2(m - mmax);
-        const float4 v = *reinterpret_cast<const float4 *>(p.seg_o + at * D + 4 * lane);
-        lsum = fmaf(w, p.seg_l[at], lsum);
-        o[0] = fmaf(w, v.x, o[0]);
-        o[1] = fmaf(w, v.y, o[1]);
-        o[2] = fmaf(w, v.z, o[2]);
-        o[3] = fmaf(w, v.w, o[3]);
+    __shared__ float comb[SHARES > 1 ? SHARES - 1 : 1][10][128];
+    TreeSplit s{};
+    if (p.by_unit) {
+        const int seq = blockIdx.x / (p.num_kv_heads * p.row_tiles), unit = blockIdx.x - seq * (p.num_kv_heads * p.row_tiles);
+        s.kvh = unit / p.row_tiles;
+        s.row_tile = unit - s.kvh * p.row_tiles;
+        int len;
+        const PrefillSeqVals v{p.query_start[seq], p.query_start[seq + 1], p.context_lens[seq]};
+        // (a unit past its sequence's chunk has no entry)
+        if (!prefill_seq(p, v, s.q0, s.chunk, len) || s.row_tile * p.tile_tokens >= s.chunk) return;
+        pdl_wait();
+        const TreeSplit t = p.tree_splits[blockIdx.x];
+        s.pieces = t.pieces;
+        s.cta = t.cta;
+        s.slot = t.slot;
+    } else {
+        pdl_wait();
+        s = p.tree_splits[blockIdx.x];
     }
+    // (a kernel that gave up on a wait leaves entries unwritten)
+    if (s.pieces <= 0 || s.cta < 0 || s.cta >= p.seg_ctas || s.pieces > p.seg_ctas - s.cta || (s.slot & ~1)) return;
+    const int r = threadIdx.x & 127, share = threadIdx.x >> 7, row = s.row_tile * p.tile_rows + r;
+    const bool live = r < p.tile_rows && row < s.chunk * p.group;
+    const int mine = live && s.pieces > share ? (s.pieces - share + SHARES - 1) / SHARES : 0;
+    auto slot = [&](int i) {
+        i = share + SHARES * i;
+        return 2 * static_cast<int64_t>(s.cta + i) + (i == 0 ? s.slot : 0);
+    };
+    constexpr int kAhead = 4;  // pieces whose loads are in flight together
+    float4 v[kAhead][2];
+    float mv[kAhead], lv[kAhead];
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (i0 + u < mine) {
+                const int64_t at = slot(i0 + u);
+                const float4 *src = reinterpret_cast<const float4 *>(p.seg_o) + (at * 32 + 2 * blockIdx.y) * 128 + r;
+                v[u][0] = src[0];
+                v[u][1] = src[128];
+                mv[u] = p.seg_m[at * 128 + r];
+                lv[u] = p.seg_l[at * 128 + r];
+            }
+    };
+    float mmax = -INFINITY, lsum = 0.f, o[8] = {};
+    for (int i0 = 0; i0 < mine; i0 += kAhead) {
+        fetch(i0);
+        float m = mmax;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (i0 + u < mine) m = fmaxf(m, mv[u]);
+        if (m == -INFINITY) continue;
+        const float by = fast_exp2(mmax - m);  // 0 before the first
+        lsum *= by;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= by;
+        mmax = m;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (i0 + u >= mine) break;
+            const float w = fast_exp2(mv[u] - m);
+            lsum = fmaf(w, lv[u], lsum);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = fmaf(w, reinterpret_cast<const float *>(v[u])[e], o[e]);
+        }
+    }
+    if constexpr (SHARES > 1) {
+        if (share > 0) {
+            comb[share - 1][8][r] = mmax;
+            comb[share - 1][9][r] = lsum;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) comb[share - 1][e][r] = o[e];
+        }
+        __syncthreads();
+        if (share > 0) return;
+        float m = mmax;
+#pragma unroll
+        for (int w = 0; w < SHARES - 1; ++w) m = fmaxf(m, comb[w][8][r]);
+        const float by = mmax == -INFINITY ? 0.f : fast_exp2(mmax - m);
+        lsum *= by;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= by;
+#pragma unroll
+        for (int w = 0; w < SHARES - 1; ++w) {
+            const float mw = comb[w][8][r], bw = mw == -INFINITY ? 0.f : fast_exp2(mw - m);
+            lsum = fmaf(bw, comb[w][9][r], lsum);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = fmaf(bw, comb[w][e][r], o[e]);
+        }
+    }
+    if (!live) return;
     const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
     const int jtok = fast_div(row, p.div_group), g = row - jtok * p.group;
     const int64_t orow = (static_cast<int64_t>(s.q0) + jtok) * p.num_q_heads + s.kvh * p.group + g;
-    *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + orow * D + 4 * lane) =
-        make_uint2(Elem<T>::pack2(o[0] * inv, o[1] * inv), Elem<T>::pack2(o[2] * inv, o[3] * inv));
+    *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + orow * D + 8 * blockIdx.y) =
+        make_uint4(Elem<T>::pack2(o[0] * inv, o[1] * inv), Elem<T>::pack2(o[2] * inv, o[3] * inv),
+                   Elem<T>::pack2(o[4] * inv, o[5] * inv), Elem<T>::pack2(o[6] * inv, o[7] * inv));
 }
 
 }  // namespace pkv

@@ -177,6 +177,9 @@ PKV_API pkv_status pkv_paged_attention_tree(const void *q, const void *k_cache, 
     // one CTA per SM, or fewer where the contexts' bound leaves no more shares
     const int64_t most = (tiles * row_tiles * num_kv_heads * num_seqs + pkv::kMinShare - 1) / pkv::kMinShare;
     const int grid = static_cast<int>(std::min<int64_t>(most, sm));
+    p.row_tiles = static_cast<int>(row_tiles);
+    p.by_unit = row_tiles * num_kv_heads * num_seqs <= grid;
+    p.seg_ctas = sm;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return dtype == PKV_F16 ? pkv::launch_tree_f16(p, tq, tk, tv, to, block_size, grid, s)
                             : pkv::launch_tree_bf16(p, tq, tk, tv, to, block_size, grid, s);
