@@ -106,6 +106,15 @@ int scored_heads_per_block_for(int group, bool int8_kv) {
     const int most = int8_kv ? 8 : 16, blocks = (group + most - 1) / most, per = (group + blocks - 1) / blocks;
     return per <= 4 ? 4 : per <= 8 ? 8 : 16;
 }
+// The sink form over an INT8 cache, whose scores take two products per code (the query and its remainder):
+// the warp MMAs, with two or three of their four head rows empty, for two heads, and for one where a block's
+// rows of a head are 2 KB or more.  Measured, MMAs / lane loops, 16 x 4112 visible tokens of 32 KV heads of 64:
+// two heads 75.8 / 104 us; one head, blocks of 32 64.0 / 72.0, of 16 75.1 / 68.6, of 8 97.9 / 87.5;
+// 8 x 4112 of heads of 128, blocks of 16 53.1 / 56.2.
+int sink_heads_per_block_for(int group, bool int8_kv, int head_dim, int block_size) {
+    if (int8_kv && (group == 2 || (group == 1 && head_dim * block_size >= 2048))) return 4;
+    return scored_heads_per_block_for(group, int8_kv);
+}
 // Query heads per CTA: the largest of 16 (16-bit caches at head_dim 128), 8, 4, 2, 1
 // dividing the group (4 to 16 run the products as warp-level MMAs, 1 or 2 as
 // per-lane loops).
@@ -130,7 +139,7 @@ pkv_status plan_decode(int num_seqs, int num_q_heads, int num_kv_heads, int head
                        int block_size, int max_context_len, int partition_size, int sm_count,
                        bool int8_kv, int *out_partition_size, int *out_num_partitions,
                        int *out_heads_per_block, int *out_needs_merge, int resident = 0,
-                       bool scored = false) {
+                       bool scored = false, bool sinks = false) {
     if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
     if (block_size != 8 && block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_context_len < 0 ||
@@ -141,7 +150,9 @@ pkv_status plan_decode(int num_seqs, int num_q_heads, int num_kv_heads, int head
     const int max_partition = pkv::DecodeGeom<128, 16>::kMaxTableEntries * block_size;
     if (partition_size > max_partition) return PKV_ERR_INVALID_ARG;
     const int group = num_q_heads / num_kv_heads;
-    const int gh = scored ? scored_heads_per_block_for(group, int8_kv) : heads_per_block_for(group, int8_kv, head_dim);
+    const int gh = sinks    ? sink_heads_per_block_for(group, int8_kv, head_dim, block_size)
+                   : scored ? scored_heads_per_block_for(group, int8_kv)
+                            : heads_per_block_for(group, int8_kv, head_dim);
     const int64_t grid_y = static_cast<int64_t>(num_kv_heads) * ((group + gh - 1) / gh);
     if (grid_y > 65535 || num_seqs > 65535) return PKV_ERR_INVALID_ARG;
 
@@ -325,13 +336,14 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache,
     // Validate the shape first (no CUDA call), then plan for the real SM count.
     pkv_status plan = plan_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                                   span, partition_size, 1, int8_kv, &part, &nparts, &gh,
-                                  &merge, 0, scored != nullptr);
+                                  &merge, 0, scored != nullptr, scored && scored->sink_form);
     if (plan != PKV_OK) return plan;
     if (partition_size == 0) {
         const int sm = pkv::current_sm_count();
         if (sm <= 0) return PKV_ERR_CUDA;
         plan = plan_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
-                           span, 0, sm, int8_kv, &part, &nparts, &gh, &merge, 0, scored != nullptr);
+                           span, 0, sm, int8_kv, &part, &nparts, &gh, &merge, 0, scored != nullptr,
+                           scored && scored->sink_form);
         if (plan != PKV_OK) return plan;
     }
     const size_t need = scored_workspace(num_seqs, num_q_heads, head_dim, nparts, span, want_weights);
@@ -521,7 +533,7 @@ PKV_API size_t pkv_decode_sinks_workspace_bytes(int num_seqs, int num_q_heads, i
     int part = 0, nparts = 0, gh = 0, merge = 0;
     const int span = scored_span(max_context_len, window, block_size, sinks);
     if (plan_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, span, partition_size, sm, int8_cache != 0,
-                    &part, &nparts, &gh, &merge, 0, true) != PKV_OK)
+                    &part, &nparts, &gh, &merge, 0, true, true) != PKV_OK)
         return static_cast<size_t>(-1);
     return scored_workspace(num_seqs, num_q_heads, head_dim, nparts, span, false);
 }

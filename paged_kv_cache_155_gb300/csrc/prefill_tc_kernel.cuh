@@ -602,6 +602,13 @@ __device__ __forceinline__ void add_bf16x2(float &l0, float &l1, uint32_t v) {
         : "+f"(l0), "+f"(l1) : "r"(v));
 }
 
+// The same for two packed fp16 values (the sink and tree forms: a row of a few tokens behind a window or at
+// the head of a context is theirs to expect).
+__device__ __forceinline__ void add_f16x2(float &l0, float &l1, uint32_t v) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.f32.f16 %0, a, %0;\n\tadd.f32.f16 %1, b, %1;\n\t}"
+        : "+f"(l0), "+f"(l1) : "r"(v));
+}
+
 // z <- z R(z^2) - shift, R of N terms times cap_out.
 template <int N, typename F>
 __device__ __forceinline__ void cap_poly(const PrefillParams &p, F &&term, float (&z)[64]) {
@@ -1405,6 +1412,7 @@ __global__ void __launch_bounds__(384, 1)
                             }
                             packed[i] = Elem<T>::pack2(p0, p1);
                             if constexpr (kScored && kBF16) add_bf16x2(l0, l1, packed[i]);
+                            else if constexpr (kSinks || kTree) add_f16x2(l0, l1, packed[i]);
                             else add_f32x2(l0, l1, p0, p1);
                         }
                         tc::tmem_st_x16(pcol + 16 * c16, packed);
