@@ -69,9 +69,9 @@ typedef enum pkv_status {
 } pkv_status;
 
 /* PKV_INT8 names an INT8 cache, PKV_INT4 a 4-bit one; only pkv_copy_blocks takes
- * PKV_INT4 as `dtype`, and it and pkv_evict_compact PKV_INT8 (the entry points of
+ * PKV_INT4 as `dtype`, and it, pkv_evict_compact and pkv_tree_commit PKV_INT8 (3 is no type; the entry points of
  * these caches below take the query / new-row dtype, fp16 or bf16). */
-typedef enum pkv_dtype { PKV_F16 = 0, PKV_BF16 = 1, PKV_INT8 = 2, PKV_INT4 = 3 } pkv_dtype;
+typedef enum pkv_dtype { PKV_F16 = 0, PKV_BF16 = 1, PKV_INT8 = 2, PKV_INT4 = 4 } pkv_dtype;
 
 /* Flags of the device status word (bitwise OR of what the kernels saw). */
 #define PKV_DEVERR_SLOT        0x1u  /* slot_mapping entry >= num_blocks*block_size  */

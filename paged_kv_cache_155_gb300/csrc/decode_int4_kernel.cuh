@@ -141,6 +141,7 @@ __device__ __forceinline__ int int4_chunks(int len) { return max(1, (len + 31) /
 __device__ __forceinline__ int int4_share(const Int4Params &p, int workers, int &total) {
     const int lane = threadIdx.x & 31;
     total = 0;
+#pragma unroll 8
     for (int seq = lane; seq < p.num_seqs; seq += 32) total += int4_chunks(int4_len(p, seq));
     total = __reduce_add_sync(0xffffffffu, total) * p.units;
     return max(kInt4MinShare, (total + workers - 1) / workers);

@@ -1701,9 +1701,10 @@ __global__ void __launch_bounds__(128 * SHARES) paged_tree_merge_kernel(const Pr
         s.row_tile = unit - s.kvh * p.row_tiles;
         int len;
         const PrefillSeqVals v{p.query_start[seq], p.query_start[seq + 1], p.context_lens[seq]};
-        // (a unit past its sequence's chunk has no entry)
-        if (!prefill_seq(p, v, s.q0, s.chunk, len) || s.row_tile * p.tile_tokens >= s.chunk) return;
+        // (every block waits, so that this grid, and with it the call, ends after the one before it)
+        const bool there = prefill_seq(p, v, s.q0, s.chunk, len) && s.row_tile * p.tile_tokens < s.chunk;
         pdl_wait();
+        if (!there) return;  // a unit past its sequence's chunk has no entry
         const TreeSplit t = p.tree_splits[blockIdx.x];
         s.pieces = t.pieces;
         s.cta = t.cta;

@@ -24,7 +24,7 @@ import torch
 
 from ._lib import DEVERR, PagedKVError, lib
 
-F16, BF16, INT8, INT4 = 0, 1, 2, 3
+F16, BF16, INT8, INT4 = 0, 1, 2, 4
 _workspaces = {}
 
 
