@@ -10,7 +10,7 @@ namespace {
 constexpr int kWorkersPerCta = 4;
 
 struct Int4Plan {
-    int tiles = 1;     // column tiles of eight heads per block
+    int heads = 8;     // heads per block: 4, 8 or 16
     int blocks = 1;    // blocks of heads per KV head
     int resident = 3;  // CTAs per SM (DecodeInt4Geom::kResident)
 };
@@ -21,12 +21,13 @@ pkv_status plan_int4(int num_seqs, int num_q_heads, int num_kv_heads, int head_d
     if (block_size != 8 && block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || max_context_len < 0)
         return PKV_ERR_INVALID_ARG;
-    // the fewest blocks of at most 16 heads that cover the group, of 8 heads where these do
+    // the fewest blocks of at most 16 heads that cover the group, of 4 or 8 heads where these do
     const int group = num_q_heads / num_kv_heads;
     plan->blocks = (group + 15) / 16;
-    plan->tiles = (group + plan->blocks - 1) / plan->blocks <= 8 ? 1 : 2;
-    plan->blocks = (group + 8 * plan->tiles - 1) / (8 * plan->tiles);
-    plan->resident = plan->tiles == 1 ? (head_dim == 64 ? 4 : 3) : (head_dim == 64 ? 3 : 2);
+    const int each = (group + plan->blocks - 1) / plan->blocks;
+    plan->heads = each <= 4 ? 4 : each <= 8 ? 8 : 16;
+    plan->blocks = (group + plan->heads - 1) / plan->heads;
+    plan->resident = plan->heads <= 8 ? (head_dim == 64 ? 4 : 3) : (head_dim == 64 ? 3 : 2);
     // all units' chunks fit the kernel's 32-bit count
     const int64_t units = static_cast<int64_t>(num_kv_heads) * plan->blocks;
     const int64_t chunks = std::max<int64_t>(1, (max_context_len + 31LL) / 32);
@@ -38,7 +39,7 @@ pkv_status plan_int4(int num_seqs, int num_q_heads, int num_kv_heads, int head_d
 // Workspace: the partials of two pieces per worker, then what the merge has to know per worker.
 size_t workspace_of(const Int4Plan &plan, int head_dim, int sm_count) {
     const size_t workers = static_cast<size_t>(sm_count) * plan.resident * kWorkersPerCta;
-    return workers * (2 * 8 * plan.tiles * (static_cast<size_t>(head_dim) + 2) * sizeof(float) + sizeof(pkv::Int4Split));
+    return workers * (2 * plan.heads * (static_cast<size_t>(head_dim) + 2) * sizeof(float) + sizeof(pkv::Int4Split));
 }
 
 }  // namespace
@@ -87,7 +88,7 @@ PKV_API pkv_status pkv_paged_attention_decode_int4(const void *q, const void *k_
     p.k_cache = k_cache;
     p.v_cache = v_cache;
     p.out = out;
-    const size_t rows = static_cast<size_t>(sm) * plan.resident * kWorkersPerCta * 2 * 8 * plan.tiles;
+    const size_t rows = static_cast<size_t>(sm) * plan.resident * kWorkersPerCta * 2 * plan.heads;
     p.seg_o = static_cast<float *>(workspace);
     p.seg_m = p.seg_o + rows * head_dim;
     p.seg_l = p.seg_m + rows;
@@ -112,8 +113,8 @@ PKV_API pkv_status pkv_paged_attention_decode_int4(const void *q, const void *k_
     p.seg_workers = sm * plan.resident * kWorkersPerCta;
     p.by_unit = static_cast<int64_t>(num_seqs) * p.units <= static_cast<int64_t>(grid) * kWorkersPerCta;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return dtype == PKV_F16 ? pkv::launch_int4_f16(p, head_dim, block_size, plan.tiles, grid, s)
-                            : pkv::launch_int4_bf16(p, head_dim, block_size, plan.tiles, grid, s);
+    return dtype == PKV_F16 ? pkv::launch_int4_f16(p, head_dim, block_size, plan.heads, grid, s)
+                            : pkv::launch_int4_bf16(p, head_dim, block_size, plan.heads, grid, s);
 }
 
 }  // extern "C"

@@ -16,6 +16,12 @@
 //    tokens (S^T = K Q^T) or the channels (O^T = V^T P^T) as the 16 rows and eight query heads as the
 //    columns, for any group of heads: unused columns are zero.  Groups of more than eight heads take
 //    two column tiles on the same K and V fragments, so their codes are widened once.
+//  * Up to four heads take their columns twice (NT = 0, "paired"): a code word's two halves are groups
+//    2 i and 2 i + 1 of one unit, and as a fragment's pair of k indices they meet four columns that are zero in
+//    the odd k (group 2 i) and four that are zero in the even k (group 2 i + 1).  So words enter the MMAs
+//    as they lie, without the byte permutes that sort them by group, and a lane scales two groups instead of four:
+//    half the scales, weights and accumulators.  (64 x 4096 tokens of 32 / 8 heads 69 us, sorted words 78; 64 x 100 to
+//    2048 tokens of 32 heads of 64 61 and 65.)
 //  * Widening costs a mask: a nibble at bits 0 .. 3 or 4 .. 7 of a 16-bit word is a subnormal fp16
 //    number, exactly c 2^-24 or c 2^-20, and MMAs take those as they are (codes_f16).  K's factor 16
 //    between the two is in the query, V's is applied to the output channel, whose accumulator holds
@@ -33,8 +39,9 @@
 //    ahead; the ring runs on from one unit to the next.  A stage is one softmax step.
 //  * The token of an MMA row is chosen so that V's four token rows of a load lie side by side
 //    (token_of_row): two-way instead of four-way shared-memory conflicts.
-// Measured: 64 x 4096 tokens of 32 / 8 heads of 128, fp16: 76 us (0.65 of measured HBM; 0.77 per further
-// token, 11 us fixed); without the arithmetic 55 us, without the copies 68.
+// Measured: 64 x 4096 tokens of 32 / 8 heads of 128, fp16: 68 us (0.73 of measured HBM; 57 us, 0.87, per
+// 64 x 4096 further tokens, so 11 fixed); with eight columns and
+// sorted words it was 55 us without the arithmetic and 68 without the copies.
 #pragma once
 
 #include "decode_kernel.cuh"
@@ -51,10 +58,12 @@ struct DecodeInt4Geom {
     static constexpr int kRecord = int4_record_bytes(D, BS);       // a block's K (or V) rows of one head
     static constexpr int kHalfBytes = kBlocks * kRecord;           // 2560 at head_dim 128
     static constexpr int kStageBytes = 2 * kHalfBytes;
-    static constexpr int kResident = NT == 1 ? (D == 64 ? 4 : 3) : (D == 64 ? 3 : 2);  // CTAs per SM, by registers
+    static constexpr int kResident = NT <= 1 ? (D == 64 ? 4 : 3) : (D == 64 ? 3 : 2);  // CTAs per SM, by registers
     // about 180 KB of stages per SM: several times the bytes that cover the memory latency
     static constexpr int kStages = 46080 / kResident / kStageBytes;
-    static constexpr int kHeads = 8 * NT;
+    static constexpr int kHeads = NT == 0 ? 4 : 8 * NT;
+    static constexpr int kTiles = NT == 0 ? 1 : NT;               // column tiles
+    static constexpr int kLaneGroups = NT == 0 ? kGroups / 2 : kGroups;  // groups whose sums a lane holds
     static constexpr int kSmemBytes = kWarps * kStages * (kStageBytes + 8 + 4);
 };
 
@@ -151,6 +160,8 @@ template <typename T, int D, int BS, int NT>
 __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) paged_decode_int4_kernel(const Int4Params p) {
     using G = DecodeInt4Geom<D, BS, NT>;
     constexpr int NW = G::kWarps, S = G::kStages, NG = G::kGroups, SB = G::kBlocks, HEADS = G::kHeads;
+    constexpr int N = G::kTiles, GL = G::kLaneGroups;
+    constexpr bool kPaired = NT == 0;
     constexpr int ROW = int4_row_bytes(D), PAR = int4_param_bytes(D);
     constexpr bool kBF16 = !std::is_same<T, __half>::value;
     pdl_trigger();  // the merge behind this grid may be placed
@@ -158,6 +169,9 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
     extern __shared__ __align__(128) unsigned char smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int mg = lane >> 2, mt = lane & 3;
+    const int par = mt >> 1;  // paired: a lane's groups are 2 i + par; else group i
+    auto head_of = [&](int n, int e) { return kPaired ? 2 * (mt & 1) + e : 8 * n + 2 * mt + e; };  // of a lane's columns
+    auto group_of = [&](int i) { return kPaired ? 2 * i + par : i; };
     unsigned char *my_stages = smem + warp * S * G::kStageBytes;
     uint64_t *my_bars = reinterpret_cast<uint64_t *>(smem + NW * S * G::kStageBytes) + warp * S;
     uint32_t *my_good = reinterpret_cast<uint32_t *>(smem + NW * S * (G::kStageBytes + 8)) + warp * S;  // blocks of a stage that were copied
@@ -245,6 +259,8 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
     constexpr float kGrow = 6.f;  // the reference moves when a maximum exceeds it by more (log2 units)
     const int tau = token_of_row(mg);
     const int va = mt, vb = 4 + (mt ^ 1);  // V's tokens of a lane: rows 2 mt and 2 mt + 1
+    // paired: the low and the high weight of a transposed word, in the half of this column's groups
+    const uint32_t sel0 = mg >> 2 ? 0x1044u : 0x4410u, sel1 = mg >> 2 ? 0x3244u : 0x4432u;
     auto load_units = [](const unsigned char *src, uint32_t (&u0)[NG / 2], uint32_t (&u1)[NG / 2]) {
         if constexpr (NG == 4) {
             const uint4 u = *reinterpret_cast<const uint4 *>(src);
@@ -258,8 +274,11 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
             u1[0] = u.y;
         }
     };
-    auto load_params = [](const unsigned char *src, uint32_t (&w)[NG]) {
-        if constexpr (NG == 4) {
+    auto load_params = [&](const unsigned char *src, uint32_t (&w)[GL]) {
+        if constexpr (kPaired) {
+#pragma unroll
+            for (int j = 0; j < GL; ++j) w[j] = *reinterpret_cast<const uint32_t *>(src + 8 * j + 4 * par);
+        } else if constexpr (NG == 4) {
             const uint4 u = *reinterpret_cast<const uint4 *>(src);
             w[0] = u.x;
             w[1] = u.y;
@@ -286,43 +305,59 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
         const int hq0 = kvh * p.group + sub * HEADS;
         const int nheads = min(HEADS, p.group - sub * HEADS);
 
-        // ---- the query: lane (mg, mt) holds column (head) mg of every column tile at channels
-        //      32 j + 8 mt + 0 .. 7, the channels of a K row's units 2 mt and 2 mt + 1.  Scaled by a
-        //      power of two (its largest magnitude into [2^9, 2^10)), then odd nibbles' by 1/16.
-        uint32_t qb[NT][NG][4], zb[NT][2];  // zb: sum(q) per group, in 16-bit pieces along k
-        float hs[NT][2];                    // score scale of heads 2 mt, 2 mt + 1, log2 units
+        // ---- the query: lane (mg, mt) holds column mg of every column tile (paired: head mg % 4 in the groups
+        //      2 i + mg / 4) at channels 32 j + 8 mt + 0 .. 7, the channels of a K row's units 2 mt and 2 mt + 1.
+        //      Scaled by a power of two (a head's largest magnitude into [2^9, 2^10)), then odd nibbles' by 1/16.
+        uint32_t qb[N][NG][4], zb[N][2];  // zb: sum(q) per group, in 16-bit pieces along k
+        float hs[N][2];                    // score scale of heads 2 mt, 2 mt + 1, log2 units
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float f[NG][8];
-            const int h = 8 * n + mg;
+        for (int n = 0; n < N; ++n) {
+            float f[GL][8];
+            const int h = kPaired ? mg & 3 : 8 * n + mg;
+            const int col_par = mg >> 2;  // paired: this column's groups
             const T *qrow = static_cast<const T *>(p.q) + (static_cast<int64_t>(seq) * p.num_q_heads + hq0 + h) * D + 8 * mt;
             float amax = 0.f;
 #pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                const uint4 u = h < nheads ? *reinterpret_cast<const uint4 *>(qrow + 32 * j) : make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < GL; ++j) {
+                const uint4 u = h < nheads ? *reinterpret_cast<const uint4 *>(qrow + 32 * (kPaired ? 2 * j + col_par : j)) : make_uint4(0, 0, 0, 0);
                 Elem<T>::to_f32x8(u, f[j]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[j][e]));
             }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            if constexpr (kPaired) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
             const int qe = row_exponent(amax);
             const float down = exp2_int(-qe) * 1024.f;
             const float up = exp2_int(qe) * (p.scale_log2 / 1024.f);
             float sum[NG];
 #pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                sum[j] = 0.f;
+            for (int j = 0; j < GL; ++j) {
+                float t = 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float fe = e & 1 ? 0.0625f : 1.f;
                     const float a = f[j][e] * down, b = f[j][4 + e] * down;
                     float ra, rb;
-                    qb[n][j][e] = pack_mma2<false>(a * fe, b * fe, ra, rb);
-                    sum[j] += a + b;
+                    if constexpr (kPaired) {
+                        // the other groups' k index stays zero
+                        qb[n][2 * j][e] = col_par ? pack_mma2<false>(0.f, a * fe, ra, rb) : pack_mma2<false>(a * fe, 0.f, ra, rb);
+                        qb[n][2 * j + 1][e] = col_par ? pack_mma2<false>(0.f, b * fe, ra, rb) : pack_mma2<false>(b * fe, 0.f, ra, rb);
+                    } else {
+                        qb[n][j][e] = pack_mma2<false>(a * fe, b * fe, ra, rb);
+                    }
+                    t += a + b;
                 }
 #pragma unroll
-                for (int o = 1; o < 4; o <<= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
+                for (int o = 1; o < 4; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+                if constexpr (kPaired) {
+                    // the zeros' sums go into the first four columns, all groups' (the halves are added later)
+                    const float u = __shfl_xor_sync(0xffffffffu, t, 16);
+                    sum[2 * j] = col_par ? 0.f : t;
+                    sum[2 * j + 1] = col_par ? 0.f : u;
+                } else {
+                    sum[j] = t;
+                }
             }
             // k of the zeros' MMA: group pair (k / 2) % (NG / 2) of piece k / NG; the pieces of a sum are its
             // rounding to the MMA's type, that of the remainder, and (bf16) of what then remains
@@ -340,18 +375,18 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
                 b -= rb;
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) hs[n][e] = __shfl_sync(0xffffffffu, up, 4 * (2 * mt + e));
+            for (int e = 0; e < 2; ++e) hs[n][e] = __shfl_sync(0xffffffffu, up, 4 * (kPaired ? 2 * (mt & 1) + e : 2 * mt + e));
         }
 
-        // ---- accumulators: O^T m-tile (j, half) holds channels 32 j + 4 mg + 2 half (d0, d1) and + 1
-        //      (d2, d3) of heads 2 mt (d0, d2) and 2 mt + 1
-        float oacc[NT][NG][2][4], zacc[NT][NG][2], m[NT][2], l[NT][2];
+        // ---- accumulators: O^T m-tile (j, half) holds channels 32 group_of(j) + 4 mg + 2 half (d0, d1) and + 1
+        //      (d2, d3) of heads head_of(n, 0) (d0, d2) and head_of(n, 1)
+        float oacc[N][GL][2][4], zacc[N][GL][2], m[N][2], l[N][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < N; ++n) {
             m[n][0] = m[n][1] = -INFINITY;
             l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-            for (int j = 0; j < NG; ++j) {
+            for (int j = 0; j < GL; ++j) {
                 zacc[n][j][0] = zacc[n][j][1] = 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) oacc[n][j][0][e] = oacc[n][j][1][e] = 0.f;
@@ -384,10 +419,10 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
             const bool partial = vis != 0xffffffffu;
             const unsigned char *kst = my_stages + s * G::kStageBytes, *vst = kst + G::kHalfBytes;
             // ---- S^T = K Q^T, tokens 8 i + tau (octets i): per group its own accumulator, then the scales
-            float sc[4][NT][2];  // [octet][column tile][heads 2 mt, 2 mt + 1]
+            float sc[4][N][2];  // [octet][column tile][heads head_of(n, 0 and 1)]
 #pragma unroll
             for (int i2 = 0; i2 < 4; i2 += 2) {
-                uint32_t u0[2][NG / 2], u1[2][NG / 2], kp[2][NG];  // words of units 2 mt, 2 mt + 1; (scale, zero)
+                uint32_t u0[2][NG / 2], u1[2][NG / 2], kp[2][GL];  // words of units 2 mt, 2 mt + 1; (scale, zero)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const unsigned char *rec = octet(kst, i2 + r);
@@ -402,51 +437,65 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
                                                                      (NG == 4 ? 8 * (mt & 1) : 0));
                     z[r] = __byte_perm(w.x, w.y, 0x7632);
                 }
-                float sz[NT][4];
+                float sz[N][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                for (int n = 0; n < N; ++n) {
                     sz[n][0] = sz[n][1] = sz[n][2] = sz[n][3] = 0.f;
                     mma_16816<kBF16>(sz[n], z[0], z[1], z[0], z[1], zb[n][0], zb[n][1]);
                 }
-                float ss[NT][4];
+                float ss[N][4];
 #pragma unroll
-                for (int j = 0; j < NG; ++j) {
-                    uint32_t ra[4], rb[4];
-                    codes_f16(group_word<NG>(u0[0], u1[0], j), ra);
-                    codes_f16(group_word<NG>(u0[1], u1[1], j), rb);
+                for (int j = 0; j < GL; ++j) {
                     const float pa = Int4Param<T>::unpack(kp[0][j]).x, pb = Int4Param<T>::unpack(kp[1][j]).x;
+                    float a[N][4];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float a[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma_16816<false>(a, ra[0], rb[0], ra[1], rb[1], qb[n][j][0], qb[n][j][1]);
-                        mma_16816<false>(a, ra[2], rb[2], ra[3], rb[3], qb[n][j][2], qb[n][j][3]);
-                        // (scalar products here and below: packed ones would take a second copy of the scale, a
-                        // move on the busier integer pipe each)
+                    for (int n = 0; n < N; ++n) a[n][0] = a[n][1] = a[n][2] = a[n][3] = 0.f;
+#pragma unroll
+                    for (int x = 0; x < (kPaired ? 2 : 1); ++x) {
+                        uint32_t ra[4], rb[4];
+                        codes_f16(kPaired ? (x ? u1[0][j] : u0[0][j]) : group_word<NG>(u0[0], u1[0], j), ra);
+                        codes_f16(kPaired ? (x ? u1[1][j] : u0[1][j]) : group_word<NG>(u0[1], u1[1], j), rb);
+#pragma unroll
+                        for (int n = 0; n < N; ++n) {
+                            const uint32_t(&q)[4] = qb[n][kPaired ? 2 * j + x : j];
+                            mma_16816<false>(a[n], ra[0], rb[0], ra[1], rb[1], q[0], q[1]);
+                            mma_16816<false>(a[n], ra[2], rb[2], ra[3], rb[3], q[2], q[3]);
+                        }
+                    }
+                    // (scalar products here and below: packed ones would take a second copy of the scale, a
+                    // move on the busier integer pipe each)
+#pragma unroll
+                    for (int n = 0; n < N; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float by = e < 2 ? pa : pb;
-                            ss[n][e] = j == 0 ? a[e] * by : fmaf(a[e], by, ss[n][e]);
+                            ss[n][e] = j == 0 ? a[n][e] * by : fmaf(a[n][e], by, ss[n][e]);
                         }
-                    }
                 }
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                for (int n = 0; n < N; ++n) {
                     constexpr float kUnit = 16777216.f;  // 2^24: the codes' unit
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[i2 + e / 2][n][e & 1] = fmaf(ss[n][e], kUnit, sz[n][e]);
+                    for (int e = 0; e < 4; ++e) {
+                        float x = fmaf(ss[n][e], kUnit, sz[n][e]);
+                        if constexpr (kPaired) x += __shfl_xor_sync(0xffffffffu, x, 2);  // the other groups'
+                        sc[i2 + e / 2][n][e & 1] = x;
+                    }
                 }
             }
             // ---- V's (scale, zero) pairs; hidden tokens' do not count, whatever their rows hold (stale
             //      bytes, NaN scales)
-            uint32_t vp[4][NG];
+            uint32_t vp[4][GL];
 #pragma unroll
             for (int i = 0; i < 4; ++i) load_params(octet(vst, i) + BS * ROW + (first_row(i) + tau) * PAR, vp[i]);
             // log2 of each token's largest V scale; the clamp keeps p (at most 2^-e) in range
             float ev[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t most = max_scale<T>(vp[i][0], vp[i][1]);
-                if constexpr (NG == 4) most = max_scale<T>(most, max_scale<T>(vp[i][2], vp[i][3]));
+                uint32_t most = vp[i][0];
+#pragma unroll
+                for (int j = 1; j < GL; ++j) most = max_scale<T>(most, vp[i][j]);
+                if constexpr (kPaired) most = max_scale<T>(most, __shfl_xor_sync(0xffffffffu, most, 2));
                 ev[i] = fmaxf(fast_log2(Int4Param<T>::unpack(most).x), -40.f);
             }
             if (partial) {
@@ -455,15 +504,15 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
                     if ((vis >> (8 * i + tau)) & 1u) continue;
                     ev[i] = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < NG; ++j) vp[i][j] = 0u;
+                    for (int j = 0; j < GL; ++j) vp[i][j] = 0u;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) sc[i][n][0] = sc[i][n][1] = 0.f;
+                    for (int n = 0; n < N; ++n) sc[i][n][0] = sc[i][n][1] = 0.f;
                 }
             }
-            float mx[NT][2];
+            float mx[N][2];
             bool grow = false;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
+            for (int n = 0; n < N; ++n) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float v = -INFINITY;
@@ -477,7 +526,7 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
             }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                for (int n = 0; n < N; ++n) {
                     float a[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -489,7 +538,7 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
                         l[n][e] *= a[e];
                     }
 #pragma unroll
-                    for (int j = 0; j < NG; ++j) {
+                    for (int j = 0; j < GL; ++j) {
                         zacc[n][j][0] *= a[0];
                         zacc[n][j][1] *= a[1];
 #pragma unroll
@@ -502,7 +551,7 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
             }
             // ---- weights
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < N; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float ref = m[n][e] == -INFINITY ? 0.f : m[n][e];
@@ -514,11 +563,11 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
                 for (int i = 0; i < 4; ++i)
                     if (!((vis >> (8 * i + tau)) & 1u)) {
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) sc[i][n][0] = sc[i][n][1] = 0.f;
+                        for (int n = 0; n < N; ++n) sc[i][n][0] = sc[i][n][1] = 0.f;
                     }
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < N; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) l[n][e] += (sc[0][n][e] + sc[1][n][e]) + (sc[2][n][e] + sc[3][n][e]);
             // ---- O^T += V^T P^T, 16 tokens at a time: the weights times a group's scales in the B layout,
@@ -538,23 +587,44 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
                         v[r][0] = *reinterpret_cast<const uint32_t *>(src);
                     }
                 }
+                if constexpr (kPaired) {
+                    // an octet per MMA: its tokens take two k indices each, one per group of the word
 #pragma unroll
-                for (int j = 0; j < NG; ++j) {
-                    uint32_t ra[4], rb[4];
-                    codes_f16_bytes(group_word<NG>(v[0], v[1], j), ra);
-                    codes_f16_bytes(group_word<NG>(v[2], v[3], j), rb);
-                    const float2 s0 = Int4Param<T>::unpack(vp[i2][j]), s1 = Int4Param<T>::unpack(vp[i2 + 1][j]);
+                    for (int r = 0; r < 2; ++r)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const __half2 ha = __floats2half2_rn(sc[i2][n][0] * s0.x, sc[i2][n][1] * s0.x);
-                        const __half2 hb = __floats2half2_rn(sc[i2 + 1][n][0] * s1.x, sc[i2 + 1][n][1] * s1.x);
-                        const uint32_t b0 = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&ha));
-                        const uint32_t b1 = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&hb));
+                        for (int j = 0; j < GL; ++j) {
+                            const int i = i2 + r;
+                            uint32_t ra[4], rb[4];
+                            codes_f16_bytes(v[2 * r][j], ra);
+                            codes_f16_bytes(v[2 * r + 1][j], rb);
+                            const float2 sz = Int4Param<T>::unpack(vp[i][j]);
+                            const __half2 h = __floats2half2_rn(sc[i][0][0] * sz.x, sc[i][0][1] * sz.x);
+                            const uint32_t w = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&h));
+                            const uint32_t b0 = __byte_perm(w, 0u, sel0), b1 = __byte_perm(w, 0u, sel1);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            zacc[n][j][e] = fmaf(sc[i2 + 1][n][e], s1.y, fmaf(sc[i2][n][e], s0.y, zacc[n][j][e]));
-                        mma_16816<false>(oacc[n][j][0], ra[0], ra[1], rb[0], rb[1], b0, b1);
-                        mma_16816<false>(oacc[n][j][1], ra[2], ra[3], rb[2], rb[3], b0, b1);
+                            for (int e = 0; e < 2; ++e) zacc[0][j][e] = fmaf(sc[i][0][e], sz.y, zacc[0][j][e]);
+                            mma_16816<false>(oacc[0][j][0], ra[0], ra[1], rb[0], rb[1], b0, b1);
+                            mma_16816<false>(oacc[0][j][1], ra[2], ra[3], rb[2], rb[3], b0, b1);
+                        }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < GL; ++j) {
+                        uint32_t ra[4], rb[4];
+                        codes_f16_bytes(group_word<NG>(v[0], v[1], j), ra);
+                        codes_f16_bytes(group_word<NG>(v[2], v[3], j), rb);
+                        const float2 s0 = Int4Param<T>::unpack(vp[i2][j]), s1 = Int4Param<T>::unpack(vp[i2 + 1][j]);
+#pragma unroll
+                        for (int n = 0; n < N; ++n) {
+                            const __half2 ha = __floats2half2_rn(sc[i2][n][0] * s0.x, sc[i2][n][1] * s0.x);
+                            const __half2 hb = __floats2half2_rn(sc[i2 + 1][n][0] * s1.x, sc[i2 + 1][n][1] * s1.x);
+                            const uint32_t b0 = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&ha));
+                            const uint32_t b1 = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&hb));
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                zacc[n][j][e] = fmaf(sc[i2 + 1][n][e], s1.y, fmaf(sc[i2][n][e], s0.y, zacc[n][j][e]));
+                            mma_16816<false>(oacc[n][j][0], ra[0], ra[1], rb[0], rb[1], b0, b1);
+                            mma_16816<false>(oacc[n][j][1], ra[2], ra[3], rb[2], rb[3], b0, b1);
+                        }
                     }
                 }
             }
@@ -573,16 +643,16 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
         const bool whole = chunk == 0 && end == chunks;
         const int64_t slot = (2 * static_cast<int64_t>(worker) + (first_piece ? 0 : 1)) * HEADS;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < N; ++n) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int h = 8 * n + 2 * mt + e;
+                const int h = head_of(n, e);
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
                 const float norm = !whole ? 1.f : l[n][e] > 0.f ? 1.f / l[n][e] : 0.f;
                 const int64_t row = static_cast<int64_t>(seq) * p.num_q_heads + hq0 + h;
 #pragma unroll
-                for (int j = 0; j < NG; ++j) {
+                for (int j = 0; j < GL; ++j) {
                     float z = zacc[n][j][e];
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
@@ -592,10 +662,10 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
                     const float r2 = fmaf(oacc[n][j][1][e] - oacc[n][j][1][2 + e], kEven, z) * norm, r3 = fmaf(oacc[n][j][1][2 + e], kOdd, z) * norm;
                     if (h >= nheads) continue;
                     if (whole)
-                        *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + row * D + 32 * j + 4 * mg) =
+                        *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + row * D + 32 * group_of(j) + 4 * mg) =
                             make_uint2(Elem<T>::pack2(r0, r1), Elem<T>::pack2(r2, r3));
                     else
-                        *reinterpret_cast<float4 *>(p.seg_o + (slot + h) * D + 32 * j + 4 * mg) = make_float4(r0, r1, r2, r3);
+                        *reinterpret_cast<float4 *>(p.seg_o + (slot + h) * D + 32 * group_of(j) + 4 * mg) = make_float4(r0, r1, r2, r3);
                 }
                 if (!whole && mg == 0 && h < nheads) {
                     p.seg_m[slot + h] = m[n][e];

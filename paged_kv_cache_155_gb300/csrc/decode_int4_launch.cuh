@@ -42,25 +42,29 @@ pkv_status launch_int4_bs(const Int4Params &p, int block_size, int grid, cudaStr
     return PKV_ERR_UNSUPPORTED;
 }
 
-// tiles: column tiles of eight heads per block (1 or 2); grid CTAs, then the merge of the units that
+// heads per block: 4 (paired), 8 or 16 (one or two column tiles); grid CTAs, then the merge of the units that
 // their workers cut.
 template <typename T>
-pkv_status launch_int4_typed(const Int4Params &p, int head_dim, int block_size, int tiles, int grid, cudaStream_t s) {
+pkv_status launch_int4_typed(const Int4Params &p, int head_dim, int block_size, int heads_per_block, int grid, cudaStream_t s) {
     pkv_status st;
     if (head_dim == 128)
-        st = tiles == 1 ? launch_int4_bs<T, 128, 1>(p, block_size, grid, s) : launch_int4_bs<T, 128, 2>(p, block_size, grid, s);
+        st = heads_per_block == 4   ? launch_int4_bs<T, 128, 0>(p, block_size, grid, s)
+             : heads_per_block == 8 ? launch_int4_bs<T, 128, 1>(p, block_size, grid, s)
+                                    : launch_int4_bs<T, 128, 2>(p, block_size, grid, s);
     else
-        st = tiles == 1 ? launch_int4_bs<T, 64, 1>(p, block_size, grid, s) : launch_int4_bs<T, 64, 2>(p, block_size, grid, s);
+        st = heads_per_block == 4   ? launch_int4_bs<T, 64, 0>(p, block_size, grid, s)
+             : heads_per_block == 8 ? launch_int4_bs<T, 64, 1>(p, block_size, grid, s)
+                                    : launch_int4_bs<T, 64, 2>(p, block_size, grid, s);
     if (st != PKV_OK) return st;
     // units cut into many pieces: four warps share a head's
     const int64_t units = static_cast<int64_t>(p.num_seqs) * p.units;
     const bool shared = p.by_unit && grid * 4 >= 16 * units;
     auto merge = head_dim == 128 ? (shared ? paged_decode_int4_merge_kernel<T, 128, 4> : paged_decode_int4_merge_kernel<T, 128, 1>)
                                  : (shared ? paged_decode_int4_merge_kernel<T, 64, 4> : paged_decode_int4_merge_kernel<T, 64, 1>);
-    const int heads = std::min(p.group, 8 * tiles);
+    const int heads = std::min(p.group, heads_per_block);
     const dim3 blocks(static_cast<unsigned>(p.by_unit ? units : grid * 4),
                       static_cast<unsigned>(shared ? heads : p.by_unit ? (heads + 3) / 4 : 1));
-    if (launch_kernel(merge, blocks, dim3(128), 0, s, true, p, 8 * tiles) != cudaSuccess) {
+    if (launch_kernel(merge, blocks, dim3(128), 0, s, true, p, heads_per_block) != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
     }
@@ -68,7 +72,7 @@ pkv_status launch_int4_typed(const Int4Params &p, int head_dim, int block_size, 
     return launch_status();
 }
 
-pkv_status launch_int4_f16(const Int4Params &p, int head_dim, int block_size, int tiles, int grid, cudaStream_t s);
-pkv_status launch_int4_bf16(const Int4Params &p, int head_dim, int block_size, int tiles, int grid, cudaStream_t s);
+pkv_status launch_int4_f16(const Int4Params &p, int head_dim, int block_size, int heads_per_block, int grid, cudaStream_t s);
+pkv_status launch_int4_bf16(const Int4Params &p, int head_dim, int block_size, int heads_per_block, int grid, cudaStream_t s);
 
 }  // namespace pkv

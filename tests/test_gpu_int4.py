@@ -166,7 +166,8 @@ def s_max(pool, table, n, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("hq,hkv,d,bs", [(1, 1, 64, 8), (4, 4, 128, 16), (8, 1, 128, 8), (32, 4, 128, 32), (12, 4, 64, 16),
-                                         (16, 1, 128, 16), (40, 2, 64, 32), (36, 1, 128, 8), (13, 1, 64, 8), (128, 8, 128, 16)])
+                                         (16, 1, 128, 16), (40, 2, 64, 32), (36, 1, 128, 8), (13, 1, 64, 8), (128, 8, 128, 16),
+                                         (32, 8, 128, 16), (6, 3, 128, 8), (3, 1, 128, 32)])
 @pytest.mark.parametrize("more", [0, 1500])
 def test_decode(hq, hkv, d, bs, dtype, more):
     dev, g = device(), torch.Generator().manual_seed(hq * 7 + d + bs)
