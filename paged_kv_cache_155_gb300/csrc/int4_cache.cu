@@ -195,7 +195,7 @@ PKV_API pkv_status pkv_reshape_and_cache_int4(const void *k_new, const void *v_n
                                               int block_size, pkv_dtype dtype, void *stream) {
     if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
     if (!supported_shape(head_dim, block_size)) return PKV_ERR_UNSUPPORTED;
-    if (num_tokens < 0 || num_kv_heads <= 0 || num_kv_heads > 65535 || num_blocks <= 0 || num_tokens > 0x7fffffffLL / num_kv_heads)
+    if (num_tokens < 0 || num_kv_heads <= 0 || num_kv_heads > 65535 || num_blocks <= 0 || num_tokens > 0x7fffff00LL / num_kv_heads)
         return PKV_ERR_INVALID_ARG;
     const int64_t half = static_cast<int64_t>(num_kv_heads) * pkv::int4_record_bytes(head_dim, block_size);
     if (block_stride_bytes < half || block_stride_bytes % 16) return PKV_ERR_INVALID_ARG;
