@@ -263,7 +263,7 @@ PKV_API pkv_status pkv_paged_attention_decode_int8(
  * calibrated.  The 32 channels of group j of one token and KV head are stored as
  *     zero z  = their smallest value (exact in the rows' type),
  *     scale s = (largest - smallest) / 15, rounded up to the rows' type,
- *     codes c = the integer nearest to (x - z) / s, ties to even, 0 when s = 0,
+ *     codes c = the integer nearest to (x - z) / s (x - z in fp32), ties to even, 0 when s = 0,
  * and read back as s * c + z: a value is off by s / 2 at most.  Values must be
  * finite (a NaN gets code 0, a group with an infinity reads back as NaN).
  * The pool is bytes, [num_blocks][2][num_kv_heads][block_size * head_dim * 5 / 8]:

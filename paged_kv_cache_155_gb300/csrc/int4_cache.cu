@@ -9,100 +9,111 @@
 
 namespace {
 
-// The nearest code of a value d above its group's zero, as a float, ties to the even code: the
-// quotient by an approximate reciprocal is off by less than one code, and the remainder d - r s,
-// exact in one FMA, says whether the next code is nearer.  (16-bit values often lie exactly halfway,
-// so the remainder decides, not the rounded quotient.)  A remainder of half a step moves an odd code
-// only: even codes compare with the next float above it.  Adding 1.5 * 2^23 rounds to nearest and
-// shows the code's last bit.  A NaN gets 0.
-__device__ __forceinline__ float int4_code(float d, float s, float rcp, float half_odd, float half_even) {
-    d = fmaxf(d, 0.f);
-    const float t = fmaf(d, rcp, 12582912.f);
-    const float r = t - 12582912.f;
-    const float e = fmaf(-r, s, d);
-    const float half = __float_as_uint(t) & 1u ? half_odd : half_even;
-    return fabsf(e) >= half ? r + copysignf(1.f, e) : r;
-}
-
-// Four codes as floats -> one 16-bit word, the first in its low nibble.
-__device__ __forceinline__ uint32_t int4_word(const float *c) {
-    const float v = fmaf(fmaf(fmaf(c[3], 16.f, c[2]), 16.f, c[1]), 16.f, c[0]);  // < 2^16, exact
-    return __float_as_uint(v + 8388608.f) & 0xffffu;
-}
-
-// (smallest, largest) of a group's 32 values, 8 in each of four lanes, packed in the rows' type; NaNs lose.
-template <typename T>
-__device__ __forceinline__ void int4_range(const uint4 &row, float &lo, float &hi) {
+// The low half: a group's smallest value, the high half: its largest one's negative; 16 values in each of
+// two lanes, packed in the rows' type.  A NaN among them comes through (kNan) or loses.
+template <typename T, bool kNan>
+__device__ __forceinline__ float2 int4_range(const uint4 (&row)[2]) {
     using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
-    const T2 *v = reinterpret_cast<const T2 *>(&row);
-    const T2 least = __hmin2(__hmin2(v[0], v[1]), __hmin2(v[2], v[3]));
-    const T2 most = __hmax2(__hmax2(v[0], v[1]), __hmax2(v[2], v[3]));
-    // the smallest value in the low half, the largest one's negative in the high half
-    T2 m;
-    m.x = __hmin(least.x, least.y);
-    m.y = __hneg(__hmax(most.x, most.y));
+    auto least = [](T2 a, T2 b) { return kNan ? __hmin2_nan(a, b) : __hmin2(a, b); };
+    auto most = [](T2 a, T2 b) { return kNan ? __hmax2_nan(a, b) : __hmax2(a, b); };
+    const T2 *v = reinterpret_cast<const T2 *>(row);
+    T2 lo = v[0], hi = v[0];
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t *>(&m), o);
-        m = __hmin2(m, *reinterpret_cast<const T2 *>(&other));
-    }
-    const float2 f = pkv::Int4Param<T>::unpack(*reinterpret_cast<const uint32_t *>(&m));
-    lo = f.x;
-    hi = -f.y;
+    for (int e = 1; e < 8; ++e) lo = least(lo, v[e]), hi = most(hi, v[e]);
+    T2 m;
+    m.x = kNan ? __hmin_nan(lo.x, lo.y) : __hmin(lo.x, lo.y);
+    m.y = __hneg(kNan ? __hmax_nan(hi.x, hi.y) : __hmax(hi.x, hi.y));
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t *>(&m), 1);
+    m = least(m, *reinterpret_cast<const T2 *>(&other));
+    return pkv::Int4Param<T>::unpack(*reinterpret_cast<const uint32_t *>(&m));
 }
 
-// Quantises the 8 channels 8 i .. 8 i + 7 of a group whose four lanes call together: the
-// two 16-bit code words of its units 2 i and 2 i + 1, and the group's (s, z) word.
+// The smallest scale with 15 s >= hi - lo, as bits: a number of the type that is surely not above it, then
+// up while 15 s (exact) is too small.
 template <typename T>
-__device__ __forceinline__ void int4_quantise(const uint4 &row, uint32_t &unit0, uint32_t &unit1, uint32_t &param) {
-    float f[8], lo, hi;
-    pkv::Elem<T>::to_f32x8(row, f);
-    int4_range<T>(row, lo, hi);
-    // the smallest scale with 15 s >= hi - lo: a number of the type that is surely not above it, then
-    // up while 15 s (exact) is too small
+__device__ __forceinline__ uint32_t int4_scale(float lo, float hi) {
     const float range = __fsub_ru(hi, lo);
     uint32_t sb = pkv::Int4Param<T>::scale_down(range * 0.06666663f);
     if (15.f * pkv::Int4Param<T>::value(sb) < range) ++sb;
     if (15.f * pkv::Int4Param<T>::value(sb) < range) ++sb;
-    const float s = pkv::Int4Param<T>::value(sb);
-    param = sb | (pkv::Int4Param<T>::bits(lo) << 16);
-    // scales whose reciprocal would overflow or vanish (zero among them) take the division
-    const bool in_range = __float_as_uint(s) - 0x0d800000u < 0x64000000u;  // 2^-100 <= s < 2^100
-    float c[8];
-    if (__all_sync(0xffffffffu, in_range)) {
-        const float rcp = pkv::fast_rcp(s), half = 0.5f * s, above = half * 1.00000012f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = int4_code(f[e] - lo, s, rcp, half, above);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = fminf(fmaxf(rintf(__fdiv_rn(f[e] - lo, s)), 0.f), 15.f);
-    }
-    unit0 = int4_word(c);
-    unit1 = int4_word(c + 4);
+    return sb;
 }
 
-// A thread quantises 8 channels of one row of K and of V; the rows of a token and then the
-// tokens follow one another.  Lanes 4 j + i hold channels 8 i .. of group j; lanes of groups j and
-// j ^ 1 trade a word, so that each stores one 32-bit word of codes (a row's are contiguous).  Bound by
-// arithmetic, some 13 operations a value: 8192 tokens of 8 heads of 128, bf16 15.3 us (with packed
-// minima, one FMA per rounding and codes packed by FMAs; with a division, conversions and a CTA per token 22 us).
-constexpr int kWriteThreads = 256;
+// Four codes, each in the low bits of a word whose other low bits are zero -> one 16-bit word, the first in
+// its low nibble (the bits above are not cleared).
+__device__ __forceinline__ uint32_t int4_word(const uint32_t *c) {
+    return c[0] + 16u * c[1] + 256u * c[2] + 4096u * c[3];
+}
+
+// Quantises the 16 channels 16 i .. 16 i + 15 of a group whose two lanes call together: the 16-bit code
+// words of its units 4 i .. 4 i + 3 in two registers, and the group's (s, z) word.
+//
+// A code is the quotient d / s, d = x - z in fp32, rounded to fp32 and then to an integer, ties to even.  The quotient
+// comes from an approximate reciprocal, a remainder d - q s (exact in one FMA) and one correction, and is
+// d / s (1 + 2^-46) before its rounding: a tie (k + 1/2) s = d gives k + 1/2 itself.  No other d rounds to a
+// tie: s has 11 bits at most, so (k + 1/2) s is a fp32 number like d, and they differ by a step of d, which
+// is more than half a step of fp32 at k + 1/2 by the factor 2 / m with the mantissa m <= 2 - 2^-10 of s.  Adding
+// 1.5 * 2^23 rounds to an integer and leaves it in the low bits.
+template <typename T>
+__device__ __forceinline__ void int4_quantise(const uint4 (&row)[2], uint32_t (&unit)[2], uint32_t &param) {
+    float2 r = int4_range<T, true>(row);
+    uint32_t sb = int4_scale<T>(r.x, -r.y);
+    float s = pkv::Int4Param<T>::value(sb), f[16];
+    pkv::Elem<T>::to_f32x8(row[0], *reinterpret_cast<float(*)[8]>(f));
+    pkv::Elem<T>::to_f32x8(row[1], *reinterpret_cast<float(*)[8]>(f + 8));
+    uint32_t c[16];
+    // 2^-100 <= s < 2^100 or 0; a scale whose reciprocal would overflow or vanish, infinite or NaN, takes the division
+    const bool in_range = s == 0.f || __float_as_uint(s) - 0x0d800000u < 0x64000000u;
+    if (__all_sync(0xffffffffu, in_range)) {
+        const float by = s == 0.f ? 0.f : pkv::fast_rcp(s);
+        const pkv::F32x2 minus_z = pkv::pack_f32(-r.x, -r.x), rcp = pkv::pack_f32(by, by), minus_s = pkv::pack_f32(-s, -s),
+                         round = pkv::pack_f32(12582912.f, 12582912.f);
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+            const pkv::F32x2 d = pkv::add2(pkv::pack_f32(f[e], f[e + 1]), minus_z), q = pkv::mul2(d, rcp);
+            const pkv::F32x2 t = pkv::add2(pkv::fma2(pkv::fma2(q, minus_s, d), rcp, q), round);
+            float t0, t1;
+            pkv::unpack_f32(t, t0, t1);
+            c[e] = __float_as_uint(t0);
+            c[e + 1] = __float_as_uint(t1);
+        }
+    } else {
+        r = int4_range<T, false>(row);
+        sb = int4_scale<T>(r.x, -r.y);
+        s = pkv::Int4Param<T>::value(sb);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) c[e] = static_cast<uint32_t>(fminf(fmaxf(rintf(__fdiv_rn(f[e] - r.x, s)), 0.f), 15.f));
+    }
+    param = sb | (pkv::Int4Param<T>::bits(r.x) << 16);
+    unit[0] = __byte_perm(int4_word(c), int4_word(c + 4), 0x5410);
+    unit[1] = __byte_perm(int4_word(c + 8), int4_word(c + 12), 0x5410);
+}
+
+// A thread quantises 16 channels of one row of K and of V; the rows of a token and then the tokens follow one
+// another.  Lanes 2 j + i hold channels 16 i .. of group j; the lanes of a row's groups trade words, so
+// that each stores eight bytes side by side (all groups of a unit, or of two).  Bound by arithmetic:
+// 8192 tokens of 8 heads of 128, bf16 8.3 us, 0.78 of measured HBM (with eight channels per lane and the remainder's comparison instead
+// of the quotient's correction 15.3, with a division and a CTA per token 22).
+constexpr int kWriteThreads = 128;
 template <typename T, int D>
 __global__ void __launch_bounds__(kWriteThreads) reshape_and_cache_int4_kernel(
     const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new, const int64_t *__restrict__ slot_mapping,
     char *__restrict__ k_cache, char *__restrict__ v_cache, int64_t num_slots, int64_t block_stride, int num_rows,
-    int num_kv_heads, int block_shift, unsigned int *status) {
-    constexpr int LANES = D / 8, NG = D / 32;
+    int num_kv_heads, pkv::FastDiv div_kv_heads, int block_shift, unsigned int *status) {
+    constexpr int LANES = D / 16;
     const int row = blockIdx.x * (kWriteThreads / LANES) + threadIdx.x / LANES;  // token * num_kv_heads + head
-    const int lane = threadIdx.x % LANES, j = lane / 4, u = 2 * (lane % 4);
+    const int lane = threadIdx.x % LANES, j = lane / 2, i = lane % 2;
     const bool there = row < num_rows;
-    uint4 x[2] = {};
+    uint4 x[2][2] = {};
     int64_t slot = -1;
-    const int n = row / num_kv_heads, h = row - n * num_kv_heads;
+    const int n = pkv::fast_div(row, div_kv_heads), h = row - n * num_kv_heads;
     if (there) {
-        x[0] = k_new[static_cast<int64_t>(row) * LANES + lane];
-        x[1] = v_new[static_cast<int64_t>(row) * LANES + lane];
+        const int64_t at = static_cast<int64_t>(row) * (D / 8) + 2 * lane;
         slot = slot_mapping[n];
+        x[0][0] = k_new[at];
+        x[0][1] = k_new[at + 1];
+        x[1][0] = v_new[at];
+        x[1][1] = v_new[at + 1];
     }
     if (slot >= num_slots) {
         if (h == 0 && lane == 0) pkv::raise_flag(status, PKV_DEVERR_SLOT);
@@ -110,17 +121,26 @@ __global__ void __launch_bounds__(kWriteThreads) reshape_and_cache_int4_kernel(
     }
     const int bs = 1 << block_shift, off = static_cast<int>(slot) & (bs - 1);
     const int64_t at = (slot >> block_shift) * block_stride + static_cast<int64_t>(h) * pkv::int4_record_bytes(D, bs);
+    const bool odd = j & 1, upper = j & 2;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        uint32_t unit0, unit1, param;
-        int4_quantise<T>(x[half], unit0, unit1, param);
-        const bool odd = j & 1;
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? unit0 : unit1, 4);
-        const uint32_t word = odd ? (other | (unit1 << 16)) : (unit0 | (other << 16));
+        uint32_t unit[2], param;
+        int4_quantise<T>(x[half], unit, param);
+        // units 4 i + 2 odd, + 1 of groups j & ~1, j | 1
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? unit[0] : unit[1], 2);
+        const uint32_t even_group = odd ? other : unit[0], odd_group = odd ? unit[1] : other;
+        uint2 w = make_uint2(__byte_perm(even_group, odd_group, 0x5410), __byte_perm(even_group, odd_group, 0x7632));
+        int place = (4 * i + 2 * odd) * 4;
+        if constexpr (D == 128) {
+            // unit 4 i + 2 odd + upper of all groups
+            const uint32_t from = __shfl_xor_sync(0xffffffffu, upper ? w.x : w.y, 4);
+            w = upper ? make_uint2(from, w.y) : make_uint2(w.x, from);
+            place = (4 * i + 2 * odd + upper) * 8;
+        }
         if (slot >= 0) {
             char *base = (half ? v_cache : k_cache) + at;
-            *reinterpret_cast<uint32_t *>(base + off * (D / 2) + ((u + odd) * NG + (j & ~1)) * 2) = word;
-            if (u == 0) *reinterpret_cast<uint32_t *>(base + bs * (D / 2) + off * (D / 8) + j * 4) = param;
+            *reinterpret_cast<uint2 *>(base + off * (D / 2) + place) = w;
+            if (i == 0) *reinterpret_cast<uint32_t *>(base + bs * (D / 2) + off * (D / 8) + j * 4) = param;
         }
     }
 }
@@ -129,7 +149,7 @@ constexpr int kReadThreads = 256;
 constexpr int kReadDepth = 4;  // vectors of a thread in flight
 
 // grid.x = pair, grid.y = chunk of a half block's vectors, grid.z = K (0) / V (1); a
-// thread writes 8 channels (16 bytes) of a row, lanes as in the write.
+// thread writes 8 channels (16 bytes) of a row: lanes 4 j + i those of 8 i .. in group j.
 template <typename T, int D>
 __global__ void __launch_bounds__(kReadThreads) dequantise_blocks_int4_kernel(
     const char *__restrict__ k4, const char *__restrict__ v4, int64_t num_blocks4, int64_t block_stride4,
@@ -207,14 +227,14 @@ PKV_API pkv_status pkv_reshape_and_cache_int4(const void *k_new, const void *v_n
     unsigned int *status = pkv::status_word_ptr();
     if (!status) return PKV_ERR_CUDA;
     const int64_t rows = num_tokens * num_kv_heads;
-    const int per_cta = kWriteThreads / (head_dim / 8);
+    const int per_cta = kWriteThreads / (head_dim / 16);
     auto kernel = dtype == PKV_F16 ? (head_dim == 128 ? reshape_and_cache_int4_kernel<__half, 128> : reshape_and_cache_int4_kernel<__half, 64>)
                                    : (head_dim == 128 ? reshape_and_cache_int4_kernel<__nv_bfloat16, 128>
                                                       : reshape_and_cache_int4_kernel<__nv_bfloat16, 64>);
     kernel<<<static_cast<unsigned>((rows + per_cta - 1) / per_cta), kWriteThreads, 0, static_cast<cudaStream_t>(stream)>>>(
         static_cast<const uint4 *>(k_new), static_cast<const uint4 *>(v_new), slot_mapping, static_cast<char *>(k_cache),
         static_cast<char *>(v_cache), num_blocks * block_size, block_stride_bytes, static_cast<int>(rows), num_kv_heads,
-        shift_of(block_size), status);
+        pkv::make_fast_div(num_kv_heads), shift_of(block_size), status);
     pkv::count_launch();
     return pkv::launch_status();
 }

@@ -140,6 +140,59 @@ __device__ __forceinline__ float fast_rcp(float x) {
     return y;
 }
 
+// Division of a non-negative int by a fixed positive divisor through one multiplication
+// (Granlund and Montgomery, "Division by Invariant Integers using Multiplication", 1994,
+// the form with a 33-bit add): l = ceil(log2 d), m = floor(2^32 (2^l - d) / d) + 1, and
+// n / d = (umulhi(m, n) + n) >> l for 0 <= n < 2^31 (umulhi(m, n) < n, so the add does
+// not wrap).  For kernels that divide by the same few launch constants.
+struct FastDiv {
+    uint32_t m, l;
+};
+inline FastDiv make_fast_div(int d) {
+    if (d < 1) d = 1;  // no launch divides by less (empty launches return before)
+    uint32_t l = 0;
+    while ((1ull << l) < static_cast<uint64_t>(d)) ++l;
+    const uint64_t m = (1ull << 32) * ((1ull << l) - static_cast<uint64_t>(d)) / static_cast<uint64_t>(d) + 1;
+    return FastDiv{static_cast<uint32_t>(m), l};
+}
+__device__ __forceinline__ int fast_div(int n, FastDiv f) {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), f.m) + static_cast<uint32_t>(n)) >> f.l);
+}
+
+// Two fp32 values in one 64-bit register and the packed arithmetic on them (sm_100 and
+// later); unlike fma_f32x2 the result is a register of its own, so a constant addend
+// needs no copy.
+using F32x2 = unsigned long long;
+__device__ __forceinline__ F32x2 pack_f32(float lo, float hi) {
+    F32x2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void unpack_f32(F32x2 v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ F32x2 fma2(F32x2 a, F32x2 b, F32x2 c) {
+    F32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ F32x2 mul2(F32x2 a, F32x2 b) {
+    F32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ F32x2 add2(F32x2 a, F32x2 b) {
+    F32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// l0 += the low, l1 += the high of two packed fp16 values.
+__device__ __forceinline__ void add_f16x2(float &l0, float &l1, uint32_t v) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.f32.f16 %0, a, %0;\n\tadd.f32.f16 %1, b, %1;\n\t}"
+        : "+f"(l0), "+f"(l1) : "r"(v));
+}
+
 // max(a, b, c) / min(a, b, c) in one instruction (sm_100 and later).
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float d;

@@ -54,25 +54,6 @@
 
 namespace pkv {
 
-// Division of a non-negative int by a fixed positive divisor through one multiplication
-// (Granlund and Montgomery, "Division by Invariant Integers using Multiplication", 1994,
-// the form with a 33-bit add): l = ceil(log2 d), m = floor(2^32 (2^l - d) / d) + 1, and
-// n / d = (umulhi(m, n) + n) >> l for 0 <= n < 2^31 (umulhi(m, n) < n, so the add does
-// not wrap).  The item arithmetic divides by the same few launch constants in every role.
-struct FastDiv {
-    uint32_t m, l;
-};
-inline FastDiv make_fast_div(int d) {
-    if (d < 1) d = 1;  // no launch divides by less (empty launches return before)
-    uint32_t l = 0;
-    while ((1ull << l) < static_cast<uint64_t>(d)) ++l;
-    const uint64_t m = (1ull << 32) * ((1ull << l) - static_cast<uint64_t>(d)) / static_cast<uint64_t>(d) + 1;
-    return FastDiv{static_cast<uint32_t>(m), l};
-}
-__device__ __forceinline__ int fast_div(int n, FastDiv f) {
-    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), f.m) + static_cast<uint32_t>(n)) >> f.l);
-}
-
 struct PrefillParams {
     const void *q;                 // [num_rows][num_q_heads][128]
     void *out;                     // [num_rows][num_q_heads][128]
@@ -554,34 +535,6 @@ struct PrefillLayout {
     static_assert(kSmemBytes <= 232448, "dynamic shared memory per block");
 };
 
-// Two fp32 values in one 64-bit register and the packed arithmetic on them (sm_100 and
-// later); unlike fma_f32x2 the result is a register of its own, so a constant addend
-// needs no copy.
-using F32x2 = unsigned long long;
-__device__ __forceinline__ F32x2 pack_f32(float lo, float hi) {
-    F32x2 d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-    return d;
-}
-__device__ __forceinline__ void unpack_f32(F32x2 v, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ F32x2 fma2(F32x2 a, F32x2 b, F32x2 c) {
-    F32x2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ F32x2 mul2(F32x2 a, F32x2 b) {
-    F32x2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ F32x2 add2(F32x2 a, F32x2 b) {
-    F32x2 d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // tanh(z) / z in powers of z^2: Chebyshev fits, relative error below 2^-24 for |z| <= 3/4
 // (six terms), 2^-21.9 for |z| <= 0.45 (four) and 2^-21 for |z| <= 1/4 (three).
 __device__ constexpr float kTanh6[6] = {1.f, -0.3333296775817871f, 0.13325515389442444f, -0.053349819034338f, 0.01959378644824028f, -0.004723952151834965f};
@@ -599,13 +552,6 @@ __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 
 // unpacking them cost 6% on 17-tile items, this 2%.)
 __device__ __forceinline__ void add_bf16x2(float &l0, float &l1, uint32_t v) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.f32.bf16 %0, a, %0;\n\tadd.f32.bf16 %1, b, %1;\n\t}"
-        : "+f"(l0), "+f"(l1) : "r"(v));
-}
-
-// The same for two packed fp16 values (the sink and tree forms: a row of a few tokens behind a window or at
-// the head of a context is theirs to expect).
-__device__ __forceinline__ void add_f16x2(float &l0, float &l1, uint32_t v) {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.f32.f16 %0, a, %0;\n\tadd.f32.f16 %1, b, %1;\n\t}"
         : "+f"(l0), "+f"(l1) : "r"(v));
 }
 

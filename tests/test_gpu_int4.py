@@ -63,6 +63,28 @@ def test_values_are_half_a_step_off_at_most(dtype):
     assert (got - x.double()).abs().le(step / 2).all()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_write_of_values_halfway_between_codes(dtype):
+    """Groups of z + m s / 2, m in 0 .. 30 with both ends: every odd m is a tie, which goes to the even code."""
+    dev, g = device(), torch.Generator().manual_seed(4)
+    t, hkv, d = 200, 2, 64
+    m = torch.randint(0, 31, (t, 2 * hkv, 2, 32), generator=g)
+    m[..., 3], m[..., 17] = 0, 30
+    unit = 2.0 ** torch.randint(-12, 4, (t, 2 * hkv, 2, 1), generator=g)
+    s = torch.randint(1, 5, (t, 2 * hkv, 2, 1), generator=g)  # 30 s + 60 <= 256: exact in eight bits
+    z = torch.randint(-60, 61, (t, 2 * hkv, 2, 1), generator=g)
+    x = ((z + m * s) * unit).flatten(2).to(dtype)
+    assert (x.double().unflatten(-1, (2, 32)) == (z + m * s) * unit.double()).all()
+    slots = torch.arange(t)
+    dp = pkv.int4_pool(13, hkv, 16, d, dev)
+    pkv.reshape_and_cache_int4(x[:, :hkv].contiguous().to(dev), x[:, hkv:].contiguous().to(dev), slots.to(dev), *pkv.split_pool(dp))
+    codes, scale, zero = refs.unpack(dp.cpu(), dtype)
+    want = torch.where(m % 4 == 1, m // 2, (m + 1) // 2)  # m / 2, ties to even
+    for half in range(2):
+        got = codes[:, half].transpose(1, 2).reshape(208, hkv, 2, 32)[:t]
+        assert torch.equal(got, want[:, half * hkv:(half + 1) * hkv])
+
+
 def test_write_of_nan_and_of_the_smallest_values():
     dev = device()
     for dtype in DTYPES:
