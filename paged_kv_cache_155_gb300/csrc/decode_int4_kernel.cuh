@@ -290,6 +290,22 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
             w[1] = u.y;
         }
     };
+    // A lane's weights of a token times its group's scale, as a fp16 pair, and the group's zero added to their sums.
+    // fp16 rows: the pair's rounding counts for the code's distance from 8 only, since 8 of it go with the zero,
+    // unrounded (p s c + p z = w (c - 8) + p (z + 8 s) with w for p s): codes stand for values around zero, so that the
+    // error is that of one more rounding of the output, where it was twice that in contexts of a few tokens.
+    auto weigh = [](const float (&p)[2], float2 sz, float (&z)[2]) {
+        const __half2 w = __floats2half2_rn(p[0] * sz.x, p[1] * sz.x);
+        const uint32_t bits = *reinterpret_cast<const uint32_t *>(&w);
+        if constexpr (!kBF16) {
+            const __half2 less = __hmul2(w, __float2half2_rn(-8.f));  // exact
+            sz.y = fmaf(8.f, sz.x, sz.y);
+            add_f16x2(z[0], z[1], *reinterpret_cast<const uint32_t *>(&less));
+        }
+        z[0] = fmaf(p[0], sz.y, z[0]);
+        z[1] = fmaf(p[1], sz.y, z[1]);
+        return bits;
+    };
     // the eight tokens 8 i .. 8 i + 7 of a stage's half: their block's record and their first row in it
     auto octet = [](const unsigned char *half, int i) { return half + 8 * i / BS * G::kRecord; };
     auto first_row = [](int i) { return 8 * i % BS; };
@@ -597,12 +613,8 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
                             uint32_t ra[4], rb[4];
                             codes_f16_bytes(v[2 * r][j], ra);
                             codes_f16_bytes(v[2 * r + 1][j], rb);
-                            const float2 sz = Int4Param<T>::unpack(vp[i][j]);
-                            const __half2 h = __floats2half2_rn(sc[i][0][0] * sz.x, sc[i][0][1] * sz.x);
-                            const uint32_t w = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&h));
+                            const uint32_t w = movmatrix_trans(weigh(sc[i][0], Int4Param<T>::unpack(vp[i][j]), zacc[0][j]));
                             const uint32_t b0 = __byte_perm(w, 0u, sel0), b1 = __byte_perm(w, 0u, sel1);
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) zacc[0][j][e] = fmaf(sc[i][0][e], sz.y, zacc[0][j][e]);
                             mma_16816<false>(oacc[0][j][0], ra[0], ra[1], rb[0], rb[1], b0, b1);
                             mma_16816<false>(oacc[0][j][1], ra[2], ra[3], rb[2], rb[3], b0, b1);
                         }
@@ -615,13 +627,8 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
                         const float2 s0 = Int4Param<T>::unpack(vp[i2][j]), s1 = Int4Param<T>::unpack(vp[i2 + 1][j]);
 #pragma unroll
                         for (int n = 0; n < N; ++n) {
-                            const __half2 ha = __floats2half2_rn(sc[i2][n][0] * s0.x, sc[i2][n][1] * s0.x);
-                            const __half2 hb = __floats2half2_rn(sc[i2 + 1][n][0] * s1.x, sc[i2 + 1][n][1] * s1.x);
-                            const uint32_t b0 = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&ha));
-                            const uint32_t b1 = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&hb));
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                zacc[n][j][e] = fmaf(sc[i2 + 1][n][e], s1.y, fmaf(sc[i2][n][e], s0.y, zacc[n][j][e]));
+                            const uint32_t b0 = movmatrix_trans(weigh(sc[i2][n], s0, zacc[n][j]));
+                            const uint32_t b1 = movmatrix_trans(weigh(sc[i2 + 1][n], s1, zacc[n][j]));
                             mma_16816<false>(oacc[n][j][0], ra[0], ra[1], rb[0], rb[1], b0, b1);
                             mma_16816<false>(oacc[n][j][1], ra[2], ra[3], rb[2], rb[3], b0, b1);
                         }
