@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
     constexpr int ROW = int4_row_bytes(D), PAR = int4_param_bytes(D);
     constexpr bool kBF16 = !std::is_same<T, __half>::value;
     pdl_trigger();  // the merge behind this grid may be placed
+    pdl_wait();     // launched ahead of the end of the kernel before it
 
     extern __shared__ __align__(128) unsigned char smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -703,6 +704,7 @@ __global__ void __launch_bounds__(128) paged_decode_int4_merge_kernel(const Int4
     constexpr int PER = D / 32;
     using Part = typename std::conditional<PER == 4, float4, float2>::type;
     __shared__ float comb[WPH == 4 ? 4 : 1][D + 2];  // the four warps' (o, m, l) of a head
+    pdl_trigger();
     pdl_wait();
     Int4Split s = p.splits[blockIdx.x];
     if (p.by_unit) {

@@ -23,7 +23,7 @@ pkv_status launch_int4_one(const Int4Params &p, int grid, cudaStream_t stream) {
             return PKV_ERR_CUDA;
         configured_devices.fetch_or(bit, std::memory_order_acq_rel);
     }
-    if (launch_kernel(paged_decode_int4_kernel<T, D, BS, NT>, dim3(static_cast<unsigned>(grid)), dim3(G::kWarps * 32), G::kSmemBytes, stream, false,
+    if (launch_kernel(paged_decode_int4_kernel<T, D, BS, NT>, dim3(static_cast<unsigned>(grid)), dim3(G::kWarps * 32), G::kSmemBytes, stream, true,
                       p) != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;

@@ -310,6 +310,7 @@ __global__ void __launch_bounds__(128, (GH >= 4 && sizeof(KT) == 2) ? (GH == 16 
 
     // the merge kernel, launched behind this one, may be placed as this grid's CTAs run
     if (p.trigger_dependents) pdl_trigger();
+    if constexpr (kSinks) pdl_wait();  // launched ahead of the end of the kernel before it
     if (p.wait_prior_grid && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 &&
         blockIdx.z == gridDim.z - 1)
         pdl_wait();  // uniform over the CTA; normally dispatched last, when nothing is left to wait for
@@ -1469,6 +1470,7 @@ __device__ __forceinline__ void merge_rows(const DecodeParams &p, int num_rows, 
 
 template <typename T, int D, int WPR, bool kSinks = false>
 __global__ void __launch_bounds__(128) paged_decode_merge_kernel(const DecodeParams p, int num_rows) {
+    if constexpr (kSinks) pdl_trigger();
     pdl_wait();
     merge_rows<T, D, WPR, false, kSinks>(p, num_rows, blockIdx.x);
 }

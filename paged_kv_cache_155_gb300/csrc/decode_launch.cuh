@@ -75,7 +75,7 @@ pkv_status launch_decode_typed(const DecodeParams &p, const DecodeMaps &m, int h
                                int block_size, int gh, dim3 grid, int merge_rows, cudaStream_t s,
                                const WeightParams &w = WeightParams{}) {
     pkv_status st = PKV_ERR_UNSUPPORTED;
-    const bool overlap = p.wait_prior_grid != 0;
+    const bool overlap = kSinks || p.wait_prior_grid != 0;
     if (head_dim == 128) {
         if (block_size == 8) st = launch_decode_gh<T, KT, 128, 8, kScored, kSinks>(p, m, gh, grid, s, overlap);
         else if (block_size == 16) st = launch_decode_gh<T, KT, 128, 16, kScored, kSinks>(p, m, gh, grid, s, overlap);

@@ -219,7 +219,11 @@ pkv_status prefill_impl(
         auto *plan = static_cast<pkv::PrefillPlan *>(workspace);
         p.plan = plan;
         p.order = pkv::kOrderPlanned;
-        (sink_form ? pkv::paged_prefill_plan_kernel<true> : pkv::paged_prefill_plan_kernel<false>)<<<1, pkv::kPlanThreads, 0, s>>>(p, plan);
+        if (pkv::launch_kernel(sink_form ? pkv::paged_prefill_plan_kernel<true> : pkv::paged_prefill_plan_kernel<false>, dim3(1),
+                               dim3(pkv::kPlanThreads), 0, s, sink_form, p, plan) != cudaSuccess) {
+            cudaGetLastError();
+            return PKV_ERR_CUDA;
+        }
         pkv::count_launch();
         if (st = pkv::launch_status(); st != PKV_OK) return st;
     }

@@ -25,7 +25,7 @@ pkv_status launch_prefill_one(const PrefillParams &p, const CUtensorMap &tq, con
     }
     // planned order: placed while the plan kernel before it still runs
     if (launch_kernel(paged_prefill_tc_kernel<T, BS, ORDER, kForm>, dim3(grid), dim3(PrefillLayout::kThreads),
-                      PrefillLayout::kSmemBytes, stream, ORDER == kOrderPlanned, tq, tk, tv, to, p) != cudaSuccess) {
+                      PrefillLayout::kSmemBytes, stream, ORDER == kOrderPlanned || kForm == kTreeForm, tq, tk, tv, to, p) != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
     }

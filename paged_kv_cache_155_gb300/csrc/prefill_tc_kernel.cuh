@@ -793,6 +793,7 @@ __global__ void __launch_bounds__(384, 1)
     StreamShare *share_slot = reinterpret_cast<StreamShare *>(sm + L::kOffByLen);
     if constexpr (kTree) {
         pdl_trigger();  // the merge behind this grid may be placed
+        pdl_wait();  // launched ahead of the end of the kernel before it
         if (warp == 2) {
             const StreamShare mine = stream_share(p, lane);
             if (lane == 0) *share_slot = mine;
@@ -1503,6 +1504,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_prefill_plan_kernel(const 
     __shared__ int warp_sum[kPlanThreads / 32];
     __shared__ int total;
     pdl_trigger();
+    if constexpr (kSinks) pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int count = p.num_seqs * p.row_tiles;  // <= kMaxPlanEntries
     bucket[tid] = 0;
@@ -1640,6 +1642,7 @@ template <typename T, int SHARES>
 __global__ void __launch_bounds__(128 * SHARES) paged_tree_merge_kernel(const PrefillParams p) {
     constexpr int D = 128;
     __shared__ float comb[SHARES > 1 ? SHARES - 1 : 1][10][128];
+    pdl_trigger();
     TreeSplit s{};
     if (p.by_unit) {
         const int seq = blockIdx.x / (p.num_kv_heads * p.row_tiles), unit = blockIdx.x - seq * (p.num_kv_heads * p.row_tiles);
