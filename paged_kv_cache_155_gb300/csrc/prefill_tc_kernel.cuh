@@ -103,6 +103,8 @@ struct PrefillParams {
                                        // so that a warp's rows store side by side, and [..][128 rows]
     struct TreeSplit *tree_splits;     // the cut units, see TreeSplit
     int by_unit, seg_ctas;             // its index; CTAs that the partials have room for
+    int abreast;                       // CTAs that walk one share side by side (1 or 2), see StreamShare
+    FastDiv div_tile_tokens;
 };
 // The fixed form's largest cap_out, and the exponent that its weights may reach: the reference
 // is what a score of cap_out exceeds that by.  So weights lie in 2^-100 .. 2^50: a product with
@@ -357,45 +359,50 @@ __device__ __forceinline__ void planned_item(const PrefillParams &p, int i, cons
 // units that are cut (its first and its last), whose partials are merged, and whole units between.
 // A draft's few rows per context leave this kernel bound by the context's bytes, so an even share of
 // them is what a split has to give.
+// Where drafts take several row tiles (and the KV heads are even), two CTAs walk a share abreast: two row tiles
+// of a KV head at a time, so that the second read of a KV tile comes from L2, and an odd last row tile of two KV
+// heads (128 x 64 nodes of 64 / 8 heads behind 1024 tokens 320 us, one by one 394; 16 x 4-63 behind 4096-8192 143, 148).
 struct StreamShare {
-    int seq, pos;  // the first unit's sequence, and the share's first tile counted in that sequence
+    int seq, kvh, row_tile, tile;  // where it begins
     int left;      // tiles of the share
     int quota;     // tiles of every share (the last ones' may be shorter)
+    int last;      // abreast: at the last, odd row tiles
 };
 // A cut unit.  The table is indexed by unit -- (sequence, KV head, row tile), with row tiles by the host's
 // bound -- when there are no more of them than CTAs, else by the CTA in whose share it begins (at most
 // one goes on past a share).  Few units, cut into many pieces, then have a few merging blocks: one per
 // CTA, most of which find nothing, ran in several waves behind the kernel, whose registers leave them no room.
 struct TreeSplit {
-    int pieces;     // CTAs that hold pieces of the unit; 0: not cut (or none begins in this share)
+    int pieces;     // CTAs (all, or every other one) that hold pieces of the unit; 0: not cut (or none begins in this share)
     int cta, slot;  // the first of them, and its piece's slot (0 in the others)
     int q0, chunk;  // the unit's sequence
     int kvh, row_tile;
     int pad;
 };
 constexpr int kMinShare = 2;  // tiles of a share, at least
-// KV tiles of one unit and units of a sequence (no tiles: an empty or bad sequence)
-__device__ __forceinline__ int stream_tiles(const PrefillParams &p, const PrefillSeqVals &v, int &units) {
+// KV tiles of a unit and row tiles of a sequence (none: an empty or bad sequence)
+__device__ __forceinline__ int stream_tiles(const PrefillParams &p, const PrefillSeqVals &v, int &row_tiles) {
     int q0, chunk, len;
-    units = 0;
+    row_tiles = 0;
     if (!prefill_seq(p, v, q0, chunk, len) || chunk == 0) return 0;
-    units = (chunk + p.tile_tokens - 1) / p.tile_tokens * p.num_kv_heads;
+    row_tiles = fast_div(chunk + p.tile_tokens - 1, p.div_tile_tokens);
     return (len + 127) / 128;
 }
 // This CTA's share, by one warp.
 __device__ __forceinline__ StreamShare stream_share(const PrefillParams &p, int lane) {
     auto tiles_of = [&](int seq) {
         if (seq >= p.num_seqs) return 0;
-        int units;
-        const int n = stream_tiles(p, PrefillSeqVals{p.query_start[seq], p.query_start[seq + 1], p.context_lens[seq]}, units);
-        return n * units;
+        int row_tiles;
+        const int n = stream_tiles(p, PrefillSeqVals{p.query_start[seq], p.query_start[seq + 1], p.context_lens[seq]}, row_tiles);
+        return n * row_tiles * p.num_kv_heads / p.abreast;
     };
     const int mine0 = tiles_of(lane);  // sequences 0 .. 31, kept for the second pass
     int total = mine0;
     for (int seq = 32 + lane; seq < p.num_seqs; seq += 32) total += tiles_of(seq);
     total = __reduce_add_sync(0xffffffffu, total);
-    StreamShare s{0, 0, 0, max(kMinShare, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x))};
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * s.quota;
+    const int shares = static_cast<int>(gridDim.x) / p.abreast;
+    StreamShare s{0, 0, 0, 0, 0, max(kMinShare, (total + shares - 1) / shares), 0};
+    const int64_t first = static_cast<int64_t>(static_cast<int>(blockIdx.x) / p.abreast) * s.quota;
     if (first >= total) return s;
     s.left = min(s.quota, total - static_cast<int>(first));
     int before = 0;
@@ -411,58 +418,84 @@ __device__ __forceinline__ StreamShare stream_share(const PrefillParams &p, int 
         if (past) {
             const int l = __ffs(past) - 1;
             s.seq = s0 + l;
-            s.pos = static_cast<int>(first) - (before + __shfl_sync(0xffffffffu, incl - mine, l));
+            const int pos = static_cast<int>(first) - (before + __shfl_sync(0xffffffffu, incl - mine, l));
+            int row_tiles;
+            const int tiles = stream_tiles(p, PrefillSeqVals{p.query_start[s.seq], p.query_start[s.seq + 1], p.context_lens[s.seq]}, row_tiles);
+            const int unit = pos / tiles, odd = p.abreast == 2 ? blockIdx.x & 1 : 0, per_head = row_tiles / p.abreast;
+            s.tile = pos - unit * tiles;
+            s.last = unit >= per_head * p.num_kv_heads;
+            s.kvh = s.last ? 2 * (unit - per_head * p.num_kv_heads) + odd : unit / per_head;
+            s.row_tile = s.last ? row_tiles - 1 : p.abreast * (unit - s.kvh * per_head) + odd;
             return s;
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
     }
 }
-// A role's walk over the share's items.
+// A role's walk over the share's items.  It goes by counters: every role walks, and runtime divisions cost
+// 128 x 16 nodes behind 1024 tokens up to 30 of 143 us.
 struct StreamWalk {
-    StreamShare s;
-    PrefillSeqVals v;
-    int tiles, units;  // of sequence s.seq
-    bool first;
+    int seq, kvh, row_tile, tile, left;
+    int q0, chunk, len, row_tiles;  // of sequence seq
+    bool last, first;               // StreamShare::last; no item given yet
     __device__ __forceinline__ void start(const PrefillParams &p, const StreamShare &share) {
-        s = share;
+        seq = share.seq;
+        kvh = share.kvh;
+        row_tile = share.row_tile;
+        tile = share.tile;
+        left = share.left;
+        last = share.last;
         first = true;
-        if (s.left > 0) load(p);
+        if (left > 0) load(p);
     }
-    __device__ __forceinline__ void load(const PrefillParams &p) {
-        v = PrefillSeqVals{p.query_start[s.seq], p.query_start[s.seq + 1], p.context_lens[s.seq]};
-        tiles = stream_tiles(p, v, units);
+    __device__ __forceinline__ bool load(const PrefillParams &p) {
+        const PrefillSeqVals v{p.query_start[seq], p.query_start[seq + 1], p.context_lens[seq]};
+        q0 = v.q0;
+        chunk = v.q1 - v.q0;
+        len = v.len;
+        return stream_tiles(p, v, row_tiles) > 0;
     }
-    // the next item; false at the end.  last: the tiles of its unit behind it (0: the unit ends here)
+    // the next item; false at the end.  behind: the tiles of its unit behind it (0: the unit ends here)
     __device__ __forceinline__ bool next(const PrefillParams &p, PrefillItem &it, int &behind) {
-        if (s.left <= 0) return false;
-        while (s.pos >= tiles * units) {  // (the share's tiles lie in later sequences)
-            ++s.seq;
-            s.pos = 0;
-            load(p);
-        }
-        const int unit = s.pos / tiles, tile = s.pos - unit * tiles;
-        const int n = min(tiles - tile, s.left);
-        it.seq = s.seq;
-        it.q0 = v.q0;
-        it.chunk = v.q1 - v.q0;
-        it.len = v.len;
-        const int row_tiles = (it.chunk + p.tile_tokens - 1) / p.tile_tokens;
-        it.kvh = unit / row_tiles;
-        it.row_tile = unit - it.kvh * row_tiles;
-        it.rows = it.chunk * p.group;
-        it.row0 = it.row_tile * p.tile_rows;
-        it.base_pos = it.len - it.chunk;
+        if (left <= 0) return false;
+        const int tiles = (len + 127) / 128, n = min(tiles - tile, left);
+        it.seq = seq;
+        it.q0 = q0;
+        it.chunk = chunk;
+        it.len = len;
+        it.kvh = kvh;
+        it.row_tile = row_tile;
+        it.rows = chunk * p.group;
+        it.row0 = row_tile * p.tile_rows;
+        it.base_pos = len - chunk;
         it.tok_lo = tile * 128;
-        it.tok_hi = min(it.len, (tile + n) * 128);
+        it.tok_hi = min(len, (tile + n) * 128);
         it.ntiles = n;
         it.lo = it.gap = 0;
         it.partial = n < tiles;
         it.split = first ? 0 : 1;
         behind = tiles - tile - n;
         first = false;
-        s.pos += n;
-        s.left -= n;
+        left -= n;
+        tile = 0;
+        row_tile += p.abreast;
+        if (left > 0 && row_tile > row_tiles - p.abreast + static_cast<int>(p.abreast == 2 && (blockIdx.x & 1))) forward(p);
         return true;
+    }
+    // to the next KV head (or pair), or the next sequence that has work (the share's tiles are there)
+    __device__ __forceinline__ void forward(const PrefillParams &p) {
+        const int odd = p.abreast == 2 ? blockIdx.x & 1 : 0;
+        kvh += last ? 2 : 1;
+        row_tile = last ? row_tiles - 1 : odd;
+        if (kvh < p.num_kv_heads) return;
+        if (!last && (row_tiles & (p.abreast - 1))) {
+            last = true;
+        } else {
+            do ++seq;
+            while (!load(p));
+            last = row_tiles < p.abreast;
+        }
+        kvh = last ? odd : 0;
+        row_tile = last ? row_tiles - 1 : odd;
     }
 };
 
@@ -820,7 +853,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t tmem = *tmem_slot;
     constexpr bool kPlanned = ORDER == kOrderPlanned;
     int num_items = p.num_items;
-    StreamWalk walk;  // stream order: this role's walk
+    StreamWalk walk{};  // stream order: this role's walk
     int behind = 0;
     if constexpr (kTree) {
         num_items = 0x7fffffff;
@@ -843,7 +876,9 @@ __global__ void __launch_bounds__(384, 1)
         uint64_t *empty = kv ? v_empty : k_empty;
         const CUtensorMap *map = kv ? &tmap_v : &tmap_k;
         unsigned char *ring = sm + (kv ? L::kOffV : L::kOffK);
-        const uint64_t policy = l2_policy_evict_last();  // every row tile of the sequence reads it
+        // every row tile of the sequence reads it; a tree's few do at the same time, or once (64 x 16 nodes behind
+        // 1024-4096 tokens 122 us, evicted last 137)
+        const uint64_t policy = kTree ? l2_policy_evict_first() : l2_policy_evict_last();
         const uint64_t q_policy = l2_policy_evict_first();
         int last_issue[4] = {-1, -1, -1, -1};
         static_assert(L::kKS <= 4 && L::kVS <= 4 && L::kQB <= 2, "drain bookkeeping");
@@ -1169,7 +1204,7 @@ __global__ void __launch_bounds__(384, 1)
             return true;
         };
         PrefillRow view{0, 0, 0.f};
-        TreeSplit split{};  // tree form
+        if (kTree && !p.by_unit && warp == 2 && lane == 0) p.tree_splits[blockIdx.x].pieces = 0;
         PrefillEntry ahead{};  // planned order: the next item's entry
         if constexpr (kPlanned) ahead = load_entry(p, prefill_slot_item<ORDER>(p, 0), num_items);
         if constexpr (kPlanned) {
@@ -1202,10 +1237,12 @@ __global__ void __launch_bounds__(384, 1)
                 if (live) tree_row = p.tree_mask + static_cast<int64_t>(it.q0 + jtok) * p.mask_words;
                 if (it.tok_lo == 0) {
                     // the unit begins in this share; if it goes on, its pieces are in this CTA and the next ones
-                    split = TreeSplit{behind > 0 ? 1 + (behind + walk.s.quota - 1) / walk.s.quota : 0, static_cast<int>(blockIdx.x),
-                                      it.split, it.q0, it.chunk, it.kvh, it.row_tile, 0};
-                    if (p.by_unit && warp == 2 && lane == 0)
-                        p.tree_splits[(it.seq * p.num_kv_heads + it.kvh) * p.row_tiles + it.row_tile] = split;
+                    // (by CTA, the last unit that begins here is the one that can go on)
+                    if (warp == 2 && lane == 0)
+                        p.tree_splits[p.by_unit ? (it.seq * p.num_kv_heads + it.kvh) * p.row_tiles + it.row_tile
+                                                : static_cast<int>(blockIdx.x)] =
+                            TreeSplit{behind > 0 ? 1 + (behind + share_slot->quota - 1) / share_slot->quota : 0,
+                                      static_cast<int>(blockIdx.x), it.split, it.q0, it.chunk, it.kvh, it.row_tile, 0};
                 }
             }
             for (int j = 0; j < it.ntiles && ok; ++j, ++jt) {
@@ -1478,9 +1515,6 @@ __global__ void __launch_bounds__(384, 1)
                 }
             }
         }
-        if constexpr (kTree) {
-            if (!p.by_unit && warp == 2 && lane == 0) p.tree_splits[blockIdx.x] = split;
-        }
     }
 
     // ---- tear-down: both issuers drained their MMAs; TMEM is freed
@@ -1663,13 +1697,13 @@ __global__ void __launch_bounds__(128 * SHARES) paged_tree_merge_kernel(const Pr
         s = p.tree_splits[blockIdx.x];
     }
     // (a kernel that gave up on a wait leaves entries unwritten)
-    if (s.pieces <= 0 || s.cta < 0 || s.cta >= p.seg_ctas || s.pieces > p.seg_ctas - s.cta || (s.slot & ~1)) return;
+    if (s.pieces <= 0 || s.cta < 0 || s.cta >= p.seg_ctas || p.abreast * (s.pieces - 1) >= p.seg_ctas - s.cta || (s.slot & ~1)) return;
     const int r = threadIdx.x & 127, share = threadIdx.x >> 7, row = s.row_tile * p.tile_rows + r;
     const bool live = r < p.tile_rows && row < s.chunk * p.group;
     const int mine = live && s.pieces > share ? (s.pieces - share + SHARES - 1) / SHARES : 0;
     auto slot = [&](int i) {
         i = share + SHARES * i;
-        return 2 * static_cast<int64_t>(s.cta + i) + (i == 0 ? s.slot : 0);
+        return 2 * static_cast<int64_t>(s.cta + p.abreast * i) + (i == 0 ? s.slot : 0);
     };
     constexpr int kAhead = 4;  // pieces whose loads are in flight together
     float4 v[kAhead][2];

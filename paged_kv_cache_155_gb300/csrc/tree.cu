@@ -170,6 +170,7 @@ PKV_API pkv_status pkv_paged_attention_tree(const void *q, const void *k_cache, 
     p.block_size = block_size;
     p.div_kv_heads = pkv::make_fast_div(num_kv_heads);
     p.div_group = pkv::make_fast_div(group);
+    p.div_tile_tokens = pkv::make_fast_div(tile_tokens);
     p.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
     p.tree_mask = tree_mask;
     p.mask_words = mask_words;
@@ -178,8 +179,9 @@ PKV_API pkv_status pkv_paged_attention_tree(const void *q, const void *k_cache, 
     p.seg_l = p.seg_m + static_cast<size_t>(sm) * kSegRows;
     p.tree_splits = reinterpret_cast<pkv::TreeSplit *>(p.seg_l + static_cast<size_t>(sm) * kSegRows);
     // one CTA per SM, or fewer where the contexts' bound leaves no more shares
-    const int64_t most = (tiles * row_tiles * num_kv_heads * num_seqs + pkv::kMinShare - 1) / pkv::kMinShare;
-    const int grid = static_cast<int>(std::min<int64_t>(most, sm));
+    p.abreast = row_tiles > 1 && num_kv_heads % 2 == 0 && sm > 1 ? 2 : 1;
+    const int64_t most = (tiles * row_tiles * num_kv_heads * num_seqs / p.abreast + pkv::kMinShare - 1) / pkv::kMinShare;
+    const int grid = static_cast<int>(std::min<int64_t>(most, sm / p.abreast)) * p.abreast;
     p.row_tiles = static_cast<int>(row_tiles);
     p.by_unit = row_tiles * num_kv_heads * num_seqs <= grid;
     p.seg_ctas = sm;
