@@ -81,6 +81,14 @@ def test_many_sequences_of_every_length():
     run(device(), F16, 16, 4, 8, [0] * 40 + [900], [1] * 40 + [100], seed=4)
 
 
+@pytest.mark.parametrize("hkv", [2, 3, 4])
+@pytest.mark.parametrize("seqs", [6, 60])
+def test_drafts_of_one_to_eight_row_tiles(hkv, seqs):
+    """Row tiles side by side and alone, their units whole and cut, with sequences that draft nothing between."""
+    cached = [i * 211 % 700 for i in range(seqs)]
+    run(device(), BF16, 16 * hkv, hkv, 16, cached, [i * 13 % 62 + (i == seqs - 1) for i in range(seqs)], seed=seqs + hkv)
+
+
 def test_wide_masks_and_any_bits():
     g = torch.Generator().manual_seed(5)
     masks = [torch.rand((n, n), generator=g) < 0.4 for n in (200, 130, 90, 5)]  # not only ancestors: any bits
