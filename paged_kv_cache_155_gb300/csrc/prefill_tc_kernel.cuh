@@ -1677,6 +1677,9 @@ __global__ void __launch_bounds__(128 * SHARES) paged_tree_merge_kernel(const Pr
     constexpr int D = 128;
     __shared__ float comb[SHARES > 1 ? SHARES - 1 : 1][10][128];
     pdl_trigger();
+    // Nothing is read before: the attention may itself have been launched ahead of what writes the lengths.  And every
+    // block waits, so that this grid, and with it the call, ends after the one before it.
+    pdl_wait();
     TreeSplit s{};
     if (p.by_unit) {
         const int seq = blockIdx.x / (p.num_kv_heads * p.row_tiles), unit = blockIdx.x - seq * (p.num_kv_heads * p.row_tiles);
@@ -1684,16 +1687,13 @@ __global__ void __launch_bounds__(128 * SHARES) paged_tree_merge_kernel(const Pr
         s.row_tile = unit - s.kvh * p.row_tiles;
         int len;
         const PrefillSeqVals v{p.query_start[seq], p.query_start[seq + 1], p.context_lens[seq]};
-        // (every block waits, so that this grid, and with it the call, ends after the one before it)
-        const bool there = prefill_seq(p, v, s.q0, s.chunk, len) && s.row_tile * p.tile_tokens < s.chunk;
-        pdl_wait();
-        if (!there) return;  // a unit past its sequence's chunk has no entry
+        // a unit past its sequence's chunk has no entry
+        if (!prefill_seq(p, v, s.q0, s.chunk, len) || s.row_tile * p.tile_tokens >= s.chunk) return;
         const TreeSplit t = p.tree_splits[blockIdx.x];
         s.pieces = t.pieces;
         s.cta = t.cta;
         s.slot = t.slot;
     } else {
-        pdl_wait();
         s = p.tree_splits[blockIdx.x];
     }
     // (a kernel that gave up on a wait leaves entries unwritten)

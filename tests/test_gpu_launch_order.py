@@ -139,3 +139,32 @@ def test_a_run_of_calls_that_read_each_others_results():
     for k in results[0]:
         assert torch.equal(results[0][k], results[1][k]), k
     check_no_device_flags(dev)
+
+
+def test_drafts_behind_the_commit_that_gives_their_lengths():
+    """A tree's attention whose context lengths the commit right before it writes, at the end of long moves."""
+    dev, g = device(), torch.Generator().manual_seed(3)
+    seqs, hkv, nodes, cached = 4, 8, 64, 900
+    blocks = -(-(cached + 2 * nodes) // BS)
+    tables = torch.randperm(seqs * blocks, generator=g).to(torch.int32).reshape(seqs, blocks).to(dev)
+    kv = torch.randn((seqs * blocks, 2, hkv, BS, 128), generator=g).to(BF16).to(dev)
+    start = (torch.arange(seqs + 1) * nodes).to(torch.int32).to(dev)
+    lens = torch.full((seqs,), cached + nodes, dtype=torch.int32, device=dev)
+    path = torch.arange(1, nodes, dtype=torch.int32).repeat(seqs, 1).to(dev)
+    taken = torch.full((seqs,), nodes - 1, dtype=torch.int32, device=dev)
+    after = torch.zeros(seqs, dtype=torch.int32, device=dev)
+    mask = torch.cat([words_of(ancestors(8, g), 1) for _ in range(seqs)]).to(dev)
+    few = (torch.arange(seqs + 1) * 8).to(torch.int32).to(dev)
+    q = torch.randn((seqs * 8, 4 * hkv, 128), generator=g).to(BF16).to(dev)
+    commit = pkv.prepare_tree_commit(*pkv.split_pool(kv), tables, start, lens, path, taken, after, max_query_len=nodes,
+                                     max_context_len=cached + nodes)
+    attend = pkv.prepare_paged_attention_tree(q, *pkv.split_pool(kv), tables, few, after, mask, max_query_len=8,
+                                              max_context_len=cached + nodes)
+    for _ in range(50):
+        after.zero_()
+        attend.result.zero_()
+        commit()
+        got = attend().clone()
+        torch.cuda.synchronize()
+        assert torch.equal(got, attend())
+    check_no_device_flags(dev)
