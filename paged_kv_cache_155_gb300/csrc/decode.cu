@@ -87,6 +87,8 @@ constexpr int kTargetWaves = 8;        // CTA waves the automatic split aims for
 constexpr int kMinAutoPartition = 256; // tokens: below this the per-CTA set-up dominates
 constexpr int kMergeShare = 32;        // a partition's K/V bytes >= this x its partial bytes
 constexpr double kScoredFillSlack = 0.03;
+constexpr double kLaneFillSlack = 0.05;  // the sink form's lane loops
+constexpr int kShortSpan = 2304;         // tokens of a sink form's span
 constexpr double kFillSlack = 0.15;    // wave fill given up for fewer, longer partitions (two-per-SM forms)
 
 // Decode CTAs resident per SM for each kernel form (their stage budgets and
@@ -191,8 +193,21 @@ pkv_status plan_decode(int num_seqs, int num_q_heads, int num_kv_heads, int head
         // partitions within kScoredFillSlack of the best.  Measured: 32 x 4096 tokens of 32
         // heads in 2 instead of 3 partitions 317 us against 328; 2 x 32768 tokens of 64 / 8
         // heads in 57 instead of 61 (exactly two waves) 55.6 against 62.0.
-        const double slack = scored ? kScoredFillSlack : kFillSlack;
-        if (n > 1 && (scored || (units * n < target && slots <= 2LL * sm_count))) {
+        // The sink form's spans are alike, windows that are full, so splitting them evens nothing out: one partition each,
+        // without a merge, wherever that fills the SMs half and the spans are short, or fills them well.  (Warp MMAs want
+        // full waves.)  Measured, one / split: INT8, 32 heads of 64, window 1024, 16 contexts 21.6 / 27.2 us, 64 contexts
+        // 60.5 / 78.4; bf16 32 / 8 heads of 128, window 1024, 48 contexts 35.1 / 40.3, but 64 (1.1 waves) 55.5 / 49.5;
+        // window 4096, 16 contexts of 32 INT8 heads in blocks of 8 (0.56 waves) 97.9 / 87.6.  Else, lane loops take few
+        // partitions that fill their waves: 16 contexts of 32 INT8 heads of 64, window 4096, in 5 63.9, in 10 69.0.
+        const bool lanes = sinks && gh < 4;
+        const double waves = static_cast<double>(units) / static_cast<double>(slots);
+        const int64_t whole = (len + align - 1) / align * align;
+        const bool one = sinks && waves >= 0.5 && (waves >= 0.8 || len <= kShortSpan) && whole <= max_partition &&
+                         (lanes || waves < 1.0 || waves / std::ceil(waves) >= 0.8);
+        const double slack = lanes ? kLaneFillSlack : scored ? kScoredFillSlack : kFillSlack;
+        if (one && whole > 0) {
+            p = whole;
+        } else if (n > 1 && (scored || (units * n < target && slots <= 2LL * sm_count))) {
             auto fill = [&](int64_t parts) {  // CTAs / (rounds x slots)
                 const int64_t ctas = units * parts;
                 return static_cast<double>(ctas) / static_cast<double>((ctas + slots - 1) / slots * slots);
@@ -201,9 +216,10 @@ pkv_status plan_decode(int num_seqs, int num_q_heads, int num_kv_heads, int head
                 return ((len + k - 1) / k + align - 1) / align * align;
             };
             double best = fill(n);
-            for (int64_t k = (n + 1) / 2; k < n; ++k)
+            const int64_t fewest = lanes ? 1 : (n + 1) / 2;
+            for (int64_t k = fewest; k < n; ++k)
                 if (part_for(k) <= max_partition) best = std::max(best, fill((len + part_for(k) - 1) / part_for(k)));
-            for (int64_t k = (n + 1) / 2; k < n; ++k) {
+            for (int64_t k = fewest; k < n; ++k) {
                 const int64_t pk = part_for(k);
                 if (pk <= max_partition && fill((len + pk - 1) / pk) >= best - slack) {
                     p = pk;
