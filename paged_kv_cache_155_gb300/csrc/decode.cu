@@ -111,8 +111,8 @@ int scored_heads_per_block_for(int group, bool int8_kv) {
 // The sink form over an INT8 cache, whose scores take two products per code (the query and its remainder):
 // the warp MMAs, with two or three of their four head rows empty, for two heads, and for one where a block's
 // rows of a head are 2 KB or more.  Measured, MMAs / lane loops, 16 x 4112 visible tokens of 32 KV heads of 64:
-// two heads 75.8 / 104 us; one head, blocks of 32 64.0 / 72.0, of 16 75.1 / 68.6, of 8 97.9 / 87.5;
-// 8 x 4112 of heads of 128, blocks of 16 53.1 / 56.2.
+// two heads 68.2 / 93.9 us; one head, blocks of 32 56.3 / 55.2, of 16 68.0 / 60.6, of 8 105 / 80.6;
+// 8 x 4112 of heads of 128, blocks of 16 52.9 / 55.8.
 int sink_heads_per_block_for(int group, bool int8_kv, int head_dim, int block_size) {
     if (int8_kv && (group == 2 || (group == 1 && head_dim * block_size >= 2048))) return 4;
     return scored_heads_per_block_for(group, int8_kv);
