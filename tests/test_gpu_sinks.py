@@ -83,6 +83,14 @@ def test_decode_in_partitions_that_cut_the_gap(part, window, sinks):
     _decode(device(), F16, 4, 1, 128, 16, [500, 90, 33, 299], window, sinks, part=part, int8=True, seed=part)
 
 
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("hq,hkv,d,seqs", [(8, 8, 64, 64), (16, 4, 128, 64), (8, 8, 64, 9), (64, 8, 64, 30)])
+def test_decode_of_batches_that_fill_the_machine(hq, hkv, d, seqs, int8):
+    """Spans whole in one block, or in few partitions: contexts from none to several spans, most of them full."""
+    lens = [0, 1, 19, 20, 21, 170] + [160 + i * 97 % 700 for i in range(seqs - 6)]
+    _decode(device(), F16, hq, hkv, d, 16, lens, 150, 20, int8=int8, seed=seqs + hq)
+
+
 def test_decode_equals_the_windowed_one_without_first_tokens():
     dev, g = device(), torch.Generator().manual_seed(4)
     lens, bs = [700, 64, 3], 16
