@@ -64,7 +64,8 @@ __device__ __forceinline__ void int4_quantise(const uint4 (&row)[2], uint32_t (&
     pkv::Elem<T>::to_f32x8(row[0], *reinterpret_cast<float(*)[8]>(f));
     pkv::Elem<T>::to_f32x8(row[1], *reinterpret_cast<float(*)[8]>(f + 8));
     uint32_t c[16];
-    // 2^-100 <= s < 2^100 or 0; a scale whose reciprocal would overflow or vanish, infinite or NaN, takes the division
+    // 2^-100 <= s < 2^100 or 0; a scale whose reciprocal would overflow or vanish, infinite (a spread past fp32's range too)
+    // or NaN, takes the division
     const bool in_range = s == 0.f || __float_as_uint(s) - 0x0d800000u < 0x64000000u;
     if (__all_sync(0xffffffffu, in_range)) {
         const float by = s == 0.f ? 0.f : pkv::fast_rcp(s);
@@ -81,10 +82,13 @@ __device__ __forceinline__ void int4_quantise(const uint4 (&row)[2], uint32_t (&
         }
     } else {
         r = int4_range<T, false>(row);
-        sb = int4_scale<T>(r.x, -r.y);
+        // a group that spreads over more than fp32 holds is taken by quarters (exact: its values are bf16)
+        const float by = -r.y - r.x == INFINITY ? 0.25f : 1.f;
+        sb = int4_scale<T>(r.x * by, -r.y * by);
         s = pkv::Int4Param<T>::value(sb);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) c[e] = static_cast<uint32_t>(fminf(fmaxf(rintf(__fdiv_rn(f[e] - r.x, s)), 0.f), 15.f));
+        for (int e = 0; e < 16; ++e) c[e] = static_cast<uint32_t>(fminf(fmaxf(rintf(__fdiv_rn(f[e] * by - r.x * by, s)), 0.f), 15.f));
+        if (by != 1.f) sb = pkv::Int4Param<T>::bits(4.f * s);
     }
     param = sb | (pkv::Int4Param<T>::bits(r.x) << 16);
     unit[0] = __byte_perm(int4_word(c), int4_word(c + 4), 0x5410);
