@@ -315,8 +315,9 @@ PKV_API size_t pkv_decode_int4_workspace_bytes(int num_seqs, int num_q_heads, in
  * The contexts' work is cut evenly on the device, whatever their lengths, so there is
  * no partition size; workspace >= pkv_decode_int4_workspace_bytes(...) is always
  * needed, and calls that may overlap need one each.  Tokens past a context, in its last
- * block, may hold anything.  A query is held to 2^-24 of its largest channel, and V's
- * groups should have scales of at least 2^-50.  Other arguments and errors as
+ * block, may hold anything.  A query is held to 2^-24 of its largest channel.  Each
+ * group of a V row is as exact as if all had its scale, down to 2^-90 of the row's largest (rows
+ * whose scales lie 2^8 or more apart, 0 among them, take up to twice the time).  Other arguments and errors as
  * pkv_paged_attention_decode; the result depends on the batch's lengths within the
  * roundings (they decide where a context is cut), not on the blocks' places.
  */

@@ -28,7 +28,12 @@
 //    one nibble position only.  (With the exponent of 1024.0 set above the nibbles, as an offset to be
 //    taken away again, and 16 tokens a step, 64 x 4096 tokens of 32 / 8 heads took 106 us; so 83.)
 //  * The weights' reference is the running maximum of s_t + log2(max_j sV[t,j]), not of s_t, so that
-//    p_t sV[t,j], what fp16 has to hold, is at most 2^6 and near 1 where it counts, whatever V's scale is.
+//    p_t sV[t,j], what fp16 has to hold, is at most 2^12 and 2^6 or more where it counts, whatever V's scale is:
+//    as long as a token's groups have scales within 2^8 of its largest one.  From the first chunk on that holds another
+//    token (or scales or zeros near the ends of bf16's range), a worker weighs the rest of its share with exponents per
+//    chunk, head and group (int4_work_own), so that a small group next to a large one is as exact as alone.  Measured, all
+//    rows alike / a zero group in every row: 64 x 4096 tokens, 32 / 8 heads 70 / 86 us, 128 / 8 heads 120 / 180; without
+//    the test and the other form 68.7 and 120.
 //  * Every warp is a worker of its own: the 32-token chunks of all (sequence, KV head) units stand in one
 //    row and are cut into equal shares, so that any mix of lengths keeps all warps busy to the end and
 //    none waits for another (CTAs as workers, whose warps join their sums, measured the same on long contexts
@@ -91,6 +96,16 @@ struct Int4Params {
     float scale_log2;
 };
 constexpr int kInt4MinShare = 2;  // chunks of a share, at least
+// V's rows that a chunk weighs as they are: the largest scale in 2^kInt4Low .. 2^kInt4High, the others within kInt4Ratio
+// of it (fp16 holds p sV in full down to 2^-14, and the reference's tokens have 2^kInt4Head or more), zeros up to
+// 2^kInt4Zero.  Beyond, the reference is taken from the clamped scale, or from the zero / 2^kInt4ZeroLift, so that
+// p <= 2^42, p sV <= 2^97 and p zV <= 2^102: their sums over any context stay in fp32's range.
+constexpr float kInt4Ratio = 1.f / 256.f;  // 2^-8
+constexpr int kInt4Low = -30, kInt4High = 40, kInt4Zero = 60, kInt4ZeroLift = 90;
+constexpr float kInt4Head = 6.f;
+// bf16 (scale, zero) words: 2^kInt4High, 2^kInt4Zero, and -2^kInt4Low kInt4Ratio, 2^kInt4Zero
+constexpr uint32_t kInt4Most = ((kInt4High + 127) << 7) | ((kInt4Zero + 127) << 23);
+constexpr uint32_t kInt4Least = 0x8000u | ((kInt4Low - 8 + 127) << 7) | ((kInt4Zero + 127) << 23);
 
 // The token (0 .. 7) of MMA row r: rows 2 t, which one lane load of V takes for t = 0 .. 3, are
 // tokens 0 .. 3, and rows 2 t + 1 tokens 5, 4, 7, 6.
@@ -127,16 +142,31 @@ __device__ __forceinline__ float fast_log2(float x) {
     return y;
 }
 
-// The larger scale (low half) of two (scale, zero) words, in the low half.
+// a * b + c of two halves of the type
 template <typename T>
-__device__ __forceinline__ uint32_t max_scale(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t fma_halves(uint32_t a, float b, uint32_t c) {
     if constexpr (std::is_same<T, __half>::value) {
-        const __half2 m = __hmax2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
-        return *reinterpret_cast<const uint32_t *>(&m);
+        const __half2 d = __hfma2(*reinterpret_cast<const __half2 *>(&a), __float2half2_rn(b), *reinterpret_cast<const __half2 *>(&c));
+        return *reinterpret_cast<const uint32_t *>(&d);
     } else {
-        const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
-        return *reinterpret_cast<const uint32_t *>(&m);
+        const __nv_bfloat162 d = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&a), __float2bfloat162_rn(b),
+                                         *reinterpret_cast<const __nv_bfloat162 *>(&c));
+        return *reinterpret_cast<const uint32_t *>(&d);
     }
+}
+
+// The larger and the smaller halves of two (scale, zero) words: the scale's in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    const T2 m = __hmax2(*reinterpret_cast<const T2 *>(&a), *reinterpret_cast<const T2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&m);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t min_halves(uint32_t a, uint32_t b) {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    const T2 m = __hmin2(*reinterpret_cast<const T2 *>(&a), *reinterpret_cast<const T2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&m);
 }
 
 // A sequence's length as the kernels take it, and its chunks (at least one, possibly empty: an
@@ -156,16 +186,29 @@ __device__ __forceinline__ int int4_share(const Int4Params &p, int workers, int 
     return max(kInt4MinShare, (total + workers - 1) / workers);
 }
 
-template <typename T, int D, int BS, int NT>
-__global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) paged_decode_int4_kernel(const Int4Params p) {
+// Where a worker goes on: its piece and the piece's next chunk, the chunks that are left of its share from the piece's first
+// on, its ring's next stage, and what it has summed.
+template <int N, int GL>
+struct Int4At {
+    int seq, unit, chunk, c, left, s;
+    uint32_t phase;
+    bool first_piece;
+    Int4Split split;
+    float oacc[N][GL][2][4], zacc[N][GL][2], m[N][2], l[N][2];
+};
+template <int D, int BS, int NT>
+using Int4AtOf = Int4At<DecodeInt4Geom<D, BS, NT>::kTiles, DecodeInt4Geom<D, BS, NT>::kLaneGroups>;
+
+// A worker's pieces from `at` on.  Without kOwn it stops at the first chunk with a row that wants exponents of its own, with
+// no copy in flight: false, and `at` is there.  With kOwn it goes on there, and takes all that is left.
+template <typename T, int D, int BS, int NT, bool kOwn>
+__device__ __forceinline__ bool int4_work(const Int4Params &p, const int worker, const int share, Int4AtOf<D, BS, NT> &at) {
     using G = DecodeInt4Geom<D, BS, NT>;
     constexpr int NW = G::kWarps, S = G::kStages, NG = G::kGroups, SB = G::kBlocks, HEADS = G::kHeads;
     constexpr int N = G::kTiles, GL = G::kLaneGroups;
     constexpr bool kPaired = NT == 0;
     constexpr int ROW = int4_row_bytes(D), PAR = int4_param_bytes(D);
     constexpr bool kBF16 = !std::is_same<T, __half>::value;
-    pdl_trigger();  // the merge behind this grid may be placed
-    pdl_wait();     // launched ahead of the end of the kernel before it
 
     extern __shared__ __align__(128) unsigned char smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -176,50 +219,14 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
     unsigned char *my_stages = smem + warp * S * G::kStageBytes;
     uint64_t *my_bars = reinterpret_cast<uint64_t *>(smem + NW * S * G::kStageBytes) + warp * S;
     uint32_t *my_good = reinterpret_cast<uint32_t *>(smem + NW * S * (G::kStageBytes + 8)) + warp * S;  // blocks of a stage that were copied
-    if (lane == 0) {
-        for (int s = 0; s < S; ++s) mbar_init(&my_bars[s], 1);
-        fence_mbar_init();
-    }
-    __syncwarp();
-
-    // ---- this worker's share: chunks [first, first + left) of the row
-    const int worker = blockIdx.x * NW + warp;
-    int total;
-    const int share = int4_share(p, gridDim.x * NW, total);
-    const int64_t first = static_cast<int64_t>(worker) * share;
-    int left = first < total ? min(share, total - static_cast<int>(first)) : 0;
-    if (left == 0) {
-        if (lane == 0 && !p.by_unit) p.splits[worker].pieces = 0;
-        return;
-    }
-    int seq = 0, unit = 0, chunk = 0;  // where the share begins
-    for (int s0 = 0, before = 0;; s0 += 32) {
-        const int mine = s0 + lane < p.num_seqs ? int4_chunks(int4_len(p, s0 + lane)) : 0;
-        int incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += u;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, static_cast<int64_t>(before + incl) * p.units > first);
-        if (past) {
-            const int l = __ffs(past) - 1;
-            const int n = __shfl_sync(0xffffffffu, mine, l);
-            const int pos = static_cast<int>(first - static_cast<int64_t>(before + __shfl_sync(0xffffffffu, incl - mine, l)) * p.units);
-            seq = s0 + l;
-            unit = pos / n;
-            chunk = pos - unit * n;
-            break;
-        }
-        before += __shfl_sync(0xffffffffu, incl, 31);
-    }
+    int seq = at.seq, unit = at.unit, chunk = at.chunk, left = at.left;
 
     // ---- the copies' walk, up to S chunks ahead: lanes 2 i and 2 i + 1 copy block i's K and V records of
     //      a chunk.  A lane's table entry of the next chunk is read while the one before it is copied.
     const uint64_t policy = l2_policy_evict_first();
     const char *const cache0 = static_cast<const char *>(lane & 1 ? p.v_cache : p.k_cache);
     const char *cache = cache0 + static_cast<int64_t>(unit / p.blocks) * G::kRecord;  // of the unit's KV head
-    int i_seq = seq, i_unit = unit, i_chunk = chunk, i_left = left, i_len = int4_len(p, seq), i_entry = -1;
+    int i_seq = seq, i_unit = unit, i_chunk = at.c, i_left = left - (at.c - chunk), i_len = int4_len(p, seq), i_entry = -1;
     auto fetch = [&]() {
         i_entry = -1;
         const int at = i_chunk * SB + (lane >> 1);
@@ -255,9 +262,11 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
         fetch();
     };
     fetch();
-    for (int s = 0; s < S && i_left > 0; ++s) issue(s);
+    int s = at.s;  // the next chunk's stage and its barrier's phase
+    uint32_t phase = at.phase;
+    for (int k = 0; k < S && i_left > 0; ++k) issue(s + k < S ? s + k : s + k - S);
 
-    constexpr float kGrow = 6.f;  // the reference moves when a maximum exceeds it by more (log2 units)
+    constexpr float kGrow = kInt4Head + 6.f;  // the reference, kInt4Head below a maximum, moves when one exceeds it by more
     const int tau = token_of_row(mg);
     const int va = mt, vb = 4 + (mt ^ 1);  // V's tokens of a lane: rows 2 mt and 2 mt + 1
     // paired: the low and the high weight of a transposed word, in the half of this column's groups
@@ -295,26 +304,74 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
     // fp16 rows: the pair's rounding counts for the code's distance from 8 only, since 8 of it go with the zero,
     // unrounded (p s c + p z = w (c - 8) + p (z + 8 s) with w for p s): codes stand for values around zero, so that the
     // error is that of one more rounding of the output, where it was twice that in contexts of a few tokens.
-    auto weigh = [](const float (&p)[2], float2 sz, float (&z)[2]) {
-        const __half2 w = __floats2half2_rn(p[0] * sz.x, p[1] * sz.x);
+    // kOwn: the pair is taken times down (powers of two), whose inverses are up.
+    auto weigh = [](const float (&p)[2], float2 sz, float (&z)[2], const float (&down)[2], const float (&up)[2]) {
+        const __half2 w = kOwn ? __floats2half2_rn(p[0] * sz.x * down[0], p[1] * sz.x * down[1]) : __floats2half2_rn(p[0] * sz.x, p[1] * sz.x);
         const uint32_t bits = *reinterpret_cast<const uint32_t *>(&w);
         if constexpr (!kBF16) {
-            const __half2 less = __hmul2(w, __float2half2_rn(-8.f));  // exact
+            if constexpr (kOwn) {
+                z[0] = fmaf(__low2float(w), -8.f * up[0], z[0]);
+                z[1] = fmaf(__high2float(w), -8.f * up[1], z[1]);
+            } else {
+                const __half2 less = __hmul2(w, __float2half2_rn(-8.f));  // exact
+                add_f16x2(z[0], z[1], *reinterpret_cast<const uint32_t *>(&less));
+            }
             sz.y = fmaf(8.f, sz.x, sz.y);
-            add_f16x2(z[0], z[1], *reinterpret_cast<const uint32_t *>(&less));
         }
         z[0] = fmaf(p[0], sz.y, z[0]);
         z[1] = fmaf(p[1], sz.y, z[1]);
         return bits;
     };
+    // Waits for the copies in flight from chunk c + k on (chunk c's stage is s); by any lane.
+    auto drain = [&](int c, int k) {
+        bool done = true;
+        for (; k < S && k < left - (c - chunk); ++k)
+            done &= mbar_wait_bounded(&my_bars[s + k < S ? s + k : s + k - S], s + k < S ? phase : phase ^ 1u, kDrainTimeoutNs);
+        return done;
+    };
+    // Whether one of four tokens' rows wants exponents of its own, from their largest and smallest (scale, zero) words: the
+    // sign of a difference.
+    auto wants_own = [](const uint32_t (&top)[4], const uint32_t (&least)[4]) {
+        uint32_t below = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i += 2)
+            below |= fma_halves<T>(__byte_perm(top[i], top[i + 1], 0x5410), -kInt4Ratio, __byte_perm(least[i], least[i + 1], 0x5410));
+        if constexpr (kBF16) {
+            const uint32_t high = max_halves<T>(max_halves<T>(top[0], top[1]), max_halves<T>(top[2], top[3]));
+            const uint32_t low = min_halves<T>(min_halves<T>(least[0], least[1]), min_halves<T>(least[2], least[3]));
+            below |= fma_halves<T>(high, -1.f, kInt4Most) | fma_halves<T>(low, 1.f, kInt4Least);
+        }
+        return (below & 0x80008000u) != 0;
+    };
+    // The exponent, per column of this lane, of its tokens' largest |w|; the power of two that brings it into [2^11, 2^12), and
+    // that one's inverse.
+    auto exponents = [](float w0, float w1) {
+        uint32_t x = (__float_as_uint(w0) >> 23) | ((__float_as_uint(w1) >> 23) << 16);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) x = __vmaxu2(x, __shfl_xor_sync(0xffffffffu, x, o));
+        return x;
+    };
+    auto powers = [](uint32_t x, float (&down)[2], float (&up)[2]) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int k = max(static_cast<int>(x >> (16 * e) & 0xffffu) - 127 - 11, -100);
+            down[e] = exp2_int(-k);
+            up[e] = exp2_int(k);
+        }
+    };
+    auto add_back = [](float (&to)[2][4], const float (&sum)[2][4], const float (&up)[2]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) to[h][e] = fmaf(sum[h][e], up[e & 1], to[h][e]);
+    };
     // the eight tokens 8 i .. 8 i + 7 of a stage's half: their block's record and their first row in it
     auto octet = [](const unsigned char *half, int i) { return half + 8 * i / BS * G::kRecord; };
     auto first_row = [](int i) { return 8 * i % BS; };
 
-    int s = 0;  // the next chunk's stage and its barrier's phase
-    uint32_t phase = 0;
-    Int4Split split{0, 0, 0, 0, 0};
-    for (bool first_piece = true; left > 0; first_piece = false) {
+    Int4Split split = at.split;
+    bool resume = kOwn;
+    for (bool first_piece = at.first_piece; left > 0; first_piece = false) {
         const int ctx = p.context_lens[seq], len = min(max(ctx, 0), p.len_cap);
         const int chunks = int4_chunks(len), end = min(chunks, chunk + left);
         if (chunk == 0 && unit == 0 && ctx != len && lane == 0) raise_flag(p.status, PKV_DEVERR_CONTEXT_LEN);
@@ -409,20 +466,35 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
                 for (int e = 0; e < 4; ++e) oacc[n][j][0][e] = oacc[n][j][1][e] = 0.f;
             }
         }
-        for (int c = chunk; c < end; ++c) {
+        int c = chunk;
+        if constexpr (kOwn) {
+            if (resume) {
+                c = at.c;
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) m[n][e] = at.m[n][e], l[n][e] = at.l[n][e];
+#pragma unroll
+                    for (int j = 0; j < GL; ++j) {
+                        zacc[n][j][0] = at.zacc[n][j][0], zacc[n][j][1] = at.zacc[n][j][1];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) oacc[n][j][0][e] = at.oacc[n][j][0][e], oacc[n][j][1][e] = at.oacc[n][j][1][e];
+                    }
+                }
+            }
+            resume = false;
+        }
+        for (; c < end; ++c) {
             const bool ok = mbar_wait_bounded(&my_bars[s], phase, kWaitTimeoutNs);
             if (__any_sync(0xffffffffu, !ok)) {
                 // give up: flag it, let this warp's copies still in flight land, stop
                 if (lane == 0) {
                     raise_flag(p.status, PKV_DEVERR_TIMEOUT);
-                    for (int k = 0; k < S && k < left - (c - chunk); ++k) {
-                        const int at = s + k < S ? s + k : s + k - S;
-                        mbar_wait_bounded(&my_bars[at], s + k < S ? phase : phase ^ 1u, kDrainTimeoutNs);
-                    }
+                    drain(c, 0);
                     if (!p.by_unit) p.splits[worker].pieces = 0;
                 }
                 __syncwarp();
-                return;
+                return true;
             }
             // tokens of the stage that count: in the context, and their block copied
             const int valid = len - c * 32;  // >= 1, but 0 for an empty context
@@ -505,26 +577,40 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
             uint32_t vp[4][GL];
 #pragma unroll
             for (int i = 0; i < 4; ++i) load_params(octet(vst, i) + BS * ROW + (first_row(i) + tau) * PAR, vp[i]);
-            // log2 of each token's largest V scale; the clamp keeps p (at most 2^-e) in range
+            // log2 of each token's largest V scale; the clamps keep p (about 2^-e) in range
             float ev[4];
+            uint32_t top[4], least[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t most = vp[i][0];
+                top[i] = least[i] = vp[i][0];
 #pragma unroll
-                for (int j = 1; j < GL; ++j) most = max_scale<T>(most, vp[i][j]);
-                if constexpr (kPaired) most = max_scale<T>(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                ev[i] = fmaxf(fast_log2(Int4Param<T>::unpack(most).x), -40.f);
+                for (int j = 1; j < GL; ++j) top[i] = max_halves<T>(top[i], vp[i][j]), least[i] = min_halves<T>(least[i], vp[i][j]);
+                if constexpr (kPaired) top[i] = max_halves<T>(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+                ev[i] = fmaxf(fast_log2(Int4Param<T>::unpack(top[i]).x), static_cast<float>(kInt4Low));
             }
+            if constexpr (kOwn && kBF16) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float z = 0.f;
+#pragma unroll
+                    for (int j = 0; j < GL; ++j) z = fmaxf(z, fabsf(Int4Param<T>::unpack(vp[i][j]).y));
+                    if constexpr (kPaired) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 2));
+                    ev[i] = fmaxf(fminf(ev[i], static_cast<float>(kInt4High)), fast_log2(z) - static_cast<float>(kInt4ZeroLift));
+                }
+            }
+            bool odd = !kOwn && wants_own(top, least);  // one of this lane's rows
             if (partial) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if ((vis >> (8 * i + tau)) & 1u) continue;
                     ev[i] = -INFINITY;
+                    top[i] = least[i] = kBF16 ? 0x3f80u : 0x3c00u;  // as one that wants none
 #pragma unroll
                     for (int j = 0; j < GL; ++j) vp[i][j] = 0u;
 #pragma unroll
                     for (int n = 0; n < N; ++n) sc[i][n][0] = sc[i][n][1] = 0.f;
                 }
+                odd = !kOwn && wants_own(top, least);
             }
             float mx[N][2];
             bool grow = false;
@@ -541,7 +627,36 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
                     grow |= v > m[n][e] + kGrow;  // from -inf at the first visible token
                 }
             }
-            if (__any_sync(0xffffffffu, grow)) {
+            if (__any_sync(0xffffffffu, grow || odd)) {
+                if (!kOwn && __any_sync(0xffffffffu, odd)) {
+                    // the ring goes on behind the copies in flight, whose chunks are read again
+                    if (!__all_sync(0xffffffffu, drain(c, 1))) {
+                        if (lane == 0) {
+                            raise_flag(p.status, PKV_DEVERR_TIMEOUT);
+                            if (!p.by_unit) p.splits[worker].pieces = 0;
+                        }
+                        return true;
+                    }
+                    fence_proxy_async_smem();
+                    const int next = s + min(S, left - (c - chunk));
+                    at.seq = seq, at.unit = unit, at.chunk = chunk, at.c = c, at.left = left;
+                    at.s = next < S ? next : next - S;
+                    at.phase = next < S ? phase : phase ^ 1u;
+                    at.first_piece = first_piece;
+                    at.split = split;
+#pragma unroll
+                    for (int n = 0; n < N; ++n) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) at.m[n][e] = m[n][e], at.l[n][e] = l[n][e];
+#pragma unroll
+                        for (int j = 0; j < GL; ++j) {
+                            at.zacc[n][j][0] = zacc[n][j][0], at.zacc[n][j][1] = zacc[n][j][1];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) at.oacc[n][j][0][e] = oacc[n][j][0][e], at.oacc[n][j][1][e] = oacc[n][j][1][e];
+                        }
+                    }
+                    return false;
+                }
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
                     float a[2];
@@ -549,8 +664,8 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
                     for (int e = 0; e < 2; ++e) {
                         a[e] = 1.f;
                         if (mx[n][e] > m[n][e] + kGrow) {
-                            a[e] = fast_exp2(m[n][e] - mx[n][e]);  // 0 when m = -inf
-                            m[n][e] = mx[n][e];
+                            a[e] = fast_exp2(m[n][e] - (mx[n][e] - kInt4Head));  // 0 when m = -inf
+                            m[n][e] = mx[n][e] - kInt4Head;
                         }
                         l[n][e] *= a[e];
                     }
@@ -588,7 +703,22 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
 #pragma unroll
                 for (int e = 0; e < 2; ++e) l[n][e] += (sc[0][n][e] + sc[1][n][e]) + (sc[2][n][e] + sc[3][n][e]);
             // ---- O^T += V^T P^T, 16 tokens at a time: the weights times a group's scales in the B layout,
-            //      unit mg of tokens va, vb of both octets as the A fragments
+            //      unit mg of tokens va, vb of both octets as the A fragments.  kOwn: each head's weights of a group are
+            //      brought to 2^12 at most by a power of two before they are rounded, and their sums back.
+            uint32_t ex[kOwn ? N : 1][kOwn ? GL : 1];
+            if constexpr (kOwn) {
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                    for (int j = 0; j < GL; ++j) {
+                        float w[2] = {0.f, 0.f};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) w[e] = fmaxf(w[e], fabsf(sc[i][n][e] * Int4Param<T>::unpack(vp[i][j]).x));
+                        ex[n][j] = exponents(w[0], w[1]);
+                    }
+            }
 #pragma unroll
             for (int i2 = 0; i2 < 4; i2 += 2) {
                 uint32_t v[4][NG / 2];
@@ -610,14 +740,19 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
                     for (int r = 0; r < 2; ++r)
 #pragma unroll
                         for (int j = 0; j < GL; ++j) {
-                            const int i = i2 + r;
+                            const float(&p)[2] = sc[i2 + r][0];
+                            const float2 sz = Int4Param<T>::unpack(vp[i2 + r][j]);
                             uint32_t ra[4], rb[4];
                             codes_f16_bytes(v[2 * r][j], ra);
                             codes_f16_bytes(v[2 * r + 1][j], rb);
-                            const uint32_t w = movmatrix_trans(weigh(sc[i][0], Int4Param<T>::unpack(vp[i][j]), zacc[0][j]));
+                            float down[2], up[2], sum[2][4] = {};
+                            if constexpr (kOwn) powers(ex[0][j], down, up);
+                            const uint32_t w = movmatrix_trans(weigh(p, sz, zacc[0][j], down, up));
                             const uint32_t b0 = __byte_perm(w, 0u, sel0), b1 = __byte_perm(w, 0u, sel1);
-                            mma_16816<false>(oacc[0][j][0], ra[0], ra[1], rb[0], rb[1], b0, b1);
-                            mma_16816<false>(oacc[0][j][1], ra[2], ra[3], rb[2], rb[3], b0, b1);
+                            float(&to)[2][4] = kOwn ? sum : oacc[0][j];
+                            mma_16816<false>(to[0], ra[0], ra[1], rb[0], rb[1], b0, b1);
+                            mma_16816<false>(to[1], ra[2], ra[3], rb[2], rb[3], b0, b1);
+                            if constexpr (kOwn) add_back(oacc[0][j], sum, up);
                         }
                 } else {
 #pragma unroll
@@ -628,10 +763,15 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
                         const float2 s0 = Int4Param<T>::unpack(vp[i2][j]), s1 = Int4Param<T>::unpack(vp[i2 + 1][j]);
 #pragma unroll
                         for (int n = 0; n < N; ++n) {
-                            const uint32_t b0 = movmatrix_trans(weigh(sc[i2][n], s0, zacc[n][j]));
-                            const uint32_t b1 = movmatrix_trans(weigh(sc[i2 + 1][n], s1, zacc[n][j]));
-                            mma_16816<false>(oacc[n][j][0], ra[0], ra[1], rb[0], rb[1], b0, b1);
-                            mma_16816<false>(oacc[n][j][1], ra[2], ra[3], rb[2], rb[3], b0, b1);
+                            const float(&p0)[2] = sc[i2][n], (&p1)[2] = sc[i2 + 1][n];
+                            float down[2], up[2], sum[2][4] = {};
+                            if constexpr (kOwn) powers(ex[n][j], down, up);
+                            const uint32_t b0 = movmatrix_trans(weigh(p0, s0, zacc[n][j], down, up));
+                            const uint32_t b1 = movmatrix_trans(weigh(p1, s1, zacc[n][j], down, up));
+                            float(&to)[2][4] = kOwn ? sum : oacc[n][j];
+                            mma_16816<false>(to[0], ra[0], ra[1], rb[0], rb[1], b0, b1);
+                            mma_16816<false>(to[1], ra[2], ra[3], rb[2], rb[3], b0, b1);
+                            if constexpr (kOwn) add_back(oacc[n][j], sum, up);
                         }
                     }
                 }
@@ -693,6 +833,70 @@ __global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) pag
         }
     }
     if (lane == 0 && !p.by_unit) p.splits[worker] = split;
+    return true;
+}
+
+// Apart from the kernel, so that its registers are not spent on it.
+template <typename T, int D, int BS, int NT>
+__device__ __noinline__ void int4_work_own(const Int4Params &p, const int worker, const int share, Int4AtOf<D, BS, NT> &at) {
+    int4_work<T, D, BS, NT, true>(p, worker, share, at);
+}
+
+
+template <typename T, int D, int BS, int NT>
+__global__ void __launch_bounds__(128, DecodeInt4Geom<D, BS, NT>::kResident) paged_decode_int4_kernel(const __grid_constant__ Int4Params p) {
+    using G = DecodeInt4Geom<D, BS, NT>;
+    constexpr int NW = G::kWarps, S = G::kStages;
+    pdl_trigger();  // the merge behind this grid may be placed
+    pdl_wait();     // launched ahead of the end of the kernel before it
+
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint64_t *my_bars = reinterpret_cast<uint64_t *>(smem + NW * S * G::kStageBytes) + warp * S;
+    if (lane == 0) {
+        for (int s = 0; s < S; ++s) mbar_init(&my_bars[s], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+
+    // ---- this worker's share: chunks [first, first + left) of the row
+    const int worker = blockIdx.x * NW + warp;
+    int total;
+    const int share = int4_share(p, gridDim.x * NW, total);
+    const int64_t first = static_cast<int64_t>(worker) * share;
+    int left = first < total ? min(share, total - static_cast<int>(first)) : 0;
+    if (left == 0) {
+        if (lane == 0 && !p.by_unit) p.splits[worker].pieces = 0;
+        return;
+    }
+    int seq = 0, unit = 0, chunk = 0;  // where the share begins
+    for (int s0 = 0, before = 0;; s0 += 32) {
+        const int mine = s0 + lane < p.num_seqs ? int4_chunks(int4_len(p, s0 + lane)) : 0;
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, static_cast<int64_t>(before + incl) * p.units > first);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            const int n = __shfl_sync(0xffffffffu, mine, l);
+            const int pos = static_cast<int>(first - static_cast<int64_t>(before + __shfl_sync(0xffffffffu, incl - mine, l)) * p.units);
+            seq = s0 + l;
+            unit = pos / n;
+            chunk = pos - unit * n;
+            break;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+
+    Int4AtOf<D, BS, NT> at;
+    at.seq = seq, at.unit = unit, at.chunk = at.c = chunk, at.left = left, at.s = 0;
+    at.phase = 0u;
+    at.first_piece = true;
+    at.split = Int4Split{0, 0, 0, 0, 0};
+    if (!int4_work<T, D, BS, NT, false>(p, worker, share, at)) int4_work_own<T, D, BS, NT>(p, worker, share, at);
 }
 
 // Log-sum-exp merge of the cut units: entry blockIdx.x of their table.  WPH warps share a head's pieces:
