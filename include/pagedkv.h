@@ -265,7 +265,9 @@ PKV_API pkv_status pkv_paged_attention_decode_int8(
  *     scale s = (largest - smallest) / 15, rounded up to the rows' type,
  *     codes c = the integer nearest to (x - z) / s (x - z in fp32), ties to even, 0 when s = 0,
  * and read back as s * c + z: a value is off by s / 2 at most.  Values must be
- * finite (a NaN gets code 0, a group with an infinity reads back as NaN).
+ * finite (a NaN gets code 0, a group with an infinity reads back as NaN); one past the
+ * type's range, as the rounded-up scale can make of the largest code, counts as its largest
+ * finite value, when it is read back and in the decode's outputs.
  * The pool is bytes, [num_blocks][2][num_kv_heads][block_size * head_dim * 5 / 8]:
  * a head's record of a block holds the codes of its tokens, head_dim / 2 bytes
  * each, then head_dim / 32 (scale, zero) pairs for each of its tokens.  With

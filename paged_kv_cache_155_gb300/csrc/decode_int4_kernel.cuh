@@ -811,7 +811,7 @@ __device__ __forceinline__ bool int4_work(const Int4Params &p, const int worker,
                     if (h >= nheads) continue;
                     if (whole)
                         *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + row * D + 32 * group_of(j) + 4 * mg) =
-                            make_uint2(Elem<T>::pack2(r0, r1), Elem<T>::pack2(r2, r3));
+                            make_uint2(Int4Param<T>::pack2_finite(r0, r1), Int4Param<T>::pack2_finite(r2, r3));
                     else
                         *reinterpret_cast<float4 *>(p.seg_o + (slot + h) * D + 32 * group_of(j) + 4 * mg) = make_float4(r0, r1, r2, r3);
                 }
@@ -989,7 +989,7 @@ __global__ void __launch_bounds__(128) paged_decode_int4_merge_kernel(const Int4
         const float norm = lsum > 0.f ? 1.f / lsum : 0.f;
         T *dst = static_cast<T *>(p.out) + (static_cast<int64_t>(s.seq) * p.num_q_heads + kvh * p.group + sub * heads + h) * D + PER * lane;
 #pragma unroll
-        for (int e = 0; e < PER; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = Elem<T>::pack2(o[e] * norm, o[e + 1] * norm);
+        for (int e = 0; e < PER; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = Int4Param<T>::pack2_finite(o[e] * norm, o[e + 1] * norm);
     }
 }
 

@@ -4,7 +4,8 @@
 // group j holds a zero z (its smallest value), a scale s (the smallest value of the rows'
 // type that is at least (max - min) / 15) and codes c in 0 .. 15 that stand for s c + z.
 // z is one of the row's own values and s is rounded up, so every value lies in
-// [z, z + 15 s] and no code saturates: a value is off by s / 2 at most.
+// [z, z + 15 s] and no code saturates: a value is off by s / 2 at most.  z + 15 s itself may
+// lie past the type's range, by less than s / 2: what is read back stops at its largest finite value.
 //
 // A block's record of one KV head holds the codes of its tokens, head_dim / 2 bytes each,
 // then the (s, z) pairs of its tokens, head_dim / 32 of them each: 80 bytes a token at
@@ -36,6 +37,12 @@ struct Int4Param<__half> {
     static __device__ __forceinline__ float2 unpack(uint32_t w) {
         return __half22float2(*reinterpret_cast<const __half2 *>(&w));
     }
+    // two values rounded to the type, those past its range to its largest finite ones (NaN stays)
+    static __device__ __forceinline__ uint32_t pack2_finite(float a, float b) {
+        uint32_t d;
+        asm("cvt.rn.satfinite.f16x2.f32 %0, %2, %1;" : "=r"(d) : "f"(a), "f"(b));
+        return d;
+    }
 };
 
 template <>
@@ -45,6 +52,11 @@ struct Int4Param<__nv_bfloat16> {
     static __device__ __forceinline__ float value(uint32_t b) { return __uint_as_float(b << 16); }
     static __device__ __forceinline__ float2 unpack(uint32_t w) {
         return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    static __device__ __forceinline__ uint32_t pack2_finite(float a, float b) {
+        uint32_t d;
+        asm("cvt.rn.satfinite.bf16x2.f32 %0, %2, %1;" : "=r"(d) : "f"(a), "f"(b));
+        return d;
     }
 };
 

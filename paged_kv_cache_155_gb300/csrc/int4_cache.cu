@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kReadThreads) dequantise_blocks_int4_kernel(
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float a = static_cast<float>((codes >> (8 * e)) & 15u), b = static_cast<float>((codes >> (8 * e + 4)) & 15u);
-            w[e] = pkv::Elem<T>::pack2(fmaf(a, sz.x, sz.y), fmaf(b, sz.x, sz.y));
+            w[e] = pkv::Int4Param<T>::pack2_finite(fmaf(a, sz.x, sz.y), fmaf(b, sz.x, sz.y));
         }
         if (i < total) to[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
