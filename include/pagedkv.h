@@ -598,12 +598,13 @@ PKV_API pkv_status pkv_paged_attention_tree(
  *   accepted       [num_seqs][max_accepted] int32, device: chunk tokens in ascending
  *                  order.  One that does not ascend or lies outside the chunk raises
  *                  PKV_DEVERR_KEPT and is skipped (the rows behind it are then
- *                  unspecified); a length that does not fit raises it too and moves nothing.
+ *                  unspecified); a length that does not fit raises it too and counts as 0.
  *   query_start, context_lens, max_query_len, max_context_len   as
  *                  pkv_paged_attention_tree; a sequence out of contract raises
  *                  PKV_DEVERR_CONTEXT_LEN and is left as it is.
- *   new_context_lens   [num_seqs] int32, device, or NULL: the lengths afterwards; must
- *                  not overlap context_lens (PKV_ERR_INVALID_ARG).
+ *   new_context_lens   [num_seqs] int32, device, or NULL: the lengths afterwards, of a
+ *                  sequence out of contract the length that it came with; must not
+ *                  overlap context_lens (PKV_ERR_INVALID_ARG).
  * The blocks that get rows must belong to their sequence alone (pkv_bm_make_private).
  */
 PKV_API pkv_status pkv_tree_commit(void *k_cache, void *v_cache, int64_t num_blocks,

@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
     const bool lead = threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0;
     if (q0 < 0 || chunk < 0 || chunk > p.qlen_cap || base < 0 || len > p.len_cap) {
         if (lead) pkv::raise_flag(p.status, PKV_DEVERR_CONTEXT_LEN);
+        if (lead && p.new_context_lens) p.new_context_lens[seq] = len;
         return;
     }
     int n = p.accepted_lens[seq];
