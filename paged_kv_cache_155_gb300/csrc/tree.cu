@@ -38,13 +38,14 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
     pkv::pdl_wait();
     const int seq = blockIdx.z;
     const int q0 = p.query_start[seq], q1 = p.query_start[seq + 1], len = p.context_lens[seq];
-    const int chunk = q1 - q0, base = len - chunk;
     const bool lead = threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0;
-    if (q0 < 0 || chunk < 0 || chunk > p.qlen_cap || base < 0 || len > p.len_cap) {
+    // (compared before they are subtracted: any values may stand here)
+    if (q0 < 0 || q1 < q0 || q1 - q0 > p.qlen_cap || len < q1 - q0 || len > p.len_cap) {
         if (lead) pkv::raise_flag(p.status, PKV_DEVERR_CONTEXT_LEN);
         if (lead && p.new_context_lens) p.new_context_lens[seq] = len;
         return;
     }
+    const int chunk = q1 - q0, base = len - chunk;
     int n = p.accepted_lens[seq];
     if (n < 0 || n > p.max_accepted || n > chunk) {
         if (lead) pkv::raise_flag(p.status, PKV_DEVERR_KEPT);

@@ -29,3 +29,18 @@ def test_every_sequence_gets_a_length():
         assert got.tolist() == [6, 3, 17, 5, 1]
         before[0, :, :, 4], before[0, :, :, 5] = before[0, :, :, 6], before[0, :, :, 7]
         assert torch.equal(kv, before)
+
+
+def test_lengths_and_starts_of_any_value():
+    """Differences of what the arrays hold that do not fit 32 bits are refused like any other."""
+    low, high = -2 ** 31, 2 ** 31 - 1
+    for lens, starts, good in (([low, low + 3, -1, high, 9], [0, 5, 10, 15, 20, 25], [4]),
+                               ([9, 9, 9, 9, 9], [0, 5, low, high, 0, 5], [0, 4]),
+                               ([low, high, 16, low + 5, 9], [-5, 0, 0, low, high, 5], [])):
+        new, kv, before = _commit(lens, starts, [[2, 3, 1]] * 5, [2] * 5)
+        assert pkv.get_device_error(device())[1] == ["context_len"]
+        want = list(lens)
+        for i in good:
+            want[i] = 6  # four cached tokens and two nodes
+            before[2 * i, :, :, 4], before[2 * i, :, :, 5] = before[2 * i, :, :, 6], before[2 * i, :, :, 7]
+        assert new.tolist() == want and torch.equal(kv, before)
