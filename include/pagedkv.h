@@ -604,7 +604,7 @@ PKV_API pkv_status pkv_paged_attention_tree(
  *                  PKV_DEVERR_CONTEXT_LEN and is left as it is.
  *   new_context_lens   [num_seqs] int32, device, or NULL: the lengths afterwards, of a
  *                  sequence out of contract the length that it came with; must not
- *                  overlap context_lens (PKV_ERR_INVALID_ARG).
+ *                  overlap the other index arrays (PKV_ERR_INVALID_ARG).
  * The blocks that get rows must belong to their sequence alone (pkv_bm_make_private).
  */
 PKV_API pkv_status pkv_tree_commit(void *k_cache, void *v_cache, int64_t num_blocks,

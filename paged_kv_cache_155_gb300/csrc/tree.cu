@@ -215,10 +215,15 @@ PKV_API pkv_status pkv_tree_commit(void *k_cache, void *v_cache, int64_t num_blo
           reinterpret_cast<uintptr_t>(context_lens) | reinterpret_cast<uintptr_t>(accepted) |
           reinterpret_cast<uintptr_t>(accepted_lens) | reinterpret_cast<uintptr_t>(new_context_lens)) & 3u))
         return PKV_ERR_INVALID_ARG;
-    // every CTA of a sequence reads its length: the new ones need a place of their own
-    const uintptr_t a = reinterpret_cast<uintptr_t>(context_lens), b = reinterpret_cast<uintptr_t>(new_context_lens);
-    const uintptr_t bytes = 4 * static_cast<uintptr_t>(num_seqs);
-    if (new_context_lens && a < b + bytes && b < a + bytes) return PKV_ERR_INVALID_ARG;
+    // every CTA of a sequence reads its entries of these: the new lengths need a place of their own
+    auto meets = [&](const int32_t *in, int64_t count) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(new_context_lens);
+        return a < b + 4 * static_cast<uintptr_t>(num_seqs) && b < a + 4 * static_cast<uintptr_t>(count);
+    };
+    const int64_t seqs = num_seqs;
+    if (new_context_lens && (meets(context_lens, seqs) || meets(query_start, seqs + 1) || meets(accepted_lens, seqs) ||
+                             meets(accepted, seqs * max_accepted) || meets(block_tables, seqs * max_blocks_per_seq)))
+        return PKV_ERR_INVALID_ARG;
     unsigned int *status = pkv::status_word_ptr();
     if (!status) return PKV_ERR_CUDA;
     const int row_vecs = head_dim * elem / 16;

@@ -1175,7 +1175,7 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torc
                 max_context_len: int) -> torch.Tensor:
     """Move the K and V rows of each sequence's accepted path (chunk tokens, ascending: accepted
     int32 [B, n], accepted_lens int32 [B]) to the front of its chunk, in place; returns the
-    context lengths afterwards (``new_context_lens``, which must not be ``context_lens``).
+    context lengths afterwards (``new_context_lens``, which must not overlap the other index tensors).
     16-bit and INT8 caches; the blocks that get rows must belong to their sequence alone."""
     return prepare_tree_commit(k_cache, v_cache, block_tables, query_start, context_lens, accepted, accepted_lens,
                                new_context_lens, max_query_len=max_query_len, max_context_len=max_context_len)()
@@ -1196,8 +1196,11 @@ def prepare_tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tabl
     for name, t in (("accepted_lens", accepted_lens), ("new_context_lens", new_context_lens)):
         if t.dtype != torch.int32 or t.numel() != b or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 [num_seqs]")
-    if abs(new_context_lens.data_ptr() - context_lens.data_ptr()) < 4 * b:
-        raise ValueError("new_context_lens must not overlap context_lens")
+    at = new_context_lens.data_ptr()
+    for name, t in (("context_lens", context_lens), ("query_start", query_start), ("accepted_lens", accepted_lens),
+                    ("accepted", accepted), ("block_tables", block_tables)):
+        if b and t.data_ptr() < at + 4 * b and at < t.data_ptr() + 4 * t.numel():
+            raise ValueError(f"new_context_lens must not overlap {name}")
     _one_device(k_cache, v_cache=v_cache, block_tables=block_tables, query_start=query_start, context_lens=context_lens,
                 accepted=accepted, accepted_lens=accepted_lens, new_context_lens=new_context_lens)
     args = (k_cache.data_ptr(), v_cache.data_ptr(), nb, stride, hkv, d, bs, block_tables.data_ptr(),
