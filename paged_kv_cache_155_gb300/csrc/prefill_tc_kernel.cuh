@@ -157,10 +157,10 @@ __device__ __forceinline__ PrefillSeqVals prefill_seq_vals(const PrefillParams &
 __device__ __forceinline__ bool prefill_seq(const PrefillParams &p, const PrefillSeqVals &v, int &q0,
                                             int &chunk, int &len) {
     q0 = v.q0;
-    chunk = v.q1 - v.q0;
+    chunk = static_cast<int>(static_cast<unsigned>(v.q1) - static_cast<unsigned>(v.q0));
     len = v.len;
-    return q0 >= 0 && chunk >= 0 && v.q1 <= p.num_rows && chunk <= p.qlen_cap && len >= chunk &&
-           len <= p.len_cap;
+    // (q0 <= q1: a difference that does not fit 32 bits is none)
+    return q0 >= 0 && v.q1 >= q0 && v.q1 <= p.num_rows && chunk <= p.qlen_cap && len >= chunk && len <= p.len_cap;
 }
 
 // Scored form: the tokens that chunk tokens j0 .. j1 of a sequence see between them,
