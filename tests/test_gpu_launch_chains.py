@@ -100,7 +100,7 @@ def test_behind_a_kernel_that_lets_it_start_early(first, second):
     with torch.cuda.graph(graph):
         produce()
         call()
-    for _ in range(3):
+    for _ in range(TIMES):
         reset()
         graph.replay()
         torch.cuda.synchronize()
