@@ -503,11 +503,13 @@ PKV_API pkv_status pkv_paged_attention_decode_scored_int8(
 /* ------------------------------------------------------------------------
  * A sliding window with a few first tokens that stay visible (attention sinks): a
  * query at position p sees the tokens t <= p with
- *     t < sinks   or   t > p - window        (window >= 1, sinks >= 0),
- * so an endless stream keeps a bounded cache.  Blocks that lie wholly between the
- * first tokens and the window are not read and their table entries are never
- * dereferenced: they may be freed.  What their remaining rows hold does not
- * matter for the decode (NaN and infinities included).
+ *     t < sinks   or   t > p - window        (window >= 1, sinks >= 0).
+ * Blocks that lie wholly between the first tokens and the window are not read and
+ * their table entries are never dereferenced, so a caller who places blocks itself may
+ * give them to others, and an endless stream then needs a bounded number of blocks
+ * (its table still has an entry per block of the whole stream).  pkv_bm_* gives back whole
+ * sequences and tails only.  What the remaining rows between hold does not matter
+ * for the decode (NaN and infinities included).
  * ------------------------------------------------------------------------ */
 
 /* Workspace of pkv_paged_attention_decode_sinks (int8_cache 0) or its INT8-cache

@@ -88,7 +88,7 @@ constexpr int kMinAutoPartition = 256; // tokens: below this the per-CTA set-up 
 constexpr int kMergeShare = 32;        // a partition's K/V bytes >= this x its partial bytes
 constexpr double kScoredFillSlack = 0.03;
 constexpr double kLaneFillSlack = 0.05;  // the sink form's lane loops
-constexpr int kShortSpan = 2304;         // tokens of a sink form's span
+constexpr int kShortSpan = 2304;         // tokens of a sink form's span that need not fill the SMs well
 constexpr double kFillSlack = 0.15;    // wave fill given up for fewer, longer partitions (two-per-SM forms)
 
 // Decode CTAs resident per SM for each kernel form (their stage budgets and
@@ -111,7 +111,7 @@ int scored_heads_per_block_for(int group, bool int8_kv) {
 // The sink form over an INT8 cache, whose scores take two products per code (the query and its remainder):
 // the warp MMAs, with two or three of their four head rows empty, for two heads, and for one where a block's
 // rows of a head are 2 KB or more.  Measured, MMAs / lane loops, 16 x 4112 visible tokens of 32 KV heads of 64:
-// two heads 68.2 / 93.9 us; one head, blocks of 32 56.3 / 55.2, of 16 68.0 / 60.6, of 8 105 / 80.6;
+// two heads 68.2 / 93.9 us; one head, blocks of 32 56.3 / 55.2, of 16 68.0 / 60.8, of 8 105 / 80.6;
 // 8 x 4112 of heads of 128, blocks of 16 52.9 / 55.8.
 int sink_heads_per_block_for(int group, bool int8_kv, int head_dim, int block_size) {
     if (int8_kv && (group == 2 || (group == 1 && head_dim * block_size >= 2048))) return 4;
@@ -193,12 +193,17 @@ pkv_status plan_decode(int num_seqs, int num_q_heads, int num_kv_heads, int head
         // partitions within kScoredFillSlack of the best.  Measured: 32 x 4096 tokens of 32
         // heads in 2 instead of 3 partitions 317 us against 328; 2 x 32768 tokens of 64 / 8
         // heads in 57 instead of 61 (exactly two waves) 55.6 against 62.0.
-        // The sink form's spans are alike, windows that are full, so splitting them evens nothing out: one partition each,
-        // without a merge, wherever that fills the SMs half and the spans are short, or fills them well.  (Warp MMAs want
-        // full waves.)  Measured, one / split: INT8, 32 heads of 64, window 1024, 16 contexts 21.6 / 27.2 us, 64 contexts
-        // 60.5 / 78.4; bf16 32 / 8 heads of 128, window 1024, 48 contexts 35.1 / 40.3, but 64 (1.1 waves) 55.5 / 49.5;
-        // window 4096, 16 contexts of 32 INT8 heads in blocks of 8 (0.56 waves) 97.9 / 87.6.  Else, lane loops take few
-        // partitions that fill their waves: 16 contexts of 32 INT8 heads of 64, window 4096, in 5 63.9, in 10 69.0.
+        // The sink form's spans are alike as long as the windows are full, and splitting them then evens nothing out: one
+        // partition each, without a merge, wherever that fills the SMs half and the spans are short, or fills them well.  (Warp
+        // MMAs want full waves.)  Measured, one / the best split: INT8, 32 heads of 64, window 1024, 16 contexts (0.56 waves)
+        // 21.2 / 25.1 us, 64 contexts 60.5 / 78.4; bf16 32 / 8 heads of 128, window 1024, 52 contexts (0.91 waves) 37.4 / 41.9, but
+        // 64 (1.1 waves) 55.5 / 49.5.  At 0.56 waves and 4096 tokens INT8 wants the split, 68.5 / 61.2 (in blocks of 8 97.9 /
+        // 87.6), and at 3000 52.0 / 49.0; bf16 does not, 62.5 / 65.3 and 82.1 / 84.5: kShortSpan stays below both.
+        // Contexts shorter than the window, which differ, are not looked at (their lengths are on the device), and there
+        // the longest decides: 52 bf16 contexts of up to 2288 tokens, evenly spread, 49.4 / 51.1, but one of 2288 among ones
+        // of up to 572 36.3 / 20.1; 32 of them 36.2 / 34.6 and 34.5 / 16.9.  A caller who has such a batch gives partition_size.
+        // Else, lane loops take few partitions that fill their waves: 16 contexts of 32 INT8 heads of 64, window 4096, in 5
+        // 61.2, in 8 67.1.
         const bool lanes = sinks && gh < 4;
         const double waves = static_cast<double>(units) / static_cast<double>(slots);
         const int64_t whole = (len + align - 1) / align * align;

@@ -21,7 +21,7 @@
 //    the odd k (group 2 i) and four that are zero in the even k (group 2 i + 1).  So words enter the MMAs
 //    as they lie, without the byte permutes that sort them by group, and a lane scales two groups instead of four:
 //    half the scales, weights and accumulators.  (64 x 4096 tokens of 32 / 8 heads 69 us, sorted words 78; 64 x 100 to
-//    2048 tokens of 32 heads of 64 61 and 65.)
+//    2048 tokens of 32 heads of 64 61 and 65; both without a test of V's scales.)
 //  * Widening costs a mask: a nibble at bits 0 .. 3 or 4 .. 7 of a 16-bit word is a subnormal fp16
 //    number, exactly c 2^-24 or c 2^-20, and MMAs take those as they are (codes_f16).  K's factor 16
 //    between the two is in the query, V's is applied to the output channel, whose accumulator holds
@@ -44,9 +44,9 @@
 //    ahead; the ring runs on from one unit to the next.  A stage is one softmax step.
 //  * The token of an MMA row is chosen so that V's four token rows of a load lie side by side
 //    (token_of_row): two-way instead of four-way shared-memory conflicts.
-// Measured: 64 x 4096 tokens of 32 / 8 heads of 128, fp16: 68 us (0.73 of measured HBM; 57 us, 0.87, per
-// 64 x 4096 further tokens, so 11 fixed); with eight columns and
-// sorted words it was 55 us without the arithmetic and 68 without the copies.
+// Measured: 64 x 4096 tokens of 32 / 8 heads of 128, fp16: 70 us (0.71 of measured HBM; 59 us, 0.84, per
+// 64 x 4096 further tokens, so 11 fixed); with eight columns and sorted words, and without a test of V's
+// scales, it was 55 us without the arithmetic and 68 without the copies.
 #pragma once
 
 #include "decode_kernel.cuh"

@@ -3,7 +3,7 @@
 //   pkv_dequantise_blocks_int4    blocks of a 4-bit pool -> blocks of a 16-bit pool
 // Both move a few bytes per value and are bound by memory: 2 + 5/8 bytes a value each way.  They are launched
 // ahead, like the other short kernels that follow one another in a step, and wait for the kernel before them with
-// their blocks in place (8192 tokens written and read back: 16.4 us instead of 21.3 for the two).
+// their blocks in place (8192 tokens written and read back: 15.6 us one behind the other, 21.3 launched in the usual way).
 #include <type_traits>
 
 #include "int4.cuh"
@@ -98,7 +98,7 @@ __device__ __forceinline__ void int4_quantise(const uint4 (&row)[2], uint32_t (&
 // A thread quantises 16 channels of one row of K and of V; the rows of a token and then the tokens follow one
 // another.  Lanes 2 j + i hold channels 16 i .. of group j; the lanes of a row's groups trade words, so
 // that each stores eight bytes side by side (all groups of a unit, or of two).  Bound by arithmetic:
-// 8192 tokens of 8 heads of 128, bf16 8.3 us, 0.78 of measured HBM (with eight channels per lane and the remainder's comparison instead
+// 8192 tokens of 8 heads of 128, bf16 8.0 us, 0.81 of measured HBM (with eight channels per lane and the remainder's comparison instead
 // of the quotient's correction 15.3, with a division and a CTA per token 22).
 constexpr int kWriteThreads = 128;
 template <typename T, int D>

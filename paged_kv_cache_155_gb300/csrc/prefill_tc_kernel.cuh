@@ -876,8 +876,10 @@ __global__ void __launch_bounds__(384, 1)
         uint64_t *empty = kv ? v_empty : k_empty;
         const CUtensorMap *map = kv ? &tmap_v : &tmap_k;
         unsigned char *ring = sm + (kv ? L::kOffV : L::kOffK);
-        // every row tile of the sequence reads it; a tree's few do at the same time, or once (64 x 16 nodes behind
-        // 1024-4096 tokens 122 us, evicted last 137)
+        // every row tile of the sequence reads it; a tree's do so two at a time, and drafts have one or two mostly, so that
+        // nothing reads it again: evicted first / last, 64 / 8 heads, one row tile (64 x 16 nodes behind 1024-4096 tokens) 124 / 133
+        // us, two (16 x 32 behind 4096-8192) 106 / 107.  With four a later pair does read it again, and loses 2%: 16 x 63
+        // nodes 230 / 226, 64 x 64 behind 1024 180 / 176.
         const uint64_t policy = kTree ? l2_policy_evict_first() : l2_policy_evict_last();
         const uint64_t q_policy = l2_policy_evict_first();
         int last_issue[4] = {-1, -1, -1, -1};

@@ -1000,7 +1000,8 @@ def paged_attention_decode_sinks(q: torch.Tensor, k_cache: torch.Tensor, v_cache
                                  sinks: int, max_context_len: Optional[int] = None, partition_size: int = 0,
                                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """paged_attention_decode over the last ``window`` tokens of each context and its first
-    ``sinks`` ones; the blocks between are not read and may be freed."""
+    ``sinks`` ones; the blocks between are not read, and a caller who places blocks itself may give them
+    to others."""
     return prepare_paged_attention_decode_sinks(q, k_cache, v_cache, block_tables, context_lens, scale, out,
                                                 window=window, sinks=sinks, max_context_len=max_context_len,
                                                 partition_size=partition_size, workspace=workspace)()
