@@ -279,7 +279,8 @@ PKV_API pkv_status pkv_paged_attention_decode_int8(
 /*
  * pkv_reshape_and_cache_int4 -- pkv_reshape_and_cache into a 4-bit cache: the rows
  * k_new, v_new ([num_tokens][num_kv_heads][head_dim], dtype) quantised as above
- * and stored at their slots.  Slot rules and errors as pkv_reshape_and_cache;
+ * and stored at their slots.  Slot rules and errors as pkv_reshape_and_cache (two
+ * tokens that share a slot may leave codes of one and scales of the other);
  * num_kv_heads <= 65535, num_tokens * num_kv_heads <= 2^31 - 256.
  */
 PKV_API pkv_status pkv_reshape_and_cache_int4(const void *k_new, const void *v_new,

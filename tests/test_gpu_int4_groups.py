@@ -22,6 +22,8 @@ def _v(n, hkv, d, powers, kind, dtype, g):
     factor = torch.exp2(p[at]).expand(n, -1).clone()
     if kind == "late":  # ordinary rows but for a few
         factor[(t != n // 2) & (t != n - 1)] = 2.0 ** powers[0]
+    if kind == "offsets":  # zeros much larger than the scales, of either sign
+        x = (2 + x.clamp(-1, 1) / 8) * (1 - 2 * (t % 2))[:, None, None, None]
     x *= factor[:, None, :, None]
     if kind == "zeros":  # whole groups, and whole rows, of one value
         x[t % 3 == 0, :, 0] = 0
@@ -62,7 +64,7 @@ SHAPES = [(3, 3, 64, 8), (4, 1, 128, 16), (6, 2, 128, 32), (8, 1, 128, 8), (14, 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("hq,hkv,d,bs", SHAPES)
-@pytest.mark.parametrize("kind", ["apart", "turns", "late", "zeros"])
+@pytest.mark.parametrize("kind", ["apart", "turns", "late", "zeros", "offsets"])
 def test_groups_of_different_scales(hq, hkv, d, bs, kind, dtype):
     for i, powers in enumerate(APART + FAR[dtype]):
         run(dtype, hq, hkv, d, bs, [1, 2, 17, 33, 150, 64, 400], powers, kind, seed=hq + d + i)
